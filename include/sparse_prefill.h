@@ -321,6 +321,69 @@ sps_status sps_kv_append(const sps_plan* plan, const void* k_new, const void* v_
                          void* v_scales, void* workspace, sps_stream_t stream);
 
 /*
+ * The rotation of queries and keys by position (host struct; its pointers are device memory).
+ *   inv_freq     device FP32 [rotary_dim / 2]: angle per position of each pair, finite (a scaled
+ *                or interpolated schedule is one more set of frequencies)
+ *   positions    device int32 [num_axes][T]: each token's position on each axis (time, height,
+ *                width, ...), any 32-bit value; NULL: the token's cache position on every axis
+ *   rotary_dim   R: the first R dims of a head are rotated, the others pass through; a multiple
+ *                of 16, 0 (no rotation) .. head_dim
+ *   num_axes     1 .. 4
+ *   interleaved  pair j is dims (2 j, 2 j + 1) if non-zero, else (j, j + R / 2)
+ *   pair_axis    axis of each pair, in [0, num_axes)
+ * Pair j of a token turns by positions[pair_axis[j]] * inv_freq[j] radians:
+ * (a, b) -> (a cos - b sin, b cos + a sin).  The angle is reduced exactly (in 64-bit fractions of
+ * a turn), so far positions lose nothing.
+ */
+typedef struct {
+  const float* inv_freq;
+  const int32_t* positions;
+  int32_t rotary_dim;
+  int32_t num_axes;
+  int32_t interleaved;
+  uint8_t pair_axis[64];
+} sps_rope;
+
+/*
+ * sps_qk_norm_rope -- queries and keys of the batch's new tokens, before indexer_scores and the
+ * attention: each head's row is divided by its root mean square, multiplied by a weight and
+ * rotated, in one pass, in FP32 with one rounding at the end.
+ *   q            device BF16, token i's H rows at q + i * q_token_stride (elements); k likewise
+ *                with H_kv rows, or NULL (then k_out is NULL too)
+ *   q_weight, k_weight  device FP32 [D], or NULL: no norm of those rows
+ *   eps          added to the mean square (>= 0)
+ *   rope         or NULL: no rotation
+ *   q_out        device, [T][H][D] at q_out_token_stride: SPS_BF16, or SPS_E4M3 codes of
+ *                y / q_scale (FP32 division, nearest even, saturating; q_scale finite and > 0)
+ *   k_out        device BF16, at k_out_token_stride
+ * Buffers are 16-byte aligned; strides are multiples of 8 elements (16 for E4M3 codes) and at
+ * least the rows of a token, so q and k may be views of one projection's output.  An output may
+ * be its own input (same address and stride); other overlaps are not allowed.  `workspace` is the
+ * plan's uploaded workspace (token positions).
+ */
+sps_status sps_qk_norm_rope(const sps_plan* plan, const void* q, int64_t q_token_stride,
+                            const void* k, int64_t k_token_stride, const float* q_weight,
+                            const float* k_weight, float eps, const sps_rope* rope, void* q_out,
+                            int64_t q_out_token_stride, sps_dtype q_out_dtype, float q_scale,
+                            void* k_out, int64_t k_out_token_stride, void* workspace,
+                            sps_stream_t stream);
+
+/*
+ * sps_kv_append_rope -- sps_kv_append with the key's norm and rotation on the way: key rows as
+ * sps_qk_norm_rope makes them (k_weight NULL: no norm; rope NULL: no rotation), value rows as they
+ * are, into the slots sps_kv_append writes.  A BF16 cache takes the FP32 result rounded once; an
+ * NVFP4 cache takes it quantised by sps_kv_append's rule, with no rounding before that.
+ *   k_new, v_new  device BF16, token i's H_kv rows at + i * {k,v}_token_stride elements (16-byte
+ *                 aligned, strides multiples of 8, >= H_kv * D)
+ * The other arguments and the device status are those of sps_kv_append.
+ */
+sps_status sps_kv_append_rope(const sps_plan* plan, const void* k_new, int64_t k_token_stride,
+                              const void* v_new, int64_t v_token_stride, const float* k_weight,
+                              float eps, const sps_rope* rope, const int32_t* page_table,
+                              void* k_cache, void* v_cache, void* k_scales, void* v_scales,
+                              void* workspace, sps_stream_t stream);
+
+/*
  * sps_quantize_e4m3 -- per-tensor E4M3 query codes: codes[i] = E4M3(x[i] / scale) (FP32
  * division, nearest even, saturating at 448); x BF16, n a multiple of 16, both 16-byte
  * aligned, scale finite and > 0 (the pages' E4M3 query with its per-tensor scale).

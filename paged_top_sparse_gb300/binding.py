@@ -53,6 +53,12 @@ class PlanInfo(ctypes.Structure):
         "off_entries", "off_fwd_task_count")]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * 64)]
+
+
 _lib = None
 
 
@@ -91,6 +97,10 @@ def lib(path: str | None = None):
     L.sps_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.sps_quantize_e4m3.argtypes = [vp, i64, f32, vp, vp]
     L.sps_absmax_bf16.argtypes = [vp, i64, vp, vp]
+    rp = ctypes.POINTER(RopeArgs)
+    L.sps_qk_norm_rope.argtypes = [vp, vp, i64, vp, i64, vp, vp, f32, rp, vp, i64, ctypes.c_int,
+                                   f32, vp, i64, vp, vp]
+    L.sps_kv_append_rope.argtypes = [vp, vp, i64, vp, i64, vp, f32, rp, vp, vp, vp, vp, vp, vp, vp]
     L.partial_combine_bf16.argtypes = L.partial_combine.argtypes
     L.partial_combine_f16.argtypes = L.partial_combine.argtypes
     L.sparse_prefill_fwd_noalloc.argtypes = [vp, vp, f32, vp, vp, vp, vp, vp, vp, vp, i64, vp, i64,
@@ -147,6 +157,7 @@ class Plan:
                                      ctypes.byref(ws)))
         self.workspace_bytes = ws.value
         self.head_dim, self.top_k = head_dim, top_k
+        self.num_tokens = sum(int(x) for x in q_lens)
 
     def info(self) -> PlanInfo:
         inf = PlanInfo()
@@ -261,6 +272,78 @@ def sps_kv_append(plan: Plan, k_new, v_new, page_table, k_cache, v_cache, k_scal
     _check(lib().sps_kv_append(plan.handle, _ptr(k_new), _ptr(v_new), _ptr(page_table),
                                _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
                                _ptr(workspace), _stream(stream)))
+
+
+class Rope:
+    """A rotation by position (``sps_rope``): ``inv_freq`` FP32 [rotary_dim / 2] and, where the
+    tokens have positions of their own, ``positions`` int32 [axes][T] (one axis: also [T]), both
+    on the device and kept alive here; ``pair_axis``: the axis of each pair (default 0)."""
+
+    def __init__(self, inv_freq, positions=None, pair_axis=None, interleaved=False):
+        self.inv_freq, self.positions = inv_freq, positions
+        n, axes = inv_freq.numel(), 1
+        _expect(inv_freq, "float32", "inv_freq")
+        if n > 64:
+            raise ValueError("at most 64 pairs (rotary_dim 128)")
+        if positions is not None:
+            _expect(positions, "int32", "positions")
+            axes = positions.shape[0] if positions.dim() == 2 else 1
+        ax = [int(a) for a in pair_axis] if pair_axis is not None else [0] * n
+        if len(ax) != n or any(not 0 <= a < 256 for a in ax):
+            raise ValueError("pair_axis needs one axis per pair")
+        self.args = RopeArgs(_ptr(inv_freq), _ptr(positions), 2 * n, axes, int(bool(interleaved)),
+                             (ctypes.c_uint8 * 64)(*ax))
+
+
+def _expect(t, dtype, name):
+    """A contiguous tensor of the named torch dtype (or None)."""
+    if t is not None and (str(t.dtype) != "torch." + dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor")
+
+
+def _rope(rope, plan):
+    if rope is None:
+        return None
+    if rope.positions is not None and rope.positions.shape[-1] != plan.num_tokens:
+        raise ValueError(f"positions must be [axes][{plan.num_tokens}]")
+    return ctypes.byref(rope.args)
+
+
+def _token_stride(t, plan, heads, name):
+    """Elements between the tokens of a [T][heads][D] view whose rows are contiguous."""
+    T, D = plan.num_tokens, plan.head_dim
+    if tuple(t.shape) != (T, heads, D) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must be [{T}][{heads}][{D}] with contiguous rows")
+    return t.stride(0) if T > 1 else heads * D
+
+
+def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_scale, k_out,
+                     workspace, stream=None):
+    """Norm per head and rotation of q [T][H][D] and k [T][H_kv][D] (or None); token strides come
+    from the tensors.  A one-byte ``q_out`` takes E4M3 codes of the result / ``q_scale``."""
+    H, G = plan.problem.num_q_heads, plan.problem.num_kv_heads
+    _expect(q_weight, "float32", "q_weight")
+    _expect(k_weight, "float32", "k_weight")
+    _check(lib().sps_qk_norm_rope(
+        plan.handle, _ptr(q), _token_stride(q, plan, H, "q"), _ptr(k),
+        0 if k is None else _token_stride(k, plan, G, "k"), _ptr(q_weight), _ptr(k_weight),
+        float(eps), _rope(rope, plan), _ptr(q_out), _token_stride(q_out, plan, H, "q_out"),
+        E4M3 if q_out.element_size() == 1 else BF16, float(q_scale), _ptr(k_out),
+        0 if k_out is None else _token_stride(k_out, plan, G, "k_out"), _ptr(workspace),
+        _stream(stream)))
+
+
+def sps_kv_append_rope(plan: Plan, k_new, v_new, k_weight, eps, rope, page_table, k_cache, v_cache,
+                       k_scales, v_scales, workspace, stream=None):
+    """``sps_kv_append`` with the key's norm and rotation on the way; k_new / v_new [T][H_kv][D]
+    may be views with a token stride."""
+    G = plan.problem.num_kv_heads
+    _expect(k_weight, "float32", "k_weight")
+    _check(lib().sps_kv_append_rope(
+        plan.handle, _ptr(k_new), _token_stride(k_new, plan, G, "k_new"), _ptr(v_new),
+        _token_stride(v_new, plan, G, "v_new"), _ptr(k_weight), float(eps), _rope(rope, plan),
+        _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        _ptr(workspace), _stream(stream)))
 
 
 def sps_quantize_e4m3(x_bf16, scale: float, codes, stream=None):

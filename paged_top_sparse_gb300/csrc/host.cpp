@@ -702,6 +702,127 @@ sps_status sps_kv_append(const sps_plan* pl, const void* k_new, const void* v_ne
                   "kv append launch");
 }
 
+namespace {
+
+// A caller's rotation checked and copied for the kernels; rope NULL: none.
+sps_status make_rope(const sps_rope* rope, int head_dim, const char* who, DevRope* out) {
+  *out = DevRope{};
+  if (!rope) return SPS_OK;
+  const int r = rope->rotary_dim;
+  if (r < 0 || r > head_dim)
+    return fail(SPS_EINVAL, "%s: rotary_dim %d outside [0, head_dim]", who, r);
+  if (r % 16) return fail(SPS_EUNSUPPORTED, "%s: rotary_dim must be a multiple of 16", who);
+  if (rope->num_axes < 1 || rope->num_axes > 4)
+    return fail(SPS_EINVAL, "%s: num_axes must be in [1, 4] (got %d)", who, rope->num_axes);
+  if (r == 0) return SPS_OK;
+  if (!rope->inv_freq || !aligned(rope->inv_freq, 4) ||
+      (rope->positions && !aligned(rope->positions, 4)))
+    return fail(SPS_EINVAL, "%s: inv_freq must be given, it and positions 4-byte aligned", who);
+  for (int j = 0; j < r / 2; ++j)
+    if (rope->pair_axis[j] >= rope->num_axes)
+      return fail(SPS_EINVAL, "%s: pair_axis[%d] = %d outside [0, num_axes)", who, j,
+                  rope->pair_axis[j]);
+  out->inv_freq = rope->inv_freq;
+  out->positions = rope->positions;
+  out->rot = r;
+  memcpy(out->axis, rope->pair_axis, sizeof out->axis);
+  return SPS_OK;
+}
+
+bool rows_ok(const void* x, int64_t stride, int64_t row_elems, int64_t multiple) {
+  return x && aligned(x, 16) && stride >= row_elems && stride % multiple == 0;
+}
+
+}  // namespace
+
+sps_status sps_qk_norm_rope(const sps_plan* pl, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const float* q_weight, const float* k_weight,
+                            float eps, const sps_rope* rope, void* q_out, int64_t q_out_stride,
+                            sps_dtype q_out_dtype, float q_scale, void* k_out,
+                            int64_t k_out_stride, void* ws, sps_stream_t stream) {
+  sps_status st = check_plan_ws(pl, ws);
+  if (st != SPS_OK) return st;
+  const sps_problem& p = pl->pb;
+  const bool e4m3 = q_out_dtype == SPS_E4M3;
+  if (!e4m3 && q_out_dtype != SPS_BF16)
+    return fail(SPS_EUNSUPPORTED, "sps_qk_norm_rope: q_out must be BF16 or E4M3");
+  if (!k != !k_out) return fail(SPS_EINVAL, "sps_qk_norm_rope: k and k_out go together");
+  const int64_t qn = (int64_t)p.num_q_heads * p.head_dim, kn = (int64_t)p.num_kv_heads * p.head_dim;
+  if (!rows_ok(q, q_stride, qn, 8) || !rows_ok(q_out, q_out_stride, qn, e4m3 ? 16 : 8) ||
+      (k && (!rows_ok(k, k_stride, kn, 8) || !rows_ok(k_out, k_out_stride, kn, 8))))
+    return fail(SPS_EINVAL,
+                "sps_qk_norm_rope: buffers must be non-NULL and 16-byte aligned, token strides "
+                "multiples of 16 bytes and at least a token's rows");
+  if ((q_weight && !aligned(q_weight, 4)) || (k_weight && !aligned(k_weight, 4)))
+    return fail(SPS_EINVAL, "sps_qk_norm_rope: misaligned weight");
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(SPS_EINVAL, "sps_qk_norm_rope: eps must be finite and >= 0");
+  if (e4m3 && (!(q_scale > 0.f) || !std::isfinite(q_scale)))
+    return fail(SPS_EINVAL, "sps_qk_norm_rope: q_scale must be finite and > 0");
+  DevRope r;
+  st = make_rope(rope, p.head_dim, "sps_qk_norm_rope", &r);
+  if (st != SPS_OK) return st;
+  QkRopeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.q_out = q_out;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.eps = eps;
+  a.q_scale = q_scale;
+  return launched(launch_qk_norm_rope(make_dev_plan(pl, ws), r, a, rope && rope->interleaved, e4m3,
+                                      reinterpret_cast<cudaStream_t>(stream)),
+                  "q/k norm and rotation launch");
+}
+
+sps_status sps_kv_append_rope(const sps_plan* pl, const void* k_new, int64_t k_stride,
+                              const void* v_new, int64_t v_stride, const float* k_weight,
+                              float eps, const sps_rope* rope, const int32_t* page_table,
+                              void* k_cache, void* v_cache, void* k_scales, void* v_scales,
+                              void* ws, sps_stream_t stream) {
+  sps_status st = check_plan_ws(pl, ws);
+  if (st != SPS_OK) return st;
+  const sps_problem& p = pl->pb;
+  const bool nvfp4 = p.kv_dtype == SPS_NVFP4;
+  if (p.kv_dtype != SPS_BF16 && !nvfp4)
+    return fail(SPS_EUNSUPPORTED, "sps_kv_append_rope: the cache must be BF16 or NVFP4");
+  if (!page_table || !k_cache || !v_cache || (nvfp4 && (!k_scales || !v_scales)))
+    return fail(SPS_EINVAL, "sps_kv_append_rope: NULL pointer (an NVFP4 cache needs its scales)");
+  const int64_t kn = (int64_t)p.num_kv_heads * p.head_dim;
+  if (!rows_ok(k_new, k_stride, kn, 8) || !rows_ok(v_new, v_stride, kn, 8))
+    return fail(SPS_EINVAL,
+                "sps_kv_append_rope: k_new/v_new must be non-NULL and 16-byte aligned, token "
+                "strides multiples of 8 and at least num_kv_heads * head_dim");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(page_table, 4) ||
+      (k_weight && !aligned(k_weight, 4)))
+    return fail(SPS_EINVAL, "sps_kv_append_rope: misaligned cache, page table or weight");
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(SPS_EINVAL, "sps_kv_append_rope: eps must be finite and >= 0");
+  DevRope r;
+  st = make_rope(rope, p.head_dim, "sps_kv_append_rope", &r);
+  if (st != SPS_OK) return st;
+  KvRopeArgs a{};
+  a.k = static_cast<const uint16_t*>(k_new);
+  a.v = static_cast<const uint16_t*>(v_new);
+  a.k_weight = k_weight;
+  a.page_table = page_table;
+  a.kc = static_cast<uint8_t*>(k_cache);
+  a.vc = static_cast<uint8_t*>(v_cache);
+  a.ks = static_cast<uint8_t*>(k_scales);
+  a.vs = static_cast<uint8_t*>(v_scales);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.eps = eps;
+  return launched(launch_kv_append_rope(make_dev_plan(pl, ws), r, a, rope && rope->interleaved,
+                                        nvfp4, reinterpret_cast<cudaStream_t>(stream)),
+                  "kv append with rotation launch");
+}
+
 sps_status sps_quantize_e4m3(const void* x_bf16, int64_t n, float scale, void* codes,
                              sps_stream_t stream) {
   if (n < 0 || n % 16) return fail(SPS_EINVAL, "sps_quantize_e4m3: n must be a multiple of 16");

@@ -12,36 +12,11 @@
 //               shuffles and each lane writes its own packed codes.
 //   quantise    E4M3(x / scale) for BF16 x, 16 elements per thread.
 //   absmax      max |x| over BF16 values into one FP32 word (bit-ordered atomicMax).
-#include <cuda_fp16.h>
-
 #include "ptx.cuh"
 #include "sps_internal.h"
 
 namespace sps {
 namespace {
-
-__device__ __forceinline__ float bf16_to_f32(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
-
-// E4M3 code of x (round to nearest even, saturating).
-__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(x));
-  return r & 0xffu;
-}
-// Two E2M1 codes packed in a byte: lo in the low nibble (round to nearest even, saturating).
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, t};\n\t}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
-  return r & 0xffu;
-}
-// Value of an E4M3 code (exact).
-__device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)code));
-  return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
-}
 
 template <int D, bool NVFP4>
 __global__ void __launch_bounds__(256)

@@ -1,0 +1,62 @@
+// nvfp4.cuh -- conversion of NVFP4 tiles into tensor-core operand tiles, shared by the kernels
+// that read an NVFP4 cache in their loaders.
+#pragma once
+#include "ptx.cuh"
+
+namespace sps {
+
+// One NVFP4 tile (codes [128][D/2], then scales [128][D/16], in `raw`) into the operand tile
+// `dst`: 128 rows of D elements in the 128-byte-swizzled layout TMA writes, as FP16 products
+// code x scale (exact) in column blocks of 64 elements (16 KB each), or, with E4M3OUT, as those
+// products rounded to E4M3 (one 128-byte block per row; D = 128).  Thread t of nt converts the
+// 16-byte code chunks t, t + nt, ... (32 elements each).  Rows from `rows` on become zero, whatever
+// their codes and scales hold.
+template <int D, bool E4M3OUT>
+__device__ __forceinline__ void nvfp4_tile_convert(const uint8_t* raw, uint8_t* dst, int t, int nt,
+                                                   int rows = 128) {
+  constexpr int CPR = D / 32;  // code chunks per row
+  const uint8_t* scl = raw + 128 * D / 2;
+  for (int c = t; c < 128 * CPR; c += nt) {
+    const int row = c / CPR, i = c % CPR;
+    if (row >= rows) {
+#pragma unroll
+      for (int u = 0; u < (E4M3OUT ? 2 : 4); ++u) {
+        const int col = E4M3OUT ? 0 : 32 * i + 8 * u;
+        const uint32_t off = E4M3OUT ? sw128_offset(row, 2 * i + u)
+                                     : (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8);
+        *reinterpret_cast<uint4*>(dst + off) = make_uint4(0, 0, 0, 0);
+      }
+      continue;
+    }
+    const uint4 cw = reinterpret_cast<const uint4*>(raw)[c];
+    const uint32_t sb = *reinterpret_cast<const uint16_t*>(scl + row * (D / 16) + 2 * i);
+    const uint32_t s0 = cvt_e4m3x2((uint16_t)((sb & 0xffu) * 0x0101u));  // elements 0..15
+    const uint32_t s1 = cvt_e4m3x2((uint16_t)((sb >> 8) * 0x0101u));     // elements 16..31
+    const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+    uint32_t h[16];  // h[4 j + b]: elements 8 j + 2 b, +1 of the chunk
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        h[4 * j + b] = hmul2_u32(cvt_e2m1x2((uint16_t)((w[j] >> (8 * b)) & 0xffu)), j < 2 ? s0 : s1);
+    if (E4M3OUT) {
+      uint32_t e[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        e[u] = (uint32_t)cvt_f16x2_e4m3x2(h[2 * u]) | ((uint32_t)cvt_f16x2_e4m3x2(h[2 * u + 1]) << 16);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        *reinterpret_cast<uint4*>(dst + sw128_offset(row, 2 * i + u)) =
+            make_uint4(e[4 * u], e[4 * u + 1], e[4 * u + 2], e[4 * u + 3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int col = 32 * i + 8 * u;
+        *reinterpret_cast<uint4*>(dst + (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8)) =
+            make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+      }
+    }
+  }
+}
+
+}  // namespace sps

@@ -49,6 +49,8 @@ struct FwdTask {
 };
 
 // Everything a kernel needs about the plan, passed by value.
+struct AttCursor;
+struct AttMerge;
 struct DevPlan {
   int32_t batch, T, H, Hkv, Hg, D, K, max_pages, num_phys;
   int32_t num_buckets, max_entries, max_fwd_tasks, n_idx_tasks, total_pages;
@@ -90,6 +92,49 @@ struct DevPlan {
   // waits for its own K/V tiles), the K/V tiles of the item this many items ahead are
   // prefetched into L2 (0: none; the plan sets 1)
   int32_t fwd_prefetch;
+  // full attention: where each of its att_ctas blocks begins (block i runs up to where block
+  // i + 1 begins; [att_ctas + 1]), the tiles cut over blocks ([att_ctas]), and the rows a partial
+  // result of a cut tile may have
+  const AttCursor* att_starts;
+  const AttMerge* att_merges;
+  int32_t att_ctas, att_slot_rows;
+};
+
+// A dense attention work position: page `page` of query tile `tile` of head block `vg` (KV head
+// g = vg / head blocks per KV head) of request `req`; (batch, 0, 0, 0) is the end.
+struct AttCursor {
+  int32_t req, vg, tile, page;
+};
+// A query tile whose pages were cut over several blocks: blocks cta0 .. cta1 hold its pieces
+// (req < 0: unused entry).
+struct AttMerge {
+  int32_t req, vg, tile, cta0, cta1, pad;
+};
+
+// The rotation, as the kernels see it (sps_rope; rot 0: none).
+struct DevRope {
+  const float* inv_freq;     // [rot / 2]
+  const int32_t* positions;  // [axes][T], or null: the token's cache position on every axis
+  int32_t rot;
+  uint8_t axis[64];
+};
+struct QkRopeArgs {
+  const uint16_t *q, *k;  // k null: queries alone
+  const float *q_weight, *k_weight;
+  void* q_out;
+  uint16_t* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
+  float eps, q_scale;
+  int32_t rows_per_warp, splits;  // set by the launcher
+};
+struct KvRopeArgs {
+  const uint16_t *k, *v;
+  const float* k_weight;
+  const int32_t* page_table;
+  uint8_t *kc, *vc, *ks, *vs;
+  int64_t k_stride, v_stride;
+  float eps;
+  int32_t rows_per_warp, splits;
 };
 
 // Launch of `kern` that may overlap the previous kernel in the stream (programmatic stream
@@ -167,6 +212,18 @@ cudaError_t launch_kv_append(const DevPlan& p, bool nvfp4, const void* knew, con
 cudaError_t launch_quantize_e4m3(const void* in, int64_t n, float scale, void* out,
                                  cudaStream_t st);
 cudaError_t launch_absmax_bf16(const void* in, int64_t n, float* out, cudaStream_t st);
+
+// Norm per head and rotation of queries and keys, and the append with that rotation.
+cudaError_t launch_qk_norm_rope(const DevPlan& p, const DevRope& r, const QkRopeArgs& a,
+                                bool interleaved, bool e4m3, cudaStream_t st);
+cudaError_t launch_kv_append_rope(const DevPlan& p, const DevRope& r, const KvRopeArgs& a,
+                                  bool interleaved, bool nvfp4, cudaStream_t st);
+
+// Full attention over the paged cache (BF16 Q and cache, or E4M3 Q and NVFP4 cache).
+cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_t q_stride,
+                             float q_scale, const void* kc, const void* vc, const void* ks,
+                             const void* vs, const int32_t* page_table, void* out,
+                             int64_t out_stride, float* out_lse, void* scratch, cudaStream_t st);
 
 // Copy of n bytes from device-accessible page-locked host memory (src) to device memory (dst),
 // both 16-byte aligned, by a kernel rather than the copy engine.
