@@ -449,6 +449,40 @@ sps_status sparse_prefill_fwd_noalloc(const sps_plan* plan, const void* q, float
                                       sps_stream_t stream);
 
 /*
+ * paged_attention_fwd -- full causal attention of the batch's new tokens over the paged cache, for
+ * the layers that keep every page and for decode steps (the dense counterpart of steps 1 to 4;
+ * chunks and single tokens may be mixed in a batch): row r = (token, head h) at position t of its
+ * request reads the keys j <= t of KV head h / (H / H_kv),
+ *   out[r] = sum_j p_j v_j / sum_j p_j,  p_j = exp(softmax_scale * q_scale * q_r . k_j - max),
+ *   out_lse[r] = ln sum_j exp(softmax_scale * q_scale * q_r . k_j).
+ * The new tokens' own K/V are in the cache (sps_kv_append or sps_kv_append_rope).
+ *   q            device, the plan's q_dtype: BF16 or E4M3, token i's H rows at
+ *                q + i * q_token_stride (elements); 16-byte aligned, stride a multiple of 16 bytes
+ *   q_scale      per-tensor multiplier of the decoded q (1 for BF16), finite and > 0
+ *   k_cache, v_cache, k_scales, v_scales, page_table   as for sparse_prefill_fwd; slots behind a
+ *                request's last token may hold anything, NaN included, the others finite values
+ *   out_bf16     device BF16, token i's H rows at out_bf16 + i * out_token_stride (16-byte aligned,
+ *                stride a multiple of 8)
+ *   out_lse      device FP32 [T*H] or NULL
+ *   scratch      device, 256-byte aligned, paged_attention_scratch bytes, contents arbitrary:
+ *                partial results of tiles that are cut over the GPU
+ *   workspace    the plan's uploaded workspace
+ * Accumulation, maxima and sums are FP32; P is rounded to the 16-bit type of the second product
+ * (BF16; FP16 over an NVFP4 cache, whose code x scale products are exact there).  The result is the
+ * same bits from call to call.  A captured call may be replayed after another plan that differs
+ * in ctx_lens alone has been uploaded to the same workspace (a decode loop).  top_k is not used.
+ * A page-table entry outside [0, num_phys_pages) sets SPS_DEV_BAD_PAGE (the outputs are then
+ * undefined).
+ */
+sps_status paged_attention_scratch(const sps_plan* plan, size_t* scratch_bytes);
+sps_status paged_attention_fwd(const sps_plan* plan, const void* q, int64_t q_token_stride,
+                               float q_scale, const void* k_cache, const void* v_cache,
+                               const void* k_scales, const void* v_scales,
+                               const int32_t* page_table, void* out_bf16,
+                               int64_t out_token_stride, float* out_lse, void* scratch,
+                               size_t scratch_bytes, void* workspace, sps_stream_t stream);
+
+/*
  * sps_check_wait_timeout -- health check of the failure path every kernel relies on: a
  * one-block kernel waits on an mbarrier that nothing ever arrives on, through the same bounded
  * wait the pipelines use (their limit is 2 s; here `limit_ns`, 1 ms .. 10 s).  The wait gives

@@ -101,6 +101,9 @@ def lib(path: str | None = None):
     L.sps_qk_norm_rope.argtypes = [vp, vp, i64, vp, i64, vp, vp, f32, rp, vp, i64, ctypes.c_int,
                                    f32, vp, i64, vp, vp]
     L.sps_kv_append_rope.argtypes = [vp, vp, i64, vp, i64, vp, f32, rp, vp, vp, vp, vp, vp, vp, vp]
+    L.paged_attention_scratch.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+    L.paged_attention_fwd.argtypes = [vp, vp, i64, f32, vp, vp, vp, vp, vp, vp, i64, vp, vp,
+                                      ctypes.c_size_t, vp, vp]
     L.partial_combine_bf16.argtypes = L.partial_combine.argtypes
     L.partial_combine_f16.argtypes = L.partial_combine.argtypes
     L.sparse_prefill_fwd_noalloc.argtypes = [vp, vp, f32, vp, vp, vp, vp, vp, vp, vp, i64, vp, i64,
@@ -344,6 +347,26 @@ def sps_kv_append_rope(plan: Plan, k_new, v_new, k_weight, eps, rope, page_table
         _token_stride(v_new, plan, G, "v_new"), _ptr(k_weight), float(eps), _rope(rope, plan),
         _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
         _ptr(workspace), _stream(stream)))
+
+
+def paged_attention_scratch(plan: Plan) -> int:
+    """Bytes of device scratch that ``paged_attention_fwd`` needs for this plan."""
+    n = ctypes.c_size_t()
+    _check(lib().paged_attention_scratch(plan.handle, ctypes.byref(n)))
+    return n.value
+
+
+def paged_attention_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_scales, page_table,
+                        out, out_lse, scratch, workspace, stream=None):
+    """Full causal attention of q [T][H][D] over the paged cache into out [T][H][D] BF16 (both may
+    have a token stride) and, unless None, out_lse [T][H] FP32."""
+    H = plan.problem.num_q_heads
+    _expect(out_lse, "float32", "out_lse")
+    _check(lib().paged_attention_fwd(
+        plan.handle, _ptr(q), _token_stride(q, plan, H, "q"), float(q_scale), _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(out),
+        _token_stride(out, plan, H, "out"), _ptr(out_lse), _ptr(scratch),
+        scratch.numel() * scratch.element_size(), _ptr(workspace), _stream(stream)))
 
 
 def sps_quantize_e4m3(x_bf16, scale: float, codes, stream=None):

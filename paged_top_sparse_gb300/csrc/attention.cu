@@ -1,0 +1,756 @@
+// attention.cu -- full causal attention of a batch of new tokens (chunks and single tokens mixed)
+// over the paged K/V cache: out_r = sum_j softmax_j(scale q_r . k_j) v_j over the keys j <= t of the
+// row's request, and the log-sum-exp.
+//
+// Mathematics.  One pass over a row's pages keeps a reference maximum m, l = sum_j p_j and
+// O = sum_j p_j v_j with p_j = 2^((s_j - m) c), c = scale * q_scale * log2 e, all in FP32.  The
+// reference follows the running maximum lazily: O and l are rescaled only when the maximum has
+// grown by more than 2^8, so p stays at or below 2^8 and the tensor-memory round trip of O is rare.
+// P is rounded to the 16-bit type of V for the second product (BF16, or FP16 over an NVFP4 cache,
+// whose exact products FP16 holds); l sums the unrounded p.  FP16's narrow range is centred by a
+// factor 2^7 on p (largest 2^15, smallest normal 2^-14), which cancels in O / l.
+//
+// Rows.  The heads of one KV head's group share its keys, so a row tile packs TB tokens x HB heads
+// (HB = min(H / H_kv, 128), TB = 128 / HB) into the 128 rows of a tcgen05 accumulator; a work tile
+// is two of them (256 rows), fed by the same K and V tiles.
+//
+// Work.  The (tile, page) pairs of the batch in order (request, head block, tile, page) are cut into
+// equal runs, one per SM (att_starts, made with the plan): prompts, chunks, and a single token after
+// a long context all fill the GPU, and a tile cut by a run's end is merged from the partial results
+// of its pieces by a second small kernel.
+//
+// One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
+//   warp 0     page-table reads and the copies: Q tiles and the K, V tiles of a page into a ring
+//              (BF16: TMA with the 128-byte swizzle; NVFP4: codes and scales by bulk copies);
+//   warp 1     one thread issues every MMA: S_t = Q_t K^T, and O_t += P_t V with P in TMEM over S_t.
+//              With two row tiles their chains alternate, so one tile's products run under the
+//              other's softmax; with one row tile S alternates between S0 and S1 instead and the
+//              next page's S is computed under the present softmax;
+//   warp 2     rows of the last page behind the request's last token are zeroed in the V tile (an
+//              unwritten slot may hold NaN, and 0 * NaN would reach every row);
+//   warps 4-7, 8-11   softmax and epilogue of row tile 0 / 1, a thread per row;
+//   warps 12-15 (NVFP4)  conversion of E4M3 Q and NVFP4 K, V into FP16 operand tiles.
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "nvfp4.cuh"
+#include "ptx.cuh"
+#include "sps_internal.h"
+
+namespace sps {
+namespace {
+
+constexpr float kRescale = 8.f;   // log2 of the growth of the maximum that rescales O
+constexpr float kF16Bias = 7.f;   // log2 of the factor on FP16 p
+constexpr int kMaxCtas = 256;
+
+template <int D, bool QUANT>
+struct AttSmem {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int RAWB = 128 * D / 2 + 128 * D / 16;  // NVFP4 codes and scales of a tile
+  static constexpr int RS = QUANT ? 3 : 1;
+  static constexpr int kBudget = 227 * 1024 - 1024 - 1024;  // alignment slack, barriers
+  static constexpr int S0 = (kBudget - 2 * TILE - (QUANT ? RS * RAWB : 0)) / TILE;
+  static constexpr int STAGES = S0 > 8 ? 8 : S0;
+  static_assert(STAGES >= 4, "shared memory");
+  uint8_t q[2][TILE];
+  uint8_t kv[STAGES][TILE];
+  alignas(16) uint8_t raw[RS][QUANT ? RAWB : 16];
+  uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], raw_full[RS], raw_empty[RS];
+  // [2]: S1 as row tile 0 uses it (a work tile of one row tile); its waiters differ from those of
+  // S1 as row tile 1, so the two uses count their phases apart
+  uint64_t s_full[3], p_full[3];
+  // P V product i into O_t completes pv_done[t][i % 2]: a waiter that is two products behind the
+  // present one (one row tile) still finds the phase it asks for
+  uint64_t pv_done[2][2], o_free[2], tail_go, tail_done, done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Row packing of a head group.
+struct RowPack {
+  int HB, TB, blocks;  // heads and tokens per row tile, row-tile head blocks per KV head
+  __device__ __host__ explicit RowPack(int hg) {
+    HB = hg < 128 ? hg : 128;
+    TB = 128 / HB;
+    blocks = (hg + HB - 1) / HB;
+  }
+};
+
+// A run of pages [page0, page1) of one work tile.
+struct Piece {
+  int req, vg, tok0, ntok;  // tokens tok0 .. of the request (relative), ntok of them
+  int page0, page1, pages;  // `pages` of the whole tile
+  int q_len, ctx, flat0;    // the request's
+  int nt;                   // row tiles with rows
+};
+
+// The piece at cursor c of a block whose run ends at e; advances c.  False at the end.
+__device__ __forceinline__ bool next_piece(const DevPlan& p, const RowPack& rp, AttCursor& c,
+                                           const AttCursor& e, Piece& pc) {
+  const int tt = 2 * rp.TB, nv = p.Hkv * rp.blocks;
+  for (;;) {
+    if (c.req >= p.batch) return false;
+    if (c.req == e.req && c.vg == e.vg && c.tile == e.tile && c.page == e.page) return false;
+    const ReqInfo* ri = p.reqs + c.req;
+    const int ql = __ldg(&ri->q_len);
+    if (ql == 0) {
+      ++c.req;
+      continue;
+    }
+    const bool last = c.req == e.req && c.vg == e.vg && c.tile == e.tile;
+    pc.req = c.req;
+    pc.vg = c.vg;
+    pc.q_len = ql;
+    pc.ctx = __ldg(&ri->ctx);
+    pc.flat0 = __ldg(&ri->tok0);
+    pc.tok0 = c.tile * tt;
+    pc.ntok = min(tt, ql - pc.tok0);
+    pc.pages = ((pc.ctx + pc.tok0 + pc.ntok - 1) >> 7) + 1;
+    pc.page0 = c.page;
+    pc.page1 = last ? min(e.page, pc.pages) : pc.pages;
+    pc.nt = pc.ntok > rp.TB ? 2 : 1;
+    if (last) {
+      c = e;
+    } else {
+      c.page = 0;
+      if ((c.tile + 1) * tt < ql) {
+        ++c.tile;
+      } else {
+        c.tile = 0;
+        if (++c.vg == nv) {
+          c.vg = 0;
+          ++c.req;
+        }
+      }
+    }
+    if (pc.page0 < pc.page1) return true;
+  }
+}
+
+// Pairs of FP32 in one 64-bit register: one instruction for two elements.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_p(float a, float b) {
+  uint32_t r;
+  if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+struct AttArgs {
+  const uint8_t *q, *kc, *vc, *ks, *vs;  // NVFP4 plans (and Q's codes)
+  int64_t q_stride;
+  const int32_t* page_table;
+  uint16_t* out;
+  int64_t out_stride;
+  float* out_lse;
+  float *part, *part_lse;  // [2 att_ctas][slot rows][D], [2 att_ctas][slot rows]
+  float c;                 // softmax scale x q_scale x log2 e
+};
+
+template <int D, bool QUANT>
+__global__ void __launch_bounds__(QUANT ? 512 : 384, 1)
+attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, DevPlan p, AttArgs a) {
+  using Smem = AttSmem<D, QUANT>;
+  constexpr int TILE = Smem::TILE, S = Smem::STAGES, RS = Smem::RS, DB = D / 64;
+  constexpr uint32_t IDESC_QK = idesc_mma(!QUANT, !QUANT, 128, 128, false, false);
+  constexpr uint32_t IDESC_PV = idesc_mma(!QUANT, !QUANT, 128, D, false, true);
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int32_t* status = p.status;
+  const RowPack rp(p.Hg);
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_full[i]), QUANT ? 4 : 1);
+      mbar_init(smem_u32(&sm.q_empty[i]), 1);
+      mbar_init(smem_u32(&sm.pv_done[i][0]), 1);
+      mbar_init(smem_u32(&sm.pv_done[i][1]), 1);
+      mbar_init(smem_u32(&sm.o_free[i]), 4);
+    }
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&sm.kv_full[i]), QUANT ? 4 : 1);
+      mbar_init(smem_u32(&sm.kv_empty[i]), 1);
+    }
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(smem_u32(&sm.raw_full[i]), 1);
+      mbar_init(smem_u32(&sm.raw_empty[i]), 4);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
+    }
+    mbar_init(smem_u32(&sm.tail_go), 1);
+    mbar_init(smem_u32(&sm.tail_done), 1);
+    mbar_init(smem_u32(&sm.done), 1);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();  // from here on: what earlier kernels wrote
+  pdl_trigger();
+  const uint32_t tmem = sm.tmem_base;  // S0 S1 at columns 0, 128; O0 O1 at 256, 384
+  volatile int* abort_flag = &sm.abort_flag;
+  AttCursor cur = p.att_starts[blockIdx.x];
+  const AttCursor end = p.att_starts[blockIdx.x + 1];
+  Piece pc;
+
+  if (warp < 4) {
+    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // ------------------------------------------------ copies
+      uint32_t it = 0, qc0 = 0, qc1 = 0;
+      bool ok = true;
+      while (ok && next_piece(p, rp, cur, end, pc)) {
+        const int g = pc.vg / rp.blocks, h0 = g * p.Hg + (pc.vg % rp.blocks) * 128;
+        if (!QUANT && lane == 0) {
+          for (int t = 0; t < pc.nt && ok; ++t) {
+            uint32_t& qc = t ? qc1 : qc0;
+            ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
+            if (!ok) break;
+            ++qc;
+            const uint32_t f = smem_u32(&sm.q_full[t]);
+            mbar_expect_tx(f, DB * rp.HB * rp.TB * 128);
+            for (int db = 0; db < DB; ++db)
+              tma_load_3d(smem_u32(sm.q[t]) + db * 16384, &tmQ, db * 64, h0,
+                          pc.flat0 + pc.tok0 + t * rp.TB, f);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        int ids = 0;
+        for (int pg = pc.page0; pg < pc.page1 && ok; ++pg) {
+          const int k = (pg - pc.page0) & 31;
+          if (k == 0 && pg + lane < pc.page1) {  // the next 32 pages' tiles
+            ids = __ldg(a.page_table + (int64_t)pc.req * p.max_pages + pg + lane);
+            if (ids < 0 || ids >= p.num_phys) {
+              set_status(status, DEV_BAD_PAGE);
+              ids = 0;
+            }
+          }
+          const int tile = __shfl_sync(0xffffffffu, ids, k) * p.Hkv + g;
+          if (lane == 0) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++it) {
+              if (QUANT) {
+                const uint32_t r = it % RS, f = smem_u32(&sm.raw_full[r]), d = smem_u32(sm.raw[r]);
+                ok = mbar_wait(smem_u32(&sm.raw_empty[r]), ((it / RS) & 1) ^ 1, abort_flag, status);
+                if (!ok) break;
+                mbar_expect_tx(f, Smem::RAWB);
+                bulk_load(d, (kv ? a.vc : a.kc) + (int64_t)tile * (64 * D), 64 * D, f);
+                bulk_load(d + 64 * D, (kv ? a.vs : a.ks) + (int64_t)tile * (8 * D), 8 * D, f);
+              } else {
+                const uint32_t s = it % S, f = smem_u32(&sm.kv_full[s]);
+                ok = mbar_wait(smem_u32(&sm.kv_empty[s]), ((it / S) & 1) ^ 1, abort_flag, status);
+                if (!ok) break;
+                mbar_expect_tx(f, TILE);
+                for (int db = 0; db < DB; ++db)
+                  tma_load_2d(smem_u32(sm.kv[s]) + db * 16384, kv ? &tmV : &tmK, db * 64,
+                              tile * 128, f);
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------ MMA issuer (one thread)
+      if (lane == 0) {
+        uint32_t it = 0, qc = 0, qc1 = 0, sc[3] = {0, 0, 0}, oc0 = 0, oc1 = 0, pv0 = 0, pv1 = 0, tc = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+          if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
+        };
+        auto kv_wait = [&](uint32_t i) { wait(sm.kv_full[i % S], (i / S) & 1); };
+        auto issue_s = [&](int t, int col, uint32_t i) {  // S at column col = Q_t K_i^T
+          const uint32_t qb = smem_u32(sm.q[t]), kb = smem_u32(sm.kv[i % S]);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
+            mma_f16_ss(tmem + col, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024),
+                       IDESC_QK, kk > 0);
+          }
+        };
+        auto issue_pv = [&](int t, int col, uint32_t i, bool first) {  // O_t += P V_i
+          const uint32_t vb = smem_u32(sm.kv[i % S]);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ts(tmem + 256 + t * 128, tmem + col + kk * 8,
+                       sdesc_sw128(vb + kk * 2048, 16384, 1024), IDESC_PV, kk > 0 || !first);
+          uint32_t& pv = t ? pv1 : pv0;
+          mma_commit(smem_u32(&sm.pv_done[t][pv & 1]));
+          ++pv;
+        };
+        while (ok && next_piece(p, rp, cur, end, pc)) {
+          const int n = pc.page1 - pc.page0;
+          // rows of the last page behind the request's last token
+          const bool tail = !QUANT && pc.page1 * 128 > pc.ctx + pc.q_len;
+          kv_wait(it);
+          for (int t = 0; t < pc.nt && ok; ++t) {
+            wait(sm.q_full[t], (t ? qc1 : qc) & 1);
+            if (!ok) break;
+            issue_s(t, t * 128, it);
+            mma_commit(smem_u32(&sm.s_full[t]));
+            if (n == 1) mma_commit(smem_u32(&sm.q_empty[t]));
+          }
+          if (ok) mma_commit(smem_u32(&sm.kv_empty[it % S]));
+          for (int j = 0; j < n && ok; ++j) {
+            const uint32_t iv = it + 2 * j + 1, ik = iv + 1;
+            const bool more = j + 1 < n;
+            if (pc.nt == 1 && more) {  // the next page's S under this page's softmax
+              const int b = (j + 1) & 1;
+              kv_wait(ik);
+              if (!ok) break;
+              issue_s(0, b * 128, ik);
+              mma_commit(smem_u32(&sm.s_full[b ? 2 : 0]));
+              mma_commit(smem_u32(&sm.kv_empty[ik % S]));
+              if (j + 2 == n) mma_commit(smem_u32(&sm.q_empty[0]));
+            }
+            kv_wait(iv);
+            if (tail && !more && ok) mbar_arrive(smem_u32(&sm.tail_go));
+            for (int t = 0; t < pc.nt && ok; ++t) {
+              const int u = pc.nt == 2 ? t : ((j & 1) ? 2 : 0);  // S buffer and its barriers
+              wait(sm.p_full[u], sc[u] & 1);
+              ++sc[u];
+              if (j == 0) {
+                uint32_t& oc = t ? oc1 : oc0;
+                wait(sm.o_free[t], (oc & 1) ^ 1);
+                ++oc;
+              }
+              if (tail && !more && t == 0) {
+                wait(sm.tail_done, tc & 1);
+                ++tc;
+              }
+              if (!ok) break;
+              issue_pv(t, u ? 128 : 0, iv, j == 0);
+              if (pc.nt == 2 && more) {
+                if (t == 0) kv_wait(ik);
+                if (!ok) break;
+                issue_s(t, t * 128, ik);
+                mma_commit(smem_u32(&sm.s_full[t]));
+                if (j + 2 == n) mma_commit(smem_u32(&sm.q_empty[t]));
+              }
+            }
+            if (!ok) break;
+            mma_commit(smem_u32(&sm.kv_empty[iv % S]));
+            if (pc.nt == 2 && more) mma_commit(smem_u32(&sm.kv_empty[ik % S]));
+          }
+          it += 2 * n;
+          ++qc;
+          if (pc.nt == 2) ++qc1;
+        }
+        mma_commit(smem_u32(&sm.done));
+        mbar_wait(smem_u32(&sm.done), 0, nullptr, status);
+      }
+    } else if (warp == 2 && !QUANT) {
+      // ------------------------------------------------ zero V rows of the request's unwritten slots
+      uint32_t it = 0, tc = 0;
+      while (next_piece(p, rp, cur, end, pc)) {
+        const int n = pc.page1 - pc.page0, kv_len = pc.ctx + pc.q_len;
+        if (pc.page1 * 128 > kv_len) {
+          if (!mbar_wait(smem_u32(&sm.tail_go), tc & 1, abort_flag, status)) break;
+          ++tc;
+          const int r0 = kv_len - (pc.page1 - 1) * 128;  // rows r0 .. 127
+          uint8_t* v = sm.kv[(it + 2 * n - 1) % S];
+          for (int db = 0; db < DB; ++db)
+            for (int i = r0 * 8 + lane; i < 1024; i += 32)
+              *reinterpret_cast<uint4*>(v + db * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.tail_done));
+        }
+        it += 2 * n;
+      }
+    }
+  } else if (warp < 12) {
+    if (QUANT) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------ softmax and epilogue of row tile w
+    const int w = warp >= 8, quarter = warp % 4, row = quarter * 32 + lane;
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t obase = tmem + lane_addr + 256 + w * 128;
+    const float c = a.c, bias = QUANT ? kF16Bias : 0.f;
+    const int ti = row / rp.HB, hh = row % rp.HB;
+    uint32_t su = 0, su2 = 0, pv = 0;  // uses of this row tile's S buffers, P V products into O_w
+    bool ok = true;
+    auto pv_wait = [&](uint32_t i) {  // product i into O_w is complete
+      return mbar_wait(smem_u32(&sm.pv_done[w][i & 1]), (i >> 1) & 1, abort_flag, status);
+    };
+    while (ok && next_piece(p, rp, cur, end, pc)) {
+      if (w >= pc.nt) continue;
+      const int n = pc.page1 - pc.page0;
+      const int tok = pc.tok0 + w * rp.TB + ti;
+      const int hg = (pc.vg % rp.blocks) * 128 + hh;  // head within the KV head's group
+      const bool valid = ti < rp.TB && tok < pc.q_len && hg < p.Hg;
+      const int pos = pc.ctx + tok;
+      const bool active = __any_sync(0xffffffffu, valid);
+      float m = 0.f;
+      uint64_t lsum[2] = {0, 0};
+      for (int j = 0; j < n; ++j) {
+        const bool alt = pc.nt == 1 && (j & 1);
+        const int u = alt ? 2 : w;
+        uint32_t& uses = alt ? su2 : su;
+        if (!mbar_wait(smem_u32(&sm.s_full[u]), uses & 1, abort_flag, status)) { ok = false; break; }
+        ++uses;
+        // every product is waited for once, in order: the one that this S was issued after
+        const int behind = pc.nt == 2 ? 1 : 2;
+        if (j >= behind && !pv_wait(pv + j - behind)) { ok = false; break; }
+        if (active) {
+          tc_fence_after();
+          const uint32_t sbase = tmem + lane_addr + (u ? 128 : 0);
+          const int nvis = valid ? pos - (pc.page0 + j) * 128 + 1 : 128;
+          const bool masked = __any_sync(0xffffffffu, nvis < 128);
+          uint32_t v[4][32];
+          float mb;
+          auto load = [&]() {
+            float red[4];
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+              reg_fence(v[cc]);
+              reg_fence1(red[cc]);
+            }
+            mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+            if (masked) {
+              mb = -INFINITY;
+#pragma unroll
+              for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  if (cc * 32 + i >= nvis) v[cc][i] = 0xff800000u;  // -inf
+                  mb = fmaxf(mb, __uint_as_float(v[cc][i]));
+                }
+            }
+          };
+          load();
+          if (j == 0) {
+            m = mb == -INFINITY ? 0.f : mb;  // a row that sees nothing here keeps p = 0
+          } else {
+            const bool need = (mb - m) * c > kRescale;
+            if (__any_sync(0xffffffffu, need)) {
+              if (pc.nt == 1 && !pv_wait(pv + j - 1)) { ok = false; break; }
+              tc_fence_after();
+              const float f = need ? fast_exp2((m - mb) * c) : 1.f;
+              if (need) m = mb;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float x, y;
+                unpack_f2(lsum[h], x, y);
+                lsum[h] = pack_f2(x * f, y * f);
+              }
+#pragma unroll
+              for (int cc = 0; cc < D / 32; ++cc) {
+                tmem_ld32(obase + cc * 32, v[0]);
+                tmem_ld_wait();
+                reg_fence(v[0]);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
+                tmem_st32(obase + cc * 32, v[0]);
+              }
+              tmem_st_wait();
+              const float keep = mb;
+              load();
+              mb = keep;
+            }
+          }
+          const uint64_t c2 = pack_f2(c, c), off2 = pack_f2(bias - m * c, bias - m * c);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              const int cc = 2 * h + i / 32, e = i % 32;
+              float x, y;
+              unpack_f2(fma_f2(pack_f2(__uint_as_float(v[cc][e]), __uint_as_float(v[cc][e + 1])),
+                               c2, off2), x, y);
+              x = fast_exp2(x);
+              y = fast_exp2(y);
+              lsum[(i >> 1) & 1] = add_f2(lsum[(i >> 1) & 1], pack_f2(x, y));
+              pk[i / 2] = pack_p<QUANT>(x, y);
+            }
+            tmem_st32(sbase + h * 32, pk);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[u]));
+      }
+      if (!ok) break;
+      // the last products into O_w
+      if ((pc.nt == 1 && n > 1 && !pv_wait(pv + n - 2)) || !pv_wait(pv + n - 1)) break;
+      pv += n;
+      if (active) {
+        tc_fence_after();
+        float l;
+        {
+          float x, y, z, t;
+          unpack_f2(lsum[0], x, y);
+          unpack_f2(lsum[1], z, t);
+          l = (x + y) + (z + t);
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float lse = l > 0.f ? (m * c - bias + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        const bool whole = pc.page0 == 0 && pc.page1 == pc.pages;
+        const int64_t slot = 2 * blockIdx.x + (pc.page0 > 0 ? 0 : 1);
+        const int64_t srow = slot * p.att_slot_rows + w * 128 + row;
+        const int64_t flat = pc.flat0 + tok;
+        const int head = (pc.vg / rp.blocks) * p.Hg + hg;
+        if (valid) {
+          if (!whole) a.part_lse[srow] = lse;
+          else if (a.out_lse) a.out_lse[flat * p.H + head] = lse;
+        }
+        uint16_t* orow = a.out + flat * a.out_stride + (int64_t)head * D;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(obase + cc * 32, v);
+          tmem_ld_wait();
+          reg_fence(v);
+          if (valid && whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                o[k] = pack_p<false>(__uint_as_float(v[i + 2 * k]) * inv,
+                                     __uint_as_float(v[i + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(orow + cc * 32 + i) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(a.part + srow * D + cc * 32 + i) = make_float4(
+                  __uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
+                  __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[w]));
+    }
+  } else {
+    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    // ------------------------------------------------ operand conversion (NVFP4 plans)
+    const int ct = tid - 384;
+    uint32_t it = 0, qc0 = 0, qc1 = 0;
+    bool ok = QUANT;
+    while (ok && next_piece(p, rp, cur, end, pc)) {
+      const int h0 = (pc.vg % rp.blocks) * 128;
+      for (int t = 0; t < pc.nt && ok; ++t) {  // E4M3 Q rows, exactly, into the FP16 operand tile
+        uint32_t& qc = t ? qc1 : qc0;
+        ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
+        if (!ok) break;
+        ++qc;
+        for (int ch = ct; ch < 128 * (D / 16); ch += 128) {
+          const int r = ch / (D / 16), i = ch % (D / 16);
+          const int tok = pc.tok0 + t * rp.TB + r / rp.HB, hg = h0 + r % rp.HB;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < rp.HB * rp.TB && tok < pc.q_len && hg < p.Hg)
+            x = __ldg(reinterpret_cast<const uint4*>(
+                a.q + (pc.flat0 + tok) * a.q_stride +
+                (int64_t)((pc.vg / rp.blocks) * p.Hg + hg) * D + i * 16));
+          const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = cvt_e4m3x2((uint16_t)(wd[k / 2] >> (16 * (k & 1))));
+          uint8_t* d = sm.q[t] + (i / 4) * 16384;
+          *reinterpret_cast<uint4*>(d + sw128_offset(r, 2 * (i % 4))) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(d + sw128_offset(r, 2 * (i % 4) + 1)) =
+              make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[t]));
+      }
+      const int n2 = 2 * (pc.page1 - pc.page0);
+      for (int i = 0; i < n2 && ok; ++i, ++it) {
+        const uint32_t r = it % RS, s = it % S;
+        if (!mbar_wait(smem_u32(&sm.raw_full[r]), (it / RS) & 1, abort_flag, status) ||
+            !mbar_wait(smem_u32(&sm.kv_empty[s]), ((it / S) & 1) ^ 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        // V rows behind the request's last token become zero, whatever the slots hold
+        const int rows = (i & 1) ? min(128, pc.ctx + pc.q_len - (pc.page0 + i / 2) * 128) : 128;
+        nvfp4_tile_convert<D, false>(sm.raw[r], sm.kv[s], ct, 128, rows);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.kv_full[s]));
+          mbar_arrive(smem_u32(&sm.raw_empty[r]));
+        }
+      }
+    }
+  }
+  settle_after_abort(abort_flag);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the tiles cut over several blocks: a warp per row, out = sum_i w_i O_i / sum_i w_i with
+// w_i = exp(lse_i - max lse); a piece in which the row sees no key (lse = -inf) is never read.
+template <int D>
+__global__ void __launch_bounds__(256)
+attention_merge_kernel(DevPlan p, AttArgs a) {
+  __shared__ float wts[8][kMaxCtas];
+  pdl_wait();
+  pdl_trigger();
+  const AttMerge mg = p.att_merges[blockIdx.x];
+  if (mg.req < 0) return;
+  const RowPack rp(p.Hg);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int lr = blockIdx.y * 8 + warp, row = lr % 128;
+  const int ti = row / rp.HB, hg = (mg.vg % rp.blocks) * 128 + row % rp.HB;
+  const int tok = mg.tile * 2 * rp.TB + (lr / 128) * rp.TB + ti;
+  const ReqInfo* ri = p.reqs + mg.req;
+  if (lr >= p.att_slot_rows || ti >= rp.TB || tok >= __ldg(&ri->q_len) || hg >= p.Hg) return;
+  const int np = mg.cta1 - mg.cta0 + 1;
+  auto srow = [&](int i) {
+    return (int64_t)(i == 0 ? 2 * mg.cta0 + 1 : 2 * (mg.cta0 + i)) * p.att_slot_rows + lr;
+  };
+  float mx = -INFINITY;
+  for (int i = lane; i < np; i += 32) {
+    const float l = a.part_lse[srow(i)];
+    wts[warp][i] = l;
+    mx = fmaxf(mx, l);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float sum = 0.f;
+  for (int i = lane; i < np; i += 32) {
+    const float l = wts[warp][i], wt = l == -INFINITY ? 0.f : __expf(l - mx);
+    wts[warp][i] = wt;
+    sum += wt;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncwarp();
+  constexpr int E = D / 32;  // elements per lane
+  float acc[E] = {};
+#pragma unroll 4
+  for (int i = 0; i < np; ++i) {
+    const float wt = wts[warp][i];
+    if (wt == 0.f) continue;
+    const float* o = a.part + srow(i) * D + lane * E;
+    if (E == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(o);
+      acc[0] += wt * x.x;
+      acc[1] += wt * x.y;
+      acc[E - 2] += wt * x.z;
+      acc[E - 1] += wt * x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(o);
+      acc[0] += wt * x.x;
+      acc[1] += wt * x.y;
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int64_t flat = __ldg(&ri->tok0) + tok;
+  const int head = (mg.vg / rp.blocks) * p.Hg + hg;
+  uint16_t* out = a.out + flat * a.out_stride + (int64_t)head * D + lane * E;
+  if (E == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_p<false>(acc[0] * inv, acc[1] * inv),
+                                                pack_p<false>(acc[E - 2] * inv, acc[E - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_p<false>(acc[0] * inv, acc[1] * inv);
+  if (lane == 0 && a.out_lse)
+    a.out_lse[flat * p.H + head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+}
+
+template <int D, bool QUANT>
+cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, const void* kc,
+                          const void* vc, cudaStream_t st) {
+  alignas(64) CUtensorMap tmQ, tmK, tmV;
+  memset(&tmQ, 0, sizeof tmQ);
+  memset(&tmK, 0, sizeof tmK);
+  memset(&tmV, 0, sizeof tmV);
+  const RowPack rp(p.Hg);
+  if (!QUANT) {
+    const uint64_t rows = (uint64_t)p.num_phys * p.Hkv * 128;
+    if (!encode_tmap_3d(&tmQ, 0, const_cast<void*>(q), D, p.H, p.T, (uint64_t)D * 2,
+                        (uint64_t)a.q_stride * 2, 64, rp.HB, rp.TB, true) ||
+        !encode_tmap_2d(&tmK, 0, const_cast<void*>(kc), D, rows, (uint64_t)D * 2, 64, 128, true) ||
+        !encode_tmap_2d(&tmV, 0, const_cast<void*>(vc), D, rows, (uint64_t)D * 2, 64, 128, true))
+      return cudaErrorInvalidValue;
+  }
+  const int smem = (int)sizeof(AttSmem<D, QUANT>) + 1024;
+  auto kern = attention_kernel<D, QUANT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(p.att_ctas), dim3(QUANT ? 512 : 384), smem, st, tmQ, tmK, tmV, p, a);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attention_merge_kernel<D>, dim3(p.att_ctas, (p.att_slot_rows + 7) / 8), dim3(256),
+                 0, st, p, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_t q_stride,
+                             float q_scale, const void* kc, const void* vc, const void* ks,
+                             const void* vs, const int32_t* page_table, void* out,
+                             int64_t out_stride, float* out_lse, void* scratch, cudaStream_t st) {
+  if (p.att_ctas < 1 || p.att_ctas > kMaxCtas) return cudaErrorInvalidConfiguration;
+  AttArgs a{};
+  a.q = static_cast<const uint8_t*>(q);
+  a.kc = static_cast<const uint8_t*>(kc);
+  a.vc = static_cast<const uint8_t*>(vc);
+  a.ks = static_cast<const uint8_t*>(ks);
+  a.vs = static_cast<const uint8_t*>(vs);
+  a.q_stride = q_stride;
+  a.page_table = page_table;
+  a.out = static_cast<uint16_t*>(out);
+  a.out_stride = out_stride;
+  a.out_lse = out_lse;
+  a.part = static_cast<float*>(scratch);
+  a.part_lse = a.part + 2ll * p.att_ctas * p.att_slot_rows * p.D;
+  a.c = p.sm_scale * q_scale * 1.4426950408889634f;
+  if (p.D == 128)
+    return quant ? run_attention<128, true>(p, a, q, kc, vc, st)
+                 : run_attention<128, false>(p, a, q, kc, vc, st);
+  return quant ? run_attention<64, true>(p, a, q, kc, vc, st)
+               : run_attention<64, false>(p, a, q, kc, vc, st);
+}
+
+}  // namespace sps

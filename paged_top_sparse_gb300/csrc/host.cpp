@@ -140,6 +140,11 @@ struct sps_plan {
   int64_t fwd_ws_bytes = 0;  // the part the forward uses (the no-allocation forward's need)
   int32_t topk_nseg = 1, topk_segg = 0;
   int32_t fwd_prefetch = 0;
+  // full attention (attention.cu): where each block begins, the tiles cut over blocks
+  std::vector<AttCursor> att_starts;
+  std::vector<AttMerge> att_merges;
+  int32_t att_ctas = 0, att_slot_rows = 0;
+  int64_t off_att_starts = 0, off_att_merges = 0;
   int64_t upload_bytes = 0;  // [0, upload_bytes) of the workspace comes from `blob`
   std::vector<uint8_t> blob;
 };
@@ -240,6 +245,46 @@ void build_indexer_tasks(sps_plan* pl) {
   }
 }
 
+// Work split of the full attention: the (tile, page) pairs of the batch in order (request, head
+// block, tile, page), a tile being two row tiles of 128 / HB tokens x HB heads of a KV head's
+// group, cut into equal runs, one per SM.
+void build_attention_runs(sps_plan* pl) {
+  const sps_problem& p = pl->pb;
+  const int hg = p.num_q_heads / p.num_kv_heads, HB = std::min(hg, 128), TB = 128 / HB;
+  const int nv = p.num_kv_heads * ((hg + HB - 1) / HB), tt = 2 * TB;
+  auto pages_of = [&](const ReqInfo& ri, int tile) {
+    return (ri.ctx + std::min((tile + 1) * tt, ri.q_len) - 1) / kPage + 1;
+  };
+  int64_t total = 0;
+  int max_q = 0;
+  for (const ReqInfo& ri : pl->reqs) {
+    int64_t pages = 0;
+    for (int t = 0; t * tt < ri.q_len; ++t) pages += pages_of(ri, t);
+    total += pages * nv;
+    max_q = std::max(max_q, ri.q_len);
+  }
+  pl->att_ctas = std::min(std::max(1, num_sms()), 256);
+  pl->att_slot_rows = max_q > TB ? 256 : max_q * HB;
+  const int64_t runs = std::min<int64_t>(pl->att_ctas, total);
+  pl->att_starts.assign(pl->att_ctas + 1, AttCursor{p.batch, 0, 0, 0});
+  pl->att_merges.assign(pl->att_ctas, AttMerge{-1, 0, 0, 0, 0, 0});
+  int64_t at = 0;  // pairs before the present tile
+  int run = 0, merges = 0;
+  for (int b = 0; b < p.batch; ++b)
+    for (int v = 0; v < nv; ++v)
+      for (int t = 0; t * tt < pl->reqs[b].q_len; ++t) {
+        const int n = pages_of(pl->reqs[b], t);
+        int first = -1;
+        while (run < runs && run * total / runs < at + n) {
+          const int page = (int)(run * total / runs - at);
+          if (page > 0 && first < 0) first = run;
+          pl->att_starts[run++] = AttCursor{b, v, t, page};
+        }
+        if (first >= 0) pl->att_merges[merges++] = AttMerge{b, v, t, first - 1, run - 1, 0};
+        at += n;
+      }
+}
+
 }  // namespace
 
 extern "C" {
@@ -295,6 +340,7 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   const int64_t per_task = (int64_t)kFwdTaskGroups * 128;
   pl->max_fwd_tasks = pl->max_entries / per_task + pl->num_buckets + 1;
   build_indexer_tasks(pl);
+  build_attention_runs(pl);
 
   // workspace layout
   int64_t off = 0;
@@ -308,6 +354,8 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   pl->off_tok_pos = take(4 * pl->T);
   pl->off_tok_req = take(4 * pl->T);
   pl->off_reqs = take(sizeof(ReqInfo) * p.batch);
+  pl->off_att_starts = take(sizeof(AttCursor) * pl->att_starts.size());
+  pl->off_att_merges = take(sizeof(AttMerge) * pl->att_merges.size());
   pl->off_page_req = take(4 * std::max<int64_t>(1, pl->total_pages));
   pl->off_idx_tasks = take(sizeof(IdxTask) * std::max<size_t>(1, pl->idx_tasks.size()));
   int64_t upload_end = off;
@@ -363,6 +411,8 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   put(pl->off_tok_pos, tok_pos.data(), 4 * tok_pos.size());
   put(pl->off_tok_req, tok_req.data(), 4 * tok_req.size());
   put(pl->off_reqs, pl->reqs.data(), sizeof(ReqInfo) * pl->reqs.size());
+  put(pl->off_att_starts, pl->att_starts.data(), sizeof(AttCursor) * pl->att_starts.size());
+  put(pl->off_att_merges, pl->att_merges.data(), sizeof(AttMerge) * pl->att_merges.size());
   put(pl->off_page_req, pl->page_req.data(), 4 * pl->page_req.size());
   put(pl->off_idx_tasks, pl->idx_tasks.data(), sizeof(IdxTask) * pl->idx_tasks.size());
 
@@ -440,6 +490,10 @@ DevPlan make_dev_plan(const sps_plan* pl, void* ws) {
   d.topk_nseg = pl->topk_nseg;
   d.fwd_prefetch = pl->fwd_prefetch;
   d.topk_segg = pl->topk_segg;
+  d.att_starts = reinterpret_cast<const AttCursor*>(base + pl->off_att_starts);
+  d.att_merges = reinterpret_cast<const AttMerge*>(base + pl->off_att_merges);
+  d.att_ctas = pl->att_ctas;
+  d.att_slot_rows = pl->att_slot_rows;
   return d;
 }
 
@@ -821,6 +875,50 @@ sps_status sps_kv_append_rope(const sps_plan* pl, const void* k_new, int64_t k_s
   return launched(launch_kv_append_rope(make_dev_plan(pl, ws), r, a, rope && rope->interleaved,
                                         nvfp4, reinterpret_cast<cudaStream_t>(stream)),
                   "kv append with rotation launch");
+}
+
+sps_status paged_attention_scratch(const sps_plan* pl, size_t* bytes) {
+  if (!pl || !bytes) return fail(SPS_EINVAL, "paged_attention_scratch: plan/scratch_bytes NULL");
+  *bytes = (size_t)align_up(2ll * pl->att_ctas * pl->att_slot_rows * (pl->pb.head_dim + 1) * 4, 256);
+  return SPS_OK;
+}
+
+sps_status paged_attention_fwd(const sps_plan* pl, const void* q, int64_t q_stride, float q_scale,
+                               const void* k_cache, const void* v_cache, const void* k_scales,
+                               const void* v_scales, const int32_t* page_table, void* out_bf16,
+                               int64_t out_stride, float* out_lse, void* scratch,
+                               size_t scratch_bytes, void* ws, sps_stream_t stream) {
+  sps_status st = check_plan_ws(pl, ws);
+  if (st != SPS_OK) return st;
+  const sps_problem& p = pl->pb;
+  const bool quant = p.kv_dtype == SPS_NVFP4;
+  const int64_t n = (int64_t)p.num_q_heads * p.head_dim;
+  if (!rows_ok(q, q_stride, n, quant ? 16 : 8) || !rows_ok(out_bf16, out_stride, n, 8))
+    return fail(SPS_EINVAL,
+                "paged_attention_fwd: q and out must be non-NULL and 16-byte aligned, token "
+                "strides multiples of 16 bytes and at least num_q_heads * head_dim");
+  if (!k_cache || !v_cache || !page_table || (quant && (!k_scales || !v_scales)))
+    return fail(SPS_EINVAL, "paged_attention_fwd: NULL pointer (an NVFP4 cache needs its scales)");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || (quant && (!aligned(k_scales, 16) ||
+      !aligned(v_scales, 16))) || !aligned(page_table, 4) || (out_lse && !aligned(out_lse, 4)))
+    return fail(SPS_EINVAL, "paged_attention_fwd: caches must be 16-byte, page_table and out_lse "
+                            "4-byte aligned");
+  if (!(q_scale > 0.f) || !std::isfinite(q_scale))
+    return fail(SPS_EINVAL, "paged_attention_fwd: q_scale must be finite and > 0");
+  size_t need = 0;
+  paged_attention_scratch(pl, &need);
+  if (!scratch || !aligned(scratch, 256))
+    return fail(SPS_EINVAL, "paged_attention_fwd: scratch must be non-NULL and 256-byte aligned");
+  if (scratch_bytes < need)
+    return fail(SPS_ENOSPACE, "paged_attention_fwd: scratch of %zu bytes < %zu required",
+                scratch_bytes, need);
+  if ((int64_t)p.num_phys_pages * p.num_kv_heads > 0x7fffffff / kPage)
+    return fail(SPS_EUNSUPPORTED, "paged_attention_fwd: num_phys_pages x num_kv_heads must stay "
+                                  "below 2^24");
+  return launched(launch_attention(make_dev_plan(pl, ws), quant, q, q_stride, q_scale, k_cache,
+                                   v_cache, k_scales, v_scales, page_table, out_bf16, out_stride,
+                                   out_lse, scratch, reinterpret_cast<cudaStream_t>(stream)),
+                  "paged attention launch");
 }
 
 sps_status sps_quantize_e4m3(const void* x_bf16, int64_t n, float scale, void* codes,
