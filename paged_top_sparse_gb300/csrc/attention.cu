@@ -51,11 +51,13 @@ struct AttSmem {
   static constexpr int RAWB = 128 * D / 2 + 128 * D / 16;  // NVFP4 codes and scales of a tile
   static constexpr int RS = QUANT ? 3 : 1;
   static constexpr int kBudget = 227 * 1024 - 1024 - 1024;  // alignment slack, barriers
-  static constexpr int S0 = (kBudget - 2 * TILE - (QUANT ? RS * RAWB : 0)) / TILE;
+  static constexpr int STG = 8 * 4096;  // epilogue staging: 32 rows x 128 bytes for each warp
+  static constexpr int S0 = (kBudget - 2 * TILE - STG - (QUANT ? RS * RAWB : 0)) / TILE;
   static constexpr int STAGES = S0 > 8 ? 8 : S0;
-  static_assert(STAGES >= 4, "shared memory");
+  static_assert(STAGES >= 3, "shared memory");
   uint8_t q[2][TILE];
   uint8_t kv[STAGES][TILE];
+  uint8_t stage[8][4096];
   alignas(16) uint8_t raw[RS][QUANT ? RAWB : 16];
   uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], raw_full[RS], raw_empty[RS];
   // [2]: S1 as row tile 0 uses it (a work tile of one row tile); its waiters differ from those of
@@ -147,6 +149,22 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// Halves of sdesc_sw128: the low word of a shared address (or of an address in 16-byte units added
+// to the one of address 0), and the descriptor of a low word (1024 bytes between 8-row groups).
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t sdesc_hi(uint32_t lo) {
+  return (sdesc_sw128(0, 0, 1024) & 0xffffffff00000000ull) | lo;
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float a, float b) {
@@ -282,96 +300,145 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
     } else if (warp == 1) {
-      // ------------------------------------------------ MMA issuer (one thread)
-      if (lane == 0) {
-        uint32_t it = 0, qc = 0, qc1 = 0, sc[3] = {0, 0, 0}, oc0 = 0, oc1 = 0, pv0 = 0, pv1 = 0, tc = 0;
-        bool ok = true;
-        auto wait = [&](uint64_t& bar, uint32_t parity) {
-          if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
-        };
-        auto kv_wait = [&](uint32_t i) { wait(sm.kv_full[i % S], (i / S) & 1); };
-        auto issue_s = [&](int t, int col, uint32_t i) {  // S at column col = Q_t K_i^T
-          const uint32_t qb = smem_u32(sm.q[t]), kb = smem_u32(sm.kv[i % S]);
-          tc_fence_after();
+      // ------------------------------------------------ MMA issuer
+      // The warp runs the loop as one and an elected lane issues.  Descriptors are a constant high
+      // word and a low word that grows by the operand's offset.
+      const bool leader = elect_one();
+      const uint32_t q_lo = sdesc_lo(smem_u32(sm.q[0]), 16), kv_lo = smem_u32(sm.kv[0]) >> 4;
+      uint32_t st = 0, ph = 0;  // ring stage and phase of the next K or V tile
+      uint32_t qc0 = 0, qc1 = 0, sc0 = 0, sc1 = 0, sc2 = 0, oc0 = 0, oc1 = 0, pv0 = 0, pv1 = 0, tc = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t& bar, uint32_t parity) {
+        if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
+      };
+      auto advance = [&]() {
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
+      };
+      auto commit = [&](uint64_t& bar) {
+        if (leader) mma_commit(smem_u32(&bar));
+      };
+      auto issue_s = [&](int t, uint32_t col, uint32_t stage) {  // S at column col = Q_t K^T
+        tc_fence_after();
+        const uint32_t qa = q_lo + t * (TILE >> 4), ka = sdesc_lo(0, 16) + kv_lo + stage * (TILE >> 4);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
-            mma_f16_ss(tmem + col, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024),
-                       IDESC_QK, kk > 0);
+            const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
+            mma_f16_ss(tmem + col, sdesc_hi(qa + off), sdesc_hi(ka + off), IDESC_QK, kk > 0);
           }
-        };
-        auto issue_pv = [&](int t, int col, uint32_t i, bool first) {  // O_t += P V_i
-          const uint32_t vb = smem_u32(sm.kv[i % S]);
-          tc_fence_after();
+        }
+      };
+      auto issue_pv = [&](int t, uint32_t col, uint32_t stage, bool first) {  // O_t += P V
+        tc_fence_after();
+        const uint32_t va = sdesc_lo(0, 16384) + kv_lo + stage * (TILE >> 4);
+        uint32_t& pv = t ? pv1 : pv0;
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(tmem + 256 + t * 128, tmem + col + kk * 8,
-                       sdesc_sw128(vb + kk * 2048, 16384, 1024), IDESC_PV, kk > 0 || !first);
-          uint32_t& pv = t ? pv1 : pv0;
+            mma_f16_ts(tmem + 256 + t * 128, tmem + col + kk * 8, sdesc_hi(va + kk * (2048 >> 4)),
+                       IDESC_PV, kk > 0 || !first);
           mma_commit(smem_u32(&sm.pv_done[t][pv & 1]));
-          ++pv;
-        };
-        while (ok && next_piece(p, rp, cur, end, pc)) {
-          const int n = pc.page1 - pc.page0;
-          // rows of the last page behind the request's last token
-          const bool tail = !QUANT && pc.page1 * 128 > pc.ctx + pc.q_len;
-          kv_wait(it);
-          for (int t = 0; t < pc.nt && ok; ++t) {
-            wait(sm.q_full[t], (t ? qc1 : qc) & 1);
-            if (!ok) break;
-            issue_s(t, t * 128, it);
-            mma_commit(smem_u32(&sm.s_full[t]));
-            if (n == 1) mma_commit(smem_u32(&sm.q_empty[t]));
-          }
-          if (ok) mma_commit(smem_u32(&sm.kv_empty[it % S]));
-          for (int j = 0; j < n && ok; ++j) {
-            const uint32_t iv = it + 2 * j + 1, ik = iv + 1;
-            const bool more = j + 1 < n;
-            if (pc.nt == 1 && more) {  // the next page's S under this page's softmax
-              const int b = (j + 1) & 1;
-              kv_wait(ik);
-              if (!ok) break;
-              issue_s(0, b * 128, ik);
-              mma_commit(smem_u32(&sm.s_full[b ? 2 : 0]));
-              mma_commit(smem_u32(&sm.kv_empty[ik % S]));
-              if (j + 2 == n) mma_commit(smem_u32(&sm.q_empty[0]));
-            }
-            kv_wait(iv);
-            if (tail && !more && ok) mbar_arrive(smem_u32(&sm.tail_go));
-            for (int t = 0; t < pc.nt && ok; ++t) {
-              const int u = pc.nt == 2 ? t : ((j & 1) ? 2 : 0);  // S buffer and its barriers
-              wait(sm.p_full[u], sc[u] & 1);
-              ++sc[u];
-              if (j == 0) {
-                uint32_t& oc = t ? oc1 : oc0;
-                wait(sm.o_free[t], (oc & 1) ^ 1);
-                ++oc;
-              }
-              if (tail && !more && t == 0) {
-                wait(sm.tail_done, tc & 1);
-                ++tc;
-              }
-              if (!ok) break;
-              issue_pv(t, u ? 128 : 0, iv, j == 0);
-              if (pc.nt == 2 && more) {
-                if (t == 0) kv_wait(ik);
-                if (!ok) break;
-                issue_s(t, t * 128, ik);
-                mma_commit(smem_u32(&sm.s_full[t]));
-                if (j + 2 == n) mma_commit(smem_u32(&sm.q_empty[t]));
-              }
-            }
-            if (!ok) break;
-            mma_commit(smem_u32(&sm.kv_empty[iv % S]));
-            if (pc.nt == 2 && more) mma_commit(smem_u32(&sm.kv_empty[ik % S]));
-          }
-          it += 2 * n;
-          ++qc;
-          if (pc.nt == 2) ++qc1;
         }
-        mma_commit(smem_u32(&sm.done));
-        mbar_wait(smem_u32(&sm.done), 0, nullptr, status);
+        ++pv;
+      };
+      while (ok && next_piece(p, rp, cur, end, pc)) {
+        const int n = pc.page1 - pc.page0;
+        // rows of the last page behind the request's last token
+        const bool tail = !QUANT && pc.page1 * 128 > pc.ctx + pc.q_len;
+        wait(sm.kv_full[st], ph);
+        wait(sm.q_full[0], qc0 & 1);
+        ++qc0;
+        if (!ok) break;
+        issue_s(0, 0, st);
+        commit(sm.s_full[0]);
+        if (n == 1) commit(sm.q_empty[0]);
+        if (pc.nt == 2) {
+          wait(sm.q_full[1], qc1 & 1);
+          ++qc1;
+          if (!ok) break;
+          issue_s(1, 128, st);
+          commit(sm.s_full[1]);
+          if (n == 1) commit(sm.q_empty[1]);
+        }
+        commit(sm.kv_empty[st]);
+        advance();
+        for (int j = 0; j < n; ++j) {
+          const bool more = j + 1 < n;
+          const uint32_t vs = st, vph = ph;
+          advance();
+          const uint32_t kst = st, kph = ph;
+          if (more) advance();
+          if (pc.nt == 2) {
+            wait(sm.kv_full[vs], vph);
+            if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
+            wait(sm.p_full[0], sc0 & 1);
+            ++sc0;
+            if (j == 0) {
+              wait(sm.o_free[0], (oc0 & 1) ^ 1);
+              ++oc0;
+            }
+            if (tail && !more) {
+              wait(sm.tail_done, tc & 1);
+              ++tc;
+            }
+            if (!ok) break;
+            issue_pv(0, 0, vs, j == 0);
+            if (more) {
+              wait(sm.kv_full[kst], kph);
+              if (!ok) break;
+              issue_s(0, 0, kst);
+              commit(sm.s_full[0]);
+              if (j + 2 == n) commit(sm.q_empty[0]);
+            }
+            wait(sm.p_full[1], sc1 & 1);
+            ++sc1;
+            if (j == 0) {
+              wait(sm.o_free[1], (oc1 & 1) ^ 1);
+              ++oc1;
+            }
+            if (!ok) break;
+            issue_pv(1, 128, vs, j == 0);
+            commit(sm.kv_empty[vs]);
+            if (more) {
+              issue_s(1, 128, kst);
+              commit(sm.s_full[1]);
+              commit(sm.kv_empty[kst]);
+              if (j + 2 == n) commit(sm.q_empty[1]);
+            }
+          } else {
+            const bool odd = j & 1;  // this page's S buffer
+            if (more) {              // the next page's S under this page's softmax
+              wait(sm.kv_full[kst], kph);
+              if (!ok) break;
+              issue_s(0, odd ? 0 : 128, kst);
+              commit(sm.s_full[odd ? 0 : 2]);
+              commit(sm.kv_empty[kst]);
+              if (j + 2 == n) commit(sm.q_empty[0]);
+            }
+            wait(sm.kv_full[vs], vph);
+            if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
+            wait(sm.p_full[odd ? 2 : 0], (odd ? sc2 : sc0) & 1);
+            if (odd) ++sc2;
+            else ++sc0;
+            if (j == 0) {
+              wait(sm.o_free[0], (oc0 & 1) ^ 1);
+              ++oc0;
+            }
+            if (tail && !more) {
+              wait(sm.tail_done, tc & 1);
+              ++tc;
+            }
+            if (!ok) break;
+            issue_pv(0, odd ? 128 : 0, vs, j == 0);
+            commit(sm.kv_empty[vs]);
+          }
+        }
       }
+      commit(sm.done);
+      mbar_wait(smem_u32(&sm.done), 0, nullptr, status);
     } else if (warp == 2 && !QUANT) {
       // ------------------------------------------------ zero V rows of the request's unwritten slots
       uint32_t it = 0, tc = 0;
@@ -533,15 +600,38 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (!whole) a.part_lse[srow] = lse;
           else if (a.out_lse) a.out_lse[flat * p.H + head] = lse;
         }
-        uint16_t* orow = a.out + flat * a.out_stride + (int64_t)head * D;
+        // a thread holds a row; the warp turns 128 bytes of each of its 32 rows at a time in its
+        // staging area, so that eight lanes write 128 contiguous bytes of a row (a thread writing
+        // its own row would cost a memory transaction per 16 bytes)
+        uint8_t* stg = sm.stage[warp - 4];
+        const uint32_t vrows = __ballot_sync(0xffffffffu, valid);
+        const int64_t obyte = whole ? (flat * a.out_stride + (int64_t)head * D) * 2 : srow * D * 4;
+        uint8_t* const base = whole ? reinterpret_cast<uint8_t*>(a.out)
+                                    : reinterpret_cast<uint8_t*>(a.part);
+        auto flush = [&](int chunk) {  // 128-byte piece `chunk` of every row
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + lane / 8;
+            const uint4 x = *reinterpret_cast<const uint4*>(stg + sw128_offset(r, lane % 8));
+            const int64_t at = __shfl_sync(0xffffffffu, obyte, r);
+            if (vrows >> r & 1)
+              *reinterpret_cast<uint4*>(base + at + chunk * 128 + (lane % 8) * 16) = x;
+          }
+          __syncwarp();
+        };
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t v[32];
-          __syncwarp();
           tmem_ld32(obase + cc * 32, v);
           tmem_ld_wait();
           reg_fence(v);
-          if (valid && whole) {
+          if (cc == D / 32 - 1) {  // O is read: the next work tile's products may begin
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[w]));
+          }
+          if (whole) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint32_t o[4];
@@ -549,16 +639,20 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               for (int k = 0; k < 4; ++k)
                 o[k] = pack_p<false>(__uint_as_float(v[i + 2 * k]) * inv,
                                      __uint_as_float(v[i + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(orow + cc * 32 + i) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, (cc & 1) * 4 + i / 8)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
             }
-          } else if (valid) {
+            if (cc & 1) flush(cc / 2);
+          } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(a.part + srow * D + cc * 32 + i) = make_float4(
+              *reinterpret_cast<float4*>(stg + sw128_offset(lane, i / 4)) = make_float4(
                   __uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
                   __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+            flush(cc);
           }
         }
+        continue;
       }
       tc_fence_before();
       __syncwarp();
