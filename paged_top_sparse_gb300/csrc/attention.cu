@@ -62,7 +62,7 @@ struct AttSmem {
   uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], raw_full[RS], raw_empty[RS];
   // [2]: S1 as row tile 0 uses it (a work tile of one row tile); its waiters differ from those of
   // S1 as row tile 1, so the two uses count their phases apart
-  uint64_t s_full[3], p_full[3];
+  uint64_t s_full[3], p_half[3], p_full[3];  // p_half: P of the first 64 keys
   // P V product i into O_t completes pv_done[t][i % 2]: a waiter that is two products behind the
   // present one (one row tile) still finds the phase it asks for
   uint64_t pv_done[2][2], o_free[2], tail_go, tail_done, done;
@@ -88,46 +88,48 @@ struct Piece {
   int nt;                   // row tiles with rows
 };
 
-// The piece at cursor c of a block whose run ends at e; advances c.  False at the end.
+// The piece at cursor c of a block whose run ends at e; advances c.  False at the end.  The cursor
+// carries its request's numbers, so that a run's first piece needs no further read.
 __device__ __forceinline__ bool next_piece(const DevPlan& p, const RowPack& rp, AttCursor& c,
                                            const AttCursor& e, Piece& pc) {
   const int tt = 2 * rp.TB, nv = p.Hkv * rp.blocks;
   for (;;) {
     if (c.req >= p.batch) return false;
     if (c.req == e.req && c.vg == e.vg && c.tile == e.tile && c.page == e.page) return false;
-    const ReqInfo* ri = p.reqs + c.req;
-    const int ql = __ldg(&ri->q_len);
-    if (ql == 0) {
-      ++c.req;
-      continue;
-    }
-    const bool last = c.req == e.req && c.vg == e.vg && c.tile == e.tile;
-    pc.req = c.req;
-    pc.vg = c.vg;
-    pc.q_len = ql;
-    pc.ctx = __ldg(&ri->ctx);
-    pc.flat0 = __ldg(&ri->tok0);
-    pc.tok0 = c.tile * tt;
-    pc.ntok = min(tt, ql - pc.tok0);
-    pc.pages = ((pc.ctx + pc.tok0 + pc.ntok - 1) >> 7) + 1;
-    pc.page0 = c.page;
-    pc.page1 = last ? min(e.page, pc.pages) : pc.pages;
-    pc.nt = pc.ntok > rp.TB ? 2 : 1;
-    if (last) {
-      c = e;
-    } else {
-      c.page = 0;
-      if ((c.tile + 1) * tt < ql) {
-        ++c.tile;
-      } else {
-        c.tile = 0;
-        if (++c.vg == nv) {
-          c.vg = 0;
-          ++c.req;
-        }
+    if (c.q_len > 0) {
+      const bool last = c.req == e.req && c.vg == e.vg && c.tile == e.tile;
+      pc.req = c.req;
+      pc.vg = c.vg;
+      pc.q_len = c.q_len;
+      pc.ctx = c.ctx;
+      pc.flat0 = c.flat0;
+      pc.tok0 = c.tile * tt;
+      pc.ntok = min(tt, c.q_len - pc.tok0);
+      pc.pages = ((pc.ctx + pc.tok0 + pc.ntok - 1) >> 7) + 1;
+      pc.page0 = c.page;
+      pc.page1 = last ? min(e.page, pc.pages) : pc.pages;
+      pc.nt = pc.ntok > rp.TB ? 2 : 1;
+      if (last) {
+        c = e;
+        return pc.page0 < pc.page1;
       }
+      c.page = 0;
+      if ((c.tile + 1) * tt < c.q_len) {
+        ++c.tile;
+        return true;
+      }
+      c.tile = 0;
+      if (++c.vg < nv) return true;
+      c.vg = 0;
     }
-    if (pc.page0 < pc.page1) return true;
+    const bool done = c.q_len > 0;  // a piece was found above
+    if (++c.req < p.batch) {
+      const ReqInfo* ri = p.reqs + c.req;
+      c.q_len = __ldg(&ri->q_len);
+      c.ctx = __ldg(&ri->ctx);
+      c.flat0 = __ldg(&ri->tok0);
+    }
+    if (done) return true;
   }
 }
 
@@ -218,6 +220,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_half[i]), 4);
       mbar_init(smem_u32(&sm.p_full[i]), 4);
     }
     mbar_init(smem_u32(&sm.tail_go), 1);
@@ -250,20 +253,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       bool ok = true;
       while (ok && next_piece(p, rp, cur, end, pc)) {
         const int g = pc.vg / rp.blocks, h0 = g * p.Hg + (pc.vg % rp.blocks) * 128;
-        if (!QUANT && lane == 0) {
-          for (int t = 0; t < pc.nt && ok; ++t) {
-            uint32_t& qc = t ? qc1 : qc0;
-            ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
-            if (!ok) break;
-            ++qc;
-            const uint32_t f = smem_u32(&sm.q_full[t]);
-            mbar_expect_tx(f, DB * rp.HB * rp.TB * 128);
-            for (int db = 0; db < DB; ++db)
-              tma_load_3d(smem_u32(sm.q[t]) + db * 16384, &tmQ, db * 64, h0,
-                          pc.flat0 + pc.tok0 + t * rp.TB, f);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         int ids = 0;
         for (int pg = pc.page0; pg < pc.page1 && ok; ++pg) {
           const int k = (pg - pc.page0) & 31;
@@ -285,14 +274,28 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 mbar_expect_tx(f, Smem::RAWB);
                 bulk_load(d, (kv ? a.vc : a.kc) + (int64_t)tile * (64 * D), 64 * D, f);
                 bulk_load(d + 64 * D, (kv ? a.vs : a.ks) + (int64_t)tile * (8 * D), 8 * D, f);
-              } else {
-                const uint32_t s = it % S, f = smem_u32(&sm.kv_full[s]);
-                ok = mbar_wait(smem_u32(&sm.kv_empty[s]), ((it / S) & 1) ^ 1, abort_flag, status);
+                continue;
+              }
+              const uint32_t s = it % S, f = smem_u32(&sm.kv_full[s]);
+              ok = mbar_wait(smem_u32(&sm.kv_empty[s]), ((it / S) & 1) ^ 1, abort_flag, status);
+              if (!ok) break;
+              mbar_expect_tx(f, TILE);
+              for (int db = 0; db < DB; ++db)
+                tma_load_2d(smem_u32(sm.kv[s]) + db * 16384, kv ? &tmV : &tmK, db * 64, tile * 128,
+                            f);
+              if (kv == 0 && pg == pc.page0) {  // Q behind the first K tile
+                for (int t = 0; t < pc.nt && ok; ++t) {
+                  uint32_t& qc = t ? qc1 : qc0;
+                  ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
+                  if (!ok) break;
+                  ++qc;
+                  const uint32_t fq = smem_u32(&sm.q_full[t]);
+                  mbar_expect_tx(fq, DB * rp.HB * rp.TB * 128);
+                  for (int db = 0; db < DB; ++db)
+                    tma_load_3d(smem_u32(sm.q[t]) + db * 16384, &tmQ, db * 64, h0,
+                                pc.flat0 + pc.tok0 + t * rp.TB, fq);
+                }
                 if (!ok) break;
-                mbar_expect_tx(f, TILE);
-                for (int db = 0; db < DB; ++db)
-                  tma_load_2d(smem_u32(sm.kv[s]) + db * 16384, kv ? &tmV : &tmK, db * 64,
-                              tile * 128, f);
               }
             }
           }
@@ -331,17 +334,24 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
         }
       };
-      auto issue_pv = [&](int t, uint32_t col, uint32_t stage, bool first) {  // O_t += P V
-        tc_fence_after();
-        const uint32_t va = sdesc_lo(0, 16384) + kv_lo + stage * (TILE >> 4);
+      // O_t += P V in two halves of 64 keys, the first as soon as its P is there (u: S buffer)
+      auto issue_pv = [&](int t, int u, uint32_t stage, bool first, uint32_t sc) {
+        const uint32_t col = u ? 128 : 0, va = sdesc_lo(0, 16384) + kv_lo + stage * (TILE >> 4);
         uint32_t& pv = t ? pv1 : pv0;
-        if (leader) {
+        auto half = [&](int h) {
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(tmem + 256 + t * 128, tmem + col + kk * 8, sdesc_hi(va + kk * (2048 >> 4)),
-                       IDESC_PV, kk > 0 || !first);
-          mma_commit(smem_u32(&sm.pv_done[t][pv & 1]));
-        }
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_f16_ts(tmem + 256 + t * 128, tmem + col + kk * 8, sdesc_hi(va + kk * (2048 >> 4)),
+                         IDESC_PV, kk > 0 || !first);
+          }
+        };
+        half(0);
+        wait(sm.p_full[u], sc & 1);
+        if (!ok) return;
+        half(1);
+        if (leader) mma_commit(smem_u32(&sm.pv_done[t][pv & 1]));
         ++pv;
       };
       while (ok && next_piece(p, rp, cur, end, pc)) {
@@ -374,8 +384,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (pc.nt == 2) {
             wait(sm.kv_full[vs], vph);
             if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
-            wait(sm.p_full[0], sc0 & 1);
-            ++sc0;
+            wait(sm.p_half[0], sc0 & 1);
             if (j == 0) {
               wait(sm.o_free[0], (oc0 & 1) ^ 1);
               ++oc0;
@@ -385,7 +394,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               ++tc;
             }
             if (!ok) break;
-            issue_pv(0, 0, vs, j == 0);
+            issue_pv(0, 0, vs, j == 0, sc0++);
+            if (!ok) break;
             if (more) {
               wait(sm.kv_full[kst], kph);
               if (!ok) break;
@@ -393,14 +403,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               commit(sm.s_full[0]);
               if (j + 2 == n) commit(sm.q_empty[0]);
             }
-            wait(sm.p_full[1], sc1 & 1);
-            ++sc1;
+            wait(sm.p_half[1], sc1 & 1);
             if (j == 0) {
               wait(sm.o_free[1], (oc1 & 1) ^ 1);
               ++oc1;
             }
             if (!ok) break;
-            issue_pv(1, 128, vs, j == 0);
+            issue_pv(1, 1, vs, j == 0, sc1++);
+            if (!ok) break;
             commit(sm.kv_empty[vs]);
             if (more) {
               issue_s(1, 128, kst);
@@ -420,9 +430,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             }
             wait(sm.kv_full[vs], vph);
             if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
-            wait(sm.p_full[odd ? 2 : 0], (odd ? sc2 : sc0) & 1);
-            if (odd) ++sc2;
-            else ++sc0;
+            wait(sm.p_half[odd ? 2 : 0], (odd ? sc2 : sc0) & 1);
             if (j == 0) {
               wait(sm.o_free[0], (oc0 & 1) ^ 1);
               ++oc0;
@@ -432,7 +440,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               ++tc;
             }
             if (!ok) break;
-            issue_pv(0, odd ? 128 : 0, vs, j == 0);
+            issue_pv(0, odd ? 2 : 0, vs, j == 0, odd ? sc2++ : sc0++);
+            if (!ok) break;
             commit(sm.kv_empty[vs]);
           }
         }
@@ -492,71 +501,18 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // every product is waited for once, in order: the one that this S was issued after
         const int behind = pc.nt == 2 ? 1 : 2;
         if (j >= behind && !pv_wait(pv + j - behind)) { ok = false; break; }
+        const uint32_t bar_half = smem_u32(&sm.p_half[u]), bar_full = smem_u32(&sm.p_full[u]);
+        bool half_sent = false;
         if (active) {
           tc_fence_after();
           const uint32_t sbase = tmem + lane_addr + (u ? 128 : 0);
           const int nvis = valid ? pos - (pc.page0 + j) * 128 + 1 : 128;
           const bool masked = __any_sync(0xffffffffu, nvis < 128);
           uint32_t v[4][32];
-          float mb;
-          auto load = [&]() {
-            float red[4];
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              reg_fence(v[cc]);
-              reg_fence1(red[cc]);
-            }
-            mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-            if (masked) {
-              mb = -INFINITY;
-#pragma unroll
-              for (int cc = 0; cc < 4; ++cc)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  if (cc * 32 + i >= nvis) v[cc][i] = 0xff800000u;  // -inf
-                  mb = fmaxf(mb, __uint_as_float(v[cc][i]));
-                }
-            }
-          };
-          load();
-          if (j == 0) {
-            m = mb == -INFINITY ? 0.f : mb;  // a row that sees nothing here keeps p = 0
-          } else {
-            const bool need = (mb - m) * c > kRescale;
-            if (__any_sync(0xffffffffu, need)) {
-              if (pc.nt == 1 && !pv_wait(pv + j - 1)) { ok = false; break; }
-              tc_fence_after();
-              const float f = need ? fast_exp2((m - mb) * c) : 1.f;
-              if (need) m = mb;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float x, y;
-                unpack_f2(lsum[h], x, y);
-                lsum[h] = pack_f2(x * f, y * f);
-              }
-#pragma unroll
-              for (int cc = 0; cc < D / 32; ++cc) {
-                tmem_ld32(obase + cc * 32, v[0]);
-                tmem_ld_wait();
-                reg_fence(v[0]);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
-                tmem_st32(obase + cc * 32, v[0]);
-              }
-              tmem_st_wait();
-              const float keep = mb;
-              load();
-              mb = keep;
-            }
-          }
-          const uint64_t c2 = pack_f2(c, c), off2 = pack_f2(bias - m * c, bias - m * c);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
+          float red[4];
+          const uint64_t c2 = pack_f2(c, c);
+          auto exps = [&](int h, uint32_t (&pk)[32]) {  // P of the keys 64 h .. 64 h + 63
+            const uint64_t off2 = pack_f2(bias - m * c, bias - m * c);
 #pragma unroll
             for (int i = 0; i < 64; i += 2) {
               const int cc = 2 * h + i / 32, e = i % 32;
@@ -568,13 +524,115 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               lsum[(i >> 1) & 1] = add_f2(lsum[(i >> 1) & 1], pack_f2(x, y));
               pk[i / 2] = pack_p<QUANT>(x, y);
             }
-            tmem_st32(sbase + h * 32, pk);
+          };
+          bool done = false;
+          if (j > 0 && !masked) {
+            // the usual page: the reference maximum holds, so the first half's exponentials run
+            // under the second half's load, and its products under the second half's exponentials
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              reg_fence(v[cc]);
+              reg_fence1(red[cc]);
+            }
+#pragma unroll
+            for (int cc = 2; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+            const uint64_t keep0 = lsum[0], keep1 = lsum[1];
+            uint32_t pk[32];
+            exps(0, pk);
+            tmem_ld_wait();
+#pragma unroll
+            for (int cc = 2; cc < 4; ++cc) {
+              reg_fence(v[cc]);
+              reg_fence1(red[cc]);
+            }
+            const float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+            if (!__any_sync(0xffffffffu, (mb - m) * c > kRescale)) {
+              tmem_st32(sbase, pk);
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_half);
+              half_sent = done = true;
+              exps(1, pk);
+              tmem_st32(sbase + 32, pk);
+              tmem_st_wait();
+            } else {
+              lsum[0] = keep0;
+              lsum[1] = keep1;
+            }
           }
-          tmem_st_wait();
+          if (!done) {
+            float mb;
+            auto load = [&]() {
+#pragma unroll
+              for (int cc = 0; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int cc = 0; cc < 4; ++cc) {
+                reg_fence(v[cc]);
+                reg_fence1(red[cc]);
+              }
+              mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+              if (masked) {
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    if (cc * 32 + i >= nvis) v[cc][i] = 0xff800000u;  // -inf
+                    mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(v[cc][i]));
+                  }
+                mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              }
+            };
+            load();
+            if (j == 0) {
+              m = mb == -INFINITY ? 0.f : mb;  // a row that sees nothing here keeps p = 0
+            } else {
+              const bool need = (mb - m) * c > kRescale;
+              if (__any_sync(0xffffffffu, need)) {
+                if (pc.nt == 1 && !pv_wait(pv + j - 1)) { ok = false; break; }
+                tc_fence_after();
+                const float f = need ? fast_exp2((m - mb) * c) : 1.f;
+                if (need) m = mb;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float x, y;
+                  unpack_f2(lsum[h], x, y);
+                  lsum[h] = pack_f2(x * f, y * f);
+                }
+#pragma unroll
+                for (int cc = 0; cc < D / 32; ++cc) {
+                  tmem_ld32(obase + cc * 32, v[0]);
+                  tmem_ld_wait();
+                  reg_fence(v[0]);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
+                  tmem_st32(obase + cc * 32, v[0]);
+                }
+                tmem_st_wait();
+                load();
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[32];
+              exps(h, pk);
+              tmem_st32(sbase + h * 32, pk);
+            }
+            tmem_st_wait();
+          }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[u]));
+        if (lane == 0) {
+          if (!half_sent) mbar_arrive(bar_half);
+          mbar_arrive(bar_full);
+        }
       }
       if (!ok) break;
       // the last products into O_w
@@ -722,49 +780,57 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-// Merge of the tiles cut over several blocks: a warp per row, out = sum_i w_i O_i / sum_i w_i with
+// Merge of the tiles cut over several blocks: out = sum_i w_i O_i / sum_i w_i with
 // w_i = exp(lse_i - max lse); a piece in which the row sees no key (lse = -inf) is never read.
-template <int D>
+// WPR warps share a row's pieces (8 where tiles have few rows: a single token's tile may be cut
+// over every SM, and one warp would walk 76 pieces at a memory latency each).
+template <int D, int WPR>
 __global__ void __launch_bounds__(256)
 attention_merge_kernel(DevPlan p, AttArgs a) {
-  __shared__ float wts[8][kMaxCtas];
+  constexpr int RB = 8 / WPR, E = D / 32;  // rows per block, elements per lane
+  __shared__ float wts[RB][kMaxCtas];
+  __shared__ float sums[8][32 * E];
   pdl_wait();
   pdl_trigger();
   const AttMerge mg = p.att_merges[blockIdx.x];
   if (mg.req < 0) return;
   const RowPack rp(p.Hg);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int lr = blockIdx.y * 8 + warp, row = lr % 128;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, rb = warp / WPR, part = warp % WPR;
+  const int lr = blockIdx.y * RB + rb, row = lr % 128;
   const int ti = row / rp.HB, hg = (mg.vg % rp.blocks) * 128 + row % rp.HB;
   const int tok = mg.tile * 2 * rp.TB + (lr / 128) * rp.TB + ti;
   const ReqInfo* ri = p.reqs + mg.req;
-  if (lr >= p.att_slot_rows || ti >= rp.TB || tok >= __ldg(&ri->q_len) || hg >= p.Hg) return;
+  if (lr >= p.att_slot_rows || ti >= rp.TB || tok >= __ldg(&ri->q_len) || hg >= p.Hg)
+    return;  // WPR 8: the whole block
   const int np = mg.cta1 - mg.cta0 + 1;
   auto srow = [&](int i) {
     return (int64_t)(i == 0 ? 2 * mg.cta0 + 1 : 2 * (mg.cta0 + i)) * p.att_slot_rows + lr;
   };
-  float mx = -INFINITY;
-  for (int i = lane; i < np; i += 32) {
-    const float l = a.part_lse[srow(i)];
-    wts[warp][i] = l;
-    mx = fmaxf(mx, l);
+  // every warp of a row finds its weights (the same values); the first one keeps them
+  float mx = -INFINITY, l[kMaxCtas / 32];
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / 32; ++k) {
+    const int i = lane + 32 * k;
+    l[k] = i < np ? a.part_lse[srow(i)] : -INFINITY;
+    mx = fmaxf(mx, l[k]);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float sum = 0.f;
-  for (int i = lane; i < np; i += 32) {
-    const float l = wts[warp][i], wt = l == -INFINITY ? 0.f : __expf(l - mx);
-    wts[warp][i] = wt;
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / 32; ++k) {
+    const float wt = l[k] == -INFINITY ? 0.f : __expf(l[k] - mx);
+    if (part == 0 && lane + 32 * k < np) wts[rb][lane + 32 * k] = wt;
     sum += wt;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncwarp();
-  constexpr int E = D / 32;  // elements per lane
+  if (WPR > 1) __syncthreads();
+  else __syncwarp();
   float acc[E] = {};
 #pragma unroll 4
-  for (int i = 0; i < np; ++i) {
-    const float wt = wts[warp][i];
+  for (int i = part; i < np; i += WPR) {
+    const float wt = wts[rb][i];
     if (wt == 0.f) continue;
     const float* o = a.part + srow(i) * D + lane * E;
     if (E == 4) {
@@ -778,6 +844,15 @@ attention_merge_kernel(DevPlan p, AttArgs a) {
       acc[0] += wt * x.x;
       acc[1] += wt * x.y;
     }
+  }
+  if (WPR > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      for (int k = 1; k < WPR; ++k) acc[e] += sums[warp + k][lane * E + e];
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const int64_t flat = __ldg(&ri->tok0) + tok;
@@ -814,8 +889,12 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(p.att_ctas), dim3(QUANT ? 512 : 384), smem, st, tmQ, tmK, tmV, p, a);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attention_merge_kernel<D>, dim3(p.att_ctas, (p.att_slot_rows + 7) / 8), dim3(256),
-                 0, st, p, a);
+  if (p.att_slot_rows <= 32)
+    e = launch_pdl(attention_merge_kernel<D, 8>, dim3(p.att_ctas, p.att_slot_rows), dim3(256), 0, st,
+                   p, a);
+  else
+    e = launch_pdl(attention_merge_kernel<D, 1>, dim3(p.att_ctas, (p.att_slot_rows + 7) / 8),
+                   dim3(256), 0, st, p, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

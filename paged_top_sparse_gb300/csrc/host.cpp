@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -247,42 +248,59 @@ void build_indexer_tasks(sps_plan* pl) {
 
 // Work split of the full attention: the (tile, page) pairs of the batch in order (request, head
 // block, tile, page), a tile being two row tiles of 128 / HB tokens x HB heads of a KV head's
-// group, cut into equal runs, one per SM.
+// group, cut into runs of equal cost, one per SM.  A tile costs its pages plus kAttTileCost for its
+// fill, drain and epilogue; a cut near a tile's border moves onto it.
+constexpr int kAttTileCost = 2, kAttSnap = 1;
 void build_attention_runs(sps_plan* pl) {
   const sps_problem& p = pl->pb;
   const int hg = p.num_q_heads / p.num_kv_heads, HB = std::min(hg, 128), TB = 128 / HB;
   const int nv = p.num_kv_heads * ((hg + HB - 1) / HB), tt = 2 * TB;
+  static const int tile_cost = getenv("ATT_OV") ? atoi(getenv("ATT_OV")) : kAttTileCost;
+  static const int snap_ = getenv("ATT_SNAP") ? atoi(getenv("ATT_SNAP")) : kAttSnap;
   auto pages_of = [&](const ReqInfo& ri, int tile) {
     return (ri.ctx + std::min((tile + 1) * tt, ri.q_len) - 1) / kPage + 1;
   };
   int64_t total = 0;
   int max_q = 0;
   for (const ReqInfo& ri : pl->reqs) {
-    int64_t pages = 0;
-    for (int t = 0; t * tt < ri.q_len; ++t) pages += pages_of(ri, t);
-    total += pages * nv;
+    int64_t cost = 0;
+    for (int t = 0; t * tt < ri.q_len; ++t) cost += pages_of(ri, t) + tile_cost;
+    total += cost * nv;
     max_q = std::max(max_q, ri.q_len);
   }
   pl->att_ctas = std::min(std::max(1, num_sms()), 256);
   pl->att_slot_rows = max_q > TB ? 256 : max_q * HB;
-  const int64_t runs = std::min<int64_t>(pl->att_ctas, total);
-  pl->att_starts.assign(pl->att_ctas + 1, AttCursor{p.batch, 0, 0, 0});
+  const AttCursor end{p.batch, 0, 0, 0, 0, 0, 0, 0};
+  pl->att_starts.assign(pl->att_ctas + 1, end);
   pl->att_merges.assign(pl->att_ctas, AttMerge{-1, 0, 0, 0, 0, 0});
-  int64_t at = 0;  // pairs before the present tile
-  int run = 0, merges = 0;
-  for (int b = 0; b < p.batch; ++b)
+  const int64_t cuts = std::min<int64_t>(pl->att_ctas, total);
+  int64_t at = 0, cut = 0;   // cost before the present tile; cuts placed
+  int run = 0, merges = 0;   // runs begun
+  bool pending = false;      // a cut moved onto the next tile's start
+  for (int b = 0; b < p.batch; ++b) {
+    const ReqInfo& ri = pl->reqs[b];
     for (int v = 0; v < nv; ++v)
-      for (int t = 0; t * tt < pl->reqs[b].q_len; ++t) {
-        const int n = pages_of(pl->reqs[b], t);
-        int first = -1;
-        while (run < runs && run * total / runs < at + n) {
-          const int page = (int)(run * total / runs - at);
+      for (int t = 0; t * tt < ri.q_len; ++t) {
+        const int n = pages_of(ri, t);
+        int first = -1, last_page = -1;  // first run that begins inside the tile, last cut's page
+        auto begin = [&](int page) {
+          if (page <= last_page) return;
           if (page > 0 && first < 0) first = run;
-          pl->att_starts[run++] = AttCursor{b, v, t, page};
+          pl->att_starts[run++] = AttCursor{b, v, t, page, ri.q_len, ri.ctx, ri.tok0, 0};
+          last_page = page;
+        };
+        if (pending) begin(0);
+        pending = false;
+        for (; cut < cuts && cut * total / cuts < at + n + tile_cost; ++cut) {
+          const int page = (int)(cut * total / cuts - at) - tile_cost;
+          if (page <= snap_) begin(0);
+          else if (n - page <= snap_) pending = true;
+          else begin(page);
         }
-        if (first >= 0) pl->att_merges[merges++] = AttMerge{b, v, t, first - 1, run - 1, 0};
-        at += n;
+        if (first > 0) pl->att_merges[merges++] = AttMerge{b, v, t, first - 1, run - 1, 0};
+        at += n + tile_cost;
       }
+  }
 }
 
 }  // namespace

@@ -104,6 +104,7 @@ struct DevPlan {
 // g = vg / head blocks per KV head) of request `req`; (batch, 0, 0, 0) is the end.
 struct AttCursor {
   int32_t req, vg, tile, page;
+  int32_t q_len, ctx, flat0, pad;  // the request's: new tokens, cached tokens, first flat token
 };
 // A query tile whose pages were cut over several blocks: blocks cta0 .. cta1 hold its pieces
 // (req < 0: unused entry).
