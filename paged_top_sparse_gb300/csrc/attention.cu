@@ -24,8 +24,8 @@
 //              (BF16: TMA with the 128-byte swizzle; NVFP4: codes and scales by bulk copies);
 //   warp 1     one thread issues every MMA: S_t = Q_t K^T, and O_t += P_t V with P in TMEM over S_t.
 //              With two row tiles their chains alternate, so one tile's products run under the
-//              other's softmax; with one row tile S alternates between S0 and S1 instead and the
-//              next page's S is computed under the present softmax;
+//              other's softmax; with one row tile its pages alternate between the two chains
+//              (S0 O0 the even, S1 O1 the odd ones) and the epilogue merges O0 and O1;
 //   warp 2     rows of the last page behind the request's last token are zeroed in the V tile (an
 //              unwritten slot may hold NaN, and 0 * NaN would reach every row);
 //   warps 4-7, 8-11   softmax and epilogue of row tile 0 / 1, a thread per row;
@@ -49,23 +49,21 @@ template <int D, bool QUANT>
 struct AttSmem {
   static constexpr int TILE = 128 * D * 2;
   static constexpr int RAWB = 128 * D / 2 + 128 * D / 16;  // NVFP4 codes and scales of a tile
-  static constexpr int RS = QUANT ? 3 : 1;
-  static constexpr int kBudget = 227 * 1024 - 1024 - 1024;  // alignment slack, barriers
-  static constexpr int STG = 8 * 4096;  // epilogue staging: 32 rows x 128 bytes for each warp
-  static constexpr int S0 = (kBudget - 2 * TILE - STG - (QUANT ? RS * RAWB : 0)) / TILE;
+  static constexpr int RS = QUANT ? 5 : 1;
+  static constexpr int STW = QUANT ? 2048 : 4096;  // epilogue staging of a warp: 32 row pieces
+  static constexpr int kBudget = 227 * 1024 - 1536;  // less the barriers and row statistics
+  static constexpr int S0 = (kBudget - 2 * TILE - 8 * STW - (QUANT ? RS * RAWB : 0)) / TILE;
   static constexpr int STAGES = S0 > 8 ? 8 : S0;
   static_assert(STAGES >= 3, "shared memory");
   uint8_t q[2][TILE];
   uint8_t kv[STAGES][TILE];
-  uint8_t stage[8][4096];
+  uint8_t stage[8][STW];
   alignas(16) uint8_t raw[RS][QUANT ? RAWB : 16];
   uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], raw_full[RS], raw_empty[RS];
-  // [2]: S1 as row tile 0 uses it (a work tile of one row tile); its waiters differ from those of
-  // S1 as row tile 1, so the two uses count their phases apart
-  uint64_t s_full[3], p_half[3], p_full[3];  // p_half: P of the first 64 keys
-  // P V product i into O_t completes pv_done[t][i % 2]: a waiter that is two products behind the
-  // present one (one row tile) still finds the phase it asks for
-  uint64_t pv_done[2][2], o_free[2], tail_go, tail_done, done;
+  uint64_t s_full[2], p_half[2], p_full[2];  // p_half: P of the first 64 keys
+  uint64_t pv_done[2][2];                    // P V product i into O_t completes pv_done[t][i % 2]
+  uint64_t o_free[2], stat_full, tail_go, tail_done, done;
+  float2 stat[128];  // (m, l) of the odd pages' rows
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -195,17 +193,23 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   constexpr int TILE = Smem::TILE, S = Smem::STAGES, RS = Smem::RS, DB = D / 64;
   constexpr uint32_t IDESC_QK = idesc_mma(!QUANT, !QUANT, 128, 128, false, false);
   constexpr uint32_t IDESC_PV = idesc_mma(!QUANT, !QUANT, 128, D, false, true);
-  extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                      ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int32_t* status = p.status;
   const RowPack rp(p.Hg);
 
+  if (smem_u32(smem_raw) & 1023) {  // the swizzled tiles need it; dynamic shared memory has it
+    if (tid == 0) set_status(status, DEV_OVERFLOW);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.q_full[i]), QUANT ? 4 : 1);
       mbar_init(smem_u32(&sm.q_empty[i]), 1);
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_half[i]), 4);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
       mbar_init(smem_u32(&sm.pv_done[i][0]), 1);
       mbar_init(smem_u32(&sm.pv_done[i][1]), 1);
       mbar_init(smem_u32(&sm.o_free[i]), 4);
@@ -218,11 +222,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(smem_u32(&sm.raw_full[i]), 1);
       mbar_init(smem_u32(&sm.raw_empty[i]), 4);
     }
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.p_half[i]), 4);
-      mbar_init(smem_u32(&sm.p_full[i]), 4);
-    }
+    mbar_init(smem_u32(&sm.stat_full), 4);
     mbar_init(smem_u32(&sm.tail_go), 1);
     mbar_init(smem_u32(&sm.tail_done), 1);
     mbar_init(smem_u32(&sm.done), 1);
@@ -253,20 +253,46 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       bool ok = true;
       while (ok && next_piece(p, rp, cur, end, pc)) {
         const int g = pc.vg / rp.blocks, h0 = g * p.Hg + (pc.vg % rp.blocks) * 128;
-        int ids = 0;
-        for (int pg = pc.page0; pg < pc.page1 && ok; ++pg) {
-          const int k = (pg - pc.page0) & 31;
-          if (k == 0 && pg + lane < pc.page1) {  // the next 32 pages' tiles
-            ids = __ldg(a.page_table + (int64_t)pc.req * p.max_pages + pg + lane);
-            if (ids < 0 || ids >= p.num_phys) {
+        // K runs a page ahead of V: K_0, K_1, V_0, K_2, V_1, ...
+        const int n = pc.page1 - pc.page0;
+        const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
+        auto load_ids = [&](int first) {  // physical pages of the lanes' pages first + lane
+          int id = 0;
+          if (first + lane < n) {
+            id = __ldg(pages + first + lane);
+            if (id < 0 || id >= p.num_phys) {
               set_status(status, DEV_BAD_PAGE);
-              ids = 0;
+              id = 0;
             }
           }
-          const int tile = __shfl_sync(0xffffffffu, ids, k) * p.Hkv + g;
+          return id * p.Hkv + g;
+        };
+        int ids = load_ids(0), next_ids = 0, k_tile = 0;
+        for (int s = 0; s <= n && ok; ++s) {
+          const int at = s & 31, v_tile = k_tile;
+          if (s > 0 && at == 0) ids = next_ids;
+          if (at == 8) next_ids = load_ids(s - 8 + 32);
+          k_tile = __shfl_sync(0xffffffffu, ids, at);
+          if (QUANT) {
+            // the copies in flight hold too few bytes to cover the memory's latency: pages go to
+            // L2 kAhead steps before their copy (at the start all of the first ones at once)
+            constexpr int kAhead = 12;
+            const int f = s == 0 ? lane : s + kAhead;
+            const int src = f & 31;
+            const int t = s == 0 ? ids
+                                 : __shfl_sync(0xffffffffu, f / 32 == s / 32 ? ids : next_ids, src);
+            if (f < n && (s == 0 ? lane <= kAhead : lane < 4)) {
+              if (s == 0 || lane == 0) bulk_prefetch_l2(a.kc + (int64_t)t * (64 * D), 64 * D);
+              if (s == 0 || lane == 1) bulk_prefetch_l2(a.vc + (int64_t)t * (64 * D), 64 * D);
+              if (s == 0 || lane == 2) bulk_prefetch_l2(a.ks + (int64_t)t * (8 * D), 8 * D);
+              if (s == 0 || lane == 3) bulk_prefetch_l2(a.vs + (int64_t)t * (8 * D), 8 * D);
+            }
+          }
           if (lane == 0) {
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++it) {
+            for (int kv = 0; kv < 2; ++kv) {
+              if (kv ? s == 0 : s == n) continue;  // no V before, no K behind
+              const int tile = kv ? v_tile : k_tile;
               if (QUANT) {
                 const uint32_t r = it % RS, f = smem_u32(&sm.raw_full[r]), d = smem_u32(sm.raw[r]);
                 ok = mbar_wait(smem_u32(&sm.raw_empty[r]), ((it / RS) & 1) ^ 1, abort_flag, status);
@@ -274,16 +300,18 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 mbar_expect_tx(f, Smem::RAWB);
                 bulk_load(d, (kv ? a.vc : a.kc) + (int64_t)tile * (64 * D), 64 * D, f);
                 bulk_load(d + 64 * D, (kv ? a.vs : a.ks) + (int64_t)tile * (8 * D), 8 * D, f);
+                ++it;
                 continue;
               }
-              const uint32_t s = it % S, f = smem_u32(&sm.kv_full[s]);
-              ok = mbar_wait(smem_u32(&sm.kv_empty[s]), ((it / S) & 1) ^ 1, abort_flag, status);
+              const uint32_t sg = it % S, f = smem_u32(&sm.kv_full[sg]);
+              ok = mbar_wait(smem_u32(&sm.kv_empty[sg]), ((it / S) & 1) ^ 1, abort_flag, status);
               if (!ok) break;
               mbar_expect_tx(f, TILE);
               for (int db = 0; db < DB; ++db)
-                tma_load_2d(smem_u32(sm.kv[s]) + db * 16384, kv ? &tmV : &tmK, db * 64, tile * 128,
+                tma_load_2d(smem_u32(sm.kv[sg]) + db * 16384, kv ? &tmV : &tmK, db * 64, tile * 128,
                             f);
-              if (kv == 0 && pg == pc.page0) {  // Q behind the first K tile
+              ++it;
+              if (s == 0) {  // Q behind the first K tile
                 for (int t = 0; t < pc.nt && ok; ++t) {
                   uint32_t& qc = t ? qc1 : qc0;
                   ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
@@ -309,140 +337,134 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool leader = elect_one();
       const uint32_t q_lo = sdesc_lo(smem_u32(sm.q[0]), 16), kv_lo = smem_u32(sm.kv[0]) >> 4;
       uint32_t st = 0, ph = 0;  // ring stage and phase of the next K or V tile
-      uint32_t qc0 = 0, qc1 = 0, sc0 = 0, sc1 = 0, sc2 = 0, oc0 = 0, oc1 = 0, pv0 = 0, pv1 = 0, tc = 0;
+      uint32_t qc0 = 0, qc1 = 0, sc[2] = {0, 0}, oc[2] = {0, 0}, pvc[2] = {0, 0}, tc = 0;
       bool ok = true;
       auto wait = [&](uint64_t& bar, uint32_t parity) {
         if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
       };
-      auto advance = [&]() {
+      struct Tile {
+        uint32_t stage, phase;
+      };
+      auto take = [&]() {
+        const Tile x{st, ph};
         if (++st == S) {
           st = 0;
           ph ^= 1;
         }
+        return x;
       };
       auto commit = [&](uint64_t& bar) {
         if (leader) mma_commit(smem_u32(&bar));
       };
-      auto issue_s = [&](int t, uint32_t col, uint32_t stage) {  // S at column col = Q_t K^T
+      // S_t = Q_q K^T
+      auto issue_s = [&](int t, int q, const Tile& k) {
         tc_fence_after();
-        const uint32_t qa = q_lo + t * (TILE >> 4), ka = sdesc_lo(0, 16) + kv_lo + stage * (TILE >> 4);
+        const uint32_t qa = q_lo + q * (TILE >> 4),
+                       ka = sdesc_lo(0, 16) + kv_lo + k.stage * (TILE >> 4);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) >> 4;
-            mma_f16_ss(tmem + col, sdesc_hi(qa + off), sdesc_hi(ka + off), IDESC_QK, kk > 0);
+            mma_f16_ss(tmem + t * 128, sdesc_hi(qa + off), sdesc_hi(ka + off), IDESC_QK, kk > 0);
           }
         }
+        commit(sm.s_full[t]);
       };
-      // O_t += P V in two halves of 64 keys, the first as soon as its P is there (u: S buffer)
-      auto issue_pv = [&](int t, int u, uint32_t stage, bool first, uint32_t sc) {
-        const uint32_t col = u ? 128 : 0, va = sdesc_lo(0, 16384) + kv_lo + stage * (TILE >> 4);
-        uint32_t& pv = t ? pv1 : pv0;
+      // O_t (+)= P_t V in two halves of 64 keys, the first as soon as its P is there
+      auto issue_pv = [&](int t, const Tile& v, bool first, bool tail) {
+        const uint32_t va = sdesc_lo(0, 16384) + kv_lo + v.stage * (TILE >> 4);
         auto half = [&](int h) {
           tc_fence_after();
           if (leader) {
 #pragma unroll
             for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-              mma_f16_ts(tmem + 256 + t * 128, tmem + col + kk * 8, sdesc_hi(va + kk * (2048 >> 4)),
-                         IDESC_PV, kk > 0 || !first);
+              mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                         sdesc_hi(va + kk * (2048 >> 4)), IDESC_PV, kk > 0 || !first);
           }
         };
+        wait(sm.p_half[t], sc[t] & 1);
+        if (first) {
+          wait(sm.o_free[t], (oc[t] & 1) ^ 1);
+          ++oc[t];
+        }
+        if (tail) {
+          wait(sm.tail_done, tc & 1);
+          ++tc;
+        }
+        if (!ok) return;
         half(0);
-        wait(sm.p_full[u], sc & 1);
+        wait(sm.p_full[t], sc[t] & 1);
+        ++sc[t];
         if (!ok) return;
         half(1);
-        if (leader) mma_commit(smem_u32(&sm.pv_done[t][pv & 1]));
-        ++pv;
+        if (leader) mma_commit(smem_u32(&sm.pv_done[t][pvc[t] & 1]));
+        ++pvc[t];
       };
       while (ok && next_piece(p, rp, cur, end, pc)) {
         const int n = pc.page1 - pc.page0;
         // rows of the last page behind the request's last token
         const bool tail = !QUANT && pc.page1 * 128 > pc.ctx + pc.q_len;
-        wait(sm.kv_full[st], ph);
-        wait(sm.q_full[0], qc0 & 1);
-        ++qc0;
-        if (!ok) break;
-        issue_s(0, 0, st);
-        commit(sm.s_full[0]);
-        if (n == 1) commit(sm.q_empty[0]);
-        if (pc.nt == 2) {
-          wait(sm.q_full[1], qc1 & 1);
-          ++qc1;
+        {
+          const Tile k = take();
+          wait(sm.kv_full[k.stage], k.phase);
+          wait(sm.q_full[0], qc0 & 1);
+          ++qc0;
           if (!ok) break;
-          issue_s(1, 128, st);
-          commit(sm.s_full[1]);
-          if (n == 1) commit(sm.q_empty[1]);
-        }
-        commit(sm.kv_empty[st]);
-        advance();
-        for (int j = 0; j < n; ++j) {
-          const bool more = j + 1 < n;
-          const uint32_t vs = st, vph = ph;
-          advance();
-          const uint32_t kst = st, kph = ph;
-          if (more) advance();
+          issue_s(0, 0, k);
+          if (n == 1) commit(sm.q_empty[0]);
           if (pc.nt == 2) {
-            wait(sm.kv_full[vs], vph);
+            wait(sm.q_full[1], qc1 & 1);
+            ++qc1;
+            if (!ok) break;
+            issue_s(1, 1, k);
+            if (n == 1) commit(sm.q_empty[1]);
+          }
+          commit(sm.kv_empty[k.stage]);
+        }
+        if (pc.nt == 2) {
+          for (int j = 0; j < n; ++j) {
+            const bool more = j + 1 < n;
+            Tile k{};
+            if (more) k = take();
+            const Tile v = take();
+            wait(sm.kv_full[v.stage], v.phase);
             if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
-            wait(sm.p_half[0], sc0 & 1);
-            if (j == 0) {
-              wait(sm.o_free[0], (oc0 & 1) ^ 1);
-              ++oc0;
-            }
-            if (tail && !more) {
-              wait(sm.tail_done, tc & 1);
-              ++tc;
-            }
-            if (!ok) break;
-            issue_pv(0, 0, vs, j == 0, sc0++);
-            if (!ok) break;
-            if (more) {
-              wait(sm.kv_full[kst], kph);
-              if (!ok) break;
-              issue_s(0, 0, kst);
-              commit(sm.s_full[0]);
-              if (j + 2 == n) commit(sm.q_empty[0]);
-            }
-            wait(sm.p_half[1], sc1 & 1);
-            if (j == 0) {
-              wait(sm.o_free[1], (oc1 & 1) ^ 1);
-              ++oc1;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (ok) issue_pv(t, v, j == 0, t == 0 && tail && !more);
+              if (ok && more) {
+                if (t == 0) wait(sm.kv_full[k.stage], k.phase);
+                if (ok) issue_s(t, t, k);
+                if (ok && j + 2 == n) commit(sm.q_empty[t]);
+              }
             }
             if (!ok) break;
-            issue_pv(1, 1, vs, j == 0, sc1++);
-            if (!ok) break;
-            commit(sm.kv_empty[vs]);
-            if (more) {
-              issue_s(1, 128, kst);
-              commit(sm.s_full[1]);
-              commit(sm.kv_empty[kst]);
-              if (j + 2 == n) commit(sm.q_empty[1]);
-            }
-          } else {
-            const bool odd = j & 1;  // this page's S buffer
-            if (more) {              // the next page's S under this page's softmax
-              wait(sm.kv_full[kst], kph);
-              if (!ok) break;
-              issue_s(0, odd ? 0 : 128, kst);
-              commit(sm.s_full[odd ? 0 : 2]);
-              commit(sm.kv_empty[kst]);
-              if (j + 2 == n) commit(sm.q_empty[0]);
-            }
-            wait(sm.kv_full[vs], vph);
-            if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
-            wait(sm.p_half[odd ? 2 : 0], (odd ? sc2 : sc0) & 1);
-            if (j == 0) {
-              wait(sm.o_free[0], (oc0 & 1) ^ 1);
-              ++oc0;
-            }
-            if (tail && !more) {
-              wait(sm.tail_done, tc & 1);
-              ++tc;
-            }
-            if (!ok) break;
-            issue_pv(0, odd ? 2 : 0, vs, j == 0, odd ? sc2++ : sc0++);
-            if (!ok) break;
-            commit(sm.kv_empty[vs]);
+            commit(sm.kv_empty[v.stage]);
+            if (more) commit(sm.kv_empty[k.stage]);
+          }
+        } else {
+          auto next_s = [&](int i, int t) {  // S of page i
+            const Tile k = take();
+            wait(sm.kv_full[k.stage], k.phase);
+            if (!ok) return;
+            issue_s(t, 0, k);
+            commit(sm.kv_empty[k.stage]);
+            if (i + 1 == n) commit(sm.q_empty[0]);
+          };
+          auto page = [&](int j, int t) {
+            const Tile v = take();
+            wait(sm.kv_full[v.stage], v.phase);
+            const bool z = tail && j + 1 == n;
+            if (z && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
+            if (ok) issue_pv(t, v, j < 2, z);
+            if (!ok) return;
+            commit(sm.kv_empty[v.stage]);
+            if (j + 2 < n) next_s(j + 2, t);
+          };
+          if (n > 1) next_s(1, 1);
+          for (int j = 0; j < n && ok; j += 2) {
+            page(j, 0);
+            if (j + 1 < n && ok) page(j + 1, 1);
           }
         }
       }
@@ -477,15 +499,17 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t obase = tmem + lane_addr + 256 + w * 128;
     const float c = a.c, bias = QUANT ? kF16Bias : 0.f;
     const int ti = row / rp.HB, hh = row % rp.HB;
-    uint32_t su = 0, su2 = 0, pv = 0;  // uses of this row tile's S buffers, P V products into O_w
+    uint32_t su = 0, pv = 0, sx = 0;  // uses of S_w, P V products into O_w, statistics received
     bool ok = true;
     auto pv_wait = [&](uint32_t i) {  // product i into O_w is complete
       return mbar_wait(smem_u32(&sm.pv_done[w][i & 1]), (i >> 1) & 1, abort_flag, status);
     };
     while (ok && next_piece(p, rp, cur, end, pc)) {
-      if (w >= pc.nt) continue;
-      const int n = pc.page1 - pc.page0;
-      const int tok = pc.tok0 + w * rp.TB + ti;
+      // with one row tile, this warpgroup takes the pages of its parity
+      const bool split = pc.nt == 1;
+      const int np = pc.page1 - pc.page0, n = split ? (np + 1 - w) / 2 : np;
+      if (n == 0) continue;
+      const int tok = pc.tok0 + (split ? 0 : w * rp.TB) + ti;
       const int hg = (pc.vg % rp.blocks) * 128 + hh;  // head within the KV head's group
       const bool valid = ti < rp.TB && tok < pc.q_len && hg < p.Hg;
       const int pos = pc.ctx + tok;
@@ -493,36 +517,32 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float m = 0.f;
       uint64_t lsum[2] = {0, 0};
       for (int j = 0; j < n; ++j) {
-        const bool alt = pc.nt == 1 && (j & 1);
-        const int u = alt ? 2 : w;
-        uint32_t& uses = alt ? su2 : su;
-        if (!mbar_wait(smem_u32(&sm.s_full[u]), uses & 1, abort_flag, status)) { ok = false; break; }
-        ++uses;
-        // every product is waited for once, in order: the one that this S was issued after
-        const int behind = pc.nt == 2 ? 1 : 2;
-        if (j >= behind && !pv_wait(pv + j - behind)) { ok = false; break; }
-        const uint32_t bar_half = smem_u32(&sm.p_half[u]), bar_full = smem_u32(&sm.p_full[u]);
+        if (!mbar_wait(smem_u32(&sm.s_full[w]), su & 1, abort_flag, status)) { ok = false; break; }
+        ++su;
+        // every product is waited for once, in order: the one before this S
+        if (j > 0 && !pv_wait(pv + j - 1)) { ok = false; break; }
+        const uint32_t bar_half = smem_u32(&sm.p_half[w]), bar_full = smem_u32(&sm.p_full[w]);
         bool half_sent = false;
         if (active) {
           tc_fence_after();
-          const uint32_t sbase = tmem + lane_addr + (u ? 128 : 0);
-          const int nvis = valid ? pos - (pc.page0 + j) * 128 + 1 : 128;
+          const uint32_t sbase = tmem + lane_addr + w * 128;
+          const int page = pc.page0 + (split ? 2 * j + w : j);
+          const int nvis = valid ? pos - page * 128 + 1 : 128;
           const bool masked = __any_sync(0xffffffffu, nvis < 128);
           uint32_t v[4][32];
           float red[4];
           const uint64_t c2 = pack_f2(c, c);
-          auto exps = [&](int h, uint32_t (&pk)[32]) {  // P of the keys 64 h .. 64 h + 63
+          auto exps = [&](int cc, uint32_t* pk) {  // P of the keys 32 cc .. 32 cc + 31
             const uint64_t off2 = pack_f2(bias - m * c, bias - m * c);
 #pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const int cc = 2 * h + i / 32, e = i % 32;
+            for (int e = 0; e < 32; e += 2) {
               float x, y;
               unpack_f2(fma_f2(pack_f2(__uint_as_float(v[cc][e]), __uint_as_float(v[cc][e + 1])),
                                c2, off2), x, y);
               x = fast_exp2(x);
               y = fast_exp2(y);
-              lsum[(i >> 1) & 1] = add_f2(lsum[(i >> 1) & 1], pack_f2(x, y));
-              pk[i / 2] = pack_p<QUANT>(x, y);
+              lsum[(e >> 1) & 1] = add_f2(lsum[(e >> 1) & 1], pack_f2(x, y));
+              pk[e / 2] = pack_p<QUANT>(x, y);
             }
           };
           bool done = false;
@@ -542,6 +562,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const uint64_t keep0 = lsum[0], keep1 = lsum[1];
             uint32_t pk[32];
             exps(0, pk);
+            exps(1, pk + 16);
             tmem_ld_wait();
 #pragma unroll
             for (int cc = 2; cc < 4; ++cc) {
@@ -551,13 +572,15 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
             if (!__any_sync(0xffffffffu, (mb - m) * c > kRescale)) {
               tmem_st32(sbase, pk);
+              uint32_t pk2[32];
+              exps(2, pk2);  // under the store
               tmem_st_wait();
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar_half);
               half_sent = done = true;
-              exps(1, pk);
-              tmem_st32(sbase + 32, pk);
+              exps(3, pk2 + 16);
+              tmem_st32(sbase + 32, pk2);
               tmem_st_wait();
             } else {
               lsum[0] = keep0;
@@ -594,8 +617,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             } else {
               const bool need = (mb - m) * c > kRescale;
               if (__any_sync(0xffffffffu, need)) {
-                if (pc.nt == 1 && !pv_wait(pv + j - 1)) { ok = false; break; }
-                tc_fence_after();
                 const float f = need ? fast_exp2((m - mb) * c) : 1.f;
                 if (need) m = mb;
 #pragma unroll
@@ -621,7 +642,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t pk[32];
-              exps(h, pk);
+              exps(2 * h, pk);
+              exps(2 * h + 1, pk + 16);
               tmem_st32(sbase + h * 32, pk);
             }
             tmem_st_wait();
@@ -635,23 +657,45 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
       if (!ok) break;
-      // the last products into O_w
-      if ((pc.nt == 1 && n > 1 && !pv_wait(pv + n - 2)) || !pv_wait(pv + n - 1)) break;
+      if (!pv_wait(pv + n - 1)) break;  // the last product into O_w
       pv += n;
+      float l;
+      {
+        float x, y, z, t;
+        unpack_f2(lsum[0], x, y);
+        unpack_f2(lsum[1], z, t);
+        l = (x + y) + (z + t);
+      }
+      if (split && w == 1) {  // the odd pages' statistics; warpgroup 0 reads O_1 itself
+        sm.stat[row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.stat_full));
+        continue;
+      }
+      const bool two = split && np > 1;
+      float f0 = 1.f, f1 = 0.f;
+      if (two) {
+        if (!mbar_wait(smem_u32(&sm.stat_full), sx & 1, abort_flag, status)) break;
+        ++sx;
+        const float2 o = sm.stat[row];
+        if (o.y > 0.f) {  // (0: the row sees nothing in the odd pages)
+          const float mm = l > 0.f ? fmaxf(m, o.x) : o.x;
+          f0 = l > 0.f ? fast_exp2((m - mm) * c) : 0.f;
+          f1 = fast_exp2((o.x - mm) * c);
+          l = l * f0 + o.y * f1;
+          m = mm;
+        }
+      }
       if (active) {
         tc_fence_after();
-        float l;
-        {
-          float x, y, z, t;
-          unpack_f2(lsum[0], x, y);
-          unpack_f2(lsum[1], z, t);
-          l = (x + y) + (z + t);
-        }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse = l > 0.f ? (m * c - bias + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        f0 *= inv;
+        f1 *= inv;
         const bool whole = pc.page0 == 0 && pc.page1 == pc.pages;
         const int64_t slot = 2 * blockIdx.x + (pc.page0 > 0 ? 0 : 1);
-        const int64_t srow = slot * p.att_slot_rows + w * 128 + row;
+        const int64_t srow = slot * p.att_slot_rows + w * 128 + row;  // (split: w = 0)
         const int64_t flat = pc.flat0 + tok;
         const int head = (pc.vg / rp.blocks) * p.Hg + hg;
         if (valid) {
@@ -666,15 +710,21 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int64_t obyte = whole ? (flat * a.out_stride + (int64_t)head * D) * 2 : srow * D * 4;
         uint8_t* const base = whole ? reinterpret_cast<uint8_t*>(a.out)
                                     : reinterpret_cast<uint8_t*>(a.part);
-        auto flush = [&](int chunk) {  // 128-byte piece `chunk` of every row
+        constexpr int PB = Smem::STW / 32, L = PB / 16;  // bytes of a row piece, lanes that write it
+        auto place = [&](int ch) {  // 16-byte chunk ch of this thread's row piece
+          return stg + (PB == 128 ? sw128_offset(lane, ch)
+                                  : lane * 64u + (((ch ^ (lane >> 1)) & 3u) << 4));
+        };
+        auto flush = [&](int piece) {  // row piece `piece` of every row
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + lane / 8;
-            const uint4 x = *reinterpret_cast<const uint4*>(stg + sw128_offset(r, lane % 8));
+          for (int i = 0; i < L; ++i) {
+            const int r = (32 / L) * i + lane / L, ch = lane % L;
+            const uint4 x = *reinterpret_cast<const uint4*>(
+                stg + (PB == 128 ? sw128_offset(r, ch)
+                                 : r * 64u + (((ch ^ (r >> 1)) & 3u) << 4)));
             const int64_t at = __shfl_sync(0xffffffffu, obyte, r);
-            if (vrows >> r & 1)
-              *reinterpret_cast<uint4*>(base + at + chunk * 128 + (lane % 8) * 16) = x;
+            if (vrows >> r & 1) *reinterpret_cast<uint4*>(base + at + piece * PB + ch * 16) = x;
           }
           __syncwarp();
         };
@@ -682,12 +732,28 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t v[32];
           tmem_ld32(obase + cc * 32, v);
-          tmem_ld_wait();
-          reg_fence(v);
+          if (two) {
+            uint32_t x[32];
+            tmem_ld32(obase + 128 + cc * 32, x);
+            tmem_ld_wait();
+            reg_fence(v);
+            reg_fence(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = __float_as_uint(__uint_as_float(v[i]) * f0 + __uint_as_float(x[i]) * f1);
+          } else {
+            tmem_ld_wait();
+            reg_fence(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f0);
+          }
           if (cc == D / 32 - 1) {  // O is read: the next work tile's products may begin
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[w]));
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&sm.o_free[w]));
+              if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
+            }
           }
           if (whole) {
 #pragma unroll
@@ -695,26 +761,28 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               uint32_t o[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                o[k] = pack_p<false>(__uint_as_float(v[i + 2 * k]) * inv,
-                                     __uint_as_float(v[i + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, (cc & 1) * 4 + i / 8)) =
+                o[k] = pack_p<false>(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+              *reinterpret_cast<uint4*>(place((cc * 4 + i / 8) % L)) =
                   make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if (cc & 1) flush(cc / 2);
+            if ((cc + 1) * 4 % L == 0) flush(cc * 4 / L);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(stg + sw128_offset(lane, i / 4)) = make_float4(
-                  __uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
-                  __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
-            flush(cc);
+            for (int i = 0; i < 32; i += 4) {
+              *reinterpret_cast<uint4*>(place((i / 4) % L)) =
+                  make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              if ((i / 4 + 1) % L == 0) flush(cc * (8 / L) + i / 4 / L);
+            }
           }
         }
         continue;
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[w]));
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.o_free[w]));
+        if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
+      }
     }
   } else {
     if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -751,8 +819,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[t]));
       }
-      const int n2 = 2 * (pc.page1 - pc.page0);
-      for (int i = 0; i < n2 && ok; ++i, ++it) {
+      const int n = pc.page1 - pc.page0;
+      for (int i = 0; i < 2 * n && ok; ++i, ++it) {  // K_0, K_1, V_0, K_2, V_1, ...
         const uint32_t r = it % RS, s = it % S;
         if (!mbar_wait(smem_u32(&sm.raw_full[r]), (it / RS) & 1, abort_flag, status) ||
             !mbar_wait(smem_u32(&sm.kv_empty[s]), ((it / S) & 1) ^ 1, abort_flag, status)) {
@@ -760,8 +828,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           break;
         }
         // V rows behind the request's last token become zero, whatever the slots hold
-        const int rows = (i & 1) ? min(128, pc.ctx + pc.q_len - (pc.page0 + i / 2) * 128) : 128;
-        nvfp4_tile_convert<D, false>(sm.raw[r], sm.kv[s], ct, 128, rows);
+        const bool is_v = i > 0 && (i % 2 == 0 || i == 2 * n - 1);
+        const int page = pc.page0 + (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
+        const int rows = is_v ? min(128, pc.ctx + pc.q_len - page * 128) : 128;
+        nvfp4_tile_convert_row<D>(sm.raw[r], sm.kv[s], ct, rows);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -883,7 +953,8 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
         !encode_tmap_2d(&tmV, 0, const_cast<void*>(vc), D, rows, (uint64_t)D * 2, 64, 128, true))
       return cudaErrorInvalidValue;
   }
-  const int smem = (int)sizeof(AttSmem<D, QUANT>) + 1024;
+  const int smem = (int)sizeof(AttSmem<D, QUANT>);
+  static_assert(sizeof(AttSmem<D, QUANT>) <= 227 * 1024, "shared memory");
   auto kern = attention_kernel<D, QUANT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

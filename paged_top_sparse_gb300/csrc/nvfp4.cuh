@@ -9,25 +9,13 @@ namespace sps {
 // `dst`: 128 rows of D elements in the 128-byte-swizzled layout TMA writes, as FP16 products
 // code x scale (exact) in column blocks of 64 elements (16 KB each), or, with E4M3OUT, as those
 // products rounded to E4M3 (one 128-byte block per row; D = 128).  Thread t of nt converts the
-// 16-byte code chunks t, t + nt, ... (32 elements each).  Rows from `rows` on become zero, whatever
-// their codes and scales hold.
+// 16-byte code chunks t, t + nt, ... (32 elements each).
 template <int D, bool E4M3OUT>
-__device__ __forceinline__ void nvfp4_tile_convert(const uint8_t* raw, uint8_t* dst, int t, int nt,
-                                                   int rows = 128) {
+__device__ __forceinline__ void nvfp4_tile_convert(const uint8_t* raw, uint8_t* dst, int t, int nt) {
   constexpr int CPR = D / 32;  // code chunks per row
   const uint8_t* scl = raw + 128 * D / 2;
   for (int c = t; c < 128 * CPR; c += nt) {
     const int row = c / CPR, i = c % CPR;
-    if (row >= rows) {
-#pragma unroll
-      for (int u = 0; u < (E4M3OUT ? 2 : 4); ++u) {
-        const int col = E4M3OUT ? 0 : 32 * i + 8 * u;
-        const uint32_t off = E4M3OUT ? sw128_offset(row, 2 * i + u)
-                                     : (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8);
-        *reinterpret_cast<uint4*>(dst + off) = make_uint4(0, 0, 0, 0);
-      }
-      continue;
-    }
     const uint4 cw = reinterpret_cast<const uint4*>(raw)[c];
     const uint32_t sb = *reinterpret_cast<const uint16_t*>(scl + row * (D / 16) + 2 * i);
     const uint32_t s0 = cvt_e4m3x2((uint16_t)((sb & 0xffu) * 0x0101u));  // elements 0..15
@@ -55,6 +43,47 @@ __device__ __forceinline__ void nvfp4_tile_convert(const uint8_t* raw, uint8_t* 
         *reinterpret_cast<uint4*>(dst + (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8)) =
             make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
       }
+    }
+  }
+}
+
+// The same FP16 products with a thread per row (128 threads), every load ahead of the arithmetic.
+// Rows from `rows` on become zero, whatever their codes and scales hold.  A thread starts at a
+// column of its own (row / 2 or row / 4), which keeps a quarter warp's loads, and at D = 128 its
+// stores, on distinct banks.
+template <int D>
+__device__ __forceinline__ void nvfp4_tile_convert_row(const uint8_t* raw, uint8_t* dst, int row,
+                                                       int rows) {
+  constexpr int CPR = D / 32;  // 16-byte code chunks per row
+  const uint4* codes = reinterpret_cast<const uint4*>(raw) + row * CPR;
+  uint64_t sc;  // the row's scales, one byte per 16 elements
+  if (CPR == 4) sc = *reinterpret_cast<const uint64_t*>(raw + 64 * D + row * 8);
+  else sc = *reinterpret_cast<const uint32_t*>(raw + 64 * D + row * 4);
+  const int turn = CPR == 4 ? row >> 1 : row >> 2;
+  uint4 cw[CPR];
+#pragma unroll
+  for (int k = 0; k < CPR; ++k) cw[k] = codes[(k + turn) % CPR];
+  if (row >= rows) {
+    sc = 0;
+#pragma unroll
+    for (int k = 0; k < CPR; ++k) cw[k] = make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < CPR; ++k) {
+    const int i = (k + turn) % CPR;
+    const uint32_t sb = (uint32_t)(sc >> (16 * i)) & 0xffffu;
+    const uint32_t two = cvt_e4m3x2((uint16_t)sb);  // the scales of elements 0..15 and 16..31
+    const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+    const uint32_t w[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t h[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        h[b] = hmul2_u32(cvt_e2m1x2((uint16_t)(w[u] >> (8 * b))), u < 2 ? s0 : s1);
+      const int col = 32 * i + 8 * u;
+      *reinterpret_cast<uint4*>(dst + (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
 }
