@@ -45,19 +45,26 @@ constexpr float kRescale = 8.f;   // log2 of the growth of the maximum that resc
 constexpr float kF16Bias = 7.f;   // log2 of the factor on FP16 p
 constexpr int kMaxCtas = 256;
 
-template <int D, bool QUANT>
+// SINGLE: every work tile of the batch has one row tile (decode steps); the second Q tile's room
+// goes to the rings.
+template <int D, bool QUANT, bool SINGLE>
 struct AttSmem {
   static constexpr int TILE = 128 * D * 2;
   static constexpr int RAWB = 128 * D / 2 + 128 * D / 16;  // NVFP4 codes and scales of a tile
-  static constexpr int RS = QUANT ? 5 : 1;
-  static constexpr int STW = QUANT ? 2048 : 4096;  // epilogue staging of a warp: 32 row pieces
+  static constexpr int QT = SINGLE ? 1 : 2;
   static constexpr int kBudget = 227 * 1024 - 1536;  // less the barriers and row statistics
-  static constexpr int S0 = (kBudget - 2 * TILE - 8 * STW - (QUANT ? RS * RAWB : 0)) / TILE;
+  // BF16: as many K/V stages as fit beside the epilogue's staging (32 rows x 128 bytes a warp).
+  // NVFP4: four, so that a step's K and V never wait for the products of the step before; the raw
+  // ring takes the rest, and the epilogue stages in the Q tile that its products have done with.
+  static constexpr int STG = QUANT ? 0 : 8;
+  static constexpr int S0 = QUANT ? 4 : (kBudget - QT * TILE - STG * 4096) / TILE;
   static constexpr int STAGES = S0 > 8 ? 8 : S0;
-  static_assert(STAGES >= 3, "shared memory");
-  uint8_t q[2][TILE];
+  static constexpr int RS0 = QUANT ? (kBudget - (QT + STAGES) * TILE) / RAWB : 1;
+  static constexpr int RS = RS0 > 10 ? 10 : RS0;
+  static_assert(STAGES >= 4 && (!QUANT || RS >= 2), "shared memory");
+  uint8_t q[QT][TILE];
   uint8_t kv[STAGES][TILE];
-  uint8_t stage[8][STW];
+  uint8_t stage[QUANT ? 1 : 8][QUANT ? 16 : 4096];
   alignas(16) uint8_t raw[RS][QUANT ? RAWB : 16];
   uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], raw_full[RS], raw_empty[RS];
   uint64_t s_full[2], p_half[2], p_full[2];  // p_half: P of the first 64 keys
@@ -185,11 +192,11 @@ struct AttArgs {
   float c;                 // softmax scale x q_scale x log2 e
 };
 
-template <int D, bool QUANT>
+template <int D, bool QUANT, bool SINGLE>
 __global__ void __launch_bounds__(QUANT ? 512 : 384, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, DevPlan p, AttArgs a) {
-  using Smem = AttSmem<D, QUANT>;
+  using Smem = AttSmem<D, QUANT, SINGLE>;
   constexpr int TILE = Smem::TILE, S = Smem::STAGES, RS = Smem::RS, DB = D / 64;
   constexpr uint32_t IDESC_QK = idesc_mma(!QUANT, !QUANT, 128, 128, false, false);
   constexpr uint32_t IDESC_PV = idesc_mma(!QUANT, !QUANT, 128, D, false, true);
@@ -206,7 +213,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.q_full[i]), QUANT ? 4 : 1);
-      mbar_init(smem_u32(&sm.q_empty[i]), 1);
+      mbar_init(smem_u32(&sm.q_empty[i]), QUANT ? 4 : 1);  // the epilogue's warps, or the MMA
       mbar_init(smem_u32(&sm.s_full[i]), 1);
       mbar_init(smem_u32(&sm.p_half[i]), 4);
       mbar_init(smem_u32(&sm.p_full[i]), 4);
@@ -312,7 +319,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             f);
               ++it;
               if (s == 0) {  // Q behind the first K tile
-                for (int t = 0; t < pc.nt && ok; ++t) {
+                for (int t = 0; t < (SINGLE ? 1 : pc.nt) && ok; ++t) {
                   uint32_t& qc = t ? qc1 : qc0;
                   ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
                   if (!ok) break;
@@ -411,17 +418,17 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           ++qc0;
           if (!ok) break;
           issue_s(0, 0, k);
-          if (n == 1) commit(sm.q_empty[0]);
-          if (pc.nt == 2) {
+          if (!QUANT && n == 1) commit(sm.q_empty[0]);
+          if (!SINGLE && pc.nt == 2) {
             wait(sm.q_full[1], qc1 & 1);
             ++qc1;
             if (!ok) break;
             issue_s(1, 1, k);
-            if (n == 1) commit(sm.q_empty[1]);
+            if (!QUANT && n == 1) commit(sm.q_empty[1]);
           }
           commit(sm.kv_empty[k.stage]);
         }
-        if (pc.nt == 2) {
+        if (!SINGLE && pc.nt == 2) {
           for (int j = 0; j < n; ++j) {
             const bool more = j + 1 < n;
             Tile k{};
@@ -435,7 +442,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               if (ok && more) {
                 if (t == 0) wait(sm.kv_full[k.stage], k.phase);
                 if (ok) issue_s(t, t, k);
-                if (ok && j + 2 == n) commit(sm.q_empty[t]);
+                if (!QUANT && ok && j + 2 == n) commit(sm.q_empty[t]);
               }
             }
             if (!ok) break;
@@ -449,7 +456,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (!ok) return;
             issue_s(t, 0, k);
             commit(sm.kv_empty[k.stage]);
-            if (i + 1 == n) commit(sm.q_empty[0]);
+            if (!QUANT && i + 1 == n) commit(sm.q_empty[0]);
           };
           auto page = [&](int j, int t) {
             const Tile v = take();
@@ -506,7 +513,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     };
     while (ok && next_piece(p, rp, cur, end, pc)) {
       // with one row tile, this warpgroup takes the pages of its parity
-      const bool split = pc.nt == 1;
+      const bool split = SINGLE || pc.nt == 1;
       const int np = pc.page1 - pc.page0, n = split ? (np + 1 - w) / 2 : np;
       if (n == 0) continue;
       const int tok = pc.tok0 + (split ? 0 : w * rp.TB) + ti;
@@ -705,26 +712,20 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // a thread holds a row; the warp turns 128 bytes of each of its 32 rows at a time in its
         // staging area, so that eight lanes write 128 contiguous bytes of a row (a thread writing
         // its own row would cost a memory transaction per 16 bytes)
-        uint8_t* stg = sm.stage[warp - 4];
+        uint8_t* stg = QUANT ? sm.q[SINGLE ? 0 : w] + quarter * (TILE / 4) : sm.stage[warp - 4];
         const uint32_t vrows = __ballot_sync(0xffffffffu, valid);
         const int64_t obyte = whole ? (flat * a.out_stride + (int64_t)head * D) * 2 : srow * D * 4;
         uint8_t* const base = whole ? reinterpret_cast<uint8_t*>(a.out)
                                     : reinterpret_cast<uint8_t*>(a.part);
-        constexpr int PB = Smem::STW / 32, L = PB / 16;  // bytes of a row piece, lanes that write it
-        auto place = [&](int ch) {  // 16-byte chunk ch of this thread's row piece
-          return stg + (PB == 128 ? sw128_offset(lane, ch)
-                                  : lane * 64u + (((ch ^ (lane >> 1)) & 3u) << 4));
-        };
-        auto flush = [&](int piece) {  // row piece `piece` of every row
+        auto flush = [&](int piece) {  // 128-byte piece `piece` of every row
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < L; ++i) {
-            const int r = (32 / L) * i + lane / L, ch = lane % L;
-            const uint4 x = *reinterpret_cast<const uint4*>(
-                stg + (PB == 128 ? sw128_offset(r, ch)
-                                 : r * 64u + (((ch ^ (r >> 1)) & 3u) << 4)));
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + lane / 8;
+            const uint4 x = *reinterpret_cast<const uint4*>(stg + sw128_offset(r, lane % 8));
             const int64_t at = __shfl_sync(0xffffffffu, obyte, r);
-            if (vrows >> r & 1) *reinterpret_cast<uint4*>(base + at + piece * PB + ch * 16) = x;
+            if (vrows >> r & 1)
+              *reinterpret_cast<uint4*>(base + at + piece * 128 + (lane % 8) * 16) = x;
           }
           __syncwarp();
         };
@@ -762,27 +763,27 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 o[k] = pack_p<false>(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
-              *reinterpret_cast<uint4*>(place((cc * 4 + i / 8) % L)) =
+              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, (cc & 1) * 4 + i / 8)) =
                   make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if ((cc + 1) * 4 % L == 0) flush(cc * 4 / L);
+            if (cc & 1) flush(cc / 2);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              *reinterpret_cast<uint4*>(place((i / 4) % L)) =
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, i / 4)) =
                   make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-              if ((i / 4 + 1) % L == 0) flush(cc * (8 / L) + i / 4 / L);
-            }
+            flush(cc);
           }
         }
-        continue;
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.o_free[w]));
+          if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&sm.o_free[w]));
-        if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
-      }
+      if (QUANT && lane == 0) mbar_arrive(smem_u32(&sm.q_empty[w]));  // staging and Q tile are free
     }
   } else {
     if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -792,52 +793,58 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool ok = QUANT;
     while (ok && next_piece(p, rp, cur, end, pc)) {
       const int h0 = (pc.vg % rp.blocks) * 128;
-      for (int t = 0; t < pc.nt && ok; ++t) {  // E4M3 Q rows, exactly, into the FP16 operand tile
-        uint32_t& qc = t ? qc1 : qc0;
-        ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
-        if (!ok) break;
-        ++qc;
-        for (int ch = ct; ch < 128 * (D / 16); ch += 128) {
-          const int r = ch / (D / 16), i = ch % (D / 16);
-          const int tok = pc.tok0 + t * rp.TB + r / rp.HB, hg = h0 + r % rp.HB;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < rp.HB * rp.TB && tok < pc.q_len && hg < p.Hg)
-            x = __ldg(reinterpret_cast<const uint4*>(
-                a.q + (pc.flat0 + tok) * a.q_stride +
-                (int64_t)((pc.vg / rp.blocks) * p.Hg + hg) * D + i * 16));
-          const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-          uint32_t o[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = cvt_e4m3x2((uint16_t)(wd[k / 2] >> (16 * (k & 1))));
-          uint8_t* d = sm.q[t] + (i / 4) * 16384;
-          *reinterpret_cast<uint4*>(d + sw128_offset(r, 2 * (i % 4))) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(d + sw128_offset(r, 2 * (i % 4) + 1)) =
-              make_uint4(o[4], o[5], o[6], o[7]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[t]));
-      }
       const int n = pc.page1 - pc.page0;
-      for (int i = 0; i < 2 * n && ok; ++i, ++it) {  // K_0, K_1, V_0, K_2, V_1, ...
-        const uint32_t r = it % RS, s = it % S;
-        if (!mbar_wait(smem_u32(&sm.raw_full[r]), (it / RS) & 1, abort_flag, status) ||
-            !mbar_wait(smem_u32(&sm.kv_empty[s]), ((it / S) & 1) ^ 1, abort_flag, status)) {
+      for (int i = 0; i < 2 * n; ++i, ++it) {  // K_0, K_1, V_0, K_2, V_1, ...
+        const uint32_t r = it % RS, sg = it % S;
+        const bool is_v = i > 0 && (i % 2 == 0 || i == 2 * n - 1);
+        const int page = pc.page0 + (i == 2 * n - 1 ? n - 1 : i / 2 - 1);  // (of a V tile)
+        if (!mbar_wait(smem_u32(&sm.raw_full[r]), (it / RS) & 1, abort_flag, status)) {
           ok = false;
           break;
         }
+        Nvfp4Row<D> x;
         // V rows behind the request's last token become zero, whatever the slots hold
-        const bool is_v = i > 0 && (i % 2 == 0 || i == 2 * n - 1);
-        const int page = pc.page0 + (i == 2 * n - 1 ? n - 1 : i / 2 - 1);
-        const int rows = is_v ? min(128, pc.ctx + pc.q_len - page * 128) : 128;
-        nvfp4_tile_convert_row<D>(sm.raw[r], sm.kv[s], ct, rows);
+        x.load(sm.raw[r], ct, is_v && pc.ctx + pc.q_len <= page * 128 + ct);
+        if (!mbar_wait(smem_u32(&sm.kv_empty[sg]), ((it / S) & 1) ^ 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        x.store(sm.kv[sg], ct);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sm.kv_full[s]));
+          mbar_arrive(smem_u32(&sm.kv_full[sg]));
           mbar_arrive(smem_u32(&sm.raw_empty[r]));
         }
+        // E4M3 Q rows, exactly, into the FP16 operand tiles, behind the first K tile
+        for (int t = 0; i == 0 && t < (SINGLE ? 1 : pc.nt) && ok; ++t) {
+          uint32_t& qc = t ? qc1 : qc0;
+          ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
+          if (!ok) break;
+          ++qc;
+          for (int ch = ct; ch < 128 * (D / 16); ch += 128) {
+            const int row = ch / (D / 16), col = ch % (D / 16);
+            const int tok = pc.tok0 + t * rp.TB + row / rp.HB, hg = h0 + row % rp.HB;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (row < rp.HB * rp.TB && tok < pc.q_len && hg < p.Hg)
+              x = __ldg(reinterpret_cast<const uint4*>(
+                  a.q + (pc.flat0 + tok) * a.q_stride +
+                  (int64_t)((pc.vg / rp.blocks) * p.Hg + hg) * D + col * 16));
+            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = cvt_e4m3x2((uint16_t)(wd[k / 2] >> (16 * (k & 1))));
+            uint8_t* d = sm.q[t] + (col / 4) * 16384;
+            *reinterpret_cast<uint4*>(d + sw128_offset(row, 2 * (col % 4))) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(d + sw128_offset(row, 2 * (col % 4) + 1)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[t]));
+        }
+        if (!ok) break;
       }
     }
   }
@@ -937,7 +944,7 @@ attention_merge_kernel(DevPlan p, AttArgs a) {
     a.out_lse[flat * p.H + head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
 }
 
-template <int D, bool QUANT>
+template <int D, bool QUANT, bool SINGLE>
 cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, const void* kc,
                           const void* vc, cudaStream_t st) {
   alignas(64) CUtensorMap tmQ, tmK, tmV;
@@ -953,9 +960,9 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
         !encode_tmap_2d(&tmV, 0, const_cast<void*>(vc), D, rows, (uint64_t)D * 2, 64, 128, true))
       return cudaErrorInvalidValue;
   }
-  const int smem = (int)sizeof(AttSmem<D, QUANT>);
-  static_assert(sizeof(AttSmem<D, QUANT>) <= 227 * 1024, "shared memory");
-  auto kern = attention_kernel<D, QUANT>;
+  const int smem = (int)sizeof(AttSmem<D, QUANT, SINGLE>);
+  static_assert(sizeof(AttSmem<D, QUANT, SINGLE>) <= 227 * 1024, "shared memory");
+  auto kern = attention_kernel<D, QUANT, SINGLE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(p.att_ctas), dim3(QUANT ? 512 : 384), smem, st, tmQ, tmK, tmV, p, a);
@@ -990,11 +997,18 @@ cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_
   a.part = static_cast<float*>(scratch);
   a.part_lse = a.part + 2ll * p.att_ctas * p.att_slot_rows * p.D;
   a.c = p.sm_scale * q_scale * 1.4426950408889634f;
-  if (p.D == 128)
-    return quant ? run_attention<128, true>(p, a, q, kc, vc, st)
-                 : run_attention<128, false>(p, a, q, kc, vc, st);
-  return quant ? run_attention<64, true>(p, a, q, kc, vc, st)
-               : run_attention<64, false>(p, a, q, kc, vc, st);
+  const RowPack rp(p.Hg);
+  const bool single = p.att_slot_rows <= rp.TB * rp.HB;
+#define SPS_ATT(DD, QQ) \
+  return single ? run_attention<DD, QQ, true>(p, a, q, kc, vc, st) \
+                : run_attention<DD, QQ, false>(p, a, q, kc, vc, st)
+  if (p.D == 128) {
+    if (quant) SPS_ATT(128, true);
+    SPS_ATT(128, false);
+  }
+  if (quant) SPS_ATT(64, true);
+  SPS_ATT(64, false);
+#undef SPS_ATT
 }
 
 }  // namespace sps

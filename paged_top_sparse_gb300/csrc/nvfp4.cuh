@@ -47,45 +47,48 @@ __device__ __forceinline__ void nvfp4_tile_convert(const uint8_t* raw, uint8_t* 
   }
 }
 
-// The same FP16 products with a thread per row (128 threads), every load ahead of the arithmetic.
-// Rows from `rows` on become zero, whatever their codes and scales hold.  A thread starts at a
-// column of its own (row / 2 or row / 4), which keeps a quarter warp's loads, and at D = 128 its
-// stores, on distinct banks.
+// The same FP16 products with a thread per row (128 threads): a row's codes and scales in
+// registers, then its operand row.  Rows marked empty become zero, whatever their codes and scales
+// hold.  A thread starts at a column of its own (row / 2 or row / 4), which keeps a quarter warp's
+// loads, and at D = 128 its stores, on distinct banks.
 template <int D>
-__device__ __forceinline__ void nvfp4_tile_convert_row(const uint8_t* raw, uint8_t* dst, int row,
-                                                       int rows) {
-  constexpr int CPR = D / 32;  // 16-byte code chunks per row
-  const uint4* codes = reinterpret_cast<const uint4*>(raw) + row * CPR;
-  uint64_t sc;  // the row's scales, one byte per 16 elements
-  if (CPR == 4) sc = *reinterpret_cast<const uint64_t*>(raw + 64 * D + row * 8);
-  else sc = *reinterpret_cast<const uint32_t*>(raw + 64 * D + row * 4);
-  const int turn = CPR == 4 ? row >> 1 : row >> 2;
+struct Nvfp4Row {
+  static constexpr int CPR = D / 32;  // 16-byte code chunks per row
   uint4 cw[CPR];
+  uint64_t sc;  // the row's scales, one byte per 16 elements
+  __device__ __forceinline__ static int turn(int row) { return CPR == 4 ? row >> 1 : row >> 2; }
+  __device__ __forceinline__ void load(const uint8_t* raw, int row, bool empty) {
+    const uint4* codes = reinterpret_cast<const uint4*>(raw) + row * CPR;
+    if (CPR == 4) sc = *reinterpret_cast<const uint64_t*>(raw + 64 * D + row * 8);
+    else sc = *reinterpret_cast<const uint32_t*>(raw + 64 * D + row * 4);
 #pragma unroll
-  for (int k = 0; k < CPR; ++k) cw[k] = codes[(k + turn) % CPR];
-  if (row >= rows) {
-    sc = 0;
+    for (int k = 0; k < CPR; ++k) cw[k] = codes[(k + turn(row)) % CPR];
+    if (empty) {
+      sc = 0;
 #pragma unroll
-    for (int k = 0; k < CPR; ++k) cw[k] = make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int k = 0; k < CPR; ++k) {
-    const int i = (k + turn) % CPR;
-    const uint32_t sb = (uint32_t)(sc >> (16 * i)) & 0xffffu;
-    const uint32_t two = cvt_e4m3x2((uint16_t)sb);  // the scales of elements 0..15 and 16..31
-    const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
-    const uint32_t w[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      uint32_t h[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        h[b] = hmul2_u32(cvt_e2m1x2((uint16_t)(w[u] >> (8 * b))), u < 2 ? s0 : s1);
-      const int col = 32 * i + 8 * u;
-      *reinterpret_cast<uint4*>(dst + (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8)) =
-          make_uint4(h[0], h[1], h[2], h[3]);
+      for (int k = 0; k < CPR; ++k) cw[k] = make_uint4(0, 0, 0, 0);
     }
   }
-}
+  __device__ __forceinline__ void store(uint8_t* dst, int row) const {
+#pragma unroll
+    for (int k = 0; k < CPR; ++k) {
+      const int i = (k + turn(row)) % CPR;
+      // the scales of elements 0..15 and 16..31 of the chunk
+      const uint32_t two = cvt_e4m3x2((uint16_t)(sc >> (16 * i)));
+      const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+      const uint32_t w[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t h[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          h[b] = hmul2_u32(cvt_e2m1x2((uint16_t)(w[u] >> (8 * b))), u < 2 ? s0 : s1);
+        const int col = 32 * i + 8 * u;
+        *reinterpret_cast<uint4*>(dst + (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+  }
+};
 
 }  // namespace sps
