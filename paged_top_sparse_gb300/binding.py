@@ -128,15 +128,26 @@ def _check(st: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = None
 
 
 def _stream(stream):
-    import torch
+    """The cudaStream_t of ``stream``, or of the current stream.  The lookup goes past torch's
+    stream objects where it can: making one costs more than a small kernel runs."""
+    if stream is not None:
+        return stream.cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
 
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream",
+                                                         "_cuda_getDevice"))
+        _raw_stream = ((lambda: get(dev())) if get and dev else
+                       (lambda: torch.cuda.current_stream().cuda_stream))
+    return _raw_stream()
 
 
 class Plan:
@@ -161,6 +172,7 @@ class Plan:
         self.workspace_bytes = ws.value
         self.head_dim, self.top_k = head_dim, top_k
         self.num_tokens = sum(int(x) for x in q_lens)
+        self.num_q_heads, self.num_kv_heads = num_q_heads, num_kv_heads
 
     def info(self) -> PlanInfo:
         inf = PlanInfo()
@@ -296,11 +308,21 @@ class Rope:
             raise ValueError("pair_axis needs one axis per pair")
         self.args = RopeArgs(_ptr(inv_freq), _ptr(positions), 2 * n, axes, int(bool(interleaved)),
                              (ctypes.c_uint8 * 64)(*ax))
+        self.ref = ctypes.pointer(self.args)
+
+
+_dtypes = {}
 
 
 def _expect(t, dtype, name):
     """A contiguous tensor of the named torch dtype (or None)."""
-    if t is not None and (str(t.dtype) != "torch." + dtype or not t.is_contiguous()):
+    if t is None:
+        return
+    if not _dtypes:
+        import torch
+
+        _dtypes.update(float32=torch.float32, int32=torch.int32)
+    if t.dtype is not _dtypes[dtype] or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor")
 
 
@@ -309,22 +331,23 @@ def _rope(rope, plan):
         return None
     if rope.positions is not None and rope.positions.shape[-1] != plan.num_tokens:
         raise ValueError(f"positions must be [axes][{plan.num_tokens}]")
-    return ctypes.byref(rope.args)
+    return rope.ref
 
 
 def _token_stride(t, plan, heads, name):
     """Elements between the tokens of a [T][heads][D] view whose rows are contiguous."""
     T, D = plan.num_tokens, plan.head_dim
-    if tuple(t.shape) != (T, heads, D) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    st = t.stride()
+    if t.shape != (T, heads, D) or st[2] != 1 or (heads > 1 and st[1] != D):
         raise ValueError(f"{name} must be [{T}][{heads}][{D}] with contiguous rows")
-    return t.stride(0) if T > 1 else heads * D
+    return st[0] if T > 1 else heads * D
 
 
 def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_scale, k_out,
                      workspace, stream=None):
     """Norm per head and rotation of q [T][H][D] and k [T][H_kv][D] (or None); token strides come
     from the tensors.  A one-byte ``q_out`` takes E4M3 codes of the result / ``q_scale``."""
-    H, G = plan.problem.num_q_heads, plan.problem.num_kv_heads
+    H, G = plan.num_q_heads, plan.num_kv_heads
     _expect(q_weight, "float32", "q_weight")
     _expect(k_weight, "float32", "k_weight")
     _check(lib().sps_qk_norm_rope(
@@ -340,7 +363,7 @@ def sps_kv_append_rope(plan: Plan, k_new, v_new, k_weight, eps, rope, page_table
                        k_scales, v_scales, workspace, stream=None):
     """``sps_kv_append`` with the key's norm and rotation on the way; k_new / v_new [T][H_kv][D]
     may be views with a token stride."""
-    G = plan.problem.num_kv_heads
+    G = plan.num_kv_heads
     _expect(k_weight, "float32", "k_weight")
     _check(lib().sps_kv_append_rope(
         plan.handle, _ptr(k_new), _token_stride(k_new, plan, G, "k_new"), _ptr(v_new),
@@ -360,7 +383,7 @@ def paged_attention_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_sc
                         out, out_lse, scratch, workspace, stream=None):
     """Full causal attention of q [T][H][D] over the paged cache into out [T][H][D] BF16 (both may
     have a token stride) and, unless None, out_lse [T][H] FP32."""
-    H = plan.problem.num_q_heads
+    H = plan.num_q_heads
     _expect(out_lse, "float32", "out_lse")
     _check(lib().paged_attention_fwd(
         plan.handle, _ptr(q), _token_stride(q, plan, H, "q"), float(q_scale), _ptr(k_cache),
