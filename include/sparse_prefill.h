@@ -350,11 +350,12 @@ typedef struct {
  * rotated, in one pass, in FP32 with one rounding at the end.
  *   q            device BF16, token i's H rows at q + i * q_token_stride (elements); k likewise
  *                with H_kv rows, or NULL (then k_out is NULL too)
- *   q_weight, k_weight  device FP32 [D], or NULL: no norm of those rows
+ *   q_weight, k_weight  device FP32 [D], 16-byte aligned, or NULL: no norm of those rows
  *   eps          added to the mean square (>= 0)
  *   rope         or NULL: no rotation
  *   q_out        device, [T][H][D] at q_out_token_stride: SPS_BF16, or SPS_E4M3 codes of
- *                y / q_scale (FP32 division, nearest even, saturating; q_scale finite and > 0)
+ *                y * (1 / q_scale) (FP32, nearest even, saturating; q_scale and its inverse finite
+ *                and > 0)
  *   k_out        device BF16, at k_out_token_stride
  * Buffers are 16-byte aligned; strides are multiples of 8 elements (16 for E4M3 codes) and at
  * least the rows of a token, so q and k may be views of one projection's output.  An output may

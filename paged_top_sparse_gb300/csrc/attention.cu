@@ -138,25 +138,6 @@ __device__ __forceinline__ bool next_piece(const DevPlan& p, const RowPack& rp, 
   }
 }
 
-// Pairs of FP32 in one 64-bit register: one instruction for two elements.
-__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack_f2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -538,17 +519,17 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const bool masked = __any_sync(0xffffffffu, nvis < 128);
           uint32_t v[4][32];
           float red[4];
-          const uint64_t c2 = pack_f2(c, c);
+          const uint64_t c2 = pack_f32x2(c, c);
           auto exps = [&](int cc, uint32_t* pk) {  // P of the keys 32 cc .. 32 cc + 31
-            const uint64_t off2 = pack_f2(bias - m * c, bias - m * c);
+            const uint64_t off2 = pack_f32x2(bias - m * c, bias - m * c);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float x, y;
-              unpack_f2(fma_f2(pack_f2(__uint_as_float(v[cc][e]), __uint_as_float(v[cc][e + 1])),
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[cc][e]), __uint_as_float(v[cc][e + 1])),
                                c2, off2), x, y);
               x = fast_exp2(x);
               y = fast_exp2(y);
-              lsum[(e >> 1) & 1] = add_f2(lsum[(e >> 1) & 1], pack_f2(x, y));
+              lsum[(e >> 1) & 1] = add_f32x2(lsum[(e >> 1) & 1], pack_f32x2(x, y));
               pk[e / 2] = pack_p<QUANT>(x, y);
             }
           };
@@ -629,8 +610,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   float x, y;
-                  unpack_f2(lsum[h], x, y);
-                  lsum[h] = pack_f2(x * f, y * f);
+                  unpack_f32x2(lsum[h], x, y);
+                  lsum[h] = pack_f32x2(x * f, y * f);
                 }
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
@@ -669,8 +650,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float l;
       {
         float x, y, z, t;
-        unpack_f2(lsum[0], x, y);
-        unpack_f2(lsum[1], z, t);
+        unpack_f32x2(lsum[0], x, y);
+        unpack_f32x2(lsum[1], z, t);
         l = (x + y) + (z + t);
       }
       if (split && w == 1) {  // the odd pages' statistics; warpgroup 0 reads O_1 itself

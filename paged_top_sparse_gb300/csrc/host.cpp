@@ -825,12 +825,12 @@ sps_status sps_qk_norm_rope(const sps_plan* pl, const void* q, int64_t q_stride,
     return fail(SPS_EINVAL,
                 "sps_qk_norm_rope: buffers must be non-NULL and 16-byte aligned, token strides "
                 "multiples of 16 bytes and at least a token's rows");
-  if ((q_weight && !aligned(q_weight, 4)) || (k_weight && !aligned(k_weight, 4)))
-    return fail(SPS_EINVAL, "sps_qk_norm_rope: misaligned weight");
+  if ((q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16)))
+    return fail(SPS_EINVAL, "sps_qk_norm_rope: weights must be 16-byte aligned");
   if (!(eps >= 0.f) || !std::isfinite(eps))
     return fail(SPS_EINVAL, "sps_qk_norm_rope: eps must be finite and >= 0");
-  if (e4m3 && (!(q_scale > 0.f) || !std::isfinite(q_scale)))
-    return fail(SPS_EINVAL, "sps_qk_norm_rope: q_scale must be finite and > 0");
+  if (e4m3 && (!(q_scale > 0.f) || !std::isfinite(q_scale) || !std::isfinite(1.f / q_scale)))
+    return fail(SPS_EINVAL, "sps_qk_norm_rope: q_scale and its inverse must be finite and > 0");
   DevRope r;
   st = make_rope(rope, p.head_dim, "sps_qk_norm_rope", &r);
   if (st != SPS_OK) return st;
@@ -846,7 +846,7 @@ sps_status sps_qk_norm_rope(const sps_plan* pl, const void* q, int64_t q_stride,
   a.q_out_stride = q_out_stride;
   a.k_out_stride = k_out_stride;
   a.eps = eps;
-  a.q_scale = q_scale;
+  a.q_scale_inv = e4m3 ? 1.f / q_scale : 1.f;
   return launched(launch_qk_norm_rope(make_dev_plan(pl, ws), r, a, rope && rope->interleaved, e4m3,
                                       reinterpret_cast<cudaStream_t>(stream)),
                   "q/k norm and rotation launch");
@@ -871,7 +871,7 @@ sps_status sps_kv_append_rope(const sps_plan* pl, const void* k_new, int64_t k_s
                 "sps_kv_append_rope: k_new/v_new must be non-NULL and 16-byte aligned, token "
                 "strides multiples of 8 and at least num_kv_heads * head_dim");
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(page_table, 4) ||
-      (k_weight && !aligned(k_weight, 4)))
+      (k_weight && !aligned(k_weight, 16)))
     return fail(SPS_EINVAL, "sps_kv_append_rope: misaligned cache, page table or weight");
   if (!(eps >= 0.f) || !std::isfinite(eps))
     return fail(SPS_EINVAL, "sps_kv_append_rope: eps must be finite and >= 0");

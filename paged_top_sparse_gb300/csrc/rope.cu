@@ -12,9 +12,11 @@
 // sincospi.  F is off by at most two units for inv_freq <= 1, so the angle by 2^-31 turns for any
 // 32-bit position.
 //
-// Layout: D / 8 lanes hold a row, 8 elements (16 bytes) each; a warp takes one token and walks
-// its rows, 32 * 8 / D at a time, so a token's angles are made once for all its heads.  Row sums
-// and the partner halves of a rotation travel by shuffles.
+// Layout: D / 8 lanes hold a row, 8 elements (16 bytes) each; a warp takes one token and walks its
+// rows, 32 * 8 / D at a time, four such passes in flight.  Its lanes make the token's angles once
+// (two pairs each) and hand them round through shared memory; weight, cosine and sine become two
+// coefficients per element, so a row costs y = (x A + x_partner B) / rms.  Row sums and the partner
+// halves travel by shuffles.
 #include <algorithm>
 #include <cstring>
 
@@ -46,249 +48,313 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+// The pairs' frequencies as turn fractions, made once per block.
+__device__ __forceinline__ void stage_turns(const DevRope& r, uint64_t* turns) {
+  if ((int)threadIdx.x < r.rot / 2) turns[threadIdx.x] = turn_fraction(__ldg(r.inv_freq + threadIdx.x));
+  __syncthreads();
+}
+
+// Cosine and sine of every pair of a token, by the whole warp.
+__device__ __forceinline__ void token_angles(const DevRope& r, const DevPlan& p, int tok,
+                                             const uint64_t* turns, float2* cs, int lane) {
+  for (int j = lane; j < r.rot / 2; j += 32) {
+    const int pos = r.positions ? __ldg(r.positions + (int64_t)r.axis[j] * p.T + tok)
+                                : __ldg(p.tok_pos + tok);
+    const uint64_t a = (uint64_t)(int64_t)pos * turns[j];
+    // a half turn is 2^31 units of the top word: the argument of sin(pi x)
+    sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &cs[j].y, &cs[j].x);
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void load_weights(const float* w, int d, float (&o)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 1.f;
+  if (w) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<float4*>(o + 4 * i) = __ldg(reinterpret_cast<const float4*>(w + d) + i);
+  }
+}
+
+// What a lane needs to rotate its chunk of 8 elements of any row of the token:
+// y = x A + x_partner B, packed in pairs.
+template <int D, bool INTER>
+struct Rotation {
+  uint64_t A[4], B[4];
+  bool on;      // the chunk lies inside the rotated dims
+  int partner;  // lane that holds the partner elements (half-split pairs)
+  __device__ __forceinline__ void make(const DevRope& r, const float* w, const float2* cs, int lane) {
+    const int chunk = lane % (D / 8), half = r.rot / 2, d0 = chunk * 8;
+    on = d0 < r.rot;
+    partner = lane;
+    int p0 = d0;  // the partner elements' first dim
+    if (!INTER && on) {
+      partner = d0 < half ? lane + half / 8 : lane - half / 8;
+      p0 = d0 < half ? d0 + half : d0 - half;
+    }
+    float own[8], other[8], t[16], a[8], b[8];  // t: cosine and sine of the chunk's pairs in turn
+    load_weights(w, d0, own);
+    if (INTER) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = own[e ^ 1];
+    } else {
+      load_weights(w, p0, other);
+    }
+    constexpr int NP = INTER ? 4 : 8;  // pairs of a chunk
+    if (on) {
+      const float4* c4 = reinterpret_cast<const float4*>(cs + (INTER ? d0 / 2 : min(d0, p0)));
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i) *reinterpret_cast<float4*>(t + 4 * i) = c4[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = INTER ? e / 2 : e;
+      const bool first = INTER ? e % 2 == 0 : d0 < half;
+      a[e] = on ? own[e] * t[2 * j] : own[e];
+      b[e] = on ? other[e] * (first ? -t[2 * j + 1] : t[2 * j + 1]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      A[i] = pack_f32x2(a[2 * i], a[2 * i + 1]);
+      B[i] = pack_f32x2(b[2 * i], b[2 * i + 1]);
+    }
+  }
+  // This lane's chunk `raw` of a row, normalised (where `norm`), rotated and multiplied by `scale`;
+  // all 32 lanes call it.
+  __device__ __forceinline__ void apply(const uint4& raw, bool norm, float eps, float scale,
+                                        uint64_t (&y)[4]) const {
+    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint64_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack_f32x2(bf16_lo(x[i]), bf16_hi(x[i]));
+    if (norm) {
+      uint64_t s2 = mul_f32x2(v[0], v[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) s2 = fma_f32x2(v[i], v[i], s2);
+      float lo, hi;
+      unpack_f32x2(s2, lo, hi);
+      float ss = lo + hi;
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      scale *= rsqrtf(fmaf(ss, 1.f / D, eps));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint64_t q;
+      if (INTER) {
+        q = pack_f32x2(bf16_hi(x[i]), bf16_lo(x[i]));
+      } else {
+        const uint32_t o = __shfl_sync(0xffffffffu, x[i], partner);
+        q = pack_f32x2(bf16_lo(o), bf16_hi(o));
+      }
+      y[i] = mul_f32x2(v[i], A[i]);
+      if (on) y[i] = fma_f32x2(q, B[i], y[i]);  // (a dim behind R must not meet 0 * infinity)
+      y[i] = mul_f32x2(y[i], pack_f32x2(scale, scale));
+    }
+  }
+};
+
+// A warp's rows [r0, r1) of one kind, kInFlight passes loaded ahead of their arithmetic.
+constexpr int kInFlight = 4;
+template <int D, typename Load, typename Body>
+__device__ __forceinline__ void walk_rows(int r0, int r1, int sub, Load load, Body body) {
+  constexpr int RPW = 256 / D;
+  for (int base = r0; base < r1; base += kInFlight * RPW) {
+    uint4 raw[kInFlight];
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      const int row = base + k * RPW + sub;
+      raw[k] = row < r1 ? load(row) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k)
+      if (base + k * RPW < r1) body(base + k * RPW + sub, raw[k]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+  float a, b;
+  unpack_f32x2(v, a, b);
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
 
-// This lane's share of a token's rotation: cosines and sines of its 8 elements (half-split pairs:
-// the sine carries the sign of its half; interleaved: entry 2 i serves the pair 2 i, 2 i + 1).
-template <int D, bool INTER>
-struct Rotation {
-  float c[8], s[8];
-  bool on;       // this chunk lies inside the rotated dims
-  int partner;   // lane that holds the other elements of this chunk's pairs
-  __device__ void make(const DevRope& r, const DevPlan& p, int tok, int lane) {
-    constexpr int L = D / 8;
-    const int chunk = lane % L, half = r.rot / 2;
-    on = chunk * 8 < r.rot;
-    partner = lane;
-    if (!INTER && on) partner = chunk * 8 < half ? lane + half / 8 : lane - half / 8;
-    if (!on) return;
-#pragma unroll
-    for (int e = 0; e < 8; e += INTER ? 2 : 1) {
-      const int d = chunk * 8 + e;
-      const int j = INTER ? d / 2 : (d < half ? d : d - half);
-      const int pos = r.positions ? __ldg(r.positions + (int64_t)r.axis[j] * p.T + tok)
-                                  : __ldg(p.tok_pos + tok);
-      const uint64_t a = (uint64_t)(int64_t)pos * turn_fraction(__ldg(r.inv_freq + j));
-      // a half turn is 2^31 units of the top word: the argument of sin(pi x)
-      sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s[e], &c[e]);
-      if (!INTER && d < half) s[e] = -s[e];
-    }
-  }
-};
-
-// Norm (where `norm`) and rotation (where `rotate`) of this lane's chunk of a row, `w` its weights
-// in shared memory (ones without a norm); all 32 lanes call it, whatever their flags.
-template <int D, bool INTER>
-__device__ __forceinline__ void norm_rotate(const uint4& raw, const float* w, bool norm, float eps,
-                                            const Rotation<D, INTER>& rt, bool rotate, int lane,
-                                            float (&y)[8]) {
-  constexpr int L = D / 8;
-  const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-  float inv = 1.f;
-  if (__any_sync(0xffffffffu, norm)) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ss = fmaf(bf16_lo(x[i]), bf16_lo(x[i]), ss);
-      ss = fmaf(bf16_hi(x[i]), bf16_hi(x[i]), ss);
-    }
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (norm) inv = rsqrtf(fmaf(ss, 1.f / D, eps));
-  }
-  auto scaled = [&](const uint32_t (&v)[4], int chunk, float (&o)[8]) {
-    const float4 w0 = *reinterpret_cast<const float4*>(w + chunk * 8);
-    const float4 w1 = *reinterpret_cast<const float4*>(w + chunk * 8 + 4);
-    const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = bf16_lo(v[i]) * inv * ww[2 * i];
-      o[2 * i + 1] = bf16_hi(v[i]) * inv * ww[2 * i + 1];
-    }
-  };
-  scaled(x, lane % L, y);
-  if (INTER) {
-    if (rotate && rt.on) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float a = y[e], b = y[e + 1];
-        y[e] = a * rt.c[e] - b * rt.s[e];
-        y[e + 1] = b * rt.c[e] + a * rt.s[e];
-      }
-    }
-  } else {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], rt.partner);
-    if (rotate && rt.on) {
-      float q[8];
-      scaled(o, rt.partner % L, q);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = y[e] * rt.c[e] + q[e] * rt.s[e];
-    }
-  }
-}
-
-// The block's copy of a weight in shared memory: ones where there is no norm.
+// The part of [first, first + rows) passes that warp part `part` of a token walks, as rows; `at`
+// counts the passes of the kinds before it.
 template <int D>
-__device__ __forceinline__ void stage_weight(const float* w, float* sm) {
-  for (int i = threadIdx.x; i < D; i += blockDim.x) sm[i] = w ? __ldg(w + i) : 1.f;
+__device__ __forceinline__ bool my_rows(int part, int per, int rows, int& at, int& r0, int& r1) {
+  constexpr int RPW = 256 / D;
+  const int passes = (rows + RPW - 1) / RPW;
+  const int b = max(0, part * per - at), e = min(passes, (part + 1) * per - at);
+  at += passes;
+  r0 = b * RPW;
+  r1 = min(rows, e * RPW);
+  return b < e;
 }
 
 // One warp: one token, some of its rows: the H query rows, then the G key rows.
 template <int D, bool INTER, bool E4M3OUT>
 __global__ void __launch_bounds__(kWarps * 32)
-qk_norm_rope_kernel(DevPlan p, DevRope r, QkRopeArgs a) {
-  constexpr int L = D / 8, RPW = 32 / L;
-  __shared__ __align__(16) float sw[2][D];
+qk_norm_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, QkRopeArgs a) {
+  __shared__ uint64_t turns[64];
+  __shared__ __align__(16) float2 cs[kWarps][64];
   pdl_wait();
   pdl_trigger();
-  stage_weight<D>(a.q_weight, sw[0]);
-  stage_weight<D>(a.k_weight, sw[1]);
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  stage_turns(r, turns);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   const int tok = (int)(w / a.splits), part = (int)(w % a.splits);
   if (tok >= p.T) return;
-  const int rows = p.H + (a.k ? p.Hkv : 0);
-  const int r0 = part * a.rows_per_warp, r1 = min(rows, r0 + a.rows_per_warp);
-  if (r0 >= r1) return;
-  const int sub = lane / L, chunk = lane % L;
-  auto src_of = [&](int row) {
-    return row < p.H ? a.q + tok * a.q_stride + (int64_t)row * D
-                     : a.k + tok * a.k_stride + (int64_t)(row - p.H) * D;
-  };
-  // the next rows are in flight while the angles are made and the present ones are rotated
-  uint4 nxt = make_uint4(0, 0, 0, 0);
-  if (r0 + sub < r1) nxt = *reinterpret_cast<const uint4*>(src_of(r0 + sub) + chunk * 8);
+  const int sub = lane / (D / 8), chunk = lane % (D / 8);
+  token_angles(r, p, tok, turns, cs[warp], lane);
+  int at = 0, r0, r1;
   Rotation<D, INTER> rt;
-  rt.make(r, p, tok, lane);
-  for (int base = r0; base < r1; base += RPW) {
-    const int row = base + sub;
-    const uint4 raw = nxt;
-    if (row + RPW < r1) nxt = *reinterpret_cast<const uint4*>(src_of(row + RPW) + chunk * 8);
-    float y[8];
-    const bool is_q = row < p.H;
-    norm_rotate<D, INTER>(raw, sw[is_q ? 0 : 1], (is_q ? a.q_weight : a.k_weight) != nullptr, a.eps,
-                          rt, true, lane, y);
-    if (row >= r1) continue;
-    if (E4M3OUT && is_q) {
-      uint32_t o[2];
+  uint64_t y[4];
+  if (my_rows<D>(part, a.passes, p.H, at, r0, r1)) {
+    rt.make(r, a.q_weight, cs[warp], lane);
+    const uint16_t* src = a.q + tok * a.q_stride + chunk * 8;
+    uint8_t* dst = static_cast<uint8_t*>(a.q_out) +
+                   (tok * a.q_out_stride + chunk * 8) * (E4M3OUT ? 1 : 2);
+    walk_rows<D>(
+        r0, r1, sub,
+        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
+        [&](int row, const uint4& raw) {
+          rt.apply(raw, a.q_weight != nullptr, a.eps, E4M3OUT ? a.q_scale_inv : 1.f, y);
+          if (row >= r1) return;
+          if (E4M3OUT) {
+            uint32_t o[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        o[h] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[h] |= f32_to_e4m3(__fdiv_rn(y[4 * h + e], a.q_scale)) << (8 * e);
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.q_out) + tok * a.q_out_stride +
-                                (int64_t)row * D + chunk * 8) = make_uint2(o[0], o[1]);
-    } else {
-      uint16_t* dst = is_q ? static_cast<uint16_t*>(a.q_out) + tok * a.q_out_stride + (int64_t)row * D
-                           : a.k_out + tok * a.k_out_stride + (int64_t)(row - p.H) * D;
-      *reinterpret_cast<uint4*>(dst + chunk * 8) =
-          make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                     pack_bf16(y[6], y[7]));
-    }
+            for (int h = 0; h < 2; ++h)
+              o[h] = f32x2_to_e4m3x2(y[2 * h]) | (f32x2_to_e4m3x2(y[2 * h + 1]) << 16);
+            *reinterpret_cast<uint2*>(dst + (int64_t)row * D) = make_uint2(o[0], o[1]);
+          } else {
+            *reinterpret_cast<uint4*>(dst + (int64_t)row * D * 2) =
+                make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
+          }
+        });
+  }
+  if (a.k && my_rows<D>(part, a.passes, p.Hkv, at, r0, r1)) {
+    rt.make(r, a.k_weight, cs[warp], lane);
+    const uint16_t* src = a.k + tok * a.k_stride + chunk * 8;
+    uint16_t* dst = a.k_out + tok * a.k_out_stride + chunk * 8;
+    walk_rows<D>(
+        r0, r1, sub,
+        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
+        [&](int row, const uint4& raw) {
+          rt.apply(raw, a.k_weight != nullptr, a.eps, 1.f, y);
+          if (row < r1)
+            *reinterpret_cast<uint4*>(dst + (int64_t)row * D) =
+                make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
+        });
   }
 }
 
-// One warp: one token, some of its 2 G rows (the G key rows, then the G value rows).
+// 16 elements (two lanes' chunks) as NVFP4: codes of this lane's 8, and the block's scale.  The
+// rule is sps_kv_append's, divisions included.
+__device__ __forceinline__ uint32_t nvfp4_codes(const float (&y)[8], uint32_t& scode) {
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  scode = f32_to_e4m3(__fdiv_rn(amax, 6.0f));
+  const float sv = e4m3_to_f32(scode);
+  uint32_t packed = 0;
+  if (sv != 0.f) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+      packed |= f32x2_to_e2m1x2(__fdiv_rn(y[e], sv), __fdiv_rn(y[e + 1], sv)) << (4 * e);
+  }
+  return packed;
+}
+
+// One warp: one token, some of its 2 G rows: the G key rows, then the G value rows.
 template <int D, bool INTER, bool NVFP4>
 __global__ void __launch_bounds__(kWarps * 32)
-kv_append_rope_kernel(DevPlan p, DevRope r, KvRopeArgs a) {
-  constexpr int L = D / 8, RPW = 32 / L;
-  __shared__ __align__(16) float sw[D];
+kv_append_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, KvRopeArgs a) {
+  __shared__ uint64_t turns[64];
+  __shared__ __align__(16) float2 cs[kWarps][64];
   pdl_wait();
   pdl_trigger();
-  stage_weight<D>(a.k_weight, sw);
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  stage_turns(r, turns);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
   const int tok = (int)(w / a.splits), part = (int)(w % a.splits);
   if (tok >= p.T) return;
-  const int G = p.Hkv, rows = 2 * G;
-  const int r0 = part * a.rows_per_warp, r1 = min(rows, r0 + a.rows_per_warp);
-  if (r0 >= r1) return;
+  const int G = p.Hkv, sub = lane / (D / 8), chunk = lane % (D / 8);
   const int t = __ldg(p.tok_pos + tok), req = __ldg(p.tok_req + tok);
   const int phys = __ldg(a.page_table + (int64_t)req * p.max_pages + (t >> 7));
-  const int sub = lane / L, chunk = lane % L;
-  auto load = [&](int row) {
-    const uint16_t* s = row < G ? a.k + tok * a.k_stride + (int64_t)row * D
-                                : a.v + tok * a.v_stride + (int64_t)(row - G) * D;
-    return *reinterpret_cast<const uint4*>(s + chunk * 8);
-  };
-  uint4 nxt = make_uint4(0, 0, 0, 0);
-  if (r0 + sub < r1) nxt = load(r0 + sub);
+  int at = 0, r0, r1;
+  const bool keys = my_rows<D>(part, a.passes, G, at, r0, r1);
   Rotation<D, INTER> rt;
-  if (r0 < G) rt.make(r, p, tok, lane);
-  else rt.on = false, rt.partner = lane;
+  if (keys) {
+    token_angles(r, p, tok, turns, cs[warp], lane);
+    rt.make(r, a.k_weight, cs[warp], lane);
+  }
   if (phys < 0 || phys >= p.num_phys) {
     if (lane == 0) set_status(p.status, DEV_BAD_PAGE);
     return;
   }
-  for (int base = r0; base < r1; base += RPW) {
-    const int row = base + sub;
-    const bool is_k = row < G;
-    const uint4 raw = nxt;
-    if (row + RPW < r1) nxt = load(row + RPW);
-    float y[8];
-    if (__any_sync(0xffffffffu, is_k))
-      norm_rotate<D, INTER>(raw, sw, a.k_weight != nullptr, a.eps, rt, is_k, lane, y);
-    if (!is_k) {  // a value row as it is
-      const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+  const int64_t slot0 = (int64_t)phys * G * 128 + (t & 127);  // slot of head g: + 128 g
+  auto quantised = [&](int row, const float (&y)[8], uint8_t* codes, uint8_t* scales, bool live) {
+    uint32_t scode;
+    const uint32_t packed = nvfp4_codes(y, scode);
+    if (!live) return;
+    const int64_t slot = slot0 + 128 * row;
+    *reinterpret_cast<uint32_t*>(codes + slot * (D / 2) + chunk * 4) = packed;
+    if (chunk % 2 == 0) scales[slot * (D / 16) + chunk / 2] = (uint8_t)scode;
+  };
+  if (keys) {
+    const uint16_t* src = a.k + tok * a.k_stride + chunk * 8;
+    walk_rows<D>(
+        r0, r1, sub,
+        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
+        [&](int row, const uint4& raw) {
+          uint64_t y[4];
+          rt.apply(raw, a.k_weight != nullptr, a.eps, 1.f, y);
+          if (NVFP4) {
+            float f[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[2 * i] = bf16_lo(x[i]);
-        y[2 * i + 1] = bf16_hi(x[i]);
-      }
-    }
-    const int64_t slot = ((int64_t)phys * G + (is_k ? row : row - G)) * 128 + (t & 127);
-    if (!NVFP4) {
-      if (row < r1)
-        *reinterpret_cast<uint4*>((is_k ? a.kc : a.vc) + (slot * D + chunk * 8) * 2) =
-            is_k ? make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                              pack_bf16(y[6], y[7]))
-                 : raw;
-      continue;
-    }
-    float amax = 0.f;
+            for (int i = 0; i < 4; ++i) unpack_f32x2(y[i], f[2 * i], f[2 * i + 1]);
+            quantised(row, f, a.kc, a.ks, row < r1);
+          } else if (row < r1) {
+            *reinterpret_cast<uint4*>(a.kc + ((slot0 + 128 * row) * D + chunk * 8) * 2) =
+                make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
+          }
+        });
+  }
+  if (my_rows<D>(part, a.passes, G, at, r0, r1)) {  // value rows as they are
+    const uint16_t* src = a.v + tok * a.v_stride + chunk * 8;
+    walk_rows<D>(
+        r0, r1, sub,
+        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
+        [&](int row, const uint4& raw) {
+          if (NVFP4) {
+            const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+            float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // 16 elements: two lanes
-    if (row >= r1) continue;
-    const uint32_t scode = f32_to_e4m3(__fdiv_rn(amax, 6.0f));
-    const float sv = e4m3_to_f32(scode);
-    uint32_t packed = 0;
-    if (sv != 0.f) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2)
-        packed |= f32x2_to_e2m1x2(__fdiv_rn(y[e], sv), __fdiv_rn(y[e + 1], sv)) << (4 * e);
-    }
-    *reinterpret_cast<uint32_t*>((is_k ? a.kc : a.vc) + slot * (D / 2) + chunk * 4) = packed;
-    if (chunk % 2 == 0) (is_k ? a.ks : a.vs)[slot * (D / 16) + chunk / 2] = (uint8_t)scode;
+            for (int i = 0; i < 4; ++i) {
+              f[2 * i] = bf16_lo(x[i]);
+              f[2 * i + 1] = bf16_hi(x[i]);
+            }
+            quantised(row, f, a.vc, a.vs, row < r1);
+          } else if (row < r1) {
+            *reinterpret_cast<uint4*>(a.vc + ((slot0 + 128 * row) * D + chunk * 8) * 2) = raw;
+          }
+        });
   }
 }
 
-// Rows a warp walks: all of a token's where that gives every SM 32 warps, else fewer, so that a
+// Passes a warp walks: all of a token's where that gives every SM 32 warps, else fewer, so that a
 // batch of few tokens still spreads over the GPU (a decode step of 64 tokens: a warp per pass).
-int split_rows(int64_t tokens, int rows, int rpw, int* splits) {
-  const int passes = (rows + rpw - 1) / rpw;
-  const int64_t want = 32LL * num_sms();
-  const int64_t s = std::min<int64_t>(passes, std::max<int64_t>(1, (want + tokens - 1) / tokens));
-  const int per = (int)((passes + s - 1) / s);
-  *splits = (passes + per - 1) / per;
-  return per * rpw;
-}
-
 template <typename K, typename A>
-cudaError_t launch_rows(K kern, const DevPlan& p, const DevRope& r, A a, int rows, int rpw,
+cudaError_t launch_rows(K kern, const DevPlan& p, const DevRope& r, A a, int passes,
                         cudaStream_t st) {
-  a.rows_per_warp = split_rows(p.T, rows, rpw, &a.splits);
+  const int64_t want = 32LL * num_sms();
+  const int64_t s = std::min<int64_t>(passes, std::max<int64_t>(1, (want + p.T - 1) / p.T));
+  a.passes = (int)((passes + s - 1) / s);
+  a.splits = (passes + a.passes - 1) / a.passes;
   const int64_t blocks = ((int64_t)p.T * a.splits + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaError_t e = launch_pdl(kern, dim3((unsigned)blocks), dim3(kWarps * 32), 0, st, p, r, a);
@@ -299,9 +365,10 @@ cudaError_t launch_rows(K kern, const DevPlan& p, const DevRope& r, A a, int row
 
 cudaError_t launch_qk_norm_rope(const DevPlan& p, const DevRope& r, const QkRopeArgs& a,
                                 bool interleaved, bool e4m3, cudaStream_t st) {
-  const int rows = p.H + (a.k ? p.Hkv : 0);
+  const int rpw = 256 / p.D;
+  const int passes = (p.H + rpw - 1) / rpw + (a.k ? (p.Hkv + rpw - 1) / rpw : 0);
 #define SPS_QK(DD, II, EE) \
-  return launch_rows(qk_norm_rope_kernel<DD, II, EE>, p, r, a, rows, 256 / DD, st)
+  return launch_rows(qk_norm_rope_kernel<DD, II, EE>, p, r, a, passes, st)
   if (p.D == 128) {
     if (interleaved) { if (e4m3) SPS_QK(128, true, true); else SPS_QK(128, true, false); }
     else { if (e4m3) SPS_QK(128, false, true); else SPS_QK(128, false, false); }
@@ -314,9 +381,9 @@ cudaError_t launch_qk_norm_rope(const DevPlan& p, const DevRope& r, const QkRope
 
 cudaError_t launch_kv_append_rope(const DevPlan& p, const DevRope& r, const KvRopeArgs& a,
                                   bool interleaved, bool nvfp4, cudaStream_t st) {
-  const int rows = 2 * p.Hkv;
+  const int rpw = 256 / p.D, passes = 2 * ((p.Hkv + rpw - 1) / rpw);
 #define SPS_KV(DD, II, NN) \
-  return launch_rows(kv_append_rope_kernel<DD, II, NN>, p, r, a, rows, 256 / DD, st)
+  return launch_rows(kv_append_rope_kernel<DD, II, NN>, p, r, a, passes, st)
   if (p.D == 128) {
     if (interleaved) { if (nvfp4) SPS_KV(128, true, true); else SPS_KV(128, true, false); }
     else { if (nvfp4) SPS_KV(128, false, true); else SPS_KV(128, false, false); }

@@ -125,8 +125,8 @@ struct QkRopeArgs {
   void* q_out;
   uint16_t* k_out;
   int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
-  float eps, q_scale;
-  int32_t rows_per_warp, splits;  // set by the launcher
+  float eps, q_scale_inv;
+  int32_t passes, splits;  // of a warp, of a token; set by the launcher
 };
 struct KvRopeArgs {
   const uint16_t *k, *v;
@@ -135,7 +135,7 @@ struct KvRopeArgs {
   uint8_t *kc, *vc, *ks, *vs;
   int64_t k_stride, v_stride;
   float eps;
-  int32_t rows_per_warp, splits;
+  int32_t passes, splits;
 };
 
 // Launch of `kern` that may overlap the previous kernel in the stream (programmatic stream
