@@ -346,12 +346,12 @@ kv_append_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, KvRopeArgs a
   }
 }
 
-// Passes a warp walks: all of a token's where that gives every SM 32 warps, else fewer, so that a
+// Passes a warp walks: all of a token's where that gives every SM 24 warps, else fewer, so that a
 // batch of few tokens still spreads over the GPU (a decode step of 64 tokens: a warp per pass).
 template <typename K, typename A>
 cudaError_t launch_rows(K kern, const DevPlan& p, const DevRope& r, A a, int passes,
                         cudaStream_t st) {
-  const int64_t want = 32LL * num_sms();
+  const int64_t want = 24LL * num_sms();
   const int64_t s = std::min<int64_t>(passes, std::max<int64_t>(1, (want + p.T - 1) / p.T));
   a.passes = (int)((passes + s - 1) / s);
   a.splits = (passes + a.passes - 1) / a.passes;
