@@ -162,6 +162,12 @@ __device__ __forceinline__ uint32_t pack_p(float a, float b) {
   return r;
 }
 
+// Scratch slot of piece i of a cut tile: a block's first piece goes to slot 2 block when it begins
+// inside its tile, its last piece to slot 2 block + 1 when it begins its tile.
+__device__ __forceinline__ int64_t piece_slot(const AttMerge& mg, int i) {
+  return i == 0 ? 2 * mg.cta0 + 1 : 2 * (mg.cta0 + i);
+}
+
 struct AttArgs {
   const uint8_t *q, *kc, *vc, *ks, *vs;  // NVFP4 plans (and Q's codes)
   int64_t q_stride;
@@ -224,8 +230,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();  // from here on: what earlier kernels wrote
-  pdl_trigger();
+  // from here on: what earlier kernels wrote.  (No early launch of the next kernel: waiting blocks
+  // of the merge kernel measured 2 us slower on small batches, 13 us on an 8192-token prompt.)
+  pdl_wait();
   const uint32_t tmem = sm.tmem_base;  // S0 S1 at columns 0, 128; O0 O1 at 256, 384
   volatile int* abort_flag = &sm.abort_flag;
   AttCursor cur = p.att_starts[blockIdx.x];
@@ -840,89 +847,174 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
 // Merge of the tiles cut over several blocks: out = sum_i w_i O_i / sum_i w_i with
 // w_i = exp(lse_i - max lse); a piece in which the row sees no key (lse = -inf) is never read.
-// WPR warps share a row's pieces (8 where tiles have few rows: a single token's tile may be cut
-// over every SM, and one warp would walk 76 pieces at a memory latency each).
-template <int D, int WPR>
+struct MergeRow {
+  bool live;
+  int64_t flat;
+  int head;
+};
+__device__ __forceinline__ MergeRow merge_row(const DevPlan& p, const RowPack& rp,
+                                              const AttMerge& mg, int lr) {
+  const int row = lr % 128, ti = row / rp.HB, hg = (mg.vg % rp.blocks) * 128 + row % rp.HB;
+  const int tok = mg.tile * 2 * rp.TB + (lr / 128) * rp.TB + ti;
+  return {lr < p.att_slot_rows && ti < rp.TB && tok < mg.q_len && hg < p.Hg,
+          (int64_t)mg.flat0 + tok, (mg.vg / rp.blocks) * p.Hg + hg};
+}
+template <int D>
+__device__ __forceinline__ void merge_store(const DevPlan& p, const AttArgs& a, const MergeRow& r,
+                                            int lane, const float (&acc)[D / 32], float inv) {
+  uint16_t* out = a.out + r.flat * a.out_stride + (int64_t)r.head * D + lane * (D / 32);
+  if (D == 128)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_p<false>(acc[0] * inv, acc[1] * inv),
+                   pack_p<false>(acc[D / 32 - 2] * inv, acc[D / 32 - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_p<false>(acc[0] * inv, acc[1] * inv);
+}
+template <int D>
+__device__ __forceinline__ void merge_add(float (&acc)[D / 32], float wt, const float* o) {
+  if (D == 128) {
+    const float4 x = *reinterpret_cast<const float4*>(o);
+    acc[0] += wt * x.x;
+    acc[1] += wt * x.y;
+    acc[D / 32 - 2] += wt * x.z;
+    acc[D / 32 - 1] += wt * x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(o);
+    acc[0] += wt * x.x;
+    acc[1] += wt * x.y;
+  }
+}
+
+// Tiles of many rows (few pieces each): a warp takes 8 rows, a lane the weight of one of four
+// pieces of one of them, so that a warp has up to 32 rows of partial results on the way.
+constexpr int kMergeRows = 8;
+template <int D>
 __global__ void __launch_bounds__(256)
-attention_merge_kernel(DevPlan p, AttArgs a) {
-  constexpr int RB = 8 / WPR, E = D / 32;  // rows per block, elements per lane
-  __shared__ float wts[RB][kMaxCtas];
+attention_merge_rows_kernel(DevPlan p, AttArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const AttMerge mg = p.att_merges[blockIdx.x];
+  if (mg.req < 0) return;
+  const RowPack rp(p.Hg);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int lr0 = (blockIdx.y * 8 + warp) * kMergeRows;
+  const int np = mg.cta1 - mg.cta0 + 1;
+  const int k = lane % kMergeRows, ii = lane / kMergeRows;  // this lane's row and piece (mod 4)
+  const MergeRow mine = merge_row(p, rp, mg, lr0 + k);
+  const uint32_t live = __ballot_sync(0xffffffffu, mine.live);
+  if (!live) return;
+  auto lse_of = [&](int i) {
+    return mine.live && i < np
+               ? a.part_lse[piece_slot(mg, i) * p.att_slot_rows + lr0 + k]
+               : -INFINITY;
+  };
+  float mx = -INFINITY;
+  for (int c = 0; c < np; c += 4) mx = fmaxf(mx, lse_of(c + ii));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+  float sum = 0.f, acc[kMergeRows][D / 32] = {};
+  for (int c = 0; c < np; c += 4) {
+    const float l = lse_of(c + ii), wt = l == -INFINITY ? 0.f : __expf(l - mx);
+    sum += wt;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c + j >= np) break;
+      const float* o = a.part + (piece_slot(mg, c + j) * p.att_slot_rows + lr0) * D + lane * (D / 32);
+#pragma unroll
+      for (int r = 0; r < kMergeRows; ++r) {
+        const float w = __shfl_sync(0xffffffffu, wt, j * kMergeRows + r);
+        if (w != 0.f) merge_add<D>(acc[r], w, o + r * D);
+      }
+    }
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+  if (ii == 0 && mine.live && a.out_lse)
+    a.out_lse[mine.flat * p.H + mine.head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+#pragma unroll
+  for (int r = 0; r < kMergeRows; ++r) {
+    const float s = __shfl_sync(0xffffffffu, sum, r);
+    if (live >> r & 1)
+      merge_store<D>(p, a, merge_row(p, rp, mg, lr0 + r), lane, acc[r],
+                     s > 0.f ? 1.f / s : 0.f);
+  }
+}
+
+// Tiles of few rows (a single token's may be cut over every SM): a block per row, its warps share
+// the pieces; one warp would walk 76 of them at a memory latency each.
+template <int D>
+__global__ void __launch_bounds__(256)
+attention_merge_pieces_kernel(DevPlan p, AttArgs a) {
+  constexpr int E = D / 32;  // elements per lane
+  __shared__ float wts[kMaxCtas];
   __shared__ float sums[8][32 * E];
   pdl_wait();
   pdl_trigger();
   const AttMerge mg = p.att_merges[blockIdx.x];
   if (mg.req < 0) return;
   const RowPack rp(p.Hg);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, rb = warp / WPR, part = warp % WPR;
-  const int lr = blockIdx.y * RB + rb, row = lr % 128;
-  const int ti = row / rp.HB, hg = (mg.vg % rp.blocks) * 128 + row % rp.HB;
-  const int tok = mg.tile * 2 * rp.TB + (lr / 128) * rp.TB + ti;
-  const ReqInfo* ri = p.reqs + mg.req;
-  if (lr >= p.att_slot_rows || ti >= rp.TB || tok >= __ldg(&ri->q_len) || hg >= p.Hg)
-    return;  // WPR 8: the whole block
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lr = blockIdx.y;
+  const MergeRow row = merge_row(p, rp, mg, lr);
+  if (!row.live) return;  // the whole block
   const int np = mg.cta1 - mg.cta0 + 1;
-  auto srow = [&](int i) {
-    return (int64_t)(i == 0 ? 2 * mg.cta0 + 1 : 2 * (mg.cta0 + i)) * p.att_slot_rows + lr;
+  // this warp's first pieces are on the way while the weights are found
+  constexpr int kAhead = 8;
+  float x[kAhead][E];
+  auto fetch = [&](int i, float (&o)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    if (i < np) {
+      const float* src = a.part + (piece_slot(mg, i) * p.att_slot_rows + lr) * D + lane * E;
+      if (E == 4) *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(src);
+    }
   };
-  // every warp of a row finds its weights (the same values); the first one keeps them
+  // every warp finds the weights (the same values); the first one keeps them
   float mx = -INFINITY, l[kMaxCtas / 32];
 #pragma unroll
   for (int k = 0; k < kMaxCtas / 32; ++k) {
     const int i = lane + 32 * k;
-    l[k] = i < np ? a.part_lse[srow(i)] : -INFINITY;
-    mx = fmaxf(mx, l[k]);
+    l[k] = i < np ? a.part_lse[piece_slot(mg, i) * p.att_slot_rows + lr] : -INFINITY;
   }
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) fetch(warp + 8 * k, x[k]);
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / 32; ++k) mx = fmaxf(mx, l[k]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float sum = 0.f;
 #pragma unroll
   for (int k = 0; k < kMaxCtas / 32; ++k) {
     const float wt = l[k] == -INFINITY ? 0.f : __expf(l[k] - mx);
-    if (part == 0 && lane + 32 * k < np) wts[rb][lane + 32 * k] = wt;
+    if (warp == 0 && lane + 32 * k < np) wts[lane + 32 * k] = wt;
     sum += wt;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (WPR > 1) __syncthreads();
-  else __syncwarp();
+  __syncthreads();
   float acc[E] = {};
-#pragma unroll 4
-  for (int i = part; i < np; i += WPR) {
-    const float wt = wts[rb][i];
-    if (wt == 0.f) continue;
-    const float* o = a.part + srow(i) * D + lane * E;
-    if (E == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(o);
-      acc[0] += wt * x.x;
-      acc[1] += wt * x.y;
-      acc[E - 2] += wt * x.z;
-      acc[E - 1] += wt * x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(o);
-      acc[0] += wt * x.x;
-      acc[1] += wt * x.y;
+  for (int i0 = warp; i0 < np; i0 += 8 * kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + 8 * k;
+      const float wt = i < np ? wts[i] : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (wt != 0.f) acc[e] += wt * x[k][e];
     }
-  }
-  if (WPR > 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[e];
-    __syncthreads();
-    if (part) return;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      for (int k = 1; k < WPR; ++k) acc[e] += sums[warp + k][lane * E + e];
+    for (int k = 0; k < kAhead; ++k) fetch(i0 + 8 * (kAhead + k), x[k]);
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const int64_t flat = __ldg(&ri->tok0) + tok;
-  const int head = (mg.vg / rp.blocks) * p.Hg + hg;
-  uint16_t* out = a.out + flat * a.out_stride + (int64_t)head * D + lane * E;
-  if (E == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_p<false>(acc[0] * inv, acc[1] * inv),
-                                                pack_p<false>(acc[E - 2] * inv, acc[E - 1] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(out) = pack_p<false>(acc[0] * inv, acc[1] * inv);
+#pragma unroll
+  for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    for (int k = 1; k < 8; ++k) acc[e] += sums[k][lane * E + e];
+  merge_store<D>(p, a, row, lane, acc, sum > 0.f ? 1.f / sum : 0.f);
   if (lane == 0 && a.out_lse)
-    a.out_lse[flat * p.H + head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+    a.out_lse[row.flat * p.H + row.head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
 }
 
 template <int D, bool QUANT, bool SINGLE>
@@ -948,12 +1040,25 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(p.att_ctas), dim3(QUANT ? 512 : 384), smem, st, tmQ, tmK, tmV, p, a);
   if (e != cudaSuccess) return e;
-  if (p.att_slot_rows <= 32)
-    e = launch_pdl(attention_merge_kernel<D, 8>, dim3(p.att_ctas, p.att_slot_rows), dim3(256), 0, st,
-                   p, a);
-  else
-    e = launch_pdl(attention_merge_kernel<D, 1>, dim3(p.att_ctas, (p.att_slot_rows + 7) / 8),
-                   dim3(256), 0, st, p, a);
+  // att_merge_cap bounds the cut tiles of any plan of these q_lens.  An eager call of a plan without
+  // a cut tile needs no merge; a captured one keeps it, since it may be replayed over another plan's
+  // metadata (same q_lens, other contexts).
+  int merges = p.att_merge_cap;
+  if (p.att_num_merges == 0 && merges > 0) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(st, &cap);
+    if (e != cudaSuccess) return e;
+    if (cap == cudaStreamCaptureStatusNone) merges = 0;
+  }
+  if (merges > 0) {
+    if (p.att_slot_rows <= 32)
+      e = launch_pdl(attention_merge_pieces_kernel<D>, dim3(merges, p.att_slot_rows), dim3(256), 0,
+                     st, p, a);
+    else
+      e = launch_pdl(attention_merge_rows_kernel<D>,
+                     dim3(merges, (p.att_slot_rows + 8 * kMergeRows - 1) / (8 * kMergeRows)),
+                     dim3(256), 0, st, p, a);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -9,7 +9,6 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -144,7 +143,7 @@ struct sps_plan {
   // full attention (attention.cu): where each block begins, the tiles cut over blocks
   std::vector<AttCursor> att_starts;
   std::vector<AttMerge> att_merges;
-  int32_t att_ctas = 0, att_slot_rows = 0;
+  int32_t att_ctas = 0, att_slot_rows = 0, att_num_merges = 0, att_merge_cap = 0;
   int64_t off_att_starts = 0, off_att_merges = 0;
   int64_t upload_bytes = 0;  // [0, upload_bytes) of the workspace comes from `blob`
   std::vector<uint8_t> blob;
@@ -248,59 +247,105 @@ void build_indexer_tasks(sps_plan* pl) {
 
 // Work split of the full attention: the (tile, page) pairs of the batch in order (request, head
 // block, tile, page), a tile being two row tiles of 128 / HB tokens x HB heads of a KV head's
-// group, cut into runs of equal cost, one per SM.  A tile costs its pages plus kAttTileCost for its
-// fill, drain and epilogue; a cut near a tile's border moves onto it.
-constexpr int kAttTileCost = 2, kAttSnap = 1;
-void build_attention_runs(sps_plan* pl) {
-  const sps_problem& p = pl->pb;
-  const int hg = p.num_q_heads / p.num_kv_heads, HB = std::min(hg, 128), TB = 128 / HB;
-  const int nv = p.num_kv_heads * ((hg + HB - 1) / HB), tt = 2 * TB;
-  static const int tile_cost = getenv("ATT_OV") ? atoi(getenv("ATT_OV")) : kAttTileCost;
-  static const int snap_ = getenv("ATT_SNAP") ? atoi(getenv("ATT_SNAP")) : kAttSnap;
-  auto pages_of = [&](const ReqInfo& ri, int tile) {
-    return (ri.ctx + std::min((tile + 1) * tt, ri.q_len) - 1) / kPage + 1;
-  };
-  int64_t total = 0;
-  int max_q = 0;
-  for (const ReqInfo& ri : pl->reqs) {
-    int64_t cost = 0;
-    for (int t = 0; t * tt < ri.q_len; ++t) cost += pages_of(ri, t) + tile_cost;
-    total += cost * nv;
-    max_q = std::max(max_q, ri.q_len);
-  }
-  pl->att_ctas = std::min(std::max(1, num_sms()), 256);
-  pl->att_slot_rows = max_q > TB ? 256 : max_q * HB;
-  const AttCursor end{p.batch, 0, 0, 0, 0, 0, 0, 0};
-  pl->att_starts.assign(pl->att_ctas + 1, end);
-  pl->att_merges.assign(pl->att_ctas, AttMerge{-1, 0, 0, 0, 0, 0});
-  const int64_t cuts = std::min<int64_t>(pl->att_ctas, total);
-  int64_t at = 0, cut = 0;   // cost before the present tile; cuts placed
-  int run = 0, merges = 0;   // runs begun
-  bool pending = false;      // a cut moved onto the next tile's start
-  for (int b = 0; b < p.batch; ++b) {
+// group, cut into runs of about equal cost, one per SM.
+//
+// Costs are in pages (about 1.5 us): a tile's pages plus kAttTileCost for its fill, drain and
+// epilogue.  A cut inside a tile adds a piece, whose partial rows are written and merged by a
+// second kernel; so a cut at most `snap` pages from a tile's border moves onto the nearer one, and
+// the split is made for several `snap`, the one with the smallest estimate kept.  (Measured on
+// H 32 / H_kv 8, D 128: 32 single tokens after 1K cost 42 us with snap 5 and 49 with 1, a
+// 512-token prompt 15 and 20; one token after 8K, where every cut counts, 17 and 14.)
+constexpr int kAttTileCost = 2;
+
+struct AttSplit {
+  std::vector<AttCursor> starts;
+  std::vector<AttMerge> merges;
+  double estimate = 0;
+};
+
+AttSplit split_attention(const sps_plan* pl, const std::vector<int32_t>& tile_pages, int64_t total,
+                         int nv, int tt, int ctas, int snap, bool few_rows) {
+  AttSplit out;
+  const int64_t cuts = std::min<int64_t>(ctas, total);
+  int64_t at = 0, cut = 0;  // cost before the present tile; cuts placed
+  int64_t run_cost = 0, longest = 0;
+  bool pending = false;  // a cut moved onto the next tile's start
+  size_t k = 0;
+  for (int b = 0; b < pl->pb.batch; ++b) {
     const ReqInfo& ri = pl->reqs[b];
+    const int tiles = (ri.q_len + tt - 1) / tt;
     for (int v = 0; v < nv; ++v)
-      for (int t = 0; t * tt < ri.q_len; ++t) {
-        const int n = pages_of(ri, t);
-        int first = -1, last_page = -1;  // first run that begins inside the tile, last cut's page
+      for (int t = 0; t < tiles; ++t) {
+        const int n = tile_pages[k + t];
+        int first = -1, last_page = 0;  // first run that begins inside the tile, last piece's page
+        bool begun = false;             // a run begins at the tile's start
         auto begin = [&](int page) {
-          if (page <= last_page) return;
-          if (page > 0 && first < 0) first = run;
-          pl->att_starts[run++] = AttCursor{b, v, t, page, ri.q_len, ri.ctx, ri.tok0, 0};
+          if (page == 0 ? begun : page <= last_page) return;
+          if (page == 0) {
+            begun = true;
+          } else {
+            if (first < 0) first = (int)out.starts.size();
+            run_cost += page - last_page + kAttTileCost;
+          }
+          longest = std::max(longest, run_cost);
+          run_cost = 0;
+          out.starts.push_back(AttCursor{b, v, t, page, ri.q_len, ri.ctx, ri.tok0, 0});
           last_page = page;
         };
         if (pending) begin(0);
         pending = false;
-        for (; cut < cuts && cut * total / cuts < at + n + tile_cost; ++cut) {
-          const int page = (int)(cut * total / cuts - at) - tile_cost;
-          if (page <= snap_) begin(0);
-          else if (n - page <= snap_) pending = true;
+        for (; cut < cuts && cut * total / cuts < at + n + kAttTileCost; ++cut) {
+          const int page = std::max(0, (int)(cut * total / cuts - at) - kAttTileCost);
+          const bool front = page <= n - page;
+          if (page == 0 || (front && page <= snap)) begin(0);
+          else if (!front && n - page <= snap) pending = true;
           else begin(page);
         }
-        if (first > 0) pl->att_merges[merges++] = AttMerge{b, v, t, first - 1, run - 1, 0};
-        at += n + tile_cost;
+        run_cost += n - last_page + kAttTileCost;
+        if (first > 0)
+          out.merges.push_back(AttMerge{b, v, t, first - 1, (int)out.starts.size() - 1, ri.q_len,
+                                        ri.tok0, 0});
+        at += n + kAttTileCost;
       }
+    k += tiles;
   }
+  longest = std::max(longest, run_cost);
+  int64_t pieces = 0;
+  for (const AttMerge& m : out.merges) pieces += m.cta1 - m.cta0 + 1;
+  out.estimate = (double)longest;
+  if (pieces) out.estimate += few_rows ? 6 + 0.01 * pieces : 4 + 0.045 * pieces;
+  return out;
+}
+
+void build_attention_runs(sps_plan* pl) {
+  const sps_problem& p = pl->pb;
+  const int hg = p.num_q_heads / p.num_kv_heads, HB = std::min(hg, 128), TB = 128 / HB;
+  const int nv = p.num_kv_heads * ((hg + HB - 1) / HB), tt = 2 * TB;
+  std::vector<int32_t> tile_pages;  // of one head block, request by request
+  int64_t total = 0;
+  int max_q = 0;
+  for (const ReqInfo& ri : pl->reqs) {
+    for (int t = 0; t * tt < ri.q_len; ++t) {
+      tile_pages.push_back((ri.ctx + std::min((t + 1) * tt, ri.q_len) - 1) / kPage + 1);
+      total += (int64_t)(tile_pages.back() + kAttTileCost) * nv;
+    }
+    max_q = std::max(max_q, ri.q_len);
+  }
+  const int ctas = std::min(std::max(1, num_sms()), 256);
+  pl->att_ctas = ctas;
+  pl->att_slot_rows = max_q > TB ? 256 : max_q * HB;
+  pl->att_merge_cap = (int32_t)std::min<int64_t>(ctas - 1, (int64_t)tile_pages.size() * nv);
+  AttSplit best;
+  for (int snap : {1, 2, 4, 8, 1 << 20}) {
+    AttSplit x = split_attention(pl, tile_pages, total, nv, tt, ctas, snap,
+                                 pl->att_slot_rows <= 32);
+    if (best.starts.empty() || x.estimate < best.estimate) best = std::move(x);
+  }
+  pl->att_num_merges = (int32_t)best.merges.size();
+  best.starts.resize(ctas + 1, AttCursor{p.batch, 0, 0, 0, 0, 0, 0, 0});
+  best.merges.resize(ctas, AttMerge{-1, 0, 0, 0, 0, 0, 0, 0});
+  pl->att_starts.swap(best.starts);
+  pl->att_merges.swap(best.merges);
 }
 
 }  // namespace
@@ -512,6 +557,8 @@ DevPlan make_dev_plan(const sps_plan* pl, void* ws) {
   d.att_merges = reinterpret_cast<const AttMerge*>(base + pl->off_att_merges);
   d.att_ctas = pl->att_ctas;
   d.att_slot_rows = pl->att_slot_rows;
+  d.att_num_merges = pl->att_num_merges;
+  d.att_merge_cap = pl->att_merge_cap;
   return d;
 }
 

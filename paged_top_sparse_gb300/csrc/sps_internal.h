@@ -98,9 +98,10 @@ struct DevPlan {
   const AttCursor* att_starts;
   const AttMerge* att_merges;
   int32_t att_ctas, att_slot_rows;
+  int32_t att_num_merges, att_merge_cap;  // cut tiles of this plan, and of any with its q_lens
 };
 
-// A dense attention work position: page `page` of query tile `tile` of head block `vg` (KV head
+// A full-attention work position: page `page` of query tile `tile` of head block `vg` (KV head
 // g = vg / head blocks per KV head) of request `req`; (batch, 0, 0, 0) is the end.
 struct AttCursor {
   int32_t req, vg, tile, page;
@@ -109,7 +110,8 @@ struct AttCursor {
 // A query tile whose pages were cut over several blocks: blocks cta0 .. cta1 hold its pieces
 // (req < 0: unused entry).
 struct AttMerge {
-  int32_t req, vg, tile, cta0, cta1, pad;
+  int32_t req, vg, tile, cta0, cta1;
+  int32_t q_len, flat0, pad;
 };
 
 // The rotation, as the kernels see it (sps_rope; rot 0: none).
