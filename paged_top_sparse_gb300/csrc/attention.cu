@@ -34,16 +34,12 @@
 
 #include <cstring>
 
+#include "attention.cuh"
 #include "nvfp4.cuh"
-#include "ptx.cuh"
-#include "sps_internal.h"
 
 namespace sps {
+using namespace att;
 namespace {
-
-constexpr float kRescale = 8.f;   // log2 of the growth of the maximum that rescales O
-constexpr float kF16Bias = 7.f;   // log2 of the factor on FP16 p
-constexpr int kMaxCtas = 256;
 
 // SINGLE: every work tile of the batch has one row tile (decode steps); the second Q tile's room
 // goes to the rings.
@@ -75,69 +71,6 @@ struct AttSmem {
   int abort_flag;
 };
 
-// Row packing of a head group.
-struct RowPack {
-  int HB, TB, blocks;  // heads and tokens per row tile, row-tile head blocks per KV head
-  __device__ __host__ explicit RowPack(int hg) {
-    HB = hg < 128 ? hg : 128;
-    TB = 128 / HB;
-    blocks = (hg + HB - 1) / HB;
-  }
-};
-
-// A run of pages [page0, page1) of one work tile.
-struct Piece {
-  int req, vg, tok0, ntok;  // tokens tok0 .. of the request (relative), ntok of them
-  int page0, page1, pages;  // `pages` of the whole tile
-  int q_len, ctx, flat0;    // the request's
-  int nt;                   // row tiles with rows
-};
-
-// The piece at cursor c of a block whose run ends at e; advances c.  False at the end.  The cursor
-// carries its request's numbers, so that a run's first piece needs no further read.
-__device__ __forceinline__ bool next_piece(const DevPlan& p, const RowPack& rp, AttCursor& c,
-                                           const AttCursor& e, Piece& pc) {
-  const int tt = 2 * rp.TB, nv = p.Hkv * rp.blocks;
-  for (;;) {
-    if (c.req >= p.batch) return false;
-    if (c.req == e.req && c.vg == e.vg && c.tile == e.tile && c.page == e.page) return false;
-    if (c.q_len > 0) {
-      const bool last = c.req == e.req && c.vg == e.vg && c.tile == e.tile;
-      pc.req = c.req;
-      pc.vg = c.vg;
-      pc.q_len = c.q_len;
-      pc.ctx = c.ctx;
-      pc.flat0 = c.flat0;
-      pc.tok0 = c.tile * tt;
-      pc.ntok = min(tt, c.q_len - pc.tok0);
-      pc.pages = ((pc.ctx + pc.tok0 + pc.ntok - 1) >> 7) + 1;
-      pc.page0 = c.page;
-      pc.page1 = last ? min(e.page, pc.pages) : pc.pages;
-      pc.nt = pc.ntok > rp.TB ? 2 : 1;
-      if (last) {
-        c = e;
-        return pc.page0 < pc.page1;
-      }
-      c.page = 0;
-      if ((c.tile + 1) * tt < c.q_len) {
-        ++c.tile;
-        return true;
-      }
-      c.tile = 0;
-      if (++c.vg < nv) return true;
-      c.vg = 0;
-    }
-    const bool done = c.q_len > 0;  // a piece was found above
-    if (++c.req < p.batch) {
-      const ReqInfo* ri = p.reqs + c.req;
-      c.q_len = __ldg(&ri->q_len);
-      c.ctx = __ldg(&ri->ctx);
-      c.flat0 = __ldg(&ri->tok0);
-    }
-    if (done) return true;
-  }
-}
-
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -154,30 +87,11 @@ __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
 __device__ __forceinline__ uint64_t sdesc_hi(uint32_t lo) {
   return (sdesc_sw128(0, 0, 1024) & 0xffffffff00000000ull) | lo;
 }
-template <bool F16>
-__device__ __forceinline__ uint32_t pack_p(float a, float b) {
-  uint32_t r;
-  if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-
 // Scratch slot of piece i of a cut tile: a block's first piece goes to slot 2 block when it begins
 // inside its tile, its last piece to slot 2 block + 1 when it begins its tile.
 __device__ __forceinline__ int64_t piece_slot(const AttMerge& mg, int i) {
   return i == 0 ? 2 * mg.cta0 + 1 : 2 * (mg.cta0 + i);
 }
-
-struct AttArgs {
-  const uint8_t *q, *kc, *vc, *ks, *vs;  // NVFP4 plans (and Q's codes)
-  int64_t q_stride;
-  const int32_t* page_table;
-  uint16_t* out;
-  int64_t out_stride;
-  float* out_lse;
-  float *part, *part_lse;  // [2 att_ctas][slot rows][D], [2 att_ctas][slot rows]
-  float c;                 // softmax scale x q_scale x log2 e
-};
 
 template <int D, bool QUANT, bool SINGLE>
 __global__ void __launch_bounds__(QUANT ? 512 : 384, 1)
@@ -1017,6 +931,31 @@ attention_merge_pieces_kernel(DevPlan p, AttArgs a) {
     a.out_lse[row.flat * p.H + row.head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
 }
 
+template <int D>
+cudaError_t run_merge(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
+  // att_merge_cap bounds the cut tiles of any plan of these q_lens.  An eager call of a plan without
+  // a cut tile needs no merge; a captured one keeps it, since it may be replayed over another plan's
+  // metadata (same q_lens, other contexts).
+  int merges = p.att_merge_cap;
+  if (p.att_num_merges == 0 && merges > 0) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &cap);
+    if (e != cudaSuccess) return e;
+    if (cap == cudaStreamCaptureStatusNone) merges = 0;
+  }
+  cudaError_t e = cudaSuccess;
+  if (merges > 0) {
+    if (p.att_slot_rows <= 32)
+      e = launch_pdl(attention_merge_pieces_kernel<D>, dim3(merges, p.att_slot_rows), dim3(256), 0,
+                     st, p, a);
+    else
+      e = launch_pdl(attention_merge_rows_kernel<D>,
+                     dim3(merges, (p.att_slot_rows + 8 * kMergeRows - 1) / (8 * kMergeRows)),
+                     dim3(256), 0, st, p, a);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int D, bool QUANT, bool SINGLE>
 cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, const void* kc,
                           const void* vc, cudaStream_t st) {
@@ -1033,6 +972,10 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
         !encode_tmap_2d(&tmV, 0, const_cast<void*>(vc), D, rows, (uint64_t)D * 2, 64, 128, true))
       return cudaErrorInvalidValue;
   }
+  if (QUANT && SINGLE && p.att_slot_rows <= 16) {
+    cudaError_t e = launch_decode_nvfp4(p, a, st);
+    return e != cudaSuccess ? e : run_merge<D>(p, a, st);
+  }
   const int smem = (int)sizeof(AttSmem<D, QUANT, SINGLE>);
   static_assert(sizeof(AttSmem<D, QUANT, SINGLE>) <= 227 * 1024, "shared memory");
   auto kern = attention_kernel<D, QUANT, SINGLE>;
@@ -1040,26 +983,7 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(p.att_ctas), dim3(QUANT ? 512 : 384), smem, st, tmQ, tmK, tmV, p, a);
   if (e != cudaSuccess) return e;
-  // att_merge_cap bounds the cut tiles of any plan of these q_lens.  An eager call of a plan without
-  // a cut tile needs no merge; a captured one keeps it, since it may be replayed over another plan's
-  // metadata (same q_lens, other contexts).
-  int merges = p.att_merge_cap;
-  if (p.att_num_merges == 0 && merges > 0) {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    e = cudaStreamIsCapturing(st, &cap);
-    if (e != cudaSuccess) return e;
-    if (cap == cudaStreamCaptureStatusNone) merges = 0;
-  }
-  if (merges > 0) {
-    if (p.att_slot_rows <= 32)
-      e = launch_pdl(attention_merge_pieces_kernel<D>, dim3(merges, p.att_slot_rows), dim3(256), 0,
-                     st, p, a);
-    else
-      e = launch_pdl(attention_merge_rows_kernel<D>,
-                     dim3(merges, (p.att_slot_rows + 8 * kMergeRows - 1) / (8 * kMergeRows)),
-                     dim3(256), 0, st, p, a);
-  }
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return run_merge<D>(p, a, st);
 }
 
 }  // namespace

@@ -1,0 +1,389 @@
+// attention_decode.cu -- full attention of tiles of at most 16 rows (single tokens of a head group)
+// over an NVFP4 cache, bound by reading the cache.
+//
+// The tcgen05 kernel (attention.cu) brings NVFP4 tiles to the tensor core through shared memory: per
+// page of 128 keys its FP16 operand tiles cost 64 KB written and 96 KB read, 1560 cycles at 128 bytes
+// a cycle, where the page's 18 KB arrive from HBM in about 840.  With 16 rows the products are small
+// (1 MFLOP a page), so here the codes go from shared memory to registers once, become FP16 fragments
+// there, and feed the warp-level tensor instruction (mma.sync m16n8k16, FP32 accumulation); nothing
+// is written back.
+//
+// Mathematics as in attention.cu: p = 2^((s - m) c + 7) with a lazily raised reference m, l and O in
+// FP32, P rounded to FP16.
+//
+// One persistent CTA per SM: warp 8 copies pages (codes and scales of K and V, 18 KB) into a ring;
+// warps 0-7 each take 16 keys of every page with a running (m, l, O) of their own, merged through
+// shared memory at the end of a piece.
+//
+// Fragments.  Lane (g, t) = (lane / 4, lane % 4).  The order of the contracted dims is free, so a
+// lane reads 2 or 1 whole 8-byte words of a key (its dims (D / 4) t ..), and takes nibbles j and j + 4
+// of a word as a pair: both halves of a register then unpack with the same shifts.  For P V the pairs
+// run along keys: the words of two keys are interleaved by 16 bits first.  O's dims are ordered so
+// that a lane's B columns are one run of D / 8 dims of a key, under one scale.
+//
+// A nibble s.eem becomes the FP16 with sign s and exponent-mantissa bits eem at 11..9, which is the
+// E2M1 value times 2^-14 (subnormals included); times the E4M3 scale times 2^6 the product is exact,
+// value * 2^-8, and the 2^8 goes into the softmax scale and the final 1 / l.
+#include "attention.cuh"
+
+namespace sps {
+namespace att {
+namespace {
+
+constexpr int kMmaWarps = 8;
+constexpr int kDecThreads = 32 * (kMmaWarps + 1);
+
+template <int D>
+struct DecSmem {
+  static constexpr int CODES = 64 * D, SCALES = 8 * D;  // of a 128-key tile
+  static constexpr int PAGE = 2 * (CODES + SCALES);     // K codes, K scales, V codes, V scales
+  static constexpr int S0 = (227 * 1024 - kMmaWarps * 16 * D * 4 - 2048) / PAGE;
+  static constexpr int STAGES = S0 > 12 ? 12 : S0;
+  uint8_t page[STAGES][PAGE];
+  float o[kMmaWarps][16][D];
+  float2 stat[kMmaWarps][16];  // (m, l)
+  uint64_t full[STAGES], empty[STAGES], meet;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Nibbles j of both 16-bit halves of w as FP16, times 2^-14.
+template <int J>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+  const uint32_t sign = J < 3 ? w << (12 - 4 * J) : w;
+  const uint32_t em = J < 3 ? w << (9 - 4 * J) : w >> 3;
+  return (sign & 0x80008000u) | (em & 0x0E000E00u);
+}
+
+// Two E4M3 scales as FP16 times 2^6.
+__device__ __forceinline__ uint32_t scales_f16(uint32_t two) {
+  return hmul2_u32(cvt_e4m3x2((uint16_t)two), 0x54005400u);  // 64, 64
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p, AttArgs a) {
+  using Smem = DecSmem<D>;
+  constexpr int S = Smem::STAGES, WORDS = D / 32;  // WORDS: 8-code words of a key in a lane
+  constexpr int NT = D / 8;                        // column tiles of O
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int32_t* status = p.status;
+  volatile int* abort_flag = &sm.abort_flag;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&sm.full[i]), 1);
+      mbar_init(smem_u32(&sm.empty[i]), kMmaWarps);
+    }
+    mbar_init(smem_u32(&sm.meet), kMmaWarps);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();  // from here on: what earlier kernels wrote
+  const RowPack rp(p.Hg);
+  AttCursor cur = p.att_starts[blockIdx.x];
+  const AttCursor end = p.att_starts[blockIdx.x + 1];
+  Piece pc;
+  uint32_t st = 0, ph = 0;  // ring stage and phase
+  auto advance = [&]() {
+    if (++st == S) {
+      st = 0;
+      ph ^= 1;
+    }
+  };
+
+  if (warp == kMmaWarps) {
+    // ------------------------------------------------ copies
+    bool ok = true;
+    while (ok && next_piece(p, rp, cur, end, pc)) {
+      const int n = pc.page1 - pc.page0;
+      const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
+      auto load_ids = [&](int first) {  // physical tiles of the lanes' pages first + lane
+        int id = 0;
+        if (first + lane < n) {
+          id = __ldg(pages + first + lane);
+          if (id < 0 || id >= p.num_phys) {
+            set_status(status, DEV_BAD_PAGE);
+            id = 0;
+          }
+        }
+        return id * p.Hkv + pc.vg;
+      };
+      int ids = load_ids(0), next_ids = 0;
+      for (int s = 0; s < n && ok; ++s) {
+        if (s > 0 && (s & 31) == 0) ids = next_ids;
+        if ((s & 31) == 8) next_ids = load_ids(s + 24);
+        const int64_t tile = __shfl_sync(0xffffffffu, ids, s & 31);
+        if (lane == 0) {
+          ok = mbar_wait(smem_u32(&sm.empty[st]), ph ^ 1, abort_flag, status);
+          if (ok) {
+            const uint32_t f = smem_u32(&sm.full[st]), d = smem_u32(sm.page[st]);
+            mbar_expect_tx(f, Smem::PAGE);
+            bulk_load(d, a.kc + tile * Smem::CODES, Smem::CODES, f);
+            bulk_load(d + Smem::CODES, a.ks + tile * Smem::SCALES, Smem::SCALES, f);
+            bulk_load(d + Smem::PAGE / 2, a.vc + tile * Smem::CODES, Smem::CODES, f);
+            bulk_load(d + Smem::PAGE / 2 + Smem::CODES, a.vs + tile * Smem::SCALES, Smem::SCALES, f);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        advance();
+      }
+    }
+  } else {
+    // ------------------------------------------------ products: 16 keys of every page
+    const int g = lane / 4, t = lane % 4, kb = 16 * warp;
+    const float c = a.c * 256.f;  // K enters times 2^-8
+    bool ok = true;
+    uint32_t met = 0;
+    auto meet = [&]() {  // the eight warps (a bounded wait, unlike a block barrier)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.meet));
+      return mbar_wait(smem_u32(&sm.meet), met++ & 1, abort_flag, status);
+    };
+    while (ok && next_piece(p, rp, cur, end, pc)) {
+      const int n = pc.page1 - pc.page0, kv_len = pc.ctx + pc.q_len;
+      // rows g and g + 8: Q fragments, positions
+      uint32_t qf[2 * WORDS][4];  // k-step: (row g, row g + 8) x (pairs of columns 2 t and 2 t + 8)
+      int pos[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = g + 8 * h, tok = r / rp.HB, hd = r % rp.HB;
+        const bool valid = tok < pc.q_len && tok < rp.TB;
+        pos[h] = valid ? pc.ctx + tok : 0x3fffffff;
+        const uint8_t* q = a.q + (int64_t)(pc.flat0 + tok) * a.q_stride +
+                           (int64_t)(pc.vg * p.Hg + hd) * D + t * (D / 4);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          uint2 x = make_uint2(0, 0);
+          if (valid) x = __ldg(reinterpret_cast<const uint2*>(q) + w);  // dims 8 w .. of this lane's
+          // pairs (j, j + 4), as the keys' nibbles pair up
+          qf[2 * w][h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0040));
+          qf[2 * w][2 + h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0051));
+          qf[2 * w + 1][h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0062));
+          qf[2 * w + 1][2 + h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0073));
+        }
+      }
+      const int first_pos = pc.ctx;  // the smallest position of the tile
+      float o[NT][4], m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (!mbar_wait(smem_u32(&sm.full[st]), ph, abort_flag, status)) { ok = false; break; }
+        const uint8_t* kp = sm.page[st];
+        const uint8_t* vp = kp + Smem::PAGE / 2;
+        const int key0 = (pc.page0 + j) * 128 + kb;  // this warp's first key
+        // S = Q K^T for keys kb + 8 u + (column)
+        float s[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = kb + 8 * u + g;
+          uint32_t w[WORDS], sc;
+          if (D == 128) {
+            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(kp + key * 64 + t * 16);
+            sc = *reinterpret_cast<const uint16_t*>(kp + Smem::CODES + key * 8 + t * 2);
+          } else {
+            *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(kp + key * 32 + t * 8);
+            sc = kp[Smem::CODES + key * 4 + t];
+          }
+          const uint32_t two = scales_f16(sc);
+          const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
+#pragma unroll
+          for (int k = 0; k < WORDS; ++k) {
+            const uint32_t f = k < 2 ? s0 : s1;
+            mma_16816(s[u], qf[2 * k], hmul2_u32(nibbles<0>(w[k]), f), hmul2_u32(nibbles<1>(w[k]), f));
+            mma_16816(s[u], qf[2 * k + 1], hmul2_u32(nibbles<2>(w[k]), f),
+                      hmul2_u32(nibbles<3>(w[k]), f));
+          }
+        }
+        if (key0 + 15 > first_pos) {  // some key lies behind some row
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + 8 * u + 2 * t + (e & 1) > pos[e / 2]) s[u][e] = -INFINITY;
+        }
+        // the reference maximum: raised for the warp's rows together when some score asks for it
+        float mb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          mb[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+        const bool first = j == 0;
+        if (__any_sync(0xffffffffu, first || (mb[0] - m[0]) * c > kRescale ||
+                                        (mb[1] - m[1]) * c > kRescale)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = mb[h];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            if (x == -INFINITY) x = first ? 0.f : m[h];
+            const bool raise = first || x > m[h];
+            const float f = raise && !first ? fast_exp2((m[h] - x) * c) : 1.f;
+            if (raise) m[h] = x;
+            l[h] *= f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              o[i][2 * h] *= f;
+              o[i][2 * h + 1] *= f;
+            }
+          }
+        }
+        uint32_t pf[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float off = kF16Bias - m[h] * c;
+            const float x = fast_exp2(fmaf(s[u][2 * h], c, off));
+            const float y = fast_exp2(fmaf(s[u][2 * h + 1], c, off));
+            l[h] += x + y;
+            pf[2 * u + h] = pack_p<true>(x, y);
+          }
+        // O += P V: keys kb + 2 t, + 1 (first half of the contraction) and kb + 8 + 2 t, + 1; dims
+        // (D / 8) g .. of each
+        uint32_t v[4][D / 64], vs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = kb + 2 * t + (k & 1) + 8 * (k >> 1);
+          if (D == 128) {
+            *reinterpret_cast<uint2*>(v[k]) = *reinterpret_cast<const uint2*>(vp + key * 64 + g * 8);
+            vs[k] = vp[Smem::CODES + key * 8 + g];
+          } else {
+            v[k][0] = *reinterpret_cast<const uint32_t*>(vp + key * 32 + g * 4);
+            vs[k] = vp[Smem::CODES + key * 4 + g / 2];
+          }
+          // slots behind the request's last token may hold anything: zero, not NaN
+          if (key0 + (key - kb) >= kv_len) {
+            vs[k] = 0;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) v[k][i] = 0;
+          }
+        }
+        // (the codes are in registers: the stage may be refilled)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
+        advance();
+        const uint32_t sa = scales_f16(vs[0] | (vs[1] << 8)), sb = scales_f16(vs[2] | (vs[3] << 8));
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // dims 8 i + 4 h ..: the words' low or high halves
+            const uint32_t x = __byte_perm(v[0][i], v[1][i], h ? 0x7632 : 0x5410);
+            const uint32_t y = __byte_perm(v[2][i], v[3][i], h ? 0x7632 : 0x5410);
+            const int nt = 8 * i + 4 * h;
+            mma_16816(o[nt], pf, hmul2_u32(nibbles<0>(x), sa), hmul2_u32(nibbles<0>(y), sb));
+            mma_16816(o[nt + 1], pf, hmul2_u32(nibbles<1>(x), sa), hmul2_u32(nibbles<1>(y), sb));
+            mma_16816(o[nt + 2], pf, hmul2_u32(nibbles<2>(x), sa), hmul2_u32(nibbles<2>(y), sb));
+            mma_16816(o[nt + 3], pf, hmul2_u32(nibbles<3>(x), sa), hmul2_u32(nibbles<3>(y), sb));
+          }
+        }
+      }
+      if (!ok) break;
+      // the warps' results meet in shared memory.  Column tile i, column q of a tile is dim
+      // (D / 8) q + i: lane (g, t) holds dims (D / 4) t + i and (D / 4) t + D / 8 + i
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (t == 0) sm.stat[warp][g + 8 * h] = make_float2(m[h], l[h]);
+        float* row = sm.o[warp][g + 8 * h] + t * (D / 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < NT; i += 4)
+            *reinterpret_cast<float4*>(row + e * (D / 8) + i) = make_float4(
+                o[i][2 * h + e], o[i + 1][2 * h + e], o[i + 2][2 * h + e], o[i + 3][2 * h + e]);
+      }
+      if (!meet()) break;
+      {
+        const int r = tid / 16, q = tid % 16;  // row, and its dims (D / 16) q ..
+        const int tok = r / rp.HB, hd = r % rp.HB;
+        float mx = -INFINITY, sum = 0.f, f[kMmaWarps], acc[D / 16];
+#pragma unroll
+        for (int k = 0; k < kMmaWarps; ++k) {
+          const float2 x = sm.stat[k][r];
+          f[k] = x.x;
+          if (x.y > 0.f) mx = fmaxf(mx, x.x);
+        }
+#pragma unroll
+        for (int k = 0; k < kMmaWarps; ++k) {
+          const float lk = sm.stat[k][r].y;
+          f[k] = lk > 0.f ? fast_exp2((f[k] - mx) * c) : 0.f;
+          sum += lk * f[k];
+        }
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMmaWarps; ++k)
+          if (f[k] != 0.f) {
+#pragma unroll
+            for (int e = 0; e < D / 16; e += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(&sm.o[k][r][q * (D / 16) + e]);
+              acc[e] += f[k] * x.x;
+              acc[e + 1] += f[k] * x.y;
+              acc[e + 2] += f[k] * x.z;
+              acc[e + 3] += f[k] * x.w;
+            }
+          }
+        const float inv = sum > 0.f ? 256.f / sum : 0.f;  // V entered times 2^-8
+        if (tok < pc.q_len && tok < rp.TB) {
+          const float lse =
+              sum > 0.f ? (mx * c - kF16Bias + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          const int64_t flat = pc.flat0 + tok;
+          const int head = pc.vg * p.Hg + hd;
+          if (pc.page0 == 0 && pc.page1 == pc.pages) {
+            if (q == 0 && a.out_lse) a.out_lse[flat * p.H + head] = lse;
+            uint32_t w[D / 32];
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+              w[e] = pack_p<false>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+            uint16_t* out = a.out + flat * a.out_stride + (int64_t)head * D + q * (D / 16);
+            if (D == 128) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<uint4*>(w);
+            else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<uint2*>(w);
+          } else {
+            const int64_t srow =
+                (2 * (int64_t)blockIdx.x + (pc.page0 > 0 ? 0 : 1)) * p.att_slot_rows + r;
+            if (q == 0) a.part_lse[srow] = lse;
+#pragma unroll
+            for (int e = 0; e < D / 16; e += 4)
+              *reinterpret_cast<float4*>(a.part + srow * D + q * (D / 16) + e) = make_float4(
+                  acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
+          }
+        }
+      }
+      if (!meet()) break;  // the areas may be written again
+    }
+  }
+  settle_after_abort(abort_flag);
+}
+
+template <int D>
+cudaError_t run_decode(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
+  const int smem = (int)sizeof(DecSmem<D>);
+  static_assert(sizeof(DecSmem<D>) <= 227 * 1024, "shared memory");
+  auto kern = decode_nvfp4_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(p.att_ctas), dim3(kDecThreads), smem, st, p, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_nvfp4(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
+  return p.D == 128 ? run_decode<128>(p, a, st) : run_decode<64>(p, a, st);
+}
+
+}  // namespace att
+}  // namespace sps

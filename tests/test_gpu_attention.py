@@ -170,6 +170,30 @@ def test_lengths_and_page_borders(q_lens, ctx, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("H,G,D,q", [(16, 1, 128, 1), (16, 2, 64, 2), (2, 2, 128, 1), (2, 2, 64, 16),
+                                     (5, 1, 128, 3), (28, 4, 64, 2), (34, 2, 128, 1)])
+def test_tiles_of_few_rows(H, G, D, q, kv):
+    """Decode steps of up to 16 rows a tile (one case of 17), the last page from one key to full,
+    requests without a token among them."""
+    q_lens = [q, 0, q, 1, q, q, q]
+    ctx = [0, 3, 127, 128 * 3 - 1, 5000, 128 * 9 - q, 250]
+    for gain in (None, lambda i: 0.3 + 0.7 * i):
+        c = Case(H + q, q_lens, ctx, H, G, D, kv, k_gain=gain, q_pad=1, out_pad=1)
+        c.run()
+        if gain is None:
+            c.check()
+            continue
+        torch.cuda.synchronize()
+        assert c.B.sps_read_device_status(c.plan, c.ws) == 0
+        # scores grow to about 2^9 in log2 units: an FP32 rounding of s c of 2^-14 there
+        out, lse, mag, keys = c.reference()
+        p_half = 2.0 ** -8 if kv == "bf16" else 2.0 ** -11
+        tol = (p_half + 2.0 ** -12) * mag * 2 + 2.0 ** -8 * out.abs() + 2.0 ** -20
+        assert bool(((c.out.double() - out).abs() <= tol).all())
+        assert bool(((c.lse.double() - lse).abs() <= 2.0 ** -12 + lse.abs() * 2.0 ** -21).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
 def test_single_token_after_a_1m_context(kv):
     c = Case(5, [1], [(1 << 20) - 1], 8, 1, 64, kv)
     c.run()
