@@ -11,37 +11,33 @@
 // Mathematics as in attention.cu: p = 2^((s - m) c + 7) with a lazily raised reference m, l and O in
 // FP32, P rounded to FP16.
 //
-// One persistent CTA per SM: warp 8 copies pages (codes and scales of K and V, 18 KB) into a ring;
-// warps 0-7 each take 16 keys of every page with a running (m, l, O) of their own, merged through
-// shared memory at the end of a piece.
+// One persistent CTA per SM: one warp copies pages (codes and scales of K and V, 18 KB) into a ring;
+// the others take the pages' 16-key chunks in turn, each with a running (m, l, O) of its own, merged
+// through shared memory at the end of a piece.
 //
 // Fragments.  Lane (g, t) = (lane / 4, lane % 4).  The order of the contracted dims is free, so a
-// lane reads 2 or 1 whole 8-byte words of a key (its dims (D / 4) t ..), and takes nibbles j and j + 4
-// of a word as a pair: both halves of a register then unpack with the same shifts.  For P V the pairs
-// run along keys: the words of two keys are interleaved by 16 bits first.  O's dims are ordered so
-// that a lane's B columns are one run of D / 8 dims of a key, under one scale.
-//
-// A nibble s.eem becomes the FP16 with sign s and exponent-mantissa bits eem at 11..9, which is the
-// E2M1 value times 2^-14 (subnormals included); times the E4M3 scale times 2^6 the product is exact,
-// value * 2^-8, and the 2^8 goes into the softmax scale and the final 1 / l.
+// lane reads whole words of a key (its dims (D / 4) t ..), and the pairs of a B register are the two
+// codes of a byte.  For P V the pairs run along keys: the converted pairs of two keys exchange halves.
+// O's dims are ordered so that a lane's B columns are one run of D / 8 dims of a key, under one scale.
 #include "attention.cuh"
 
 namespace sps {
 namespace att {
 namespace {
 
-constexpr int kMmaWarps = 8;
+constexpr int kMmaWarps = 12;
 constexpr int kDecThreads = 32 * (kMmaWarps + 1);
 
 template <int D>
 struct DecSmem {
   static constexpr int CODES = 64 * D, SCALES = 8 * D;  // of a 128-key tile
   static constexpr int PAGE = 2 * (CODES + SCALES);     // K codes, K scales, V codes, V scales
-  static constexpr int S0 = (227 * 1024 - kMmaWarps * 16 * D * 4 - 2048) / PAGE;
+  static constexpr int S0 = (227 * 1024 - kMmaWarps * 16 * (D * 4 + 8) - D * 32 - 512) / PAGE;
   static constexpr int STAGES = S0 > 12 ? 12 : S0;
   uint8_t page[STAGES][PAGE];
   float o[kMmaWarps][16][D];
   float2 stat[kMmaWarps][16];  // (m, l)
+  uint4 qf[D / 16][32];        // Q fragments, k-step by lane
   uint64_t full[STAGES], empty[STAGES], meet;
   int abort_flag;
 };
@@ -53,19 +49,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Nibbles j of both 16-bit halves of w as FP16, times 2^-14.
-template <int J>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-  const uint32_t sign = J < 3 ? w << (12 - 4 * J) : w;
-  const uint32_t em = J < 3 ? w << (9 - 4 * J) : w >> 3;
-  return (sign & 0x80008000u) | (em & 0x0E000E00u);
-}
-
-// Two E4M3 scales as FP16 times 2^6.
-__device__ __forceinline__ uint32_t scales_f16(uint32_t two) {
-  return hmul2_u32(cvt_e4m3x2((uint16_t)two), 0x54005400u);  // 64, 64
 }
 
 template <int D>
@@ -81,7 +64,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&sm.full[i]), 1);
-      mbar_init(smem_u32(&sm.empty[i]), kMmaWarps);
+      mbar_init(smem_u32(&sm.empty[i]), 8);  // a page's chunks
     }
     mbar_init(smem_u32(&sm.meet), kMmaWarps);
     sm.abort_flag = 0;
@@ -139,73 +122,86 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       }
     }
   } else {
-    // ------------------------------------------------ products: 16 keys of every page
-    const int g = lane / 4, t = lane % 4, kb = 16 * warp;
-    const float c = a.c * 256.f;  // K enters times 2^-8
+    // ------------------------------------------------ products: chunks of 16 keys
+    const int g = lane / 4, t = lane % 4;
+    const float c = a.c;
     bool ok = true;
-    uint32_t met = 0;
-    auto meet = [&]() {  // the eight warps (a bounded wait, unlike a block barrier)
+    uint32_t met = 0, page_it = 0;  // meetings, pages before the piece
+    auto meet = [&]() {             // the product warps (a bounded wait, unlike a block barrier)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.meet));
       return mbar_wait(smem_u32(&sm.meet), met++ & 1, abort_flag, status);
     };
     while (ok && next_piece(p, rp, cur, end, pc)) {
       const int n = pc.page1 - pc.page0, kv_len = pc.ctx + pc.q_len;
-      // rows g and g + 8: Q fragments, positions
-      uint32_t qf[2 * WORDS][4];  // k-step: (row g, row g + 8) x (pairs of columns 2 t and 2 t + 8)
-      int pos[2];
+      int pos[2];  // of rows g and g + 8
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h, tok = r / rp.HB, hd = r % rp.HB;
-        const bool valid = tok < pc.q_len && tok < rp.TB;
-        pos[h] = valid ? pc.ctx + tok : 0x3fffffff;
-        const uint8_t* q = a.q + (int64_t)(pc.flat0 + tok) * a.q_stride +
-                           (int64_t)(pc.vg * p.Hg + hd) * D + t * (D / 4);
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          uint2 x = make_uint2(0, 0);
-          if (valid) x = __ldg(reinterpret_cast<const uint2*>(q) + w);  // dims 8 w .. of this lane's
-          // pairs (j, j + 4), as the keys' nibbles pair up
-          qf[2 * w][h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0040));
-          qf[2 * w][2 + h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0051));
-          qf[2 * w + 1][h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0062));
-          qf[2 * w + 1][2 + h] = cvt_e4m3x2((uint16_t)__byte_perm(x.x, x.y, 0x0073));
-        }
+        const int tok = (g + 8 * h) / rp.HB;
+        pos[h] = tok < pc.q_len && tok < rp.TB ? pc.ctx + tok : 0x3fffffff;
       }
+      // Q fragments, a k-step per warp: (row g, row g + 8) x columns 2 t and 2 t + 8, which are the
+      // lane's dims 4 k .. 4 k + 3
+      for (int k = warp; k < D / 16; k += kMmaWarps) {
+        uint32_t f[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = g + 8 * h, tok = r / rp.HB, hd = r % rp.HB;
+          uint32_t x = 0;
+          if (tok < pc.q_len && tok < rp.TB)
+            x = __ldg(reinterpret_cast<const uint32_t*>(
+                a.q + (int64_t)(pc.flat0 + tok) * a.q_stride +
+                (int64_t)(pc.vg * p.Hg + hd) * D + t * (D / 4) + 4 * k));
+          f[h] = cvt_e4m3x2((uint16_t)x);
+          f[2 + h] = cvt_e4m3x2((uint16_t)(x >> 16));
+        }
+        sm.qf[k][lane] = make_uint4(f[0], f[1], f[2], f[3]);
+      }
+      if (!meet()) break;
       const int first_pos = pc.ctx;  // the smallest position of the tile
       float o[NT][4], m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-      for (int j = 0; j < n; ++j) {
-        if (!mbar_wait(smem_u32(&sm.full[st]), ph, abort_flag, status)) { ok = false; break; }
-        const uint8_t* kp = sm.page[st];
+      bool first = true;
+      for (int ch = warp; ch < 8 * n; ch += kMmaWarps) {
+        const uint32_t it = page_it + ch / 8, stg = it % S;
+        if (!mbar_wait(smem_u32(&sm.full[stg]), (it / S) & 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        const int kb = 16 * (ch % 8);
+        const uint8_t* kp = sm.page[stg];
         const uint8_t* vp = kp + Smem::PAGE / 2;
-        const int key0 = (pc.page0 + j) * 128 + kb;  // this warp's first key
+        const int key0 = (pc.page0 + ch / 8) * 128 + kb;  // the chunk's first key
         // S = Q K^T for keys kb + 8 u + (column)
         float s[2][4];
+        uint32_t kw[2][WORDS], ks[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int key = kb + 8 * u + g;
-          uint32_t w[WORDS], sc;
           if (D == 128) {
-            *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(kp + key * 64 + t * 16);
-            sc = *reinterpret_cast<const uint16_t*>(kp + Smem::CODES + key * 8 + t * 2);
+            *reinterpret_cast<uint4*>(kw[u]) = *reinterpret_cast<const uint4*>(kp + key * 64 + t * 16);
+            ks[u] = *reinterpret_cast<const uint16_t*>(kp + Smem::CODES + key * 8 + t * 2);
           } else {
-            *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(kp + key * 32 + t * 8);
-            sc = kp[Smem::CODES + key * 4 + t];
+            *reinterpret_cast<uint2*>(kw[u]) = *reinterpret_cast<const uint2*>(kp + key * 32 + t * 8);
+            ks[u] = kp[Smem::CODES + key * 4 + t];
           }
-          const uint32_t two = scales_f16(sc);
-          const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+          ks[u] = cvt_e4m3x2((uint16_t)ks[u]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
+        }
 #pragma unroll
-          for (int k = 0; k < WORDS; ++k) {
-            const uint32_t f = k < 2 ? s0 : s1;
-            mma_16816(s[u], qf[2 * k], hmul2_u32(nibbles<0>(w[k]), f), hmul2_u32(nibbles<1>(w[k]), f));
-            mma_16816(s[u], qf[2 * k + 1], hmul2_u32(nibbles<2>(w[k]), f),
-                      hmul2_u32(nibbles<3>(w[k]), f));
+        for (int k = 0; k < D / 16; ++k) {  // 4 dims of a lane, two bytes of its word k / 2
+          const uint4 qv = sm.qf[k][lane];
+          const uint32_t qa[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t w = kw[u][k / 2] >> (16 * (k % 2));
+            const uint32_t f = __byte_perm(ks[u], ks[u], k < 4 ? 0x1010 : 0x3232);
+            mma_16816(s[u], qa, hmul2_u32(cvt_e2m1x2((uint16_t)w), f),
+                      hmul2_u32(cvt_e2m1x2((uint16_t)(w >> 8)), f));
           }
         }
         if (key0 + 15 > first_pos) {  // some key lies behind some row
@@ -220,7 +216,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           mb[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-        const bool first = j == 0;
         if (__any_sync(0xffffffffu, first || (mb[0] - m[0]) * c > kRescale ||
                                         (mb[1] - m[1]) * c > kRescale)) {
 #pragma unroll
@@ -240,6 +235,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
             }
           }
         }
+        first = false;
         uint32_t pf[4];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -273,23 +269,22 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
         }
         // (the codes are in registers: the stage may be refilled)
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
-        advance();
-        const uint32_t sa = scales_f16(vs[0] | (vs[1] << 8)), sb = scales_f16(vs[2] | (vs[3] << 8));
+        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[stg]));
+        const uint32_t sa = cvt_e4m3x2((uint16_t)(vs[0] | (vs[1] << 8)));
+        const uint32_t sb = cvt_e4m3x2((uint16_t)(vs[2] | (vs[3] << 8)));
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
+        for (int i = 0; i < D / 16; ++i) {  // dims 2 i, 2 i + 1: a byte of each key
+          uint32_t x[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // dims 8 i + 4 h ..: the words' low or high halves
-            const uint32_t x = __byte_perm(v[0][i], v[1][i], h ? 0x7632 : 0x5410);
-            const uint32_t y = __byte_perm(v[2][i], v[3][i], h ? 0x7632 : 0x5410);
-            const int nt = 8 * i + 4 * h;
-            mma_16816(o[nt], pf, hmul2_u32(nibbles<0>(x), sa), hmul2_u32(nibbles<0>(y), sb));
-            mma_16816(o[nt + 1], pf, hmul2_u32(nibbles<1>(x), sa), hmul2_u32(nibbles<1>(y), sb));
-            mma_16816(o[nt + 2], pf, hmul2_u32(nibbles<2>(x), sa), hmul2_u32(nibbles<2>(y), sb));
-            mma_16816(o[nt + 3], pf, hmul2_u32(nibbles<3>(x), sa), hmul2_u32(nibbles<3>(y), sb));
-          }
+          for (int k = 0; k < 4; ++k)
+            x[k] = cvt_e2m1x2((uint16_t)(v[k][i / 4] >> (8 * (i % 4))));
+          mma_16816(o[2 * i], pf, hmul2_u32(__byte_perm(x[0], x[1], 0x5410), sa),
+                    hmul2_u32(__byte_perm(x[2], x[3], 0x5410), sb));
+          mma_16816(o[2 * i + 1], pf, hmul2_u32(__byte_perm(x[0], x[1], 0x7632), sa),
+                    hmul2_u32(__byte_perm(x[2], x[3], 0x7632), sb));
         }
       }
+      page_it += n;
       if (!ok) break;
       // the warps' results meet in shared memory.  Column tile i, column q of a tile is dim
       // (D / 8) q + i: lane (g, t) holds dims (D / 4) t + i and (D / 4) t + D / 8 + i
@@ -307,7 +302,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
                 o[i][2 * h + e], o[i + 1][2 * h + e], o[i + 2][2 * h + e], o[i + 3][2 * h + e]);
       }
       if (!meet()) break;
-      {
+      if (tid < 256) {
         const int r = tid / 16, q = tid % 16;  // row, and its dims (D / 16) q ..
         const int tok = r / rp.HB, hd = r % rp.HB;
         float mx = -INFINITY, sum = 0.f, f[kMmaWarps], acc[D / 16];
@@ -337,7 +332,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
               acc[e + 3] += f[k] * x.w;
             }
           }
-        const float inv = sum > 0.f ? 256.f / sum : 0.f;  // V entered times 2^-8
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
         if (tok < pc.q_len && tok < rp.TB) {
           const float lse =
               sum > 0.f ? (mx * c - kF16Bias + log2f(sum)) * 0.6931471805599453f : -INFINITY;
