@@ -12,12 +12,12 @@
 // FP32, P rounded to FP16.
 //
 // One persistent CTA per SM: one warp copies pages (codes and scales of K and V, 18 KB) into a ring;
-// the others take the pages' 16-key chunks in turn, each with a running (m, l, O) of its own, merged
+// the others take the pages' 32-key chunks in turn, each with a running (m, l, O) of its own, merged
 // through shared memory at the end of a piece.
 //
 // Fragments.  Lane (g, t) = (lane / 4, lane % 4).  The order of the contracted dims is free, so a
 // lane reads whole words of a key (its dims (D / 4) t ..), and the pairs of a B register are the two
-// codes of a byte.  For P V the pairs run along keys: the converted pairs of two keys exchange halves.
+// codes of a byte.  For P V the pairs run along keys: the nibbles of two keys' words are interleaved.
 // O's dims are ordered so that a lane's B columns are one run of D / 8 dims of a key, under one scale.
 #include "attention.cuh"
 
@@ -25,7 +25,10 @@ namespace sps {
 namespace att {
 namespace {
 
-constexpr int kMmaWarps = 12;
+constexpr int kMmaWarps = 8;
+constexpr int kChunks = 4;                        // 32-key chunks of a page
+constexpr int kPageStep = kMmaWarps / kChunks;    // a warp takes a chunk of every kPageStep-th page
+static_assert(kMmaWarps % kChunks == 0, "a warp keeps its place in the page");
 constexpr int kDecThreads = 32 * (kMmaWarps + 1);
 
 template <int D>
@@ -33,7 +36,11 @@ struct DecSmem {
   static constexpr int CODES = 64 * D, SCALES = 8 * D;  // of a 128-key tile
   static constexpr int PAGE = 2 * (CODES + SCALES);     // K codes, K scales, V codes, V scales
   static constexpr int S0 = (227 * 1024 - kMmaWarps * 16 * (D * 4 + 8) - D * 32 - 512) / PAGE;
-  static constexpr int STAGES = S0 > 12 ? 12 : S0;
+  // A multiple of kPageStep: a warp then finds in a stage, each time round, the page after one that
+  // it took itself, so that the phase it waits for is never more than one ahead of the barrier's (a
+  // parity wait two phases ahead passes at once).  Between pieces the warps meet.
+  static constexpr int STAGES = (S0 > 12 ? 12 : S0) / kPageStep * kPageStep;
+  static_assert(STAGES >= 2 * kPageStep, "shared memory");
   uint8_t page[STAGES][PAGE];
   float o[kMmaWarps][16][D];
   float2 stat[kMmaWarps][16];  // (m, l)
@@ -51,6 +58,15 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The four bytes of w, two E2M1 codes each, as FP16 pairs (exact).
+__device__ __forceinline__ void cvt_e2m1x8(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p, AttArgs a) {
   using Smem = DecSmem<D>;
@@ -64,7 +80,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&sm.full[i]), 1);
-      mbar_init(smem_u32(&sm.empty[i]), 8);  // a page's chunks
+      mbar_init(smem_u32(&sm.empty[i]), kChunks);
     }
     mbar_init(smem_u32(&sm.meet), kMmaWarps);
     sm.abort_flag = 0;
@@ -165,21 +181,21 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
       bool first = true;
-      for (int ch = warp; ch < 8 * n; ch += kMmaWarps) {
-        const uint32_t it = page_it + ch / 8, stg = it % S;
+      for (int ch = warp; ch < kChunks * n; ch += kMmaWarps) {
+        const uint32_t it = page_it + ch / kChunks, stg = it % S;
         if (!mbar_wait(smem_u32(&sm.full[stg]), (it / S) & 1, abort_flag, status)) {
           ok = false;
           break;
         }
-        const int kb = 16 * (ch % 8);
+        const int kb = 32 * (ch % kChunks);
         const uint8_t* kp = sm.page[stg];
         const uint8_t* vp = kp + Smem::PAGE / 2;
-        const int key0 = (pc.page0 + ch / 8) * 128 + kb;  // the chunk's first key
+        const int key0 = (pc.page0 + ch / kChunks) * 128 + kb;  // the chunk's first key
         // S = Q K^T for keys kb + 8 u + (column)
-        float s[2][4];
-        uint32_t kw[2][WORDS], ks[2];
+        float s[4][4];
+        uint32_t kw[4][WORDS], ks[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const int key = kb + 8 * u + g;
           if (D == 128) {
             *reinterpret_cast<uint4*>(kw[u]) = *reinterpret_cast<const uint4*>(kp + key * 64 + t * 16);
@@ -188,25 +204,27 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
             *reinterpret_cast<uint2*>(kw[u]) = *reinterpret_cast<const uint2*>(kp + key * 32 + t * 8);
             ks[u] = kp[Smem::CODES + key * 4 + t];
           }
-          ks[u] = cvt_e4m3x2((uint16_t)ks[u]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {  // 4 dims of a lane, two bytes of its word k / 2
-          const uint4 qv = sm.qf[k][lane];
-          const uint32_t qa[4] = {qv.x, qv.y, qv.z, qv.w};
+        for (int u = 0; u < 4; ++u) ks[u] = cvt_e4m3x2((uint16_t)ks[u]);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t w = kw[u][k / 2] >> (16 * (k % 2));
-            const uint32_t f = __byte_perm(ks[u], ks[u], k < 4 ? 0x1010 : 0x3232);
-            mma_16816(s[u], qa, hmul2_u32(cvt_e2m1x2((uint16_t)w), f),
-                      hmul2_u32(cvt_e2m1x2((uint16_t)(w >> 8)), f));
+        for (int w = 0; w < WORDS; ++w) {  // 8 dims of a lane: two k-steps of 4
+          const uint4 q0 = sm.qf[2 * w][lane], q1 = sm.qf[2 * w + 1][lane];
+          const uint32_t qa[4] = {q0.x, q0.y, q0.z, q0.w}, qb[4] = {q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t f = __byte_perm(ks[u], ks[u], w < 2 ? 0x1010 : 0x3232);
+            uint32_t x[4];
+            cvt_e2m1x8(kw[u][w], x);
+            mma_16816(s[u], qa, hmul2_u32(x[0], f), hmul2_u32(x[1], f));
+            mma_16816(s[u], qb, hmul2_u32(x[2], f), hmul2_u32(x[3], f));
           }
         }
-        if (key0 + 15 > first_pos) {  // some key lies behind some row
+        if (key0 + 31 > first_pos) {  // some key lies behind some row
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (key0 + 8 * u + 2 * t + (e & 1) > pos[e / 2]) s[u][e] = -INFINITY;
@@ -215,7 +233,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
         float mb[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          mb[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+          mb[h] = fmaxf(fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1])),
+                        fmaxf(fmaxf(s[2][2 * h], s[2][2 * h + 1]), fmaxf(s[3][2 * h], s[3][2 * h + 1])));
         if (__any_sync(0xffffffffu, first || (mb[0] - m[0]) * c > kRescale ||
                                         (mb[1] - m[1]) * c > kRescale)) {
 #pragma unroll
@@ -236,52 +255,62 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
           }
         }
         first = false;
-        uint32_t pf[4];
+        uint32_t pf[2][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float off = kF16Bias - m[h] * c;
             const float x = fast_exp2(fmaf(s[u][2 * h], c, off));
             const float y = fast_exp2(fmaf(s[u][2 * h + 1], c, off));
             l[h] += x + y;
-            pf[2 * u + h] = pack_p<true>(x, y);
+            pf[u / 2][2 * (u % 2) + h] = pack_p<true>(x, y);
           }
-        // O += P V: keys kb + 2 t, + 1 (first half of the contraction) and kb + 8 + 2 t, + 1; dims
-        // (D / 8) g .. of each
-        uint32_t v[4][D / 64], vs[4];
+        // O += P V, 16 keys at a time: keys 2 t, 2 t + 1 (first half of the contraction) and
+        // 8 + 2 t, + 1; dims (D / 8) g .. of each
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = kb + 2 * t + (k & 1) + 8 * (k >> 1);
-          if (D == 128) {
-            *reinterpret_cast<uint2*>(v[k]) = *reinterpret_cast<const uint2*>(vp + key * 64 + g * 8);
-            vs[k] = vp[Smem::CODES + key * 8 + g];
-          } else {
-            v[k][0] = *reinterpret_cast<const uint32_t*>(vp + key * 32 + g * 4);
-            vs[k] = vp[Smem::CODES + key * 4 + g / 2];
+        for (int y = 0; y < 2; ++y) {
+          uint32_t v[4][D / 64], vs[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = kb + 16 * y + 2 * t + (k & 1) + 8 * (k >> 1);
+            if (D == 128) {
+              *reinterpret_cast<uint2*>(v[k]) = *reinterpret_cast<const uint2*>(vp + key * 64 + g * 8);
+              vs[k] = vp[Smem::CODES + key * 8 + g];
+            } else {
+              v[k][0] = *reinterpret_cast<const uint32_t*>(vp + key * 32 + g * 4);
+              vs[k] = vp[Smem::CODES + key * 4 + g / 2];
+            }
           }
-          // slots behind the request's last token may hold anything: zero, not NaN
-          if (key0 + (key - kb) >= kv_len) {
-            vs[k] = 0;
+          if (key0 + 31 >= kv_len) {  // slots behind the request's last token: zero, never NaN
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) v[k][i] = 0;
+            for (int k = 0; k < 4; ++k)
+              if (key0 + 16 * y + 2 * t + (k & 1) + 8 * (k >> 1) >= kv_len) {
+                vs[k] = 0;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) v[k][i] = 0;
+              }
           }
-        }
-        // (the codes are in registers: the stage may be refilled)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[stg]));
-        const uint32_t sa = cvt_e4m3x2((uint16_t)(vs[0] | (vs[1] << 8)));
-        const uint32_t sb = cvt_e4m3x2((uint16_t)(vs[2] | (vs[3] << 8)));
+          if (y == 1) {  // the codes are in registers: the stage may be refilled
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.empty[stg]));
+          }
+          const uint32_t sa = cvt_e4m3x2((uint16_t)(vs[0] | (vs[1] << 8)));
+          const uint32_t sb = cvt_e4m3x2((uint16_t)(vs[2] | (vs[3] << 8)));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {  // dims 2 i, 2 i + 1: a byte of each key
-          uint32_t x[4];
+          for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[k] = cvt_e2m1x2((uint16_t)(v[k][i / 4] >> (8 * (i % 4))));
-          mma_16816(o[2 * i], pf, hmul2_u32(__byte_perm(x[0], x[1], 0x5410), sa),
-                    hmul2_u32(__byte_perm(x[2], x[3], 0x5410), sb));
-          mma_16816(o[2 * i + 1], pf, hmul2_u32(__byte_perm(x[0], x[1], 0x7632), sa),
-                    hmul2_u32(__byte_perm(x[2], x[3], 0x7632), sb));
+            for (int h = 0; h < 2; ++h) {  // even and odd dims of 8
+              constexpr uint32_t LO = 0x0F0F0F0Fu;
+              const uint32_t a0 = h ? v[0][i] >> 4 : v[0][i], a1 = h ? v[1][i] : v[1][i] << 4;
+              const uint32_t b0 = h ? v[2][i] >> 4 : v[2][i], b1 = h ? v[3][i] : v[3][i] << 4;
+              uint32_t xa[4], xb[4];
+              cvt_e2m1x8((a0 & LO) | (a1 & ~LO), xa);
+              cvt_e2m1x8((b0 & LO) | (b1 & ~LO), xb);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_16816(o[8 * i + 2 * k + h], pf[y], hmul2_u32(xa[k], sa), hmul2_u32(xb[k], sb));
+            }
         }
       }
       page_it += n;
