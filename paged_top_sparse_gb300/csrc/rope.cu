@@ -155,23 +155,38 @@ struct Rotation {
   }
 };
 
-// A warp's rows [r0, r1) of one kind, kInFlight passes loaded ahead of their arithmetic.
-constexpr int kInFlight = 4;
-template <int D, typename Load, typename Body>
-__device__ __forceinline__ void walk_rows(int r0, int r1, int sub, Load load, Body body) {
-  constexpr int RPW = 256 / D;
-  for (int base = r0; base < r1; base += kInFlight * RPW) {
-    uint4 raw[kInFlight];
+// A warp's rows [r0, r1) of one kind, kInFlight passes at a time; the next ones are loaded before the
+// present ones' arithmetic, the first ones when the walk is made (ahead of the token's angles).
+constexpr int kInFlight = 2;
+template <int D, typename Load>
+struct RowWalk {
+  static constexpr int RPW = 256 / D;
+  Load load;
+  int r0, r1, sub;
+  uint4 raw[kInFlight];
+  __device__ __forceinline__ RowWalk(Load f, int b, int e, int s) : load(f), r0(b), r1(e), sub(s) {
+    fetch(r0, raw);
+  }
+  __device__ __forceinline__ void fetch(int base, uint4 (&x)[kInFlight]) const {
 #pragma unroll
     for (int k = 0; k < kInFlight; ++k) {
       const int row = base + k * RPW + sub;
-      raw[k] = row < r1 ? load(row) : make_uint4(0, 0, 0, 0);
+      x[k] = row < r1 ? load(row) : make_uint4(0, 0, 0, 0);
     }
-#pragma unroll
-    for (int k = 0; k < kInFlight; ++k)
-      if (base + k * RPW < r1) body(base + k * RPW + sub, raw[k]);
   }
-}
+  template <typename Body>
+  __device__ __forceinline__ void run(Body body) {
+    for (int base = r0; base < r1; base += kInFlight * RPW) {
+      uint4 next[kInFlight];
+      fetch(base + kInFlight * RPW, next);
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k)
+        if (base + k * RPW < r1) body(base + k * RPW + sub, raw[k]);
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) raw[k] = next[k];
+    }
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
   float a, b;
@@ -181,17 +196,16 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
   return r;
 }
 
-// The part of [first, first + rows) passes that warp part `part` of a token walks, as rows; `at`
-// counts the passes of the kinds before it.
+// The rows [r0, r1) of one kind that warp `part` of a token walks; `at` counts the passes of the
+// kinds before it.
 template <int D>
-__device__ __forceinline__ bool my_rows(int part, int per, int rows, int& at, int& r0, int& r1) {
+__device__ __forceinline__ void my_rows(int part, int per, int rows, int& at, int& r0, int& r1) {
   constexpr int RPW = 256 / D;
   const int passes = (rows + RPW - 1) / RPW;
   const int b = max(0, part * per - at), e = min(passes, (part + 1) * per - at);
   at += passes;
   r0 = b * RPW;
-  r1 = min(rows, e * RPW);
-  return b < e;
+  r1 = b < e ? min(rows, e * RPW) : r0;
 }
 
 // One warp: one token, some of its rows: the H query rows, then the G key rows.
@@ -208,46 +222,46 @@ qk_norm_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, QkRopeArgs a) 
   const int tok = (int)(w / a.splits), part = (int)(w % a.splits);
   if (tok >= p.T) return;
   const int sub = lane / (D / 8), chunk = lane % (D / 8);
+  int at = 0, q0, q1, k0, k1;
+  my_rows<D>(part, a.passes, p.H, at, q0, q1);
+  my_rows<D>(part, a.passes, a.k ? p.Hkv : 0, at, k0, k1);
+  const uint16_t* qsrc = a.q + tok * a.q_stride + chunk * 8;
+  const uint16_t* ksrc = a.k + tok * a.k_stride + chunk * 8;
+  auto qload = [&](int row) { return *reinterpret_cast<const uint4*>(qsrc + (int64_t)row * D); };
+  auto kload = [&](int row) { return *reinterpret_cast<const uint4*>(ksrc + (int64_t)row * D); };
+  RowWalk<D, decltype(qload)> qw(qload, q0, q1, sub);
   token_angles(r, p, tok, turns, cs[warp], lane);
-  int at = 0, r0, r1;
   Rotation<D, INTER> rt;
   uint64_t y[4];
-  if (my_rows<D>(part, a.passes, p.H, at, r0, r1)) {
+  if (q0 < q1) {
     rt.make(r, a.q_weight, cs[warp], lane);
-    const uint16_t* src = a.q + tok * a.q_stride + chunk * 8;
     uint8_t* dst = static_cast<uint8_t*>(a.q_out) +
                    (tok * a.q_out_stride + chunk * 8) * (E4M3OUT ? 1 : 2);
-    walk_rows<D>(
-        r0, r1, sub,
-        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
-        [&](int row, const uint4& raw) {
-          rt.apply(raw, a.q_weight != nullptr, a.eps, E4M3OUT ? a.q_scale_inv : 1.f, y);
-          if (row >= r1) return;
-          if (E4M3OUT) {
-            uint32_t o[2];
+    qw.run([&](int row, const uint4& raw) {
+      rt.apply(raw, a.q_weight != nullptr, a.eps, E4M3OUT ? a.q_scale_inv : 1.f, y);
+      if (row >= q1) return;
+      if (E4M3OUT) {
+        uint32_t o[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              o[h] = f32x2_to_e4m3x2(y[2 * h]) | (f32x2_to_e4m3x2(y[2 * h + 1]) << 16);
-            *reinterpret_cast<uint2*>(dst + (int64_t)row * D) = make_uint2(o[0], o[1]);
-          } else {
-            *reinterpret_cast<uint4*>(dst + (int64_t)row * D * 2) =
-                make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
-          }
-        });
+        for (int h = 0; h < 2; ++h)
+          o[h] = f32x2_to_e4m3x2(y[2 * h]) | (f32x2_to_e4m3x2(y[2 * h + 1]) << 16);
+        *reinterpret_cast<uint2*>(dst + (int64_t)row * D) = make_uint2(o[0], o[1]);
+      } else {
+        *reinterpret_cast<uint4*>(dst + (int64_t)row * D * 2) =
+            make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
+      }
+    });
   }
-  if (a.k && my_rows<D>(part, a.passes, p.Hkv, at, r0, r1)) {
+  if (k0 < k1) {
+    RowWalk<D, decltype(kload)> kw(kload, k0, k1, sub);
     rt.make(r, a.k_weight, cs[warp], lane);
-    const uint16_t* src = a.k + tok * a.k_stride + chunk * 8;
     uint16_t* dst = a.k_out + tok * a.k_out_stride + chunk * 8;
-    walk_rows<D>(
-        r0, r1, sub,
-        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
-        [&](int row, const uint4& raw) {
-          rt.apply(raw, a.k_weight != nullptr, a.eps, 1.f, y);
-          if (row < r1)
-            *reinterpret_cast<uint4*>(dst + (int64_t)row * D) =
-                make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
-        });
+    kw.run([&](int row, const uint4& raw) {
+      rt.apply(raw, a.k_weight != nullptr, a.eps, 1.f, y);
+      if (row < k1)
+        *reinterpret_cast<uint4*>(dst + (int64_t)row * D) =
+            make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
+    });
   }
 }
 
@@ -285,10 +299,16 @@ kv_append_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, KvRopeArgs a
   const int G = p.Hkv, sub = lane / (D / 8), chunk = lane % (D / 8);
   const int t = __ldg(p.tok_pos + tok), req = __ldg(p.tok_req + tok);
   const int phys = __ldg(a.page_table + (int64_t)req * p.max_pages + (t >> 7));
-  int at = 0, r0, r1;
-  const bool keys = my_rows<D>(part, a.passes, G, at, r0, r1);
+  int at = 0, k0, k1, v0, v1;
+  my_rows<D>(part, a.passes, G, at, k0, k1);
+  my_rows<D>(part, a.passes, G, at, v0, v1);
+  const uint16_t* ksrc = a.k + tok * a.k_stride + chunk * 8;
+  const uint16_t* vsrc = a.v + tok * a.v_stride + chunk * 8;
+  auto kload = [&](int row) { return *reinterpret_cast<const uint4*>(ksrc + (int64_t)row * D); };
+  auto vload = [&](int row) { return *reinterpret_cast<const uint4*>(vsrc + (int64_t)row * D); };
+  RowWalk<D, decltype(kload)> kw(kload, k0, k1, sub);
   Rotation<D, INTER> rt;
-  if (keys) {
+  if (k0 < k1) {
     token_angles(r, p, tok, turns, cs[warp], lane);
     rt.make(r, a.k_weight, cs[warp], lane);
   }
@@ -305,45 +325,34 @@ kv_append_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, KvRopeArgs a
     *reinterpret_cast<uint32_t*>(codes + slot * (D / 2) + chunk * 4) = packed;
     if (chunk % 2 == 0) scales[slot * (D / 16) + chunk / 2] = (uint8_t)scode;
   };
-  if (keys) {
-    const uint16_t* src = a.k + tok * a.k_stride + chunk * 8;
-    walk_rows<D>(
-        r0, r1, sub,
-        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
-        [&](int row, const uint4& raw) {
-          uint64_t y[4];
-          rt.apply(raw, a.k_weight != nullptr, a.eps, 1.f, y);
-          if (NVFP4) {
-            float f[8];
+  kw.run([&](int row, const uint4& raw) {
+    uint64_t y[4];
+    rt.apply(raw, a.k_weight != nullptr, a.eps, 1.f, y);
+    if (NVFP4) {
+      float f[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack_f32x2(y[i], f[2 * i], f[2 * i + 1]);
-            quantised(row, f, a.kc, a.ks, row < r1);
-          } else if (row < r1) {
-            *reinterpret_cast<uint4*>(a.kc + ((slot0 + 128 * row) * D + chunk * 8) * 2) =
-                make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
-          }
-        });
-  }
-  if (my_rows<D>(part, a.passes, G, at, r0, r1)) {  // value rows as they are
-    const uint16_t* src = a.v + tok * a.v_stride + chunk * 8;
-    walk_rows<D>(
-        r0, r1, sub,
-        [&](int row) { return *reinterpret_cast<const uint4*>(src + (int64_t)row * D); },
-        [&](int row, const uint4& raw) {
-          if (NVFP4) {
-            const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-            float f[8];
+      for (int i = 0; i < 4; ++i) unpack_f32x2(y[i], f[2 * i], f[2 * i + 1]);
+      quantised(row, f, a.kc, a.ks, row < k1);
+    } else if (row < k1) {
+      *reinterpret_cast<uint4*>(a.kc + ((slot0 + 128 * row) * D + chunk * 8) * 2) =
+          make_uint4(pack_bf16(y[0]), pack_bf16(y[1]), pack_bf16(y[2]), pack_bf16(y[3]));
+    }
+  });
+  RowWalk<D, decltype(vload)> vw(vload, v0, v1, sub);
+  vw.run([&](int row, const uint4& raw) {  // value rows as they are
+    if (NVFP4) {
+      const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+      float f[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f[2 * i] = bf16_lo(x[i]);
-              f[2 * i + 1] = bf16_hi(x[i]);
-            }
-            quantised(row, f, a.vc, a.vs, row < r1);
-          } else if (row < r1) {
-            *reinterpret_cast<uint4*>(a.vc + ((slot0 + 128 * row) * D + chunk * 8) * 2) = raw;
-          }
-        });
-  }
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(x[i]);
+        f[2 * i + 1] = bf16_hi(x[i]);
+      }
+      quantised(row, f, a.vc, a.vs, row < v1);
+    } else if (row < v1) {
+      *reinterpret_cast<uint4*>(a.vc + ((slot0 + 128 * row) * D + chunk * 8) * 2) = raw;
+    }
+  });
 }
 
 // Passes a warp walks: all of a token's where that gives every SM 24 warps, else fewer, so that a
