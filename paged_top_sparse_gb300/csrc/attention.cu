@@ -784,21 +784,6 @@ __device__ __forceinline__ void merge_store(const DevPlan& p, const AttArgs& a, 
   else
     *reinterpret_cast<uint32_t*>(out) = pack_p<false>(acc[0] * inv, acc[1] * inv);
 }
-template <int D>
-__device__ __forceinline__ void merge_add(float (&acc)[D / 32], float wt, const float* o) {
-  if (D == 128) {
-    const float4 x = *reinterpret_cast<const float4*>(o);
-    acc[0] += wt * x.x;
-    acc[1] += wt * x.y;
-    acc[D / 32 - 2] += wt * x.z;
-    acc[D / 32 - 1] += wt * x.w;
-  } else {
-    const float2 x = *reinterpret_cast<const float2*>(o);
-    acc[0] += wt * x.x;
-    acc[1] += wt * x.y;
-  }
-}
-
 // Tiles of many rows (few pieces each): a warp takes 8 rows, a lane the weight of one of four
 // pieces of one of them, so that a warp has up to 32 rows of partial results on the way.
 constexpr int kMergeRows = 8;
@@ -822,23 +807,50 @@ attention_merge_rows_kernel(DevPlan p, AttArgs a) {
                ? a.part_lse[piece_slot(mg, i) * p.att_slot_rows + lr0 + k]
                : -INFINITY;
   };
-  float mx = -INFINITY;
-  for (int c = 0; c < np; c += 4) mx = fmaxf(mx, lse_of(c + ii));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-  float sum = 0.f, acc[kMergeRows][D / 32] = {};
-  for (int c = 0; c < np; c += 4) {
-    const float l = lse_of(c + ii), wt = l == -INFINITY ? 0.f : __expf(l - mx);
-    sum += wt;
+  // rows of a group of pieces that are on the way together
+  constexpr int E = D / 32, kGroup = 2;
+  float x[kGroup][kMergeRows][E];
+  auto fetch = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (c + j >= np) break;
-      const float* o = a.part + (piece_slot(mg, c + j) * p.att_slot_rows + lr0) * D + lane * (D / 32);
+    for (int j = 0; j < kGroup; ++j)
 #pragma unroll
       for (int r = 0; r < kMergeRows; ++r) {
-        const float w = __shfl_sync(0xffffffffu, wt, j * kMergeRows + r);
-        if (w != 0.f) merge_add<D>(acc[r], w, o + r * D);
+        const float* src =
+            a.part + (piece_slot(mg, i0 + j) * p.att_slot_rows + lr0 + r) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[j][r][e] = 0.f;
+        if (i0 + j < np && (live >> r & 1)) {
+          if (E == 4) *reinterpret_cast<float4*>(x[j][r]) = *reinterpret_cast<const float4*>(src);
+          else *reinterpret_cast<float2*>(x[j][r]) = *reinterpret_cast<const float2*>(src);
+        }
       }
+  };
+  float l[4], mx = -INFINITY;  // the first 16 pieces' statistics, and their rows, at once
+#pragma unroll
+  for (int c = 0; c < 4; ++c) l[c] = lse_of(4 * c + ii);
+  fetch(0);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) mx = fmaxf(mx, l[c]);
+  for (int c = 16; c < np; c += 4) mx = fmaxf(mx, lse_of(c + ii));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+  float sum = 0.f, acc[kMergeRows][E] = {};
+  for (int c = 0; c < np; c += 4) {
+    const float lc = c == 0 ? l[0] : c == 4 ? l[1] : c == 8 ? l[2] : c == 12 ? l[3] : lse_of(c + ii);
+    const float wt = lc == -INFINITY ? 0.f : __expf(lc - mx);
+    sum += wt;
+#pragma unroll
+    for (int j0 = 0; j0 < 4; j0 += kGroup) {
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+        for (int r = 0; r < kMergeRows; ++r) {
+          const float w = __shfl_sync(0xffffffffu, wt, (j0 + j) * kMergeRows + r);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (w != 0.f) acc[r][e] += w * x[j][r][e];
+        }
+      if (c + j0 + kGroup < np) fetch(c + j0 + kGroup);
     }
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 8);

@@ -313,7 +313,7 @@ AttSplit split_attention(const sps_plan* pl, const std::vector<int32_t>& tile_pa
   int64_t pieces = 0;
   for (const AttMerge& m : out.merges) pieces += m.cta1 - m.cta0 + 1;
   out.estimate = (double)longest;
-  if (pieces) out.estimate += few_rows ? 6 + 0.01 * pieces : 4 + 0.045 * pieces;
+  if (pieces) out.estimate += few_rows ? 6 + 0.01 * pieces : 2.5 + 0.05 * pieces;
   return out;
 }
 
