@@ -454,24 +454,78 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               pk[e / 2] = pack_p<QUANT>(x, y);
             }
           };
-          bool done = false;
-          if (j > 0 && !masked) {
-            // the usual page: the reference maximum holds, so the first half's exponentials run
-            // under the second half's load, and its products under the second half's exponentials
+          // The usual page (`fast`): the reference maximum holds, so the first half's exponentials
+          // run under the second half's load.  The first page, a masked one, or one whose maximum
+          // asks for a rescale loads the whole row first.  (One copy of each part: code that a
+          // block runs once is fetched at a memory latency.)
+          bool fast = j > 0 && !masked;
+          uint32_t pk[32];
+          for (;;) {
+            if (fast) {
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
-            tmem_ld_wait();
+              for (int cc = 0; cc < 2; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+              tmem_ld_wait();
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              reg_fence(v[cc]);
-              reg_fence1(red[cc]);
+              for (int cc = 0; cc < 2; ++cc) {
+                reg_fence(v[cc]);
+                reg_fence1(red[cc]);
+              }
+#pragma unroll
+              for (int cc = 2; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+            } else {
+              for (bool again = true; again;) {
+                again = false;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                  reg_fence(v[cc]);
+                  reg_fence1(red[cc]);
+                }
+                float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+                if (masked) {
+                  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                  for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                      if (cc * 32 + i >= nvis) v[cc][i] = 0xff800000u;  // -inf
+                      mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(v[cc][i]));
+                    }
+                  mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                }
+                const bool need = j > 0 && (mb - m) * c > kRescale;
+                if (j == 0) {
+                  m = mb == -INFINITY ? 0.f : mb;  // a row that sees nothing here keeps p = 0
+                } else if (__any_sync(0xffffffffu, need)) {
+                  const float f = need ? fast_exp2((m - mb) * c) : 1.f;
+                  if (need) m = mb;
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float x, y;
+                    unpack_f32x2(lsum[h], x, y);
+                    lsum[h] = pack_f32x2(x * f, y * f);
+                  }
+#pragma unroll 1
+                  for (int cc = 0; cc < D / 32; ++cc) {
+                    tmem_ld32(obase + cc * 32, v[0]);
+                    tmem_ld_wait();
+                    reg_fence(v[0]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                      v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
+                    tmem_st32(obase + cc * 32, v[0]);
+                  }
+                  tmem_st_wait();
+                  again = true;
+                }
+              }
             }
-#pragma unroll
-            for (int cc = 2; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
             const uint64_t keep0 = lsum[0], keep1 = lsum[1];
-            uint32_t pk[32];
             exps(0, pk);
             exps(1, pk + 16);
+            if (!fast) break;
             tmem_ld_wait();
 #pragma unroll
             for (int cc = 2; cc < 4; ++cc) {
@@ -479,84 +533,22 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               reg_fence1(red[cc]);
             }
             const float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-            if (!__any_sync(0xffffffffu, (mb - m) * c > kRescale)) {
-              tmem_st32(sbase, pk);
-              uint32_t pk2[32];
-              exps(2, pk2);  // under the store
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar_half);
-              half_sent = done = true;
-              exps(3, pk2 + 16);
-              tmem_st32(sbase + 32, pk2);
-              tmem_st_wait();
-            } else {
-              lsum[0] = keep0;
-              lsum[1] = keep1;
-            }
+            if (!__any_sync(0xffffffffu, (mb - m) * c > kRescale)) break;
+            lsum[0] = keep0;
+            lsum[1] = keep1;
+            fast = false;
           }
-          if (!done) {
-            float mb;
-            auto load = [&]() {
-#pragma unroll
-              for (int cc = 0; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
-              tmem_ld_wait();
-#pragma unroll
-              for (int cc = 0; cc < 4; ++cc) {
-                reg_fence(v[cc]);
-                reg_fence1(red[cc]);
-              }
-              mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-              if (masked) {
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc)
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    if (cc * 32 + i >= nvis) v[cc][i] = 0xff800000u;  // -inf
-                    mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(v[cc][i]));
-                  }
-                mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-              }
-            };
-            load();
-            if (j == 0) {
-              m = mb == -INFINITY ? 0.f : mb;  // a row that sees nothing here keeps p = 0
-            } else {
-              const bool need = (mb - m) * c > kRescale;
-              if (__any_sync(0xffffffffu, need)) {
-                const float f = need ? fast_exp2((m - mb) * c) : 1.f;
-                if (need) m = mb;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float x, y;
-                  unpack_f32x2(lsum[h], x, y);
-                  lsum[h] = pack_f32x2(x * f, y * f);
-                }
-#pragma unroll
-                for (int cc = 0; cc < D / 32; ++cc) {
-                  tmem_ld32(obase + cc * 32, v[0]);
-                  tmem_ld_wait();
-                  reg_fence(v[0]);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
-                  tmem_st32(obase + cc * 32, v[0]);
-                }
-                tmem_st_wait();
-                load();
-              }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t pk[32];
-              exps(2 * h, pk);
-              exps(2 * h + 1, pk + 16);
-              tmem_st32(sbase + h * 32, pk);
-            }
-            tmem_st_wait();
-          }
+          tmem_st32(sbase, pk);
+          uint32_t pk2[32];
+          exps(2, pk2);  // under the store
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_half);  // the products of the first 64 keys may begin
+          half_sent = true;
+          exps(3, pk2 + 16);
+          tmem_st32(sbase + 32, pk2);
+          tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
@@ -631,7 +623,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
           __syncwarp();
         };
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t v[32];
           tmem_ld32(obase + cc * 32, v);
