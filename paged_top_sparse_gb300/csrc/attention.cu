@@ -15,7 +15,7 @@
 // is two of them (256 rows), fed by the same K and V tiles.
 //
 // Work.  The (tile, page) pairs of the batch in order (request, head block, tile, page) are cut into
-// equal runs, one per SM (att_starts, made with the plan): prompts, chunks, and a single token after
+// equal runs, one per SM (made with the plan): prompts, chunks, and a single token after
 // a long context all fill the GPU, and a tile cut by a run's end is merged from the partial results
 // of its pieces by a second small kernel.
 //
@@ -149,8 +149,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   pdl_wait();
   const uint32_t tmem = sm.tmem_base;  // S0 S1 at columns 0, 128; O0 O1 at 256, 384
   volatile int* abort_flag = &sm.abort_flag;
-  AttCursor cur = p.att_starts[blockIdx.x];
-  const AttCursor end = p.att_starts[blockIdx.x + 1];
+  PieceList work(p);
   Piece pc;
 
   if (warp < 4) {
@@ -160,7 +159,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // ------------------------------------------------ copies
       uint32_t it = 0, qc0 = 0, qc1 = 0;
       bool ok = true;
-      while (ok && next_piece(p, rp, cur, end, pc)) {
+      while (ok && work.next(p, rp, pc)) {
         const int g = pc.vg / rp.blocks, h0 = g * p.Hg + (pc.vg % rp.blocks) * 128;
         // K runs a page ahead of V: K_0, K_1, V_0, K_2, V_1, ...
         const int n = pc.page1 - pc.page0;
@@ -309,7 +308,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (leader) mma_commit(smem_u32(&sm.pv_done[t][pvc[t] & 1]));
         ++pvc[t];
       };
-      while (ok && next_piece(p, rp, cur, end, pc)) {
+      while (ok && work.next(p, rp, pc)) {
         const int n = pc.page1 - pc.page0;
         // rows of the last page behind the request's last token
         const bool tail = !QUANT && pc.page1 * 128 > pc.ctx + pc.q_len;
@@ -382,7 +381,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     } else if (warp == 2 && !QUANT) {
       // ------------------------------------------------ zero V rows of the request's unwritten slots
       uint32_t it = 0, tc = 0;
-      while (next_piece(p, rp, cur, end, pc)) {
+      while (work.next(p, rp, pc)) {
         const int n = pc.page1 - pc.page0, kv_len = pc.ctx + pc.q_len;
         if (pc.page1 * 128 > kv_len) {
           if (!mbar_wait(smem_u32(&sm.tail_go), tc & 1, abort_flag, status)) break;
@@ -413,7 +412,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     auto pv_wait = [&](uint32_t i) {  // product i into O_w is complete
       return mbar_wait(smem_u32(&sm.pv_done[w][i & 1]), (i >> 1) & 1, abort_flag, status);
     };
-    while (ok && next_piece(p, rp, cur, end, pc)) {
+    while (ok && work.next(p, rp, pc)) {
       // with one row tile, this warpgroup takes the pages of its parity
       const bool split = SINGLE || pc.nt == 1;
       const int np = pc.page1 - pc.page0, n = split ? (np + 1 - w) / 2 : np;
@@ -685,7 +684,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int ct = tid - 384;
     uint32_t it = 0, qc0 = 0, qc1 = 0;
     bool ok = QUANT;
-    while (ok && next_piece(p, rp, cur, end, pc)) {
+    while (ok && work.next(p, rp, pc)) {
       const int h0 = (pc.vg % rp.blocks) * 128;
       const int n = pc.page1 - pc.page0;
       for (int i = 0; i < 2 * n; ++i, ++it) {  // K_0, K_1, V_0, K_2, V_1, ...

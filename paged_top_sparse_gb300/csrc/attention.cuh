@@ -29,50 +29,39 @@ struct Piece {
   int nt;                   // row tiles with rows
 };
 
-// The piece at cursor c of a block whose run ends at e; advances c.  False at the end.  The cursor
-// carries its request's numbers, so that a run's first piece needs no further read.
-__device__ __forceinline__ bool next_piece(const DevPlan& p, const RowPack& rp, AttCursor& c,
-                                           const AttCursor& e, Piece& pc) {
-  const int tt = 2 * rp.TB, nv = p.Hkv * rp.blocks;
-  for (;;) {
-    if (c.req >= p.batch) return false;
-    if (c.req == e.req && c.vg == e.vg && c.tile == e.tile && c.page == e.page) return false;
-    if (c.q_len > 0) {
-      const bool last = c.req == e.req && c.vg == e.vg && c.tile == e.tile;
-      pc.req = c.req;
-      pc.vg = c.vg;
-      pc.q_len = c.q_len;
-      pc.ctx = c.ctx;
-      pc.flat0 = c.flat0;
-      pc.tok0 = c.tile * tt;
-      pc.ntok = min(tt, c.q_len - pc.tok0);
-      pc.pages = ((pc.ctx + pc.tok0 + pc.ntok - 1) >> 7) + 1;
-      pc.page0 = c.page;
-      pc.page1 = last ? min(e.page, pc.pages) : pc.pages;
-      pc.nt = pc.ntok > rp.TB ? 2 : 1;
-      if (last) {
-        c = e;
-        return pc.page0 < pc.page1;
-      }
-      c.page = 0;
-      if ((c.tile + 1) * tt < c.q_len) {
-        ++c.tile;
-        return true;
-      }
-      c.tile = 0;
-      if (++c.vg < nv) return true;
-      c.vg = 0;
-    }
-    const bool done = c.q_len > 0;  // a piece was found above
-    if (++c.req < p.batch) {
-      const ReqInfo* ri = p.reqs + c.req;
-      c.q_len = __ldg(&ri->q_len);
-      c.ctx = __ldg(&ri->ctx);
-      c.flat0 = __ldg(&ri->tok0);
-    }
-    if (done) return true;
+// A block's pieces in turn.  The next one is read ahead.
+struct PieceList {
+  int left, at;
+  int4 a, b;  // the next piece
+  __device__ __forceinline__ explicit PieceList(const DevPlan& p) {
+    const int4* h = reinterpret_cast<const int4*>(p.att_heads + blockIdx.x);
+    a = h[0];
+    b = h[1];
+    const int4 c = h[2];
+    left = c.x;
+    at = c.y;
   }
-}
+  __device__ __forceinline__ bool next(const DevPlan& p, const RowPack& rp, Piece& pc) {
+    if (left <= 0) return false;
+    pc.req = a.x;
+    pc.vg = a.y;
+    pc.q_len = b.y;
+    pc.ctx = b.z;
+    pc.flat0 = b.w;
+    pc.tok0 = a.z * 2 * rp.TB;
+    pc.ntok = min(2 * rp.TB, pc.q_len - pc.tok0);
+    pc.pages = ((pc.ctx + pc.tok0 + pc.ntok - 1) >> 7) + 1;
+    pc.page0 = a.w;
+    pc.page1 = b.x;
+    pc.nt = pc.ntok > rp.TB ? 2 : 1;
+    if (--left > 0) {
+      const int4* x = reinterpret_cast<const int4*>(p.att_pieces + at++);
+      a = __ldg(x);
+      b = __ldg(x + 1);
+    }
+    return true;
+  }
+};
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float a, float b) {

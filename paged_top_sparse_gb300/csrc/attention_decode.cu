@@ -89,8 +89,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
   __syncthreads();
   pdl_wait();  // from here on: what earlier kernels wrote
   const RowPack rp(p.Hg);
-  AttCursor cur = p.att_starts[blockIdx.x];
-  const AttCursor end = p.att_starts[blockIdx.x + 1];
+  PieceList work(p);
   Piece pc;
   uint32_t st = 0, ph = 0;  // ring stage and phase
   auto advance = [&]() {
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
   if (warp == kMmaWarps) {
     // ------------------------------------------------ copies
     bool ok = true;
-    while (ok && next_piece(p, rp, cur, end, pc)) {
+    while (ok && work.next(p, rp, pc)) {
       const int n = pc.page1 - pc.page0;
       const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
       auto load_ids = [&](int first) {  // physical tiles of the lanes' pages first + lane
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       if (lane == 0) mbar_arrive(smem_u32(&sm.meet));
       return mbar_wait(smem_u32(&sm.meet), met++ & 1, abort_flag, status);
     };
-    while (ok && next_piece(p, rp, cur, end, pc)) {
+    while (ok && work.next(p, rp, pc)) {
       const int n = pc.page1 - pc.page0, kv_len = pc.ctx + pc.q_len;
       int pos[2];  // of rows g and g + 8
 #pragma unroll

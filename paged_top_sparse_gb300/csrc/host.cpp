@@ -140,11 +140,13 @@ struct sps_plan {
   int64_t fwd_ws_bytes = 0;  // the part the forward uses (the no-allocation forward's need)
   int32_t topk_nseg = 1, topk_segg = 0;
   int32_t fwd_prefetch = 0;
-  // full attention (attention.cu): where each block begins, the tiles cut over blocks
-  std::vector<AttCursor> att_starts;
+  // full attention (attention.cu): the blocks' work, the tiles cut over blocks
+  std::vector<AttHead> att_heads;
+  std::vector<AttPiece> att_pieces;
   std::vector<AttMerge> att_merges;
   int32_t att_ctas = 0, att_slot_rows = 0, att_num_merges = 0, att_merge_cap = 0;
-  int64_t off_att_starts = 0, off_att_merges = 0;
+  int64_t off_att_heads = 0, off_att_pieces = 0, off_att_merges = 0;
+  int64_t att_tiles = 0;
   int64_t upload_bytes = 0;  // [0, upload_bytes) of the workspace comes from `blob`
   std::vector<uint8_t> blob;
 };
@@ -245,107 +247,216 @@ void build_indexer_tasks(sps_plan* pl) {
   }
 }
 
-// Work split of the full attention: the (tile, page) pairs of the batch in order (request, head
-// block, tile, page), a tile being two row tiles of 128 / HB tokens x HB heads of a KV head's
-// group, cut into runs of about equal cost, one per SM.
+// Work split of the full attention: tiles (two row tiles of 128 / HB tokens x HB heads of a KV head's
+// group, over the pages their last token sees) and pieces of tiles, listed for one block per SM.
 //
-// Costs are in pages (about 1.5 us): a tile's pages plus kAttTileCost for its fill, drain and
-// epilogue.  A cut inside a tile adds a piece, whose partial rows are written and merged by a
-// second kernel; so a cut at most `snap` pages from a tile's border moves onto the nearer one, and
-// the split is made for several `snap`, the one with the smallest estimate kept.  (Measured on
-// H 32 / H_kv 8, D 128: 32 single tokens after 1K cost 42 us with snap 5 and 49 with 1, a
-// 512-token prompt 15 and 20; one token after 8K, where every cut counts, 17 and 14.)
-constexpr int kAttTileCost = 2;
+// Costs are in pages (about 1.5 us): a piece's pages plus kAttTileCost for its fill, drain and
+// epilogue.  A cut tile's partial rows are written and merged by a second kernel, which is estimated
+// too; of the splits made, the one with the smallest estimate is kept.
+constexpr int kAttTileCost = 2, kAttMinPiece = 3;
 
-struct AttSplit {
-  std::vector<AttCursor> starts;
-  std::vector<AttMerge> merges;
-  double estimate = 0;
+struct AttTile {
+  int32_t req, vg, tile, pages;
+};
+struct AttRun {  // pages [page0, page1) of a tile, on block cta
+  int32_t cta, tile, page0, page1;
 };
 
-AttSplit split_attention(const sps_plan* pl, const std::vector<int32_t>& tile_pages, int64_t total,
-                         int nv, int tt, int ctas, int snap, bool few_rows) {
-  AttSplit out;
-  const int64_t cuts = std::min<int64_t>(ctas, total);
-  int64_t at = 0, cut = 0;  // cost before the present tile; cuts placed
-  int64_t run_cost = 0, longest = 0;
-  bool pending = false;  // a cut moved onto the next tile's start
-  size_t k = 0;
-  for (int b = 0; b < pl->pb.batch; ++b) {
-    const ReqInfo& ri = pl->reqs[b];
-    const int tiles = (ri.q_len + tt - 1) / tt;
-    for (int v = 0; v < nv; ++v)
-      for (int t = 0; t < tiles; ++t) {
-        const int n = tile_pages[k + t];
-        int first = -1, last_page = 0;  // first run that begins inside the tile, last piece's page
-        bool begun = false;             // a run begins at the tile's start
-        auto begin = [&](int page) {
-          if (page == 0 ? begun : page <= last_page) return;
-          if (page == 0) {
-            begun = true;
-          } else {
-            if (first < 0) first = (int)out.starts.size();
-            run_cost += page - last_page + kAttTileCost;
-          }
-          longest = std::max(longest, run_cost);
-          run_cost = 0;
-          out.starts.push_back(AttCursor{b, v, t, page, ri.q_len, ri.ctx, ri.tok0, 0});
-          last_page = page;
-        };
-        if (pending) begin(0);
-        pending = false;
-        for (; cut < cuts && cut * total / cuts < at + n + kAttTileCost; ++cut) {
-          const int page = std::max(0, (int)(cut * total / cuts - at) - kAttTileCost);
-          const bool front = page <= n - page;
-          if (page == 0 || (front && page <= snap)) begin(0);
-          else if (!front && n - page <= snap) pending = true;
-          else begin(page);
-        }
-        run_cost += n - last_page + kAttTileCost;
-        if (first > 0)
-          out.merges.push_back(AttMerge{b, v, t, first - 1, (int)out.starts.size() - 1, ri.q_len,
-                                        ri.tok0, 0});
-        at += n + kAttTileCost;
-      }
-    k += tiles;
+// What a split costs (its longest block, its cut tiles' pieces), and its runs where they are wanted.
+struct AttSplit {
+  int64_t longest = 0, cost = 0, pieces = 0;
+  int cta = -1;
+  std::vector<AttRun>* keep = nullptr;
+  void block() {
+    longest = std::max(longest, cost);
+    cost = 0;
+    ++cta;
   }
-  longest = std::max(longest, run_cost);
-  int64_t pieces = 0;
-  for (const AttMerge& m : out.merges) pieces += m.cta1 - m.cta0 + 1;
-  out.estimate = (double)longest;
-  if (pieces) out.estimate += few_rows ? 6 + 0.01 * pieces : 2.5 + 0.05 * pieces;
-  return out;
+  void run(int tile, int page0, int page1) {
+    cost += page1 - page0 + kAttTileCost;
+    if (keep) keep->push_back(AttRun{cta, tile, page0, page1});
+  }
+  double estimate(bool few_rows) const {
+    const double merge = few_rows ? 6 + 0.01 * pieces : 2.5 + 0.05 * pieces;
+    return (double)std::max(longest, cost) + (pieces ? merge : 0);
+  }
+};
+
+// The (tile, page) pairs in order, cut into runs of equal cost.  A cut at most `snap` pages from a
+// tile's border moves onto the nearer one.  (Measured on H 32 / H_kv 8, D 128: 32 single tokens after
+// 1K cost 42 us with snap 5 and 49 with 1, a 512-token prompt 15 and 20; one token after 8K, where
+// every cut counts, 17 and 14.)
+void split_runs(const std::vector<AttTile>& tiles, int64_t total, int ctas, int snap, AttSplit& out) {
+  const int64_t cuts = std::min<int64_t>(ctas, total);
+  int64_t at = 0, cut = 0, bound = 0;  // cost before the tile; cuts placed; where the next one lies
+  bool pending = true, empty = false;  // a block begins at the next tile; the present one has no work
+  for (size_t k = 0; k < tiles.size(); ++k) {
+    const int n = tiles[k].pages;
+    int page = 0;
+    auto begin = [&](int to) {  // a block begins at page `to`
+      if (to > page) {
+        out.run((int)k, page, to);
+        ++out.pieces;
+        page = to;
+        out.block();
+      } else if (to == 0 && page == 0 && !empty) {
+        out.block();
+        empty = true;
+      }
+    };
+    if (pending) begin(0);
+    pending = false;
+    for (; cut < cuts && bound < at + n + kAttTileCost; bound = ++cut * total / cuts) {
+      const int to = std::max(0, (int)(bound - at) - kAttTileCost);
+      const bool front = to <= n - to;
+      if (to == 0 || (front && to <= snap)) begin(0);
+      else if (!front && n - to <= snap) pending = true;
+      else begin(to);
+    }
+    out.run((int)k, page, n);
+    out.pieces += page > 0;
+    empty = false;
+    at += n + kAttTileCost;
+  }
 }
 
-void build_attention_runs(sps_plan* pl) {
+// Whole tiles, the largest first, each to the block with the least work as long as that stays within
+// an equal share; the tiles left over are cut to fill the blocks up.  Blocks that work at the same
+// time then read the same keys: 8 x 512 tokens after 32K reads 270 MB of keys and values that
+// consecutive runs, each block at another place, would stream past the L2 again and again.
+// (Loads only grow, so the least loaded block is found by walking a list of blocks per load.)
+bool split_shares(const std::vector<AttTile>& tiles, int64_t share, int ctas,
+                  const std::vector<int32_t>& order, AttSplit& out) {
+  std::vector<int32_t> at_load(share + 1, -1), peer(ctas);  // blocks of a load, linked
+  std::vector<int32_t> first(ctas, -1), last(ctas, -1), next(tiles.size(), -1);  // a block's tiles
+  for (int i = ctas - 1; i >= 0; --i) {
+    peer[i] = at_load[0];
+    at_load[0] = i;
+  }
+  std::vector<int32_t> rest;
+  int64_t low = 0;
+  for (int32_t k : order) {
+    while (at_load[low] < 0) ++low;
+    const int64_t load = low + tiles[k].pages + kAttTileCost;
+    if (load > share) {
+      rest.push_back(k);
+      continue;
+    }
+    const int32_t c = at_load[low];
+    at_load[low] = peer[c];
+    peer[c] = at_load[load];
+    at_load[load] = c;
+    (first[c] < 0 ? first[c] : next[last[c]]) = k;
+    last[c] = k;
+  }
+  size_t j = 0;
+  int page = 0;
+  for (; low <= share; ++low)  // the blocks with the most room first
+    for (int32_t c = at_load[low]; c >= 0; c = peer[c]) {
+      out.block();
+      for (int32_t k = first[c]; k >= 0; k = next[k]) out.run(k, 0, tiles[k].pages);
+      int64_t room = share - low;
+      while (j < rest.size() && room >= kAttTileCost + kAttMinPiece) {
+        const int n = tiles[rest[j]].pages;
+        int to = (int)std::min<int64_t>(n, page + room - kAttTileCost);
+        if (n - to < kAttMinPiece) to = n;
+        out.run(rest[j], page, to);
+        out.pieces += page > 0 || to < n;
+        room -= to - page + kAttTileCost;
+        page = to;
+        if (to < n) break;
+        ++j;
+        page = 0;
+      }
+    }
+  return j == rest.size();
+}
+
+void build_attention_work(sps_plan* pl) {
   const sps_problem& p = pl->pb;
   const int hg = p.num_q_heads / p.num_kv_heads, HB = std::min(hg, 128), TB = 128 / HB;
   const int nv = p.num_kv_heads * ((hg + HB - 1) / HB), tt = 2 * TB;
-  std::vector<int32_t> tile_pages;  // of one head block, request by request
+  std::vector<AttTile> tiles;
   int64_t total = 0;
-  int max_q = 0;
-  for (const ReqInfo& ri : pl->reqs) {
-    for (int t = 0; t * tt < ri.q_len; ++t) {
-      tile_pages.push_back((ri.ctx + std::min((t + 1) * tt, ri.q_len) - 1) / kPage + 1);
-      total += (int64_t)(tile_pages.back() + kAttTileCost) * nv;
-    }
+  int max_q = 0, max_pages = 0;
+  for (int b = 0; b < p.batch; ++b) {
+    const ReqInfo& ri = pl->reqs[b];
+    for (int v = 0; v < nv; ++v)
+      for (int t = 0; t * tt < ri.q_len; ++t) {
+        const int n = (ri.ctx + std::min((t + 1) * tt, ri.q_len) - 1) / kPage + 1;
+        tiles.push_back(AttTile{b, v, t, n});
+        total += n + kAttTileCost;
+        max_pages = std::max(max_pages, n);
+      }
     max_q = std::max(max_q, ri.q_len);
   }
   const int ctas = std::min(std::max(1, num_sms()), 256);
   pl->att_ctas = ctas;
+  pl->att_tiles = (int64_t)tiles.size();
   pl->att_slot_rows = max_q > TB ? 256 : max_q * HB;
-  pl->att_merge_cap = (int32_t)std::min<int64_t>(ctas - 1, (int64_t)tile_pages.size() * nv);
-  AttSplit best;
-  for (int snap : {1, 2, 4, 8, 1 << 20}) {
-    AttSplit x = split_attention(pl, tile_pages, total, nv, tt, ctas, snap,
-                                 pl->att_slot_rows <= 32);
-    if (best.starts.empty() || x.estimate < best.estimate) best = std::move(x);
+  pl->att_merge_cap = (int32_t)std::min<int64_t>(ctas - 1, pl->att_tiles);
+
+  // the splits' estimates: runs by snap, or shares of a size at which the left-over tiles fit
+  const bool few_rows = pl->att_slot_rows <= 32;
+  double best = 0;
+  int snap = 1;
+  int64_t share = 0;
+  for (int s : {1, 2, 4, 8, 1 << 20}) {
+    AttSplit x;
+    split_runs(tiles, total, ctas, s, x);
+    if (s == 1 || x.estimate(few_rows) < best) {
+      best = x.estimate(few_rows);
+      snap = s;
+    }
+    if (pl->att_tiles >= 8 * ctas) break;
   }
-  pl->att_num_merges = (int32_t)best.merges.size();
-  best.starts.resize(ctas + 1, AttCursor{p.batch, 0, 0, 0, 0, 0, 0, 0});
-  best.merges.resize(ctas, AttMerge{-1, 0, 0, 0, 0, 0, 0, 0});
-  pl->att_starts.swap(best.starts);
-  pl->att_merges.swap(best.merges);
+  std::vector<int32_t> order;
+  if (pl->att_tiles > ctas) {
+    std::vector<int32_t> first(max_pages + 2, 0);  // tiles by falling pages, in order
+    for (const AttTile& t : tiles) ++first[max_pages - t.pages + 1];
+    for (int i = 0; i <= max_pages; ++i) first[i + 1] += first[i];
+    order.resize(tiles.size());
+    for (size_t k = 0; k < tiles.size(); ++k) order[first[max_pages - tiles[k].pages]++] = (int32_t)k;
+    for (int64_t x = (total + ctas - 1) / ctas + kAttTileCost; (double)x < best && x < 1 << 20;
+         x += std::max<int64_t>(1, x / 64)) {
+      AttSplit out;
+      if (!split_shares(tiles, x, ctas, order, out)) continue;
+      if (out.estimate(few_rows) < best) share = x;
+      break;
+    }
+  }
+
+  std::vector<AttRun> work;
+  work.reserve(tiles.size() + 2 * ctas);
+  AttSplit out;
+  out.keep = &work;
+  if (share) split_shares(tiles, share, ctas, order, out);
+  else split_runs(tiles, total, ctas, snap, out);
+  auto piece = [&](const AttRun& r) {
+    const AttTile& t = tiles[r.tile];
+    const ReqInfo& ri = pl->reqs[t.req];
+    return AttPiece{t.req, t.vg, t.tile, r.page0, r.page1, ri.q_len, ri.ctx, ri.tok0};
+  };
+  pl->att_heads.assign(ctas, AttHead{});
+  pl->att_merges.assign(ctas, AttMerge{-1, 0, 0, 0, 0, 0, 0, 0});
+  pl->att_pieces.reserve(work.size());
+  int merges = 0;
+  for (const AttRun& r : work) {  // (a block's runs are neighbours; so are a cut tile's)
+    AttHead& h = pl->att_heads[r.cta];
+    if (h.count++ == 0) {
+      h.first = piece(r);
+      h.next = (int32_t)pl->att_pieces.size();
+    } else {
+      pl->att_pieces.push_back(piece(r));
+    }
+    const AttTile& t = tiles[r.tile];
+    if (r.page0 == 0 && r.page1 < t.pages)
+      pl->att_merges[merges++] = AttMerge{t.req, t.vg, t.tile, r.cta, r.cta,
+                                          pl->reqs[t.req].q_len, pl->reqs[t.req].tok0, 0};
+    else if (r.page0 > 0)
+      pl->att_merges[merges - 1].cta1 = r.cta;
+  }
+  pl->att_num_merges = merges;
 }
 
 }  // namespace
@@ -403,7 +514,7 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   const int64_t per_task = (int64_t)kFwdTaskGroups * 128;
   pl->max_fwd_tasks = pl->max_entries / per_task + pl->num_buckets + 1;
   build_indexer_tasks(pl);
-  build_attention_runs(pl);
+  build_attention_work(pl);
 
   // workspace layout
   int64_t off = 0;
@@ -417,8 +528,11 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   pl->off_tok_pos = take(4 * pl->T);
   pl->off_tok_req = take(4 * pl->T);
   pl->off_reqs = take(sizeof(ReqInfo) * p.batch);
-  pl->off_att_starts = take(sizeof(AttCursor) * pl->att_starts.size());
+  // (sizes that q_lens and the heads alone decide: a plan with other contexts has the same layout up
+  // to here)
+  pl->off_att_heads = take(sizeof(AttHead) * pl->att_heads.size());
   pl->off_att_merges = take(sizeof(AttMerge) * pl->att_merges.size());
+  pl->off_att_pieces = take(sizeof(AttPiece) * (pl->att_tiles + 2 * pl->att_ctas));
   pl->off_page_req = take(4 * std::max<int64_t>(1, pl->total_pages));
   pl->off_idx_tasks = take(sizeof(IdxTask) * std::max<size_t>(1, pl->idx_tasks.size()));
   int64_t upload_end = off;
@@ -474,7 +588,8 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   put(pl->off_tok_pos, tok_pos.data(), 4 * tok_pos.size());
   put(pl->off_tok_req, tok_req.data(), 4 * tok_req.size());
   put(pl->off_reqs, pl->reqs.data(), sizeof(ReqInfo) * pl->reqs.size());
-  put(pl->off_att_starts, pl->att_starts.data(), sizeof(AttCursor) * pl->att_starts.size());
+  put(pl->off_att_heads, pl->att_heads.data(), sizeof(AttHead) * pl->att_heads.size());
+  put(pl->off_att_pieces, pl->att_pieces.data(), sizeof(AttPiece) * pl->att_pieces.size());
   put(pl->off_att_merges, pl->att_merges.data(), sizeof(AttMerge) * pl->att_merges.size());
   put(pl->off_page_req, pl->page_req.data(), 4 * pl->page_req.size());
   put(pl->off_idx_tasks, pl->idx_tasks.data(), sizeof(IdxTask) * pl->idx_tasks.size());
@@ -553,7 +668,8 @@ DevPlan make_dev_plan(const sps_plan* pl, void* ws) {
   d.topk_nseg = pl->topk_nseg;
   d.fwd_prefetch = pl->fwd_prefetch;
   d.topk_segg = pl->topk_segg;
-  d.att_starts = reinterpret_cast<const AttCursor*>(base + pl->off_att_starts);
+  d.att_heads = reinterpret_cast<const AttHead*>(base + pl->off_att_heads);
+  d.att_pieces = reinterpret_cast<const AttPiece*>(base + pl->off_att_pieces);
   d.att_merges = reinterpret_cast<const AttMerge*>(base + pl->off_att_merges);
   d.att_ctas = pl->att_ctas;
   d.att_slot_rows = pl->att_slot_rows;

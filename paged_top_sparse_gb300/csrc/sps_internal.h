@@ -49,7 +49,8 @@ struct FwdTask {
 };
 
 // Everything a kernel needs about the plan, passed by value.
-struct AttCursor;
+struct AttPiece;
+struct AttHead;
 struct AttMerge;
 struct DevPlan {
   int32_t batch, T, H, Hkv, Hg, D, K, max_pages, num_phys;
@@ -92,20 +93,26 @@ struct DevPlan {
   // waits for its own K/V tiles), the K/V tiles of the item this many items ahead are
   // prefetched into L2 (0: none; the plan sets 1)
   int32_t fwd_prefetch;
-  // full attention: where each of its att_ctas blocks begins (block i runs up to where block
-  // i + 1 begins; [att_ctas + 1]), the tiles cut over blocks ([att_ctas]), and the rows a partial
-  // result of a cut tile may have
-  const AttCursor* att_starts;
+  // full attention: the work of its att_ctas blocks, the tiles cut over blocks ([att_ctas]), and the
+  // rows a partial result of a cut tile may have
+  const AttHead* att_heads;
+  const AttPiece* att_pieces;
   const AttMerge* att_merges;
   int32_t att_ctas, att_slot_rows;
   int32_t att_num_merges, att_merge_cap;  // cut tiles of this plan, and of any with its q_lens
 };
 
-// A full-attention work position: page `page` of query tile `tile` of head block `vg` (KV head
-// g = vg / head blocks per KV head) of request `req`; (batch, 0, 0, 0) is the end.
-struct AttCursor {
-  int32_t req, vg, tile, page;
-  int32_t q_len, ctx, flat0, pad;  // the request's: new tokens, cached tokens, first flat token
+// Full attention: pages [page0, page1) of query tile `tile` of head block `vg` (KV head
+// g = vg / head blocks per KV head) of request `req`, whose new tokens, cached tokens and first flat
+// token ride along.
+struct AttPiece {
+  int32_t req, vg, tile, page0;
+  int32_t page1, q_len, ctx, flat0;
+};
+// A block's work: its first piece (count 0: none), then `count` - 1 more from att_pieces[next].
+struct AttHead {
+  AttPiece first;
+  int32_t count, next, pad[2];
 };
 // A query tile whose pages were cut over several blocks: blocks cta0 .. cta1 hold its pieces
 // (req < 0: unused entry).
