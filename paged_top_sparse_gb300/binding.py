@@ -131,23 +131,24 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_raw_stream = None
+def _find_stream():
+    """The current stream's cudaStream_t.  The lookup goes past torch's stream objects where it can:
+    making one costs more than a small kernel runs.  (Replaces itself on the first call.)"""
+    global _current_stream
+    import torch
+
+    get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream",
+                                                     "_cuda_getDevice"))
+    _current_stream = ((lambda: get(dev())) if get and dev else
+                       (lambda: torch.cuda.current_stream().cuda_stream))
+    return _current_stream()
+
+
+_current_stream = _find_stream
 
 
 def _stream(stream):
-    """The cudaStream_t of ``stream``, or of the current stream.  The lookup goes past torch's
-    stream objects where it can: making one costs more than a small kernel runs."""
-    if stream is not None:
-        return stream.cuda_stream
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-
-        get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream",
-                                                         "_cuda_getDevice"))
-        _raw_stream = ((lambda: get(dev())) if get and dev else
-                       (lambda: torch.cuda.current_stream().cuda_stream))
-    return _raw_stream()
+    return _current_stream() if stream is None else stream.cuda_stream
 
 
 class Plan:
@@ -173,6 +174,9 @@ class Plan:
         self.head_dim, self.top_k = head_dim, top_k
         self.num_tokens = sum(int(x) for x in q_lens)
         self.num_q_heads, self.num_kv_heads = num_q_heads, num_kv_heads
+        # shapes of a query, and of new keys or values
+        self.q_shape = (self.num_tokens, num_q_heads, head_dim)
+        self.kv_shape = (self.num_tokens, num_kv_heads, head_dim)
 
     def info(self) -> PlanInfo:
         inf = PlanInfo()
@@ -327,49 +331,50 @@ def _expect(t, dtype, name):
 
 
 def _rope(rope, plan):
-    if rope is None:
-        return None
     if rope.positions is not None and rope.positions.shape[-1] != plan.num_tokens:
         raise ValueError(f"positions must be [axes][{plan.num_tokens}]")
     return rope.ref
 
 
-def _token_stride(t, plan, heads, name):
+def _token_stride(t, shape, name):
     """Elements between the tokens of a [T][heads][D] view whose rows are contiguous."""
-    T, D = plan.num_tokens, plan.head_dim
     st = t.stride()
-    if t.shape != (T, heads, D) or st[2] != 1 or (heads > 1 and st[1] != D):
-        raise ValueError(f"{name} must be [{T}][{heads}][{D}] with contiguous rows")
-    return st[0] if T > 1 else heads * D
+    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must be [{shape[0]}][{shape[1]}][{shape[2]}] with contiguous rows")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_scale, k_out,
                      workspace, stream=None):
     """Norm per head and rotation of q [T][H][D] and k [T][H_kv][D] (or None); token strides come
     from the tensors.  A one-byte ``q_out`` takes E4M3 codes of the result / ``q_scale``."""
-    H, G = plan.num_q_heads, plan.num_kv_heads
+    qs, ks = plan.q_shape, plan.kv_shape
     _expect(q_weight, "float32", "q_weight")
     _expect(k_weight, "float32", "k_weight")
-    _check(lib().sps_qk_norm_rope(
-        plan.handle, _ptr(q), _token_stride(q, plan, H, "q"), _ptr(k),
-        0 if k is None else _token_stride(k, plan, G, "k"), _ptr(q_weight), _ptr(k_weight),
-        float(eps), _rope(rope, plan), _ptr(q_out), _token_stride(q_out, plan, H, "q_out"),
-        E4M3 if q_out.element_size() == 1 else BF16, float(q_scale), _ptr(k_out),
-        0 if k_out is None else _token_stride(k_out, plan, G, "k_out"), _ptr(workspace),
-        _stream(stream)))
+    st = (_lib or lib()).sps_qk_norm_rope(
+        plan.handle, q.data_ptr(), _token_stride(q, qs, "q"), _ptr(k),
+        0 if k is None else _token_stride(k, ks, "k"), _ptr(q_weight), _ptr(k_weight), eps,
+        None if rope is None else _rope(rope, plan), q_out.data_ptr(),
+        _token_stride(q_out, qs, "q_out"), E4M3 if q_out.element_size() == 1 else BF16, q_scale,
+        _ptr(k_out), 0 if k_out is None else _token_stride(k_out, ks, "k_out"),
+        workspace.data_ptr(), _stream(stream))
+    if st:
+        _check(st)
 
 
 def sps_kv_append_rope(plan: Plan, k_new, v_new, k_weight, eps, rope, page_table, k_cache, v_cache,
                        k_scales, v_scales, workspace, stream=None):
     """``sps_kv_append`` with the key's norm and rotation on the way; k_new / v_new [T][H_kv][D]
     may be views with a token stride."""
-    G = plan.num_kv_heads
+    ks = plan.kv_shape
     _expect(k_weight, "float32", "k_weight")
-    _check(lib().sps_kv_append_rope(
-        plan.handle, _ptr(k_new), _token_stride(k_new, plan, G, "k_new"), _ptr(v_new),
-        _token_stride(v_new, plan, G, "v_new"), _ptr(k_weight), float(eps), _rope(rope, plan),
-        _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-        _ptr(workspace), _stream(stream)))
+    st = (_lib or lib()).sps_kv_append_rope(
+        plan.handle, k_new.data_ptr(), _token_stride(k_new, ks, "k_new"), v_new.data_ptr(),
+        _token_stride(v_new, ks, "v_new"), _ptr(k_weight), eps,
+        None if rope is None else _rope(rope, plan), page_table.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), workspace.data_ptr(), _stream(stream))
+    if st:
+        _check(st)
 
 
 def paged_attention_scratch(plan: Plan) -> int:
@@ -383,13 +388,15 @@ def paged_attention_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_sc
                         out, out_lse, scratch, workspace, stream=None):
     """Full causal attention of q [T][H][D] over the paged cache into out [T][H][D] BF16 (both may
     have a token stride) and, unless None, out_lse [T][H] FP32."""
-    H = plan.num_q_heads
+    qs = plan.q_shape
     _expect(out_lse, "float32", "out_lse")
-    _check(lib().paged_attention_fwd(
-        plan.handle, _ptr(q), _token_stride(q, plan, H, "q"), float(q_scale), _ptr(k_cache),
-        _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(out),
-        _token_stride(out, plan, H, "out"), _ptr(out_lse), _ptr(scratch),
-        scratch.numel() * scratch.element_size(), _ptr(workspace), _stream(stream)))
+    st = (_lib or lib()).paged_attention_fwd(
+        plan.handle, q.data_ptr(), _token_stride(q, qs, "q"), q_scale, k_cache.data_ptr(),
+        v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), out.data_ptr(),
+        _token_stride(out, qs, "out"), _ptr(out_lse), scratch.data_ptr(), scratch.nbytes,
+        workspace.data_ptr(), _stream(stream))
+    if st:
+        _check(st)
 
 
 def sps_quantize_e4m3(x_bf16, scale: float, codes, stream=None):

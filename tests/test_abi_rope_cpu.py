@@ -128,7 +128,7 @@ def test_binding_checks_shapes():
     q = torch.zeros(T, H, D, dtype=torch.bfloat16)
     for bad in (q[:, :2], q[:3], q.transpose(1, 2), q[..., ::2]):
         with pytest.raises(ValueError):
-            B._token_stride(bad, plan, H, "q")
-    assert B._token_stride(torch.zeros(T, H + 3, D)[:, 1:1 + H], plan, H, "q") == (H + 3) * D
+            B._token_stride(bad, plan.q_shape, "q")
+    assert B._token_stride(torch.zeros(T, H + 3, D)[:, 1:1 + H], plan.q_shape, "q") == (H + 3) * D
     with pytest.raises(ValueError):
         B._rope(B.Rope(f, positions=torch.zeros(T - 1, dtype=torch.int32)), plan)
