@@ -11,7 +11,8 @@
 // Mathematics as in attention.cu: p = 2^((s - m) c + 7) with a lazily raised reference m, l and O in
 // FP32, P rounded to FP16.
 //
-// One persistent CTA per SM: one warp copies pages (codes and scales of K and V, 18 KB) into a ring;
+// One persistent CTA per SM: two warps copy pages (codes and scales of K and V, 18 KB) into a ring
+// (one would take as long to issue a page's copies as a page may last);
 // the others take the pages' 32-key chunks in turn, each with a running (m, l, O) of its own, merged
 // through shared memory at the end of a piece.
 //
@@ -29,7 +30,8 @@ constexpr int kMmaWarps = 8;
 constexpr int kChunks = 4;                        // 32-key chunks of a page
 constexpr int kPageStep = kMmaWarps / kChunks;    // a warp takes a chunk of every kPageStep-th page
 static_assert(kMmaWarps % kChunks == 0, "a warp keeps its place in the page");
-constexpr int kDecThreads = 32 * (kMmaWarps + 1);
+constexpr int kCopyWarps = 2;  // a warp copies every kCopyWarps-th page
+constexpr int kDecThreads = 32 * (kMmaWarps + kCopyWarps);
 
 template <int D>
 struct DecSmem {
@@ -39,8 +41,8 @@ struct DecSmem {
   // A multiple of kPageStep: a warp then finds in a stage, each time round, the page after one that
   // it took itself, so that the phase it waits for is never more than one ahead of the barrier's (a
   // parity wait two phases ahead passes at once).  Between pieces the warps meet.
-  static constexpr int STAGES = (S0 > 12 ? 12 : S0) / kPageStep * kPageStep;
-  static_assert(STAGES >= 2 * kPageStep, "shared memory");
+  static constexpr int STAGES = (S0 > 12 ? 12 : S0) / 4 * 4;
+  static_assert(4 % kPageStep == 0 && 4 % kCopyWarps == 0 && STAGES >= 8, "a warp's own stages");
   uint8_t page[STAGES][PAGE];
   float o[kMmaWarps][16][D];
   float2 stat[kMmaWarps][16];  // (m, l)
@@ -91,24 +93,21 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
   const RowPack rp(p.Hg);
   PieceList work(p);
   Piece pc;
-  uint32_t st = 0, ph = 0;  // ring stage and phase
-  auto advance = [&]() {
-    if (++st == S) {
-      st = 0;
-      ph ^= 1;
-    }
-  };
 
-  if (warp == kMmaWarps) {
+  if (warp >= kMmaWarps) {
     // ------------------------------------------------ copies
+    uint32_t page_it = 0;  // pages before the piece
     bool ok = true;
     while (ok && work.next(p, rp, pc)) {
       const int n = pc.page1 - pc.page0;
       const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
-      auto load_ids = [&](int first) {  // physical tiles of the lanes' pages first + lane
+      // this warp's pages of the piece: s0, s0 + kCopyWarps, ...; a lane holds every one's tile
+      const int s0 = (int)((warp - kMmaWarps + kCopyWarps - page_it % kCopyWarps) % kCopyWarps);
+      auto load_ids = [&](int k) {  // physical tiles of its pages k + lane
+        const int s = s0 + (k + lane) * kCopyWarps;
         int id = 0;
-        if (first + lane < n) {
-          id = __ldg(pages + first + lane);
+        if (s < n) {
+          id = __ldg(pages + s);
           if (id < 0 || id >= p.num_phys) {
             set_status(status, DEV_BAD_PAGE);
             id = 0;
@@ -117,12 +116,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
         return id * p.Hkv + pc.vg;
       };
       int ids = load_ids(0), next_ids = 0;
-      for (int s = 0; s < n && ok; ++s) {
-        if (s > 0 && (s & 31) == 0) ids = next_ids;
-        if ((s & 31) == 8) next_ids = load_ids(s + 24);
-        const int64_t tile = __shfl_sync(0xffffffffu, ids, s & 31);
+      for (int s = s0, k = 0; s < n && ok; s += kCopyWarps, ++k) {
+        if (k > 0 && (k & 31) == 0) ids = next_ids;
+        if ((k & 31) == 8) next_ids = load_ids(k + 24);
+        const int64_t tile = __shfl_sync(0xffffffffu, ids, k & 31);
+        const uint32_t it = page_it + s, st = it % S;
         if (lane == 0) {
-          ok = mbar_wait(smem_u32(&sm.empty[st]), ph ^ 1, abort_flag, status);
+          ok = mbar_wait(smem_u32(&sm.empty[st]), ((it / S) & 1) ^ 1, abort_flag, status);
           if (ok) {
             const uint32_t f = smem_u32(&sm.full[st]), d = smem_u32(sm.page[st]);
             mbar_expect_tx(f, Smem::PAGE);
@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        advance();
       }
+      page_it += n;
     }
   } else {
     // ------------------------------------------------ products: chunks of 16 keys
