@@ -358,9 +358,9 @@ typedef struct {
  *                and > 0)
  *   k_out        device BF16, at k_out_token_stride
  * Buffers are 16-byte aligned; strides are multiples of 8 elements (16 for E4M3 codes) and at
- * least the rows of a token, so q and k may be views of one projection's output.  An output may
- * be its own input (same address and stride); other overlaps are not allowed.  `workspace` is the
- * plan's uploaded workspace (token positions).
+ * least the rows of a token, so q and k may be views of one projection's output.  A BF16 output
+ * may be its own input (same address and stride); other overlaps are not allowed.  `workspace` is
+ * the plan's uploaded workspace (token positions).
  */
 sps_status sps_qk_norm_rope(const sps_plan* plan, const void* q, int64_t q_token_stride,
                             const void* k, int64_t k_token_stride, const float* q_weight,
@@ -463,10 +463,11 @@ sps_status sparse_prefill_fwd_noalloc(const sps_plan* plan, const void* q, float
  *   k_cache, v_cache, k_scales, v_scales, page_table   as for sparse_prefill_fwd; slots behind a
  *                request's last token may hold anything, NaN included, the others finite values
  *   out_bf16     device BF16, token i's H rows at out_bf16 + i * out_token_stride (16-byte aligned,
- *                stride a multiple of 8)
+ *                stride a multiple of 8); q and out do not overlap
  *   out_lse      device FP32 [T*H] or NULL
  *   scratch      device, 256-byte aligned, paged_attention_scratch bytes, contents arbitrary:
- *                partial results of tiles that are cut over the GPU
+ *                partial results of tiles that are cut over the GPU; calls that may run at the same
+ *                time need scratch of their own
  *   workspace    the plan's uploaded workspace
  * Accumulation, maxima and sums are FP32; P is rounded to the 16-bit type of the second product
  * (BF16; FP16 over an NVFP4 cache, whose code x scale products are exact there).  The result is the

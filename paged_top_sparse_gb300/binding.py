@@ -174,6 +174,7 @@ class Plan:
         self.head_dim, self.top_k = head_dim, top_k
         self.num_tokens = sum(int(x) for x in q_lens)
         self.num_q_heads, self.num_kv_heads = num_q_heads, num_kv_heads
+        self.q_codes = self.problem.q_dtype == E4M3
         # shapes of a query, and of new keys or values
         self.q_shape = (self.num_tokens, num_q_heads, head_dim)
         self.kv_shape = (self.num_tokens, num_kv_heads, head_dim)
@@ -318,15 +319,19 @@ class Rope:
 _dtypes = {}
 
 
+def _dtype(name):
+    if not _dtypes:
+        import torch
+
+        _dtypes.update(float32=torch.float32, int32=torch.int32, bfloat16=torch.bfloat16)
+    return _dtypes[name]
+
+
 def _expect(t, dtype, name):
     """A contiguous tensor of the named torch dtype (or None)."""
     if t is None:
         return
-    if not _dtypes:
-        import torch
-
-        _dtypes.update(float32=torch.float32, int32=torch.int32)
-    if t.dtype is not _dtypes[dtype] or not t.is_contiguous():
+    if t.dtype is not _dtype(dtype) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor")
 
 
@@ -344,6 +349,13 @@ def _token_stride(t, shape, name):
     return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
+def _rows(t, shape, name, codes=False):
+    """The token stride of BF16 rows, or of rows of one-byte codes."""
+    if t.element_size() != 1 if codes else t.dtype is not _dtype("bfloat16"):
+        raise ValueError(f"{name} must hold {'E4M3 codes' if codes else 'bfloat16'}")
+    return _token_stride(t, shape, name)
+
+
 def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_scale, k_out,
                      workspace, stream=None):
     """Norm per head and rotation of q [T][H][D] and k [T][H_kv][D] (or None); token strides come
@@ -351,12 +363,13 @@ def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_s
     qs, ks = plan.q_shape, plan.kv_shape
     _expect(q_weight, "float32", "q_weight")
     _expect(k_weight, "float32", "k_weight")
+    codes = q_out.element_size() == 1
     st = (_lib or lib()).sps_qk_norm_rope(
-        plan.handle, q.data_ptr(), _token_stride(q, qs, "q"), _ptr(k),
-        0 if k is None else _token_stride(k, ks, "k"), _ptr(q_weight), _ptr(k_weight), eps,
+        plan.handle, q.data_ptr(), _rows(q, qs, "q"), _ptr(k),
+        0 if k is None else _rows(k, ks, "k"), _ptr(q_weight), _ptr(k_weight), eps,
         None if rope is None else _rope(rope, plan), q_out.data_ptr(),
-        _token_stride(q_out, qs, "q_out"), E4M3 if q_out.element_size() == 1 else BF16, q_scale,
-        _ptr(k_out), 0 if k_out is None else _token_stride(k_out, ks, "k_out"),
+        _rows(q_out, qs, "q_out", codes), E4M3 if codes else BF16, q_scale,
+        _ptr(k_out), 0 if k_out is None else _rows(k_out, ks, "k_out"),
         workspace.data_ptr(), _stream(stream))
     if st:
         _check(st)
@@ -369,8 +382,8 @@ def sps_kv_append_rope(plan: Plan, k_new, v_new, k_weight, eps, rope, page_table
     ks = plan.kv_shape
     _expect(k_weight, "float32", "k_weight")
     st = (_lib or lib()).sps_kv_append_rope(
-        plan.handle, k_new.data_ptr(), _token_stride(k_new, ks, "k_new"), v_new.data_ptr(),
-        _token_stride(v_new, ks, "v_new"), _ptr(k_weight), eps,
+        plan.handle, k_new.data_ptr(), _rows(k_new, ks, "k_new"), v_new.data_ptr(),
+        _rows(v_new, ks, "v_new"), _ptr(k_weight), eps,
         None if rope is None else _rope(rope, plan), page_table.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), workspace.data_ptr(), _stream(stream))
     if st:
@@ -390,10 +403,12 @@ def paged_attention_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_sc
     have a token stride) and, unless None, out_lse [T][H] FP32."""
     qs = plan.q_shape
     _expect(out_lse, "float32", "out_lse")
+    if out_lse is not None and out_lse.numel() != qs[0] * qs[1]:
+        raise ValueError(f"out_lse must be [{qs[0]}][{qs[1]}]")
     st = (_lib or lib()).paged_attention_fwd(
-        plan.handle, q.data_ptr(), _token_stride(q, qs, "q"), q_scale, k_cache.data_ptr(),
+        plan.handle, q.data_ptr(), _rows(q, qs, "q", plan.q_codes), q_scale, k_cache.data_ptr(),
         v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), out.data_ptr(),
-        _token_stride(out, qs, "out"), _ptr(out_lse), scratch.data_ptr(), scratch.nbytes,
+        _rows(out, qs, "out"), _ptr(out_lse), scratch.data_ptr(), scratch.nbytes,
         workspace.data_ptr(), _stream(stream))
     if st:
         _check(st)

@@ -988,6 +988,10 @@ sps_status sps_qk_norm_rope(const sps_plan* pl, const void* q, int64_t q_stride,
     return fail(SPS_EINVAL,
                 "sps_qk_norm_rope: buffers must be non-NULL and 16-byte aligned, token strides "
                 "multiples of 16 bytes and at least a token's rows");
+  // in place, each row lies on itself; else a warp's rows would lie on rows that others still read
+  if ((q_out == q && (e4m3 || q_out_stride != q_stride)) ||
+      (k && k_out == k && k_out_stride != k_stride))
+    return fail(SPS_EINVAL, "sps_qk_norm_rope: an output in place is BF16 and has the input's stride");
   if ((q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16)))
     return fail(SPS_EINVAL, "sps_qk_norm_rope: weights must be 16-byte aligned");
   if (!(eps >= 0.f) || !std::isfinite(eps))

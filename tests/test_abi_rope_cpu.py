@@ -85,6 +85,14 @@ def test_qk_refuses_misaligned_rows(L):
     assert e.qk(L, qw=_ptr(e.w.view(np.uint8), 2)) == 1
 
 
+def test_qk_refuses_an_output_that_lies_on_other_rows(L):
+    e = Env()
+    q, k = _ptr(e.buf["q"]), _ptr(e.buf["k"])
+    assert e.qk(L, qo=q, dt=B.E4M3) == 1  # codes over the rows that they come from
+    assert e.qk(L, qo=q, qos=H * D + 16) == 1
+    assert e.qk(L, ko=k, kos=G * D + 8) == 1
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(rotary_dim=-16), 1), (dict(rotary_dim=144), 1), (dict(rotary_dim=24), 2),
     (dict(num_axes=0), 1), (dict(num_axes=5), 1), (dict(inv_freq=None), 1),
@@ -130,5 +138,9 @@ def test_binding_checks_shapes():
         with pytest.raises(ValueError):
             B._token_stride(bad, plan.q_shape, "q")
     assert B._token_stride(torch.zeros(T, H + 3, D)[:, 1:1 + H], plan.q_shape, "q") == (H + 3) * D
+    for bad, codes in ((q.half(), False), (q.float(), False), (q, True)):
+        with pytest.raises(ValueError):
+            B._rows(bad, plan.q_shape, "q", codes)
+    assert B._rows(q, plan.q_shape, "q") == B._rows(q.to(torch.uint8), plan.q_shape, "q", True) == H * D
     with pytest.raises(ValueError):
         B._rope(B.Rope(f, positions=torch.zeros(T - 1, dtype=torch.int32)), plan)
