@@ -79,8 +79,9 @@ class Case:
         B.sps_plan_upload(self.plan, self.ws)
         self.scratch = torch.full((B.paged_attention_scratch(self.plan),), 0xFF, dtype=torch.uint8,
                                   device=DEV)  # FP32 NaN
-        self.wide = torch.full((T, H + out_pad, D), 7.0, dtype=torch.bfloat16, device=DEV)
-        self.out = self.wide[:, :H]
+        # two tokens behind the last one, which nothing may touch
+        self.wide = torch.full((T + 2, H + out_pad, D), 7.0, dtype=torch.bfloat16, device=DEV)
+        self.out = self.wide[:T, :H]
         self.lse = torch.full((T, H), float("nan"), device=DEV)
 
     @staticmethod
@@ -143,7 +144,7 @@ class Case:
         # the sum: scores as above, n / 4 additions of 2^-24 in a row
         lerr = (self.lse.double() - lse).abs()
         assert bool((lerr <= 2.0 ** -13 + keys * 2.0 ** -26 + lse.abs() * 2.0 ** -22).all()), float(lerr.max())
-        assert bool((self.wide[:, self.H:] == 7.0).all())
+        assert bool((self.wide[:, self.H:] == 7.0).all()) and bool((self.wide[self.T:] == 7.0).all())
 
 
 RAGGED = ([1, 0, 130, 7, 300, 1, 128, 1], [0, 5, 1000, 121, 0, 127, 128, 4000])
@@ -272,6 +273,56 @@ def test_captured_decode_replays_over_growing_contexts(kv):
             g.replay()
         torch.cuda.synchronize()
         full.check(now)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
+def test_capture_of_whole_tiles_replays_over_cut_ones(kv):
+    """Captured while no tile is cut over blocks (an eager call needs no merge then), replayed over
+    contexts whose tiles are, and back."""
+    H, G = 8, 2
+    for q_lens, end in (([1] * 6, [9000, 70, 300, 20000, 5, 1]), ([150, 150], [6000, 90])):
+        full = Case(47, q_lens, end, H, G, 128, kv)
+        B = full.B
+        short = [min(c, 20) for c in end]
+        plans = [B.Plan(q_lens, c, H, G, 128, 1, full.pt.shape[1], sum(full.pages),
+                        q_dtype="bf16" if kv == "bf16" else "e4m3", kv_dtype=kv)
+                 for c in (short, end)]
+        assert all(p.workspace_bytes <= full.ws.numel() for p in plans)
+        B.sps_plan_upload(plans[0], full.ws)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        full.plan = plans[0]
+        with torch.cuda.graph(g, stream=s):
+            full.run(s)
+        for plan, now in ((plans[0], short), (plans[1], end), (plans[0], short)):
+            with torch.cuda.stream(s):
+                B.sps_plan_upload(plan, full.ws, s)
+                full.out.zero_()
+                full.scratch.fill_(0xFF)
+                g.replay()
+            torch.cuda.synchronize()
+            full.check(now)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("seed", range(8))
+def test_mixed_batches(seed, kv):
+    """Single tokens, chunks and empty requests after contexts of every size: tiles kept whole, cut
+    in two and cut over many blocks in one call."""
+    rng = np.random.default_rng(100 + seed)
+    n = int(rng.choice([3, 9, 40]))
+    q_lens = [int(rng.choice([0, 1, 1, 1, 2, int(rng.integers(3, 40)), int(rng.integers(40, 600))]))
+              for _ in range(n)]
+    q_lens[0] = 1
+    ctx = [int(rng.choice([0, int(rng.integers(1, 300)), int(rng.integers(300, 2500))])) for _ in q_lens]
+    if seed % 2:
+        ctx[int(rng.integers(n))] = 30000  # one long context beside the others
+    G = int(rng.choice([1, 2]))
+    c = Case(seed, q_lens, ctx, G * int(rng.choice([1, 3, 4, 8, 16])), G, int(rng.choice([64, 128])),
+             kv, out_pad=1)
+    c.run()
+    c.check()
 
 
 def test_two_streams_with_their_own_buffers():
