@@ -64,7 +64,7 @@ struct AttSmem {
   alignas(16) uint8_t raw[RS][QUANT ? RAWB : 16];
   uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], raw_full[RS], raw_empty[RS];
   uint64_t s_full[2], p_half[2], p_full[2];  // p_half: P of the first 64 keys
-  uint64_t pv_done[2][2];                    // P V product i into O_t completes pv_done[t][i % 2]
+  uint64_t o_done[2];                        // the piece's last P V product into O_t
   uint64_t o_free[2], stat_full, tail_go, tail_done, done;
   float2 stat[128];  // (m, l) of the odd pages' rows
   uint32_t tmem_base;
@@ -118,8 +118,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(smem_u32(&sm.s_full[i]), 1);
       mbar_init(smem_u32(&sm.p_half[i]), 4);
       mbar_init(smem_u32(&sm.p_full[i]), 4);
-      mbar_init(smem_u32(&sm.pv_done[i][0]), 1);
-      mbar_init(smem_u32(&sm.pv_done[i][1]), 1);
+      mbar_init(smem_u32(&sm.o_done[i]), 1);
       mbar_init(smem_u32(&sm.o_free[i]), 4);
     }
     for (int i = 0; i < S; ++i) {
@@ -245,7 +244,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool leader = elect_one();
       const uint32_t q_lo = sdesc_lo(smem_u32(sm.q[0]), 16), kv_lo = smem_u32(sm.kv[0]) >> 4;
       uint32_t st = 0, ph = 0;  // ring stage and phase of the next K or V tile
-      uint32_t qc0 = 0, qc1 = 0, sc[2] = {0, 0}, oc[2] = {0, 0}, pvc[2] = {0, 0}, tc = 0;
+      uint32_t qc0 = 0, qc1 = 0, sc[2] = {0, 0}, oc[2] = {0, 0}, tc = 0;
       bool ok = true;
       auto wait = [&](uint64_t& bar, uint32_t parity) {
         if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
@@ -279,7 +278,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         commit(sm.s_full[t]);
       };
       // O_t (+)= P_t V in two halves of 64 keys, the first as soon as its P is there
-      auto issue_pv = [&](int t, const Tile& v, bool first, bool tail) {
+      auto issue_pv = [&](int t, const Tile& v, bool first, bool last, bool tail) {
         const uint32_t va = sdesc_lo(0, 16384) + kv_lo + v.stage * (TILE >> 4);
         auto half = [&](int h) {
           tc_fence_after();
@@ -305,8 +304,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ++sc[t];
         if (!ok) return;
         half(1);
-        if (leader) mma_commit(smem_u32(&sm.pv_done[t][pvc[t] & 1]));
-        ++pvc[t];
+        if (last) commit(sm.o_done[t]);
       };
       while (ok && work.next(p, rp, pc)) {
         const int n = pc.page1 - pc.page0;
@@ -339,7 +337,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              if (ok) issue_pv(t, v, j == 0, t == 0 && tail && !more);
+              if (ok) issue_pv(t, v, j == 0, !more, t == 0 && tail && !more);
               if (ok && more) {
                 if (t == 0) wait(sm.kv_full[k.stage], k.phase);
                 if (ok) issue_s(t, t, k);
@@ -364,7 +362,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             wait(sm.kv_full[v.stage], v.phase);
             const bool z = tail && j + 1 == n;
             if (z && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
-            if (ok) issue_pv(t, v, j < 2, z);
+            if (ok) issue_pv(t, v, j < 2, j + 2 >= n, z);
             if (!ok) return;
             commit(sm.kv_empty[v.stage]);
             if (j + 2 < n) next_s(j + 2, t);
@@ -407,11 +405,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t obase = tmem + lane_addr + 256 + w * 128;
     const float c = a.c, bias = QUANT ? kF16Bias : 0.f;
     const int ti = row / rp.HB, hh = row % rp.HB;
-    uint32_t su = 0, pv = 0, sx = 0;  // uses of S_w, P V products into O_w, statistics received
+    uint32_t su = 0, od = 0, sx = 0;  // uses of S_w, pieces in O_w, statistics received
     bool ok = true;
-    auto pv_wait = [&](uint32_t i) {  // product i into O_w is complete
-      return mbar_wait(smem_u32(&sm.pv_done[w][i & 1]), (i >> 1) & 1, abort_flag, status);
-    };
     while (ok && work.next(p, rp, pc)) {
       // with one row tile, this warpgroup takes the pages of its parity
       const bool split = SINGLE || pc.nt == 1;
@@ -426,9 +421,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       uint64_t lsum[2] = {0, 0};
       for (int j = 0; j < n; ++j) {
         if (!mbar_wait(smem_u32(&sm.s_full[w]), su & 1, abort_flag, status)) { ok = false; break; }
-        ++su;
-        // every product is waited for once, in order: the one before this S
-        if (j > 0 && !pv_wait(pv + j - 1)) { ok = false; break; }
+        ++su;  // (a commit covers what its thread issued before: the last product into O_w too)
         const uint32_t bar_half = smem_u32(&sm.p_half[w]), bar_full = smem_u32(&sm.p_full[w]);
         bool half_sent = false;
         if (active) {
@@ -557,8 +550,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
       if (!ok) break;
-      if (!pv_wait(pv + n - 1)) break;  // the last product into O_w
-      pv += n;
+      if (!mbar_wait(smem_u32(&sm.o_done[w]), od & 1, abort_flag, status)) break;
+      ++od;
       float l;
       {
         float x, y, z, t;
