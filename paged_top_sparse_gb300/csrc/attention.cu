@@ -152,7 +152,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   Piece pc;
 
   if (warp < 4) {
-    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ------------------------------------------------ copies
@@ -334,12 +334,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (more) k = take();
             const Tile v = take();
             wait(sm.kv_full[v.stage], v.phase);
+            // (converted tiles are there long before; a copied K tile may land later than its V)
+            if (QUANT && more) wait(sm.kv_full[k.stage], k.phase);
             if (tail && !more && ok && leader) mbar_arrive(smem_u32(&sm.tail_go));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (ok) issue_pv(t, v, j == 0, !more, t == 0 && tail && !more);
               if (ok && more) {
-                if (t == 0) wait(sm.kv_full[k.stage], k.phase);
+                if (!QUANT && t == 0) wait(sm.kv_full[k.stage], k.phase);
                 if (ok) issue_s(t, t, k);
                 if (!QUANT && ok && j + 2 == n) commit(sm.q_empty[t]);
               }
@@ -397,7 +399,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     }
   } else if (warp < 12) {
-    if (QUANT) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if (QUANT) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------ softmax and epilogue of row tile w
     const int w = warp >= 8, quarter = warp % 4, row = quarter * 32 + lane;
@@ -420,6 +422,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float m = 0.f;
       uint64_t lsum[2] = {0, 0};
       for (int j = 0; j < n; ++j) {
+        const int page = pc.page0 + (split ? 2 * j + w : j);
+        const int nvis = valid ? pos - page * 128 + 1 : 128;
+        const bool masked = __any_sync(0xffffffffu, nvis < 128);
         if (!mbar_wait(smem_u32(&sm.s_full[w]), su & 1, abort_flag, status)) { ok = false; break; }
         ++su;  // (a commit covers what its thread issued before: the last product into O_w too)
         const uint32_t bar_half = smem_u32(&sm.p_half[w]), bar_full = smem_u32(&sm.p_full[w]);
@@ -427,9 +432,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (active) {
           tc_fence_after();
           const uint32_t sbase = tmem + lane_addr + w * 128;
-          const int page = pc.page0 + (split ? 2 * j + w : j);
-          const int nvis = valid ? pos - page * 128 + 1 : 128;
-          const bool masked = __any_sync(0xffffffffu, nvis < 128);
           uint32_t v[4][32];
           float red[4];
           const uint64_t c2 = pack_f32x2(c, c);
@@ -672,7 +674,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (QUANT && lane == 0) mbar_arrive(smem_u32(&sm.q_empty[w]));  // staging and Q tile are free
     }
   } else {
-    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // ------------------------------------------------ operand conversion (NVFP4 plans)
     const int ct = tid - 384;
     uint32_t it = 0, qc0 = 0, qc1 = 0;

@@ -21,6 +21,7 @@
 // codes of a byte.  For P V the pairs run along keys: the nibbles of two keys' words are interleaved.
 // O's dims are ordered so that a lane's B columns are one run of D / 8 dims of a key, under one scale.
 #include "attention.cuh"
+#include "nvfp4.cuh"
 
 namespace sps {
 namespace att {
@@ -58,15 +59,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The four bytes of w, two E2M1 codes each, as FP16 pairs (exact).
-__device__ __forceinline__ void cvt_e2m1x8(uint32_t w, uint32_t (&o)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
 }
 
 template <int D>

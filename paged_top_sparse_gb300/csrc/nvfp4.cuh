@@ -47,6 +47,15 @@ __device__ __forceinline__ void nvfp4_tile_convert(const uint8_t* raw, uint8_t* 
   }
 }
 
+// The four bytes of w, two E2M1 codes each, as FP16 pairs (exact).
+__device__ __forceinline__ void cvt_e2m1x8(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+
 // The same FP16 products with a thread per row (128 threads): a row's codes and scales in
 // registers, then its operand row.  Rows marked empty become zero, whatever their codes and scales
 // hold.  A thread starts at a column of its own (row / 2 or row / 4), which keeps a quarter warp's
@@ -80,9 +89,9 @@ struct Nvfp4Row {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         uint32_t h[4];
+        cvt_e2m1x8(w[u], h);
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          h[b] = hmul2_u32(cvt_e2m1x2((uint16_t)(w[u] >> (8 * b))), u < 2 ? s0 : s1);
+        for (int b = 0; b < 4; ++b) h[b] = hmul2_u32(h[b], u < 2 ? s0 : s1);
         const int col = 32 * i + 8 * u;
         *reinterpret_cast<uint4*>(dst + (col / 64) * 16384 + sw128_offset(row, (col % 64) / 8)) =
             make_uint4(h[0], h[1], h[2], h[3]);
