@@ -9,7 +9,7 @@ namespace att {
 
 constexpr float kRescale = 8.f;   // log2 of the growth of the maximum that rescales O
 constexpr float kF16Bias = 7.f;   // log2 of the factor on FP16 p
-constexpr int kMaxCtas = 256;
+constexpr int kMaxCtas = 256;     // blocks (one per SM) that a plan lists work for, at most
 
 // Row packing of a head group.
 struct RowPack {
@@ -63,6 +63,7 @@ struct PieceList {
   }
 };
 
+// Two values rounded to nearest even in 16 bits: P for the second product, or the output.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float a, float b) {
   uint32_t r;

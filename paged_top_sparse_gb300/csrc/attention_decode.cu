@@ -1,20 +1,29 @@
 // attention_decode.cu -- full attention of tiles of at most 16 rows (single tokens of a head group)
-// over an NVFP4 cache, bound by reading the cache.
+// over an NVFP4 cache.
 //
 // The tcgen05 kernel (attention.cu) brings NVFP4 tiles to the tensor core through shared memory: per
 // page of 128 keys its FP16 operand tiles cost 64 KB written and 96 KB read, 1560 cycles at 128 bytes
 // a cycle, where the page's 18 KB arrive from HBM in about 840.  With 16 rows the products are small
 // (1 MFLOP a page), so here the codes go from shared memory to registers once, become FP16 fragments
-// there, and feed the warp-level tensor instruction (mma.sync m16n8k16, FP32 accumulation); nothing
-// is written back.
+// there, and feed the warp-level tensor instruction (mma.sync m16n8k16, FP32 accumulation);
+// nothing is written back.  64 tokens after 32K (H 32 / H_kv 2, D 128): 278 us there, 159 here;
+// one token after 8K 15 and 9.5.
+//
+// Bound: the SM's issue slots and its warp-level products.  A 32-key chunk costs its warp about
+// 64 products, 128 conversions and 128 multiplications by block scales, some 1250 cycles of one
+// scheduler, and a page gives each of the four schedulers one chunk: 1400 cycles a page measured,
+// 3.8 TB/s (copying the same pages and doing nothing takes 103 us).  Twelve product warps (161
+// us), copies issued by the last warp to leave a stage (161) and pages fetched into L2 ahead
+// (181) were no faster.
 //
 // Mathematics as in attention.cu: p = 2^((s - m) c + 7) with a lazily raised reference m, l and O in
 // FP32, P rounded to FP16.
 //
-// One persistent CTA per SM: two warps copy pages (codes and scales of K and V, 18 KB) into a ring
-// (one would take as long to issue a page's copies as a page may last);
-// the others take the pages' 32-key chunks in turn, each with a running (m, l, O) of its own, merged
-// through shared memory at the end of a piece.
+// One persistent CTA per SM: two warps copy pages (codes and scales of K and V, 18 KB) into a
+// ring (one would take as long to issue a page's copies as a page may last); the others take the
+// pages' 32-key chunks in turn (32 keys share a load of the Q fragments: 159 us, 16-key chunks
+// 184), each with a running (m, l, O) of its own, merged through shared memory at the end of a
+// piece.
 //
 // Fragments.  Lane (g, t) = (lane / 4, lane % 4).  The order of the contracted dims is free, so a
 // lane reads whole words of a key (its dims (D / 4) t ..), and the pairs of a B register are the two
@@ -31,7 +40,7 @@ constexpr int kMmaWarps = 8;
 constexpr int kChunks = 4;                        // 32-key chunks of a page
 constexpr int kPageStep = kMmaWarps / kChunks;    // a warp takes a chunk of every kPageStep-th page
 static_assert(kMmaWarps % kChunks == 0, "a warp keeps its place in the page");
-constexpr int kCopyWarps = 2;  // a warp copies every kCopyWarps-th page
+constexpr int kCopyWarps = 2;  // a warp copies every kCopyWarps-th page (D 64: one 120 us, two 103)
 constexpr int kDecThreads = 32 * (kMmaWarps + kCopyWarps);
 
 template <int D>
@@ -129,7 +138,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       page_it += n;
     }
   } else {
-    // ------------------------------------------------ products: chunks of 16 keys
+    // ------------------------------------------------ products: chunks of 32 keys
     const int g = lane / 4, t = lane % 4;
     const float c = a.c;
     bool ok = true;

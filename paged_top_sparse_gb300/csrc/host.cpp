@@ -250,7 +250,7 @@ void build_indexer_tasks(sps_plan* pl) {
 // Work split of the full attention: tiles (two row tiles of 128 / HB tokens x HB heads of a KV head's
 // group, over the pages their last token sees) and pieces of tiles, listed for one block per SM.
 //
-// Costs are in pages (about 1.5 us): a piece's pages plus kAttTileCost for its fill, drain and
+// Costs are in pages (about 1.6 us): a piece's pages plus kAttTileCost for its fill, drain and
 // epilogue.  A cut tile's partial rows are written and merged by a second kernel, which is estimated
 // too; of the splits made, the one with the smallest estimate is kept.
 constexpr int kAttTileCost = 2, kAttMinPiece = 3;
