@@ -29,6 +29,11 @@
 // lane reads whole words of a key (its dims (D / 4) t ..), and the pairs of a B register are the two
 // codes of a byte.  For P V the pairs run along keys: the nibbles of two keys' words are interleaved.
 // O's dims are ordered so that a lane's B columns are one run of D / 8 dims of a key, under one scale.
+// Tiles of at most 8 rows (groups of up to 8 heads) turn both products round, K Q^T and V^T P^T: the
+// keys, then the dims, are the instruction's 16 rows and the query rows its 8 columns, so half as
+// many products do, P crossing the warp as transposed 8 x 8 tiles.  The converted registers are the
+// same.  64 tokens after 32K, H 32: H_kv 8 564 -> 452 us (5.4 TB/s), H_kv 4 290 -> 233; one token
+// after 8K 10.6 -> 8.5.
 #include "attention.cuh"
 #include "nvfp4.cuh"
 
@@ -43,19 +48,19 @@ static_assert(kMmaWarps % kChunks == 0, "a warp keeps its place in the page");
 constexpr int kCopyWarps = 2;  // a warp copies every kCopyWarps-th page (D 64: one 120 us, two 103)
 constexpr int kDecThreads = 32 * (kMmaWarps + kCopyWarps);
 
-template <int D>
+template <int D, int ROWS>
 struct DecSmem {
   static constexpr int CODES = 64 * D, SCALES = 8 * D;  // of a 128-key tile
   static constexpr int PAGE = 2 * (CODES + SCALES);     // K codes, K scales, V codes, V scales
-  static constexpr int S0 = (227 * 1024 - kMmaWarps * 16 * (D * 4 + 8) - D * 32 - 512) / PAGE;
+  static constexpr int S0 = (227 * 1024 - kMmaWarps * ROWS * (D * 4 + 8) - D * 32 - 512) / PAGE;
   // A multiple of kPageStep: a warp then finds in a stage, each time round, the page after one that
   // it took itself, so that the phase it waits for is never more than one ahead of the barrier's (a
   // parity wait two phases ahead passes at once).  Between pieces the warps meet.
   static constexpr int STAGES = (S0 > 12 ? 12 : S0) / 4 * 4;
   static_assert(4 % kPageStep == 0 && 4 % kCopyWarps == 0 && STAGES >= 8, "a warp's own stages");
   uint8_t page[STAGES][PAGE];
-  float o[kMmaWarps][16][D];
-  float2 stat[kMmaWarps][16];  // (m, l)
+  float o[kMmaWarps][ROWS][D];
+  float2 stat[kMmaWarps][ROWS];  // (m, l)
   uint4 qf[D / 16][32];        // Q fragments, k-step by lane
   uint64_t full[STAGES], empty[STAGES], meet;
   int abort_flag;
@@ -70,9 +75,26 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+// An 8 x 8 matrix of 16-bit values, transposed over the warp.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The largest, or the sum, of a row's values over the lanes that share the row.
+template <int ROWS, typename Op>
+__device__ __forceinline__ float row_reduce(float x, Op op) {
+#pragma unroll
+  for (int o = ROWS == 16 ? 1 : 4; o < (ROWS == 16 ? 4 : 32); o <<= 1)
+    x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p, AttArgs a) {
-  using Smem = DecSmem<D>;
+  using Smem = DecSmem<D, ROWS>;
+  constexpr bool FLIP = ROWS == 8;  // keys, and then dims, as the products' 16 rows
   constexpr int S = Smem::STAGES, WORDS = D / 32;  // WORDS: 8-code words of a key in a lane
   constexpr int NT = D / 8;                        // column tiles of O
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -150,18 +172,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
     };
     while (ok && work.next(p, rp, pc)) {
       const int n = pc.page1 - pc.page0, kv_len = pc.ctx + pc.q_len;
-      int pos[2];  // of rows g and g + 8
+      int pos[2];  // of this lane's two rows of the scores
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int tok = (g + 8 * h) / rp.HB;
+        const int tok = (FLIP ? 2 * t + h : g + 8 * h) / rp.HB;
         pos[h] = tok < pc.q_len && tok < rp.TB ? pc.ctx + tok : 0x3fffffff;
       }
       // Q fragments, a k-step per warp: (row g, row g + 8) x columns 2 t and 2 t + 8, which are the
       // lane's dims 4 k .. 4 k + 3
       for (int k = warp; k < D / 16; k += kMmaWarps) {
-        uint32_t f[4];
+        uint32_t f[4] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < (FLIP ? 1 : 2); ++h) {
           const int r = g + 8 * h, tok = r / rp.HB, hd = r % rp.HB;
           uint32_t x = 0;
           if (tok < pc.q_len && tok < rp.TB)
@@ -175,9 +197,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       }
       if (!meet()) break;
       const int first_pos = pc.ctx;  // the smallest position of the tile
-      float o[NT][4], m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+      // o: column tile i of 8 dims x rows (g, g + 8), or two of them as the rows of one product
+      float o[FLIP ? NT / 2 : NT][4], m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < (FLIP ? NT / 2 : NT); ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
       bool first = true;
@@ -191,8 +214,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
         const uint8_t* kp = sm.page[stg];
         const uint8_t* vp = kp + Smem::PAGE / 2;
         const int key0 = (pc.page0 + ch / kChunks) * 128 + kb;  // the chunk's first key
-        // S = Q K^T for keys kb + 8 u + (column)
-        float s[4][4];
+        // S = Q K^T for keys kb + 8 u + (column), in s[u]; or K Q^T, keys kb + 8 u + (row) of
+        // u = 0, 1 in s[0] and u = 2, 3 in s[1]
+        float s[FLIP ? 2 : 4][4];
         uint32_t kw[4][WORDS], ks[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -204,8 +228,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
             *reinterpret_cast<uint2*>(kw[u]) = *reinterpret_cast<const uint2*>(kp + key * 32 + t * 8);
             ks[u] = kp[Smem::CODES + key * 4 + t];
           }
+          if (!FLIP || u < 2) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[u % (FLIP ? 2 : 4)][e] = 0.f;
+          }
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) ks[u] = cvt_e4m3x2((uint16_t)ks[u]);
@@ -213,59 +239,85 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
         for (int w = 0; w < WORDS; ++w) {  // 8 dims of a lane: two k-steps of 4
           const uint4 q0 = sm.qf[2 * w][lane], q1 = sm.qf[2 * w + 1][lane];
           const uint32_t qa[4] = {q0.x, q0.y, q0.z, q0.w}, qb[4] = {q1.x, q1.y, q1.z, q1.w};
+          uint32_t x[4][4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const uint32_t f = __byte_perm(ks[u], ks[u], w < 2 ? 0x1010 : 0x3232);
-            uint32_t x[4];
-            cvt_e2m1x8(kw[u][w], x);
-            mma_16816(s[u], qa, hmul2_u32(x[0], f), hmul2_u32(x[1], f));
-            mma_16816(s[u], qb, hmul2_u32(x[2], f), hmul2_u32(x[3], f));
+            cvt_e2m1x8(kw[u][w], x[u]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[u][k] = hmul2_u32(x[u][k], f);
+            if (!FLIP) {
+              mma_16816(s[u % (FLIP ? 2 : 4)], qa, x[u][0], x[u][1]);
+              mma_16816(s[u % (FLIP ? 2 : 4)], qb, x[u][2], x[u][3]);
+            } else if (u % 2) {  // 16 keys
+              const uint32_t ka[4] = {x[u - 1][0], x[u][0], x[u - 1][1], x[u][1]};
+              const uint32_t kb2[4] = {x[u - 1][2], x[u][2], x[u - 1][3], x[u][3]};
+              mma_16816(s[u / 2], ka, qa[0], qa[2]);
+              mma_16816(s[u / 2], kb2, qb[0], qb[2]);
+            }
           }
         }
+        // the score of key 8 u + .. in row h of this lane: two of them (z) of a key pair, or one
+        auto score = [&](int u, int h, int z) -> float& {
+          return FLIP ? s[u / 2 % 2][2 * (u % 2) + h] : s[u % (FLIP ? 2 : 4)][2 * h + z];
+        };
+        constexpr int NZ = FLIP ? 1 : 2;
         if (key0 + 31 > first_pos) {  // some key lies behind some row
 #pragma unroll
           for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key0 + 8 * u + 2 * t + (e & 1) > pos[e / 2]) s[u][e] = -INFINITY;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int z = 0; z < NZ; ++z)
+                if (key0 + 8 * u + (FLIP ? g : 2 * t + z) > pos[h]) score(u, h, z) = -INFINITY;
         }
         // the reference maximum: raised for the warp's rows together when some score asks for it
         float mb[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          mb[h] = fmaxf(fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1])),
-                        fmaxf(fmaxf(s[2][2 * h], s[2][2 * h + 1]), fmaxf(s[3][2 * h], s[3][2 * h + 1])));
+          mb[h] = fmaxf(fmaxf(fmaxf(score(0, h, 0), score(0, h, NZ - 1)),
+                              fmaxf(score(1, h, 0), score(1, h, NZ - 1))),
+                        fmaxf(fmaxf(score(2, h, 0), score(2, h, NZ - 1)),
+                              fmaxf(score(3, h, 0), score(3, h, NZ - 1))));
         if (__any_sync(0xffffffffu, first || (mb[0] - m[0]) * c > kRescale ||
                                         (mb[1] - m[1]) * c > kRescale)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float x = mb[h];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            float x = row_reduce<ROWS>(mb[h], [](float y, float z) { return fmaxf(y, z); });
             if (x == -INFINITY) x = first ? 0.f : m[h];
             const bool raise = first || x > m[h];
             const float f = raise && !first ? fast_exp2((m[h] - x) * c) : 1.f;
             if (raise) m[h] = x;
             l[h] *= f;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              o[i][2 * h] *= f;
-              o[i][2 * h + 1] *= f;
+            for (int i = 0; i < (FLIP ? NT / 2 : NT); ++i) {
+              o[i][FLIP ? h : 2 * h] *= f;
+              o[i][FLIP ? 2 + h : 2 * h + 1] *= f;
             }
           }
         }
         first = false;
+        // P: rows (g, g + 8) x key pairs, or (FLIP) key pairs x row g, from key g x rows (2 t, 2 t + 1)
         uint32_t pf[2][4];
+        const float off[2] = {kF16Bias - m[0] * c, kF16Bias - m[1] * c};
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u) {
+          if (FLIP) {
+            const float x = fast_exp2(fmaf(score(u, 0, 0), c, off[0]));
+            const float y = fast_exp2(fmaf(score(u, 1, 0), c, off[1]));
+            l[0] += x;
+            l[1] += y;
+            pf[u / 2][u % 2] = transpose_8x8(pack_p<true>(x, y));
+          } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float off = kF16Bias - m[h] * c;
-            const float x = fast_exp2(fmaf(s[u][2 * h], c, off));
-            const float y = fast_exp2(fmaf(s[u][2 * h + 1], c, off));
-            l[h] += x + y;
-            pf[u / 2][2 * (u % 2) + h] = pack_p<true>(x, y);
+            for (int h = 0; h < 2; ++h) {
+              const float x = fast_exp2(fmaf(score(u, h, 0), c, off[h]));
+              const float y = fast_exp2(fmaf(score(u, h, 1), c, off[h]));
+              l[h] += x + y;
+              pf[u / 2][2 * (u % 2) + h] = pack_p<true>(x, y);
+            }
           }
+        }
         // O += P V, 16 keys at a time: keys 2 t, 2 t + 1 (first half of the contraction) and
         // 8 + 2 t, + 1; dims (D / 8) g .. of each
 #pragma unroll
@@ -308,30 +360,45 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
               cvt_e2m1x8((a0 & LO) | (a1 & ~LO), xa);
               cvt_e2m1x8((b0 & LO) | (b1 & ~LO), xb);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_16816(o[8 * i + 2 * k + h], pf[y], hmul2_u32(xa[k], sa), hmul2_u32(xb[k], sb));
+              for (int k = 0; k < 4; ++k) {
+                xa[k] = hmul2_u32(xa[k], sa);
+                xb[k] = hmul2_u32(xb[k], sb);
+                if (!FLIP) {
+                  mma_16816(o[(8 * i + 2 * k + h) % (FLIP ? NT / 2 : NT)], pf[y], xa[k], xb[k]);
+                } else if (k % 2) {  // column tiles 8 i + 2 (k - 1) + h and 8 i + 2 k + h
+                  const uint32_t va[4] = {xa[k - 1], xa[k], xb[k - 1], xb[k]};
+                  mma_16816(o[4 * i + 2 * h + k / 2], va, pf[y][0], pf[y][1]);
+                }
+              }
             }
         }
       }
       page_it += n;
       if (!ok) break;
       // the warps' results meet in shared memory.  Column tile i, column q of a tile is dim
-      // (D / 8) q + i: lane (g, t) holds dims (D / 4) t + i and (D / 4) t + D / 8 + i
+      // (D / 8) q + i: lane (g, t) holds dims (D / 4) t + i and (D / 4) t + D / 8 + i of its rows, or
+      // (FLIP) dims (D / 8) g + i
+      auto dim_of = [&](int i, int h, int e) {
+        const int k = i / 2 % 4;
+        return FLIP ? o[(4 * (i / 8) + 2 * (i % 2) + k / 2) % (NT / 2)][2 * (k % 2) + h]
+                    : o[i % (FLIP ? NT / 2 : NT)][2 * h + e];
+      };
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if (t == 0) sm.stat[warp][g + 8 * h] = make_float2(m[h], l[h]);
-        float* row = sm.o[warp][g + 8 * h] + t * (D / 4);
+        const int r = FLIP ? 2 * t + h : g + 8 * h;
+        l[h] = row_reduce<ROWS>(l[h], [](float y, float z) { return y + z; });
+        if ((FLIP ? g : t) == 0) sm.stat[warp][r] = make_float2(m[h], l[h]);
+        float* row = sm.o[warp][r] + (FLIP ? g * (D / 8) : t * (D / 4));
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < (FLIP ? 1 : 2); ++e)
 #pragma unroll
           for (int i = 0; i < NT; i += 4)
-            *reinterpret_cast<float4*>(row + e * (D / 8) + i) = make_float4(
-                o[i][2 * h + e], o[i + 1][2 * h + e], o[i + 2][2 * h + e], o[i + 3][2 * h + e]);
+            *reinterpret_cast<float4*>(row + e * (D / 8) + i) =
+                make_float4(dim_of(i, h, e), dim_of(i + 1, h, e), dim_of(i + 2, h, e),
+                            dim_of(i + 3, h, e));
       }
       if (!meet()) break;
-      if (tid < 256) {
+      if (tid < 16 * ROWS) {
         const int r = tid / 16, q = tid % 16;  // row, and its dims (D / 16) q ..
         const int tok = r / rp.HB, hd = r % rp.HB;
         float mx = -INFINITY, sum = 0.f, f[kMmaWarps], acc[D / 16];
@@ -393,11 +460,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
   settle_after_abort(abort_flag);
 }
 
-template <int D>
+template <int D, int ROWS>
 cudaError_t run_decode(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
-  const int smem = (int)sizeof(DecSmem<D>);
-  static_assert(sizeof(DecSmem<D>) <= 227 * 1024, "shared memory");
-  auto kern = decode_nvfp4_kernel<D>;
+  const int smem = (int)sizeof(DecSmem<D, ROWS>);
+  static_assert(sizeof(DecSmem<D, ROWS>) <= 227 * 1024, "shared memory");
+  auto kern = decode_nvfp4_kernel<D, ROWS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(p.att_ctas), dim3(kDecThreads), smem, st, p, a);
@@ -406,7 +473,9 @@ cudaError_t run_decode(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_decode_nvfp4(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
-  return p.D == 128 ? run_decode<128>(p, a, st) : run_decode<64>(p, a, st);
+  if (p.att_slot_rows <= 8)
+    return p.D == 128 ? run_decode<128, 8>(p, a, st) : run_decode<64, 8>(p, a, st);
+  return p.D == 128 ? run_decode<128, 16>(p, a, st) : run_decode<64, 16>(p, a, st);
 }
 
 }  // namespace att

@@ -172,7 +172,8 @@ def test_lengths_and_page_borders(q_lens, ctx, kv):
 
 @pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
 @pytest.mark.parametrize("H,G,D,q", [(16, 1, 128, 1), (16, 2, 64, 2), (2, 2, 128, 1), (2, 2, 64, 16),
-                                     (5, 1, 128, 3), (28, 4, 64, 2), (34, 2, 128, 1)])
+                                     (5, 1, 128, 3), (28, 4, 64, 2), (34, 2, 128, 1),
+                                     (8, 1, 128, 1), (3, 1, 128, 2), (8, 2, 64, 2), (7, 1, 64, 1)])
 def test_tiles_of_few_rows(H, G, D, q, kv):
     """Decode steps of up to 16 rows a tile (one case of 17), the last page from one key to full,
     requests without a token among them."""
