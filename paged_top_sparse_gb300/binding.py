@@ -174,6 +174,8 @@ class Plan:
         self.head_dim, self.top_k = head_dim, top_k
         self.num_tokens = sum(int(x) for x in q_lens)
         self.num_q_heads, self.num_kv_heads = num_q_heads, num_kv_heads
+        _load_types()
+        self.table_size = n * max_pages_per_req
         self.q_codes = self.problem.q_dtype == E4M3
         # shapes of a query, and of new keys or values
         self.q_shape = (self.num_tokens, num_q_heads, head_dim)
@@ -302,11 +304,12 @@ class Rope:
     def __init__(self, inv_freq, positions=None, pair_axis=None, interleaved=False):
         self.inv_freq, self.positions = inv_freq, positions
         n, axes = inv_freq.numel(), 1
-        _expect(inv_freq, "float32", "inv_freq")
+        _load_types()
+        _vector(inv_freq, _F32, n, "inv_freq")
         if n > 64:
             raise ValueError("at most 64 pairs (rotary_dim 128)")
         if positions is not None:
-            _expect(positions, "int32", "positions")
+            _vector(positions, _I32, positions.numel(), "positions")
             axes = positions.shape[0] if positions.dim() == 2 else 1
         ax = [int(a) for a in pair_axis] if pair_axis is not None else [0] * n
         if len(ax) != n or any(not 0 <= a < 256 for a in ax):
@@ -316,23 +319,27 @@ class Rope:
         self.ref = ctypes.pointer(self.args)
 
 
-_dtypes = {}
+_F32 = _I32 = _BF16 = None
 
 
-def _dtype(name):
-    if not _dtypes:
-        import torch
+def _load_types():
+    global _F32, _I32, _BF16
+    import torch
 
-        _dtypes.update(float32=torch.float32, int32=torch.int32, bfloat16=torch.bfloat16)
-    return _dtypes[name]
+    _F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
 
 
-def _expect(t, dtype, name):
-    """A contiguous tensor of the named torch dtype (or None)."""
-    if t is None:
-        return
-    if t.dtype is not _dtype(dtype) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor")
+def _vector(t, dtype, numel, name):
+    """A contiguous tensor of the type and size (or None)."""
+    if t is not None and (t.dtype is not dtype or t.numel() != numel or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements")
+
+
+def _table(t, plan):
+    """The page table's address; rows behind the batch's are allowed."""
+    if t.dtype is not _I32 or t.numel() < plan.table_size or not t.is_contiguous():
+        raise ValueError(f"page_table must be a contiguous int32 tensor of >= {plan.table_size} entries")
+    return t.data_ptr()
 
 
 def _rope(rope, plan):
@@ -341,19 +348,15 @@ def _rope(rope, plan):
     return rope.ref
 
 
-def _token_stride(t, shape, name):
-    """Elements between the tokens of a [T][heads][D] view whose rows are contiguous."""
-    st = t.stride()
-    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
-        raise ValueError(f"{name} must be [{shape[0]}][{shape[1]}][{shape[2]}] with contiguous rows")
-    return st[0] if shape[0] > 1 else shape[1] * shape[2]
-
-
 def _rows(t, shape, name, codes=False):
-    """The token stride of BF16 rows, or of rows of one-byte codes."""
-    if t.element_size() != 1 if codes else t.dtype is not _dtype("bfloat16"):
-        raise ValueError(f"{name} must hold {'E4M3 codes' if codes else 'bfloat16'}")
-    return _token_stride(t, shape, name)
+    """Elements between the tokens of a [T][heads][D] view of BF16, or of one-byte codes, whose rows
+    are contiguous."""
+    st = t.stride()
+    if (t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1)
+            or (t.element_size() != 1 if codes else t.dtype is not _BF16)):
+        raise ValueError(f"{name} must be [{shape[0]}][{shape[1]}][{shape[2]}] "
+                         f"{'codes' if codes else 'bfloat16'} with contiguous rows")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_scale, k_out,
@@ -361,8 +364,8 @@ def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_s
     """Norm per head and rotation of q [T][H][D] and k [T][H_kv][D] (or None); token strides come
     from the tensors.  A one-byte ``q_out`` takes E4M3 codes of the result / ``q_scale``."""
     qs, ks = plan.q_shape, plan.kv_shape
-    _expect(q_weight, "float32", "q_weight")
-    _expect(k_weight, "float32", "k_weight")
+    _vector(q_weight, _F32, plan.head_dim, "q_weight")
+    _vector(k_weight, _F32, plan.head_dim, "k_weight")
     codes = q_out.element_size() == 1
     st = (_lib or lib()).sps_qk_norm_rope(
         plan.handle, q.data_ptr(), _rows(q, qs, "q"), _ptr(k),
@@ -380,11 +383,11 @@ def sps_kv_append_rope(plan: Plan, k_new, v_new, k_weight, eps, rope, page_table
     """``sps_kv_append`` with the key's norm and rotation on the way; k_new / v_new [T][H_kv][D]
     may be views with a token stride."""
     ks = plan.kv_shape
-    _expect(k_weight, "float32", "k_weight")
+    _vector(k_weight, _F32, plan.head_dim, "k_weight")
     st = (_lib or lib()).sps_kv_append_rope(
         plan.handle, k_new.data_ptr(), _rows(k_new, ks, "k_new"), v_new.data_ptr(),
         _rows(v_new, ks, "v_new"), _ptr(k_weight), eps,
-        None if rope is None else _rope(rope, plan), page_table.data_ptr(), k_cache.data_ptr(),
+        None if rope is None else _rope(rope, plan), _table(page_table, plan), k_cache.data_ptr(),
         v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), workspace.data_ptr(), _stream(stream))
     if st:
         _check(st)
@@ -402,12 +405,10 @@ def paged_attention_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_sc
     """Full causal attention of q [T][H][D] over the paged cache into out [T][H][D] BF16 (both may
     have a token stride) and, unless None, out_lse [T][H] FP32."""
     qs = plan.q_shape
-    _expect(out_lse, "float32", "out_lse")
-    if out_lse is not None and out_lse.numel() != qs[0] * qs[1]:
-        raise ValueError(f"out_lse must be [{qs[0]}][{qs[1]}]")
+    _vector(out_lse, _F32, qs[0] * qs[1], "out_lse")
     st = (_lib or lib()).paged_attention_fwd(
         plan.handle, q.data_ptr(), _rows(q, qs, "q", plan.q_codes), q_scale, k_cache.data_ptr(),
-        v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), out.data_ptr(),
+        v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), _table(page_table, plan), out.data_ptr(),
         _rows(out, qs, "out"), _ptr(out_lse), scratch.data_ptr(), scratch.nbytes,
         workspace.data_ptr(), _stream(stream))
     if st:

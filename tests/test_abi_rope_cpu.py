@@ -136,11 +136,20 @@ def test_binding_checks_shapes():
     q = torch.zeros(T, H, D, dtype=torch.bfloat16)
     for bad in (q[:, :2], q[:3], q.transpose(1, 2), q[..., ::2]):
         with pytest.raises(ValueError):
-            B._token_stride(bad, plan.q_shape, "q")
-    assert B._token_stride(torch.zeros(T, H + 3, D)[:, 1:1 + H], plan.q_shape, "q") == (H + 3) * D
+            B._rows(bad, plan.q_shape, "q")
+    wide = torch.zeros(T, H + 3, D, dtype=torch.bfloat16)
+    assert B._rows(wide[:, 1:1 + H], plan.q_shape, "q") == (H + 3) * D
     for bad, codes in ((q.half(), False), (q.float(), False), (q, True)):
         with pytest.raises(ValueError):
             B._rows(bad, plan.q_shape, "q", codes)
+    with pytest.raises(ValueError):
+        B.sps_qk_norm_rope(plan, q, None, torch.ones(D // 2), None, 1e-6, None, q, 1.0, None, q)
+    with pytest.raises(ValueError):
+        B.sps_kv_append_rope(plan, q[:, :G], q[:, G:], None, 1e-6, None,
+                             torch.zeros(1, dtype=torch.int64), q, q, None, None, q)
+    with pytest.raises(ValueError):
+        B.paged_attention_fwd(plan, q, 1.0, q, q, None, None, torch.zeros(0, dtype=torch.int32), q,
+                              None, q, q)
     assert B._rows(q, plan.q_shape, "q") == B._rows(q.to(torch.uint8), plan.q_shape, "q", True) == H * D
     with pytest.raises(ValueError):
         B._rope(B.Rope(f, positions=torch.zeros(T - 1, dtype=torch.int32)), plan)
