@@ -27,8 +27,8 @@
 // 8192-token prompt 367 us (1.50 PFLOP/s, 0.77 of a large library product at boost clocks, 0.86
 // of its sustained rate), 8 x 512 after 32K 1.40 ms (1.59).  Single tokens: the cache's bytes; 64
 // after 32K (2.16 GB) 320 us, 6.75 TB/s. An NVFP4 cache adds the conversion of each tile in the
-// same SM's issue slots: four chunks of 200 to 700 after 2K to 9K 147 us (0.93 PFLOP/s), 64 x 3
-// tokens after 32K 248 us.
+// same SM's issue slots: four chunks of 200 to 700 after 2K to 9K 140 us (0.98 PFLOP/s), 64 x 3
+// tokens after 32K 242 us.
 //
 // One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
 //   warp 0     page-table reads and the copies: Q tiles and the K, V tiles of a page into a ring
@@ -716,24 +716,35 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           mbar_arrive(smem_u32(&sm.kv_full[sg]));
           mbar_arrive(smem_u32(&sm.raw_empty[r]));
         }
-        // E4M3 Q rows, exactly, into the FP16 operand tiles, behind the first K tile
+        // E4M3 Q rows, exactly, into the FP16 operand tiles, behind the first K tile (behind as many
+        // tiles as the ring holds measured the same)
         for (int t = 0; i == 0 && t < (SINGLE ? 1 : pc.nt) && ok; ++t) {
+          // this thread's 16-byte chunks of the tile, all on the way at once (one after another
+          // they took 5400 cycles of a piece's start)
+          constexpr int QCH = D / 16;
+          uint4 qx[QCH];
+#pragma unroll
+          for (int k = 0; k < QCH; ++k) {
+            const int ch = ct + 128 * k, row = ch / QCH, col = ch % QCH;
+            const int tok = pc.tok0 + t * rp.TB + row / rp.HB, hg = h0 + row % rp.HB;
+            qx[k] = make_uint4(0, 0, 0, 0);
+            if (row < rp.HB * rp.TB && tok < pc.q_len && hg < p.Hg)
+              qx[k] = __ldg(reinterpret_cast<const uint4*>(
+                  a.q + (pc.flat0 + tok) * a.q_stride +
+                  (int64_t)((pc.vg / rp.blocks) * p.Hg + hg) * D + col * 16));
+          }
           uint32_t& qc = t ? qc1 : qc0;
           ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
           if (!ok) break;
           ++qc;
-          for (int ch = ct; ch < 128 * (D / 16); ch += 128) {
-            const int row = ch / (D / 16), col = ch % (D / 16);
-            const int tok = pc.tok0 + t * rp.TB + row / rp.HB, hg = h0 + row % rp.HB;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (row < rp.HB * rp.TB && tok < pc.q_len && hg < p.Hg)
-              x = __ldg(reinterpret_cast<const uint4*>(
-                  a.q + (pc.flat0 + tok) * a.q_stride +
-                  (int64_t)((pc.vg / rp.blocks) * p.Hg + hg) * D + col * 16));
-            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < QCH; ++k) {
+            const int ch = ct + 128 * k, row = ch / QCH, col = ch % QCH;
+            const uint32_t wd[4] = {qx[k].x, qx[k].y, qx[k].z, qx[k].w};
             uint32_t o[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = cvt_e4m3x2((uint16_t)(wd[k / 2] >> (16 * (k & 1))));
+            for (int e = 0; e < 8; ++e)
+              o[e] = cvt_e4m3x2((uint16_t)(wd[e / 2] >> (16 * (e & 1))));
             uint8_t* d = sm.q[t] + (col / 4) * 16384;
             *reinterpret_cast<uint4*>(d + sw128_offset(row, 2 * (col % 4))) =
                 make_uint4(o[0], o[1], o[2], o[3]);
