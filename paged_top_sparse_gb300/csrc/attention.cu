@@ -27,8 +27,8 @@
 // 8192-token prompt 367 us (1.50 PFLOP/s, 0.77 of a large library product at boost clocks, 0.86
 // of its sustained rate), 8 x 512 after 32K 1.40 ms (1.59).  Single tokens: the cache's bytes; 64
 // after 32K (2.16 GB) 320 us, 6.75 TB/s. An NVFP4 cache adds the conversion of each tile in the
-// same SM's issue slots: four chunks of 200 to 700 after 2K to 9K 140 us (0.98 PFLOP/s), 64 x 3
-// tokens after 32K 242 us.
+// same SM's issue slots: four chunks of 200 to 700 after 2K to 9K 138 us (0.99 PFLOP/s), 64 x 3
+// tokens after 32K 225 us.
 //
 // One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
 //   warp 0     page-table reads and the copies: Q tiles and the K, V tiles of a page into a ring
@@ -193,13 +193,15 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           k_tile = __shfl_sync(0xffffffffu, ids, at);
           if (QUANT) {
             // the copies in flight hold too few bytes to cover the memory's latency: pages go to
-            // L2 kAhead steps before their copy (at the start all of the first ones at once)
-            constexpr int kAhead = 12;
+            // L2 kAhead steps before their copy (at the start all of the first ones at once, but
+            // for those whose copies come right behind: fetched twice they cost 64 x 3 tokens
+            // after 32K 225 -> 243 us; without any such start 247)
+            constexpr int kAhead = 8, kDirect = 2;
             const int f = s == 0 ? lane : s + kAhead;
             const int src = f & 31;
             const int t = s == 0 ? ids
                                  : __shfl_sync(0xffffffffu, f / 32 == s / 32 ? ids : next_ids, src);
-            if (f < n && (s == 0 ? lane <= kAhead : lane < 4)) {
+            if (f < n && (s == 0 ? lane > kDirect && lane <= kAhead : lane < 4)) {
               if (s == 0 || lane == 0) bulk_prefetch_l2(a.kc + (int64_t)t * (64 * D), 64 * D);
               if (s == 0 || lane == 1) bulk_prefetch_l2(a.vc + (int64_t)t * (64 * D), 64 * D);
               if (s == 0 || lane == 2) bulk_prefetch_l2(a.ks + (int64_t)t * (8 * D), 8 * D);
