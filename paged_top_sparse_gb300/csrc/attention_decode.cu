@@ -9,12 +9,12 @@
 // nothing is written back.  64 tokens after 32K (H 32 / H_kv 2, D 128): 278 us there, 159 here;
 // one token after 8K 15 and 9.5.
 //
-// Bound: the SM's issue slots and its warp-level products.  A 32-key chunk costs its warp about
-// 64 products, 128 conversions and 128 multiplications by block scales, some 1250 cycles of one
-// scheduler, and a page gives each of the four schedulers one chunk: 1400 cycles a page measured,
-// 3.8 TB/s (copying the same pages and doing nothing takes 103 us).  Twelve product warps (161
-// us), copies issued by the last warp to leave a stage (161) and pages fetched into L2 ahead
-// (181) were no faster.
+// Bound: the warps' own chains of conversion and product.  A 32-key chunk costs its warp about 64
+// products, 128 conversions and 128 multiplications by block scales, a page gives each of the four
+// schedulers one chunk, and two or three warps a scheduler hide only part of each other's waits: 64
+// tokens after 32K read 4.0 TB/s with issue slots 45 %, the tensor pipe 40 % and DRAM 51 % busy
+// (copying the same pages and doing nothing takes 103 us).  Copies issued by the last warp to leave a
+// stage (161 us) and pages fetched into L2 ahead (181) were no faster.
 //
 // Mathematics as in attention.cu: p = 2^((s - m) c + 7) with a lazily raised reference m, l and O in
 // FP32, P rounded to FP16.
@@ -32,8 +32,7 @@
 // Tiles of at most 8 rows (groups of up to 8 heads) turn both products round, K Q^T and V^T P^T: the
 // keys, then the dims, are the instruction's 16 rows and the query rows its 8 columns, so half as
 // many products do, P crossing the warp as transposed 8 x 8 tiles.  The converted registers are the
-// same.  64 tokens after 32K, H 32: H_kv 8 564 -> 452 us (5.4 TB/s), H_kv 4 290 -> 233; one token
-// after 8K 10.6 -> 8.5.
+// same.  64 tokens after 32K, H 32: H_kv 8 564 -> 452 us, H_kv 4 290 -> 233 (with 8 warps).
 #include "attention.cuh"
 #include "nvfp4.cuh"
 
@@ -41,26 +40,31 @@ namespace sps {
 namespace att {
 namespace {
 
-constexpr int kMmaWarps = 8;
-constexpr int kChunks = 4;                        // 32-key chunks of a page
-constexpr int kPageStep = kMmaWarps / kChunks;    // a warp takes a chunk of every kPageStep-th page
-static_assert(kMmaWarps % kChunks == 0, "a warp keeps its place in the page");
+constexpr int kChunks = 4;     // 32-key chunks of a page
 constexpr int kCopyWarps = 2;  // a warp copies every kCopyWarps-th page (D 64: one 120 us, two 103)
-constexpr int kDecThreads = 32 * (kMmaWarps + kCopyWarps);
+// Product warps: 12 where 128 registers (four warps a scheduler) hold the accumulators, else 8.
+// 64 tokens after 32K: 8 rows, D 128, H_kv 8 457 us with 8 and 412 with 12; D 64 306 and 266; 16
+// rows, D 64 103 and 90, D 128 158 and 161.  (A context of a few pages loses 0.5 us of 9 by them.)
+template <int D, int ROWS>
+constexpr int kWarps = D * ROWS <= 1024 ? 12 : 8;
 
 template <int D, int ROWS>
 struct DecSmem {
+  static constexpr int WARPS = kWarps<D, ROWS>;
+  static constexpr int STEP = WARPS / kChunks;  // a warp takes a chunk of every STEP-th page
+  static_assert(WARPS % kChunks == 0, "a warp keeps its place in the page");
+  static constexpr int UNIT = STEP % kCopyWarps ? STEP * kCopyWarps : STEP;
   static constexpr int CODES = 64 * D, SCALES = 8 * D;  // of a 128-key tile
   static constexpr int PAGE = 2 * (CODES + SCALES);     // K codes, K scales, V codes, V scales
-  static constexpr int S0 = (227 * 1024 - kMmaWarps * ROWS * (D * 4 + 8) - D * 32 - 512) / PAGE;
-  // A multiple of kPageStep: a warp then finds in a stage, each time round, the page after one that
-  // it took itself, so that the phase it waits for is never more than one ahead of the barrier's (a
-  // parity wait two phases ahead passes at once).  Between pieces the warps meet.
-  static constexpr int STAGES = (S0 > 12 ? 12 : S0) / 4 * 4;
-  static_assert(4 % kPageStep == 0 && 4 % kCopyWarps == 0 && STAGES >= 8, "a warp's own stages");
+  static constexpr int S0 = (227 * 1024 - WARPS * ROWS * (D * 4 + 8) - D * 32 - 512) / PAGE;
+  // A multiple of STEP and kCopyWarps: a warp then finds in a stage, each time round, the page after
+  // one that it took itself, so that the phase it waits for is never more than one ahead of the
+  // barrier's (a parity wait two phases ahead passes at once).  Between pieces the warps meet.
+  static constexpr int STAGES = (S0 > 12 ? 12 : S0) / UNIT * UNIT;
+  static_assert(UNIT % STEP == 0 && UNIT % kCopyWarps == 0 && STAGES >= 6, "stages");
   uint8_t page[STAGES][PAGE];
-  float o[kMmaWarps][ROWS][D];
-  float2 stat[kMmaWarps][ROWS];  // (m, l)
+  float o[WARPS][ROWS][D];
+  float2 stat[WARPS][ROWS];  // (m, l)
   uint4 qf[D / 16][32];        // Q fragments, k-step by lane
   uint64_t full[STAGES], empty[STAGES], meet;
   int abort_flag;
@@ -92,8 +96,10 @@ __device__ __forceinline__ float row_reduce(float x, Op op) {
 }
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p, AttArgs a) {
+__global__ void __launch_bounds__(32 * (kWarps<D, ROWS> + kCopyWarps), 1)
+decode_nvfp4_kernel(DevPlan p, AttArgs a) {
   using Smem = DecSmem<D, ROWS>;
+  constexpr int WARPS = Smem::WARPS;
   constexpr bool FLIP = ROWS == 8;  // keys, and then dims, as the products' 16 rows
   constexpr int S = Smem::STAGES, WORDS = D / 32;  // WORDS: 8-code words of a key in a lane
   constexpr int NT = D / 8;                        // column tiles of O
@@ -107,7 +113,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       mbar_init(smem_u32(&sm.full[i]), 1);
       mbar_init(smem_u32(&sm.empty[i]), kChunks);
     }
-    mbar_init(smem_u32(&sm.meet), kMmaWarps);
+    mbar_init(smem_u32(&sm.meet), WARPS);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
   PieceList work(p);
   Piece pc;
 
-  if (warp >= kMmaWarps) {
+  if (warp >= WARPS) {
     // ------------------------------------------------ copies
     uint32_t page_it = 0;  // pages before the piece
     bool ok = true;
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       const int n = pc.page1 - pc.page0;
       const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
       // this warp's pages of the piece: s0, s0 + kCopyWarps, ...; a lane holds every one's tile
-      const int s0 = (int)((warp - kMmaWarps + kCopyWarps - page_it % kCopyWarps) % kCopyWarps);
+      const int s0 = (int)((warp - WARPS + kCopyWarps - page_it % kCopyWarps) % kCopyWarps);
       auto load_ids = [&](int k) {  // physical tiles of its pages k + lane
         const int s = s0 + (k + lane) * kCopyWarps;
         int id = 0;
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       }
       // Q fragments, a k-step per warp: (row g, row g + 8) x columns 2 t and 2 t + 8, which are the
       // lane's dims 4 k .. 4 k + 3
-      for (int k = warp; k < D / 16; k += kMmaWarps) {
+      for (int k = warp; k < D / 16; k += WARPS) {
         uint32_t f[4] = {};
 #pragma unroll
         for (int h = 0; h < (FLIP ? 1 : 2); ++h) {
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
       bool first = true;
-      for (int ch = warp; ch < kChunks * n; ch += kMmaWarps) {
+      for (int ch = warp; ch < kChunks * n; ch += WARPS) {
         const uint32_t it = page_it + ch / kChunks, stg = it % S;
         if (!mbar_wait(smem_u32(&sm.full[stg]), (it / S) & 1, abort_flag, status)) {
           ok = false;
@@ -401,15 +407,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
       if (tid < 16 * ROWS) {
         const int r = tid / 16, q = tid % 16;  // row, and its dims (D / 16) q ..
         const int tok = r / rp.HB, hd = r % rp.HB;
-        float mx = -INFINITY, sum = 0.f, f[kMmaWarps], acc[D / 16];
+        float mx = -INFINITY, sum = 0.f, f[WARPS], acc[D / 16];
 #pragma unroll
-        for (int k = 0; k < kMmaWarps; ++k) {
+        for (int k = 0; k < WARPS; ++k) {
           const float2 x = sm.stat[k][r];
           f[k] = x.x;
           if (x.y > 0.f) mx = fmaxf(mx, x.x);
         }
 #pragma unroll
-        for (int k = 0; k < kMmaWarps; ++k) {
+        for (int k = 0; k < WARPS; ++k) {
           const float lk = sm.stat[k][r].y;
           f[k] = lk > 0.f ? fast_exp2((f[k] - mx) * c) : 0.f;
           sum += lk * f[k];
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_nvfp4_kernel(DevPlan p,
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) acc[e] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kMmaWarps; ++k)
+        for (int k = 0; k < WARPS; ++k)
           if (f[k] != 0.f) {
 #pragma unroll
             for (int e = 0; e < D / 16; e += 4) {
@@ -467,7 +473,8 @@ cudaError_t run_decode(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
   auto kern = decode_nvfp4_kernel<D, ROWS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(p.att_ctas), dim3(kDecThreads), smem, st, p, a);
+  return launch_pdl(kern, dim3(p.att_ctas), dim3(32 * (kWarps<D, ROWS> + kCopyWarps)), smem, st, p,
+                    a);
 }
 
 }  // namespace
