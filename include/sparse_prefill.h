@@ -472,7 +472,9 @@ sps_status sparse_prefill_fwd_noalloc(const sps_plan* plan, const void* q, float
  * Accumulation, maxima and sums are FP32; P is rounded to the 16-bit type of the second product
  * (BF16; FP16 over an NVFP4 cache, whose code x scale products are exact there).  The result is the
  * same bits from call to call.  A captured call may be replayed after another plan that differs
- * in ctx_lens alone has been uploaded to the same workspace (a decode loop).  top_k is not used.
+ * in ctx_lens alone has been uploaded to the same workspace (a decode loop; the workspace is as
+ * large as the largest of those plans asks).  So may a captured sps_qk_norm_rope or
+ * sps_kv_append_rope.  top_k is not used.
  * A page-table entry outside [0, num_phys_pages) sets SPS_DEV_BAD_PAGE (the outputs are then
  * undefined).
  */

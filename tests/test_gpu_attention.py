@@ -430,3 +430,68 @@ def test_step_of_norm_rotation_append_and_attention(kv):
     y = torch.cat((n_[..., :64] * c_ - n_[..., 64:] * s_, n_[..., 64:] * c_ + n_[..., :64] * s_), -1)
     rel = float((k - y.transpose(0, 1)).norm() / y.norm())
     assert rel <= (2.0 ** -8 if kv == "bf16" else 0.25)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("H,G,D", [(16, 1, 128), (8, 2, 64)])
+def test_captured_decode_step_equals_the_eager_calls(H, G, D, kv):
+    """One graph of norm and rotation, append and attention, replayed while the contexts grow over
+    page borders: the same bits as eager calls on a cache of their own."""
+    from paged_top_sparse_gb300 import binding as B
+
+    ctx, steps, pages = [126, 500, 0], 4, 5
+    n = len(ctx)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(H + D)
+    pt = torch.arange(n * pages, dtype=torch.int32, device=DEV).flip(0).reshape(n, pages)
+    rope = B.Rope((1e4 ** (-torch.arange(D // 2, device=DEV, dtype=torch.float64) * 2 / D)).float())
+    w = 1 + 0.1 * torch.randn(D, generator=g, device=DEV)
+    quant = kv == "nvfp4"
+
+    class Side:
+        def __init__(self):
+            shape = (n * pages, G, 128, D // 2 if quant else D)
+            dt = torch.uint8 if quant else torch.bfloat16
+            self.kc, self.vc = (torch.zeros(shape, dtype=dt, device=DEV) for _ in "kv")
+            self.ks = self.vs = None
+            if quant:
+                self.ks, self.vs = (torch.zeros((n * pages, G, 128, D // 16), dtype=torch.uint8, device=DEV)
+                                    for _ in "kv")
+            self.x = torch.zeros((n, H + 2 * G, D), dtype=torch.bfloat16, device=DEV)
+            self.q = torch.zeros((n, H, D), dtype=torch.uint8 if quant else torch.bfloat16, device=DEV)
+            self.out = torch.zeros((n, H, D), dtype=torch.bfloat16, device=DEV)
+            self.ws = torch.zeros(max(p.workspace_bytes for p in plans), dtype=torch.uint8, device=DEV)
+            self.scratch = torch.zeros(B.paged_attention_scratch(plans[0]), dtype=torch.uint8, device=DEV)
+
+        def step(self, plan, stream=None):
+            x, s = self.x, 0.02 if quant else 1.0
+            B.sps_qk_norm_rope(plan, x[:, :H], None, w, None, 1e-6, rope, self.q, s, None, self.ws, stream)
+            B.sps_kv_append_rope(plan, x[:, H:H + G], x[:, H + G:], w, 1e-6, rope, pt, self.kc, self.vc,
+                                 self.ks, self.vs, self.ws, stream)
+            B.paged_attention_fwd(plan, self.q, s, self.kc, self.vc, self.ks, self.vs, pt, self.out, None,
+                                  self.scratch, self.ws, stream)
+
+    plans = [B.Plan([1] * n, [c + i for c in ctx], H, G, D, 1, pages, n * pages,
+                    q_dtype="e4m3" if quant else "bf16", kv_dtype=kv) for i in range(steps)]
+    a, b = Side(), Side()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    B.sps_plan_upload(plans[0], a.ws, s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        a.step(plans[0], s)
+    for i, plan in enumerate(plans):
+        x = torch.randn((n, H + 2 * G, D), generator=g, device=DEV).bfloat16()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            a.x.copy_(x)
+            B.sps_plan_upload(plan, a.ws, s)
+            graph.replay()
+        b.x.copy_(x)
+        B.sps_plan_upload(plan, b.ws)
+        b.step(plan)
+        torch.cuda.synchronize()
+        assert B.sps_read_device_status(plan, a.ws) == 0
+        assert torch.equal(a.q, b.q) and torch.equal(a.kc, b.kc) and torch.equal(a.vc, b.vc)
+        assert torch.equal(a.out, b.out) and bool(torch.isfinite(a.out.float()).all())
+        assert not bool((a.out == 0).all())
