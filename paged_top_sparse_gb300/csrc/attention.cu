@@ -885,13 +885,15 @@ attention_merge_pieces_kernel(DevPlan p, AttArgs a) {
   constexpr int E = D / 32;  // elements per lane
   __shared__ float wts[kMaxCtas];
   __shared__ float sums[8][32 * E];
-  pdl_wait();
-  pdl_trigger();
+  // The entry is the plan's: the products' kernel lets nothing begin before its blocks end, and
+  // they began after the upload.  (One token after 8K 10.3 -> 10.1 us, 32 after 1K 36.4 -> 35.6.)
   const AttMerge mg = p.att_merges[blockIdx.x];
-  if (mg.req < 0) return;
   const RowPack rp(p.Hg);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lr = blockIdx.y;
   const MergeRow row = merge_row(p, rp, mg, lr);
+  pdl_wait();
+  pdl_trigger();
+  if (mg.req < 0) return;
   if (!row.live) return;  // the whole block
   const int np = mg.cta1 - mg.cta0 + 1;
   // this warp's first pieces are on the way while the weights are found
