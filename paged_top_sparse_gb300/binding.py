@@ -173,7 +173,6 @@ class Plan:
         self.workspace_bytes = ws.value
         self.head_dim, self.top_k = head_dim, top_k
         self.num_tokens = sum(int(x) for x in q_lens)
-        self.num_q_heads, self.num_kv_heads = num_q_heads, num_kv_heads
         _load_types()
         self.table_size = n * max_pages_per_req
         self.q_codes = self.problem.q_dtype == E4M3
