@@ -253,7 +253,9 @@ void build_indexer_tasks(sps_plan* pl) {
 // Costs are in pages (about 1.6 us): a piece's pages plus kAttTileCost for its fill, drain and
 // epilogue.  A cut tile's partial rows are written and merged by a second kernel, which is estimated
 // too; of the splits made, the one with the smallest estimate is kept.
-constexpr int kAttTileCost = 2, kAttMinPiece = 3;
+// A left-over piece has at least kAttMinPiece pages (32 tokens after 1K: 3 cost 36.0 us, 5 34.4; 8
+// cost four chunks after 2K to 9K 3 % more), and a tile cost of 1 or 3 measured slower or the same.
+constexpr int kAttTileCost = 2, kAttMinPiece = 5;
 
 struct AttTile {
   int32_t req, vg, tile, pages;
