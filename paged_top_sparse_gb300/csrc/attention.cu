@@ -43,6 +43,7 @@
 //   warps 12-15 (NVFP4)  conversion of E4M3 Q and NVFP4 K, V into FP16 operand tiles.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "attention.cuh"
@@ -79,6 +80,7 @@ struct AttSmem {
   uint64_t o_free[2], stat_full, tail_go, tail_done, done;
   float2 stat[128];  // (m, l) of the odd pages' rows
   uint32_t tmem_base;
+  uint32_t progress;  // pieces begun, by the MMA warp
   int abort_flag;
 };
 
@@ -144,6 +146,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     mbar_init(smem_u32(&sm.tail_go), 1);
     mbar_init(smem_u32(&sm.tail_done), 1);
     mbar_init(smem_u32(&sm.done), 1);
+    sm.progress = 0;
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -159,6 +162,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   pdl_wait();
   const uint32_t tmem = sm.tmem_base;  // S0 S1 at columns 0, 128; O0 O1 at 256, 384
   volatile int* abort_flag = &sm.abort_flag;
+  // Two roles skip pieces that are not theirs (the second softmax warpgroup those of one page and
+  // one row tile, warp 2 those without a tail), so one wait of theirs may last as long as a block's
+  // other pieces: its deadline follows the pieces.
+  volatile uint32_t* progress = &sm.progress;
   PieceList work(p);
   Piece pc;
 
@@ -319,7 +326,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         half(1);
         if (last) commit(sm.o_done[t]);
       };
+      uint32_t begun = 0;
       while (ok && work.next(p, rp, pc)) {
+        if (leader) *progress = ++begun;
         const int n = pc.page1 - pc.page0;
         // rows of the last page behind the request's last token
         const bool tail = !QUANT && pc.page1 * 128 > pc.ctx + pc.q_len;
@@ -397,7 +406,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       while (work.next(p, rp, pc)) {
         const int n = pc.page1 - pc.page0, kv_len = pc.ctx + pc.q_len;
         if (pc.page1 * 128 > kv_len) {
-          if (!mbar_wait(smem_u32(&sm.tail_go), tc & 1, abort_flag, status)) break;
+          if (!mbar_wait_beside(smem_u32(&sm.tail_go), tc & 1, abort_flag, status, progress,
+                                a.skip_wait_ns))
+            break;
           ++tc;
           const int r0 = kv_len - (pc.page1 - 1) * 128;  // rows r0 .. 127
           uint8_t* v = sm.kv[(it + 2 * n - 1) % S];
@@ -439,7 +450,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int page = pc.page0 + (split ? 2 * j + w : j);
         const int nvis = valid ? pos - page * 128 + 1 : 128;
         const bool masked = __any_sync(0xffffffffu, nvis < 128);
-        if (!mbar_wait(smem_u32(&sm.s_full[w]), su & 1, abort_flag, status)) { ok = false; break; }
+        if (!mbar_wait_beside(smem_u32(&sm.s_full[w]), su & 1, abort_flag, status, progress,
+                              a.skip_wait_ns)) {
+          ok = false;
+          break;
+        }
         ++su;  // (a commit covers what its thread issued before: the last product into O_w too)
         const uint32_t bar_half = smem_u32(&sm.p_half[w]), bar_full = smem_u32(&sm.p_full[w]);
         bool half_sent = false;
@@ -1011,7 +1026,14 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
   return run_merge<D>(p, a, st);
 }
 
+std::atomic<uint64_t> g_skip_wait_ns{kWaitLimitNs};
+
 }  // namespace
+
+// Limit of the waits that follow the block's pieces, for a test of them (0: the library's).
+extern "C" void sps_internal_attention_wait(int64_t limit_ns) {
+  g_skip_wait_ns = limit_ns > 0 ? (uint64_t)limit_ns : kWaitLimitNs;
+}
 
 cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_t q_stride,
                              float q_scale, const void* kc, const void* vc, const void* ks,
@@ -1032,6 +1054,7 @@ cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_
   a.part = static_cast<float*>(scratch);
   a.part_lse = a.part + 2ll * p.att_ctas * p.att_slot_rows * p.D;
   a.c = p.sm_scale * q_scale * 1.4426950408889634f;
+  a.skip_wait_ns = g_skip_wait_ns.load(std::memory_order_relaxed);
   const RowPack rp(p.Hg);
   const bool single = p.att_slot_rows <= rp.TB * rp.HB;
 #define SPS_ATT(DD, QQ) \

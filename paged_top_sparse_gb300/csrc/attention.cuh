@@ -81,6 +81,7 @@ struct AttArgs {
   float* out_lse;
   float *part, *part_lse;  // [2 att_ctas][slot rows][D], [2 att_ctas][slot rows]
   float c;                 // softmax scale x q_scale x log2 e
+  uint64_t skip_wait_ns;   // limit of a wait that follows the block's pieces
 };
 
 // Single tokens over an NVFP4 cache (tiles of at most 16 rows): the products' part of launch_attention.

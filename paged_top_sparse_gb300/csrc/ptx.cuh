@@ -85,6 +85,32 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same wait for a role that takes part in only some of the block's work, and so may wait while
+// the others go through any amount of it: the deadline starts again whenever the word at `progress`,
+// which a role in step with the work advances, has changed.
+__device__ __forceinline__ bool mbar_wait_beside(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                 int32_t* status, const volatile uint32_t* progress,
+                                                 uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = globaltimer_ns();
+  uint32_t seen = *progress;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (*abort) return false;
+      const uint32_t now = *progress;
+      if (now != seen) {
+        seen = now;
+        t0 = globaltimer_ns();
+      } else if (globaltimer_ns() - t0 > limit_ns) {
+        set_status(status, DEV_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // After a role gave up (an abort), every thread of the block waits this long before the block
 // exits, so that copies its producers had already issued finish landing in its shared memory
 // (a copy takes microseconds); only the abort path pays it.  Placed before the kernel's final
