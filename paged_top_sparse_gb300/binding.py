@@ -174,7 +174,7 @@ class Plan:
         self.head_dim, self.top_k = head_dim, top_k
         self.num_tokens = sum(int(x) for x in q_lens)
         _load_types()
-        self.table_size = n * max_pages_per_req
+        self.table_width, self.table_size = max_pages_per_req, n * max_pages_per_req
         self.q_codes = self.problem.q_dtype == E4M3
         # shapes of a query, and of new keys or values
         self.q_shape = (self.num_tokens, num_q_heads, head_dim)
@@ -335,9 +335,12 @@ def _vector(t, dtype, numel, name):
 
 
 def _table(t, plan):
-    """The page table's address; rows behind the batch's are allowed."""
-    if t.dtype is not _I32 or t.numel() < plan.table_size or not t.is_contiguous():
-        raise ValueError(f"page_table must be a contiguous int32 tensor of >= {plan.table_size} entries")
+    """The page table's address: rows of max_pages_per_req entries, or those in one flat vector; rows
+    behind the batch's are allowed."""
+    if (t.dtype is not _I32 or t.numel() < plan.table_size or not t.is_contiguous()
+            or (t.dim() > 1 and t.shape[-1] != plan.table_width)):
+        raise ValueError(f"page_table must be a contiguous int32 tensor of >= {plan.table_size} entries "
+                         f"in rows of {plan.table_width}")
     return t.data_ptr()
 
 
