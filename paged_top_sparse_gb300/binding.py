@@ -174,8 +174,13 @@ class Plan:
         self.head_dim, self.top_k = head_dim, top_k
         self.num_tokens = sum(int(x) for x in q_lens)
         _load_types()
-        self.table_width, self.table_size = max_pages_per_req, n * max_pages_per_req
+        self.table_shape, self.table_size = (n, max_pages_per_req), n * max_pages_per_req
         self.q_codes = self.problem.q_dtype == E4M3
+        self.quant_kv = self.problem.kv_dtype == NVFP4
+        # bytes of a cache (an NVFP4 one's scales: an eighth of them), and the types that may hold it
+        elems = num_phys_pages * num_kv_heads * page_size * head_dim
+        self.cache_bytes = elems // 2 if self.quant_kv else elems * 2
+        self.cache_types = _CODES if self.quant_kv else _BITS16
         # shapes of a query, and of new keys or values
         self.q_shape = (self.num_tokens, num_q_heads, head_dim)
         self.kv_shape = (self.num_tokens, num_kv_heads, head_dim)
@@ -318,14 +323,16 @@ class Rope:
         self.ref = ctypes.pointer(self.args)
 
 
-_F32 = _I32 = _BF16 = None
+_F32 = _I32 = _BF16 = _BITS16 = _CODES = None
 
 
 def _load_types():
-    global _F32, _I32, _BF16
+    global _F32, _I32, _BF16, _BITS16, _CODES
     import torch
 
     _F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+    _BITS16 = {torch.bfloat16, torch.int16, torch.uint16}
+    _CODES = {torch.uint8, torch.int8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)}
 
 
 def _vector(t, dtype, numel, name):
@@ -337,10 +344,35 @@ def _vector(t, dtype, numel, name):
 def _table(t, plan):
     """The page table's address: rows of max_pages_per_req entries, or those in one flat vector; rows
     behind the batch's are allowed."""
-    if (t.dtype is not _I32 or t.numel() < plan.table_size or not t.is_contiguous()
-            or (t.dim() > 1 and t.shape[-1] != plan.table_width)):
+    if (t.dtype is not _I32 or not t.is_contiguous()
+            or (t.shape != plan.table_shape
+                and (t.numel() < plan.table_size or (t.dim() > 1 and t.shape[-1] != plan.table_shape[1])))):
         raise ValueError(f"page_table must be a contiguous int32 tensor of >= {plan.table_size} entries "
-                         f"in rows of {plan.table_width}")
+                         f"in rows of {plan.table_shape[1]}")
+    return t.data_ptr()
+
+
+def _caches(plan, k, v, k_scales, v_scales):
+    """The addresses of the caches, and of an NVFP4 cache's scales: contiguous, of the plan's type (or
+    raw elements of its size), with the plan's pages at least."""
+    n, types = plan.cache_bytes, plan.cache_types
+    if (k.nbytes < n or v.nbytes < n or k.dtype not in types or v.dtype not in types
+            or not k.is_contiguous() or not v.is_contiguous()):
+        for t, name in ((k, "k_cache"), (v, "v_cache")):
+            if t.nbytes < n or t.dtype not in types or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous "
+                                 f"{'NVFP4 codes' if plan.quant_kv else 'bfloat16'} of >= {n} bytes")
+    if not plan.quant_kv:
+        return k.data_ptr(), v.data_ptr(), None, None
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if (t is None or t.element_size() != 1 or t.nbytes < n // 8 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous bytes, >= {n // 8}")
+    return k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr()
+
+
+def _workspace(t, plan):
+    if t.nbytes < plan.workspace_bytes:
+        raise ValueError(f"workspace must hold >= {plan.workspace_bytes} bytes")
     return t.data_ptr()
 
 
@@ -375,7 +407,7 @@ def sps_qk_norm_rope(plan: Plan, q, k, q_weight, k_weight, eps, rope, q_out, q_s
         None if rope is None else _rope(rope, plan), q_out.data_ptr(),
         _rows(q_out, qs, "q_out", codes), E4M3 if codes else BF16, q_scale,
         _ptr(k_out), 0 if k_out is None else _rows(k_out, ks, "k_out"),
-        workspace.data_ptr(), _stream(stream))
+        _workspace(workspace, plan), _stream(stream))
     if st:
         _check(st)
 
@@ -389,8 +421,9 @@ def sps_kv_append_rope(plan: Plan, k_new, v_new, k_weight, eps, rope, page_table
     st = (_lib or lib()).sps_kv_append_rope(
         plan.handle, k_new.data_ptr(), _rows(k_new, ks, "k_new"), v_new.data_ptr(),
         _rows(v_new, ks, "v_new"), _ptr(k_weight), eps,
-        None if rope is None else _rope(rope, plan), _table(page_table, plan), k_cache.data_ptr(),
-        v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), workspace.data_ptr(), _stream(stream))
+        None if rope is None else _rope(rope, plan), _table(page_table, plan),
+        *_caches(plan, k_cache, v_cache, k_scales, v_scales),
+        _workspace(workspace, plan), _stream(stream))
     if st:
         _check(st)
 
@@ -409,10 +442,10 @@ def paged_attention_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_sc
     qs = plan.q_shape
     _vector(out_lse, _F32, qs[0] * qs[1], "out_lse")
     st = (_lib or lib()).paged_attention_fwd(
-        plan.handle, q.data_ptr(), _rows(q, qs, "q", plan.q_codes), q_scale, k_cache.data_ptr(),
-        v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales), _table(page_table, plan), out.data_ptr(),
-        _rows(out, qs, "out"), _ptr(out_lse), scratch.data_ptr(), scratch.nbytes,
-        workspace.data_ptr(), _stream(stream))
+        plan.handle, q.data_ptr(), _rows(q, qs, "q", plan.q_codes), q_scale,
+        *_caches(plan, k_cache, v_cache, k_scales, v_scales),
+        _table(page_table, plan), out.data_ptr(), _rows(out, qs, "out"), _ptr(out_lse),
+        scratch.data_ptr(), scratch.nbytes, _workspace(workspace, plan), _stream(stream))
     if st:
         _check(st)
 
