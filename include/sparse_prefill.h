@@ -430,9 +430,9 @@ sps_status sps_dequantize(sps_dtype in_dtype, const void* in, const void* scales
  *
  * Rules.
  *   - The array holds 48 MiB per device and every GPU that loads the library keeps it until
- *     the process exits.  A plan whose workspace_bytes exceeds 48 MiB is rejected with
- *     SPS_ENOSPACE (for example 16K tokens x 32 heads x top-16 needs more); split the batch or
- *     use sparse_prefill_fwd.
+ *     the process exits.  A plan whose forward needs more of it (workspace_bytes, less what only
+ *     the top-k and paged_attention_fwd use) is rejected with SPS_ENOSPACE (for example 16K
+ *     tokens x 32 heads x top-16); split the batch or use sparse_prefill_fwd.
  *   - The first call on a device looks up the array's device address (once per device, with
  *     that device current); make that first call before any stream capture on the device.
  *   - All calls on a device share the one array, and it keeps the last call's contents (each

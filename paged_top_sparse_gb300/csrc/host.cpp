@@ -137,7 +137,8 @@ struct sps_plan {
           off_bucket_offsets = 0, off_entries = 0, off_fwd_tasks = 0, off_topk_lists = -1,
           off_topk_meta = -1, off_topk_gmax = -1,
           ws_bytes = 0;
-  int64_t fwd_ws_bytes = 0;  // the part the forward uses (the no-allocation forward's need)
+  // the part the forward uses: [fwd_base, fwd_base + fwd_ws_bytes), the no-allocation forward's need
+  int64_t fwd_base = 0, fwd_ws_bytes = 0;
   int32_t topk_nseg = 1, topk_segg = 0;
   int32_t fwd_prefetch = 0;
   // full attention (attention.cu): the blocks' work, the tiles cut over blocks
@@ -525,16 +526,18 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
     off = align_up(off + std::max<int64_t>(bytes, 4), 256);
     return o;
   };
+  // the full attention's tables, in front: the no-allocation forward leaves them out.  (Their sizes
+  // and those up to off_page_req follow from q_lens and the heads alone: a plan with other contexts
+  // has the same layout up to there.)
+  pl->off_att_heads = take(sizeof(AttHead) * pl->att_heads.size());
+  pl->off_att_merges = take(sizeof(AttMerge) * pl->att_merges.size());
+  pl->off_att_pieces = take(sizeof(AttPiece) * (pl->att_tiles + 2 * pl->att_ctas));
+  pl->fwd_base = off;
   pl->off_status = take(4);
   pl->off_counters = take(16 * 4);
   pl->off_tok_pos = take(4 * pl->T);
   pl->off_tok_req = take(4 * pl->T);
   pl->off_reqs = take(sizeof(ReqInfo) * p.batch);
-  // (sizes that q_lens and the heads alone decide: a plan with other contexts has the same layout up
-  // to here)
-  pl->off_att_heads = take(sizeof(AttHead) * pl->att_heads.size());
-  pl->off_att_merges = take(sizeof(AttMerge) * pl->att_merges.size());
-  pl->off_att_pieces = take(sizeof(AttPiece) * (pl->att_tiles + 2 * pl->att_ctas));
   pl->off_page_req = take(4 * std::max<int64_t>(1, pl->total_pages));
   pl->off_idx_tasks = take(sizeof(IdxTask) * std::max<size_t>(1, pl->idx_tasks.size()));
   int64_t upload_end = off;
@@ -558,7 +561,7 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   if (idx_fp16)
     pl->off_kconv = take(2 * std::max<int64_t>(1, pl->total_pages) * p.num_kv_heads * kPage *
                          p.head_dim);
-  pl->fwd_ws_bytes = off;
+  pl->fwd_ws_bytes = off - pl->fwd_base;
   // at most 128 entries per bucket on average: most work items are a single group
   pl->fwd_prefetch = pl->max_entries <= 128 * std::max<int64_t>(1, pl->num_buckets) ? 1 : 0;
   // Top-k with top_k <= 16 runs a thread per row, so long rows of a small batch leave few
@@ -581,7 +584,7 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   }
   pl->ws_bytes = off;
 
-  // the host image of [0, upload_end): the status word and counters (zero), then the metadata
+  // the host image of [0, upload_end): the metadata, the status word and counters (zero)
   pl->upload_bytes = upload_end;
   pl->blob.assign(pl->upload_bytes, 0);
   auto put = [&](int64_t o, const void* src, size_t n) {
@@ -707,7 +710,7 @@ sps_status sps_plan_upload(const sps_plan* pl, void* ws, size_t ws_bytes, sps_st
                 (long long)pl->ws_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  // one copy: zeroed status word and counters, then the plan metadata
+  // one copy: the plan metadata, the zeroed status word and counters
   cudaError_t e = g_staging.upload(base, pl->blob.data(), pl->upload_bytes, s, true);
   if (e != cudaSuccess) return cuda_fail(e, "plan upload");
   return SPS_OK;
@@ -1302,12 +1305,14 @@ sps_status sps_internal_fwd_noalloc(const sps_plan* pl, const void* q, float q_s
                 "array holds %zu; split the batch or use sparse_prefill_fwd with a workspace",
                 (long long)pl->fwd_ws_bytes, scratch_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t* base = static_cast<uint8_t*>(scratch);
   // the array keeps the previous call's contents: one copy zeroes the status word and
   // counters and writes this plan's metadata over the old one
-  cudaError_t e = g_staging.upload(base, pl->blob.data(), pl->upload_bytes, s, false);
+  cudaError_t e = g_staging.upload(scratch, pl->blob.data() + pl->fwd_base,
+                                   pl->upload_bytes - pl->fwd_base, s, false);
   if (e != cudaSuccess) return cuda_fail(e, "plan metadata -> scratch");
-  DevPlan d = make_dev_plan(pl, scratch);
+  // (offsets count from the workspace's start, fwd_base bytes in front of the array)
+  DevPlan d = make_dev_plan(pl, reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(scratch) -
+                                                        (uintptr_t)pl->fwd_base));
   if (dev_status) d.status = dev_status;
   e = launch_inversion(d, idx, lse, lse_split_stride, s);
   if (e != cudaSuccess) return cuda_fail(e, "inversion launch");
