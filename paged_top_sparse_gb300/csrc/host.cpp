@@ -1321,3 +1321,14 @@ sps_status sps_internal_fwd_noalloc(const sps_plan* pl, const void* q, float q_s
                                  lse_split_stride, s),
                   "forward launch");
 }
+
+// The full attention's tables as they are uploaded, for the tests of the work split: their start, and
+// in `info` the offsets of heads, pieces, merges and of what follows them, the blocks, the rows of a
+// slot, the cut tiles and their cap.
+extern "C" const uint8_t* sps_internal_attention_tables(const sps_plan* pl, int64_t* info) {
+  const int64_t v[8] = {pl->off_att_heads, pl->off_att_pieces,    pl->off_att_merges,
+                        pl->fwd_base,      pl->att_ctas,          pl->att_slot_rows,
+                        pl->att_num_merges, pl->att_merge_cap};
+  memcpy(info, v, sizeof v);
+  return pl->blob.data();
+}
