@@ -261,66 +261,69 @@ constexpr int kAttTileCost = 2, kAttMinPiece = 5;
 struct AttTile {
   int32_t req, vg, tile, pages;
 };
-struct AttRun {  // pages [page0, page1) of a tile, on block cta
-  int32_t cta, tile, page0, page1;
+
+// The tiles, and the cost in front of each: `at` has one entry more.
+struct AttTiles {
+  std::vector<AttTile> list;
+  std::vector<int64_t> at;
+  int max_pages = 0;
 };
 
-// What a split costs (its longest block, its cut tiles' pieces), and its runs where they are wanted.
-struct AttSplit {
-  int64_t longest = 0, cost = 0, pieces = 0;
-  int cta = -1;
-  std::vector<AttRun>* keep = nullptr;
-  void block() {
-    longest = std::max(longest, cost);
-    cost = 0;
-    ++cta;
-  }
-  void run(int tile, int page0, int page1) {
-    cost += page1 - page0 + kAttTileCost;
-    if (keep) keep->push_back(AttRun{cta, tile, page0, page1});
-  }
-  double estimate(bool few_rows) const {
-    const double merge = few_rows ? 6 + 0.01 * pieces : 2.5 + 0.05 * pieces;
-    return (double)std::max(longest, cost) + (pieces ? merge : 0);
-  }
+// What a split costs: its longest block, and its cut tiles' pieces to merge.
+double split_estimate(int64_t longest, int64_t pieces, bool few_rows) {
+  const double merge = few_rows ? 6 + 0.01 * pieces : 2.5 + 0.05 * pieces;
+  return (double)longest + (pieces ? merge : 0);
+}
+
+// A block's begin (or cut): a tile and a page of it.
+struct AttPos {
+  int32_t tile, page;
 };
 
 // The (tile, page) pairs in order, cut into runs of equal cost.  A cut at most `snap` pages from a
 // tile's border moves onto the nearer one.  (Measured on H 32 / H_kv 8, D 128: 32 single tokens after
 // 1K cost 42 us with snap 5 and 49 with 1, a 512-token prompt 15 and 20; one token after 8K, where
 // every cut counts, 17 and 14.)
-void split_runs(const std::vector<AttTile>& tiles, int64_t total, int ctas, int snap, AttSplit& out) {
-  const int64_t cuts = std::min<int64_t>(ctas, total);
-  int64_t at = 0, cut = 0, bound = 0;  // cost before the tile; cuts placed; where the next one lies
-  bool pending = true, empty = false;  // a block begins at the next tile; the present one has no work
-  for (size_t k = 0; k < tiles.size(); ++k) {
-    const int n = tiles[k].pages;
-    int page = 0;
-    auto begin = [&](int to) {  // a block begins at page `to`
-      if (to > page) {
-        out.run((int)k, page, to);
-        ++out.pieces;
-        page = to;
-        out.block();
-      } else if (to == 0 && page == 0 && !empty) {
-        out.block();
-        empty = true;
-      }
-    };
-    if (pending) begin(0);
-    pending = false;
-    for (; cut < cuts && bound < at + n + kAttTileCost; bound = ++cut * total / cuts) {
-      const int to = std::max(0, (int)(bound - at) - kAttTileCost);
-      const bool front = to <= n - to;
-      if (to == 0 || (front && to <= snap)) begin(0);
-      else if (!front && n - to <= snap) pending = true;
-      else begin(to);
-    }
-    out.run((int)k, page, n);
-    out.pieces += page > 0;
-    empty = false;
-    at += n + kAttTileCost;
+// `cuts` are the equal runs' begins, a page below the cost of a tile's start counted as its page 0;
+// `begins` are the blocks' begins after the snap.
+struct AttRuns {
+  std::vector<AttPos> begins;
+  int64_t longest = 0, pieces = 0;
+};
+std::vector<AttPos> equal_cuts(const AttTiles& t, int ctas) {
+  const int64_t total = t.at.back(), n = std::min<int64_t>(ctas, total);
+  std::vector<AttPos> cuts(n);
+  size_t k = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t bound = i * total / n;
+    // (a cut is usually a few tiles behind the one before, or many)
+    if (bound >= t.at[k + 1]) k = std::upper_bound(t.at.begin() + k + 1, t.at.end(), bound) - t.at.begin() - 1;
+    cuts[i] = AttPos{(int32_t)k, (int32_t)std::max<int64_t>(0, bound - t.at[k] - kAttTileCost)};
   }
+  return cuts;
+}
+void split_runs(const AttTiles& t, const std::vector<AttPos>& cuts, int snap, AttRuns& out) {
+  out.begins.clear();
+  out.longest = out.pieces = 0;
+  out.begins.push_back(AttPos{0, 0});
+  int64_t from = 0;  // cost in front of the present block
+  auto begin = [&](int32_t tile, int32_t page) {
+    const AttPos& l = out.begins.back();
+    if (tile < l.tile || (tile == l.tile && page <= l.page)) return;
+    const int64_t border = t.at[tile] + page;
+    out.longest = std::max(out.longest, border + (page ? kAttTileCost : 0) - from);
+    out.pieces += page == 0 ? 0 : l.tile == tile && l.page ? 1 : 2;  // the piece in front, and the rest
+    from = border;
+    out.begins.push_back(AttPos{tile, page});
+  };
+  for (const AttPos& c : cuts) {
+    const int n = t.list[c.tile].pages;
+    const bool front = c.page <= n - c.page;
+    if (c.page == 0 || (front && c.page <= snap)) begin(c.tile, 0);
+    else if (front || n - c.page > snap) begin(c.tile, c.page);
+    else if (c.tile + 1 < (int32_t)t.list.size()) begin(c.tile + 1, 0);
+  }
+  out.longest = std::max(out.longest, t.at.back() - from);
 }
 
 // Whole tiles, the largest first, each to the block with the least work as long as that stays within
@@ -328,136 +331,179 @@ void split_runs(const std::vector<AttTile>& tiles, int64_t total, int ctas, int 
 // time then read the same keys: 8 x 512 tokens after 32K reads 270 MB of keys and values that
 // consecutive runs, each block at another place, would stream past the L2 again and again.
 // (Loads only grow, so the least loaded block is found by walking a list of blocks per load.)
-bool split_shares(const std::vector<AttTile>& tiles, int64_t share, int ctas,
-                  const std::vector<int32_t>& order, AttSplit& out) {
-  std::vector<int32_t> at_load(share + 1, -1), peer(ctas);  // blocks of a load, linked
-  std::vector<int32_t> first(ctas, -1), last(ctas, -1), next(tiles.size(), -1);  // a block's tiles
-  for (int i = ctas - 1; i >= 0; --i) {
-    peer[i] = at_load[0];
-    at_load[0] = i;
-  }
+struct AttShares {
+  std::vector<int32_t> order;             // tiles by falling pages
+  std::vector<int32_t> at_load, peer;     // blocks of a load, linked
+  std::vector<int32_t> first, last, next; // a block's tiles, linked
   std::vector<int32_t> rest;
-  int64_t low = 0;
-  for (int32_t k : order) {
-    while (at_load[low] < 0) ++low;
-    const int64_t load = low + tiles[k].pages + kAttTileCost;
-    if (load > share) {
-      rest.push_back(k);
-      continue;
-    }
-    const int32_t c = at_load[low];
-    at_load[low] = peer[c];
-    peer[c] = at_load[load];
-    at_load[load] = c;
-    (first[c] < 0 ? first[c] : next[last[c]]) = k;
-    last[c] = k;
+  int64_t share = 0, low = 0, longest = 0, pieces = 0;
+
+  void sort(const AttTiles& t) {
+    std::vector<int32_t> from(t.max_pages + 2, 0);
+    for (const AttTile& x : t.list) ++from[t.max_pages - x.pages + 1];
+    for (int i = 0; i <= t.max_pages; ++i) from[i + 1] += from[i];
+    order.resize(t.list.size());
+    for (size_t k = 0; k < t.list.size(); ++k)
+      order[from[t.max_pages - t.list[k].pages]++] = (int32_t)k;
   }
-  size_t j = 0;
-  int page = 0;
-  for (; low <= share; ++low)  // the blocks with the most room first
-    for (int32_t c = at_load[low]; c >= 0; c = peer[c]) {
-      out.block();
-      for (int32_t k = first[c]; k >= 0; k = next[k]) out.run(k, 0, tiles[k].pages);
-      int64_t room = share - low;
-      while (j < rest.size() && room >= kAttTileCost + kAttMinPiece) {
-        const int n = tiles[rest[j]].pages;
-        int to = (int)std::min<int64_t>(n, page + room - kAttTileCost);
-        if (n - to < kAttMinPiece) to = n;
-        out.run(rest[j], page, to);
-        out.pieces += page > 0 || to < n;
-        room -= to - page + kAttTileCost;
-        page = to;
-        if (to < n) break;
-        ++j;
-        page = 0;
-      }
+  // The whole tiles' places, and what is left over.
+  void place(const AttTiles& t, int64_t s, int ctas) {
+    share = s;
+    at_load.assign(share + 1, -1);
+    peer.resize(ctas);
+    first.assign(ctas, -1);
+    last.assign(ctas, -1);
+    next.assign(t.list.size(), -1);
+    rest.clear();
+    for (int i = ctas - 1; i >= 0; --i) {
+      peer[i] = at_load[0];
+      at_load[0] = i;
     }
-  return j == rest.size();
-}
+    low = 0;
+    for (int32_t k : order) {
+      while (at_load[low] < 0) ++low;
+      const int64_t load = low + t.list[k].pages + kAttTileCost;
+      if (load > share) {
+        rest.push_back(k);
+        continue;
+      }
+      const int32_t c = at_load[low];
+      at_load[low] = peer[c];
+      peer[c] = at_load[load];
+      at_load[load] = c;
+      (first[c] < 0 ? first[c] : next[last[c]]) = k;
+      last[c] = k;
+    }
+  }
+  // The blocks in turn, the ones with the most room first, filled up with the left-over tiles:
+  // block() at each, run(tile, page0, page1) for its pieces.  False: some do not fit.
+  template <typename Block, typename Run>
+  bool fill(const AttTiles& t, Block block, Run run) {
+    longest = pieces = 0;
+    size_t j = 0;
+    int page = 0;
+    for (int64_t l = low; l <= share; ++l)
+      for (int32_t c = at_load[l]; c >= 0; c = peer[c]) {
+        block(c);
+        int64_t room = share - l;
+        while (j < rest.size() && room >= kAttTileCost + kAttMinPiece) {
+          const int n = t.list[rest[j]].pages;
+          int to = (int)std::min<int64_t>(n, page + room - kAttTileCost);
+          if (n - to < kAttMinPiece) to = n;
+          run(rest[j], page, to);
+          pieces += page > 0 || to < n;
+          room -= to - page + kAttTileCost;
+          page = to;
+          if (to < n) break;
+          ++j;
+          page = 0;
+        }
+        longest = std::max(longest, share - room);
+      }
+    return j == rest.size();
+  }
+};
 
 void build_attention_work(sps_plan* pl) {
   const sps_problem& p = pl->pb;
   const int hg = p.num_q_heads / p.num_kv_heads, HB = std::min(hg, 128), TB = 128 / HB;
   const int nv = p.num_kv_heads * ((hg + HB - 1) / HB), tt = 2 * TB;
-  std::vector<AttTile> tiles;
-  int64_t total = 0;
-  int max_q = 0, max_pages = 0;
+  AttTiles tiles;
+  int64_t count = 0;
+  int max_q = 0;
+  for (const ReqInfo& ri : pl->reqs) {
+    count += (int64_t)nv * ((ri.q_len + tt - 1) / tt);
+    max_q = std::max(max_q, ri.q_len);
+  }
+  tiles.list.resize(count);
+  tiles.at.resize(count + 1);
+  int64_t k = 0, at = 0;
   for (int b = 0; b < p.batch; ++b) {
     const ReqInfo& ri = pl->reqs[b];
     for (int v = 0; v < nv; ++v)
       for (int t = 0; t * tt < ri.q_len; ++t) {
         const int n = (ri.ctx + std::min((t + 1) * tt, ri.q_len) - 1) / kPage + 1;
-        tiles.push_back(AttTile{b, v, t, n});
-        total += n + kAttTileCost;
-        max_pages = std::max(max_pages, n);
+        tiles.list[k] = AttTile{b, v, t, n};
+        tiles.at[k++] = at;
+        at += n + kAttTileCost;
+        tiles.max_pages = std::max(tiles.max_pages, n);
       }
-    max_q = std::max(max_q, ri.q_len);
   }
+  tiles.at[k] = at;
+  const int64_t total = at;
   const int ctas = std::min(std::max(1, num_sms()), 256);
   pl->att_ctas = ctas;
-  pl->att_tiles = (int64_t)tiles.size();
+  pl->att_tiles = count;
   pl->att_slot_rows = max_q > TB ? 256 : max_q * HB;
-  pl->att_merge_cap = (int32_t)std::min<int64_t>(ctas - 1, pl->att_tiles);
+  pl->att_merge_cap = (int32_t)std::min<int64_t>(ctas - 1, count);
 
   // the splits' estimates: runs by snap, or shares of a size at which the left-over tiles fit
   const bool few_rows = pl->att_slot_rows <= 32;
+  const std::vector<AttPos> cuts = equal_cuts(tiles, ctas);
+  AttRuns runs, trial;
   double best = 0;
-  int snap = 1;
-  int64_t share = 0;
   for (int s : {1, 2, 4, 8, 1 << 20}) {
-    AttSplit x;
-    split_runs(tiles, total, ctas, s, x);
-    if (s == 1 || x.estimate(few_rows) < best) {
-      best = x.estimate(few_rows);
-      snap = s;
+    split_runs(tiles, cuts, s, trial);
+    const double x = split_estimate(trial.longest, trial.pieces, few_rows);
+    if (s == 1 || x < best) {
+      best = x;
+      std::swap(runs, trial);
     }
-    if (pl->att_tiles >= 8 * ctas) break;
+    if (count >= 8 * ctas) break;
   }
-  std::vector<int32_t> order;
-  if (pl->att_tiles > ctas) {
-    std::vector<int32_t> first(max_pages + 2, 0);  // tiles by falling pages, in order
-    for (const AttTile& t : tiles) ++first[max_pages - t.pages + 1];
-    for (int i = 0; i <= max_pages; ++i) first[i + 1] += first[i];
-    order.resize(tiles.size());
-    for (size_t k = 0; k < tiles.size(); ++k) order[first[max_pages - tiles[k].pages]++] = (int32_t)k;
+  AttShares shares;
+  bool shared = false;
+  if (count > ctas) {
+    shares.sort(tiles);
     for (int64_t x = (total + ctas - 1) / ctas + kAttTileCost; (double)x < best && x < 1 << 20;
          x += std::max<int64_t>(1, x / 64)) {
-      AttSplit out;
-      if (!split_shares(tiles, x, ctas, order, out)) continue;
-      if (out.estimate(few_rows) < best) share = x;
+      shares.place(tiles, x, ctas);
+      if (!shares.fill(tiles, [](int) {}, [](int, int, int) {})) continue;
+      shared = split_estimate(shares.longest, shares.pieces, few_rows) < best;
       break;
     }
   }
 
-  std::vector<AttRun> work;
-  work.reserve(tiles.size() + 2 * ctas);
-  AttSplit out;
-  out.keep = &work;
-  if (share) split_shares(tiles, share, ctas, order, out);
-  else split_runs(tiles, total, ctas, snap, out);
-  auto piece = [&](const AttRun& r) {
-    const AttTile& t = tiles[r.tile];
-    const ReqInfo& ri = pl->reqs[t.req];
-    return AttPiece{t.req, t.vg, t.tile, r.page0, r.page1, ri.q_len, ri.ctx, ri.tok0};
-  };
   pl->att_heads.assign(ctas, AttHead{});
   pl->att_merges.assign(ctas, AttMerge{-1, 0, 0, 0, 0, 0, 0, 0});
-  pl->att_pieces.reserve(work.size());
-  int merges = 0;
-  for (const AttRun& r : work) {  // (a block's runs are neighbours; so are a cut tile's)
-    AttHead& h = pl->att_heads[r.cta];
+  pl->att_pieces.reserve(count + 2 * ctas);
+  int merges = 0, cta = -1;
+  auto run = [&](int tile, int page0, int page1) {  // a piece more of block `cta`
+    const AttTile& t = tiles.list[tile];
+    const ReqInfo& ri = pl->reqs[t.req];
+    const AttPiece x{t.req, t.vg, t.tile, page0, page1, ri.q_len, ri.ctx, ri.tok0};
+    AttHead& h = pl->att_heads[cta];
     if (h.count++ == 0) {
-      h.first = piece(r);
+      h.first = x;
       h.next = (int32_t)pl->att_pieces.size();
     } else {
-      pl->att_pieces.push_back(piece(r));
+      pl->att_pieces.push_back(x);
     }
-    const AttTile& t = tiles[r.tile];
-    if (r.page0 == 0 && r.page1 < t.pages)
-      pl->att_merges[merges++] = AttMerge{t.req, t.vg, t.tile, r.cta, r.cta,
-                                          pl->reqs[t.req].q_len, pl->reqs[t.req].tok0, 0};
-    else if (r.page0 > 0)
-      pl->att_merges[merges - 1].cta1 = r.cta;
+    if (page0 == 0 && page1 < t.pages)
+      pl->att_merges[merges++] = AttMerge{t.req, t.vg, t.tile, cta, cta, ri.q_len, ri.tok0, 0};
+    else if (page0 > 0)
+      pl->att_merges[merges - 1].cta1 = cta;
+  };
+  if (shared) {
+    shares.fill(
+        tiles,
+        [&](int c) {
+          ++cta;
+          for (int32_t i = shares.first[c]; i >= 0; i = shares.next[i]) run(i, 0, tiles.list[i].pages);
+        },
+        run);
+  } else {
+    for (size_t i = 0; i < runs.begins.size(); ++i) {
+      ++cta;
+      const bool end = i + 1 == runs.begins.size();
+      const AttPos to = end ? AttPos{(int32_t)count, 0} : runs.begins[i + 1];
+      for (AttPos x = runs.begins[i]; x.tile < to.tile; x = AttPos{x.tile + 1, 0})
+        run(x.tile, x.page, tiles.list[x.tile].pages);
+      if (to.page) {
+        const AttPos& x = runs.begins[i];
+        run(to.tile, x.tile == to.tile ? x.page : 0, to.page);
+      }
+    }
   }
   pl->att_num_merges = merges;
 }
