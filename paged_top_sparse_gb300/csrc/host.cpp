@@ -213,38 +213,53 @@ void build_indexer_tasks(sps_plan* pl) {
   const int Hg = p.num_q_heads / p.num_kv_heads;
   const int nh = (Hg % 2 == 0) ? 2 : 1;
   const int64_t target = 4LL * std::max(1, num_sms());
-  int chunk = 128;
-  for (;;) {
-    std::vector<IdxTask> tasks;
-    for (int b = 0; b < p.batch; ++b) {
-      const ReqInfo& ri = pl->reqs[b];
+  // items and their page counts at a chunk size, found without listing them
+  auto count = [&](int chunk, std::vector<int64_t>& by_pages) {
+    by_pages.assign(chunk + 1, 0);
+    int64_t n = 0;
+    for (const ReqInfo& ri : pl->reqs)
       for (int i0 = 0; i0 < ri.q_len; i0 += kPage) {
-        int ntok = std::min(kPage, ri.q_len - i0);
-        int o_last = (ri.ctx + i0 + ntok - 1) / kPage;
-        for (int g = 0; g < p.num_kv_heads; ++g)
-          for (int hl = 0; hl < Hg; hl += nh)
-            for (int pb = 0; pb <= o_last; pb += chunk) {
-              IdxTask t;
-              t.req = b;
-              t.g = g;
-              t.h0 = g * Hg + hl;
-              t.nh = nh;
-              t.tok0 = ri.tok0 + i0;
-              t.ntok = ntok;
-              t.page_begin = pb;
-              t.page_end = std::min(o_last + 1, pb + chunk);
-              tasks.push_back(t);
-            }
+        const int pages = (ri.ctx + std::min(i0 + kPage, ri.q_len) - 1) / kPage + 1;
+        by_pages[chunk] += pages / chunk;
+        if (pages % chunk) ++by_pages[pages % chunk];
+        n += (pages + chunk - 1) / chunk;
       }
+    const int64_t heads = (int64_t)p.num_kv_heads * (Hg / nh);
+    for (int64_t& x : by_pages) x *= heads;
+    return n * heads;
+  };
+  int chunk = 128;
+  std::vector<int64_t> at;
+  int64_t total = count(chunk, at);
+  while (total < target && chunk > 8) total = count(chunk /= 2, at);
+  // each page count's place in the list, the largest first
+  int64_t next = 0;
+  for (int n = chunk; n >= 1; --n) {
+    const int64_t c = at[n];
+    at[n] = next;
+    next += c;
+  }
+  pl->idx_tasks.resize(total);
+  for (int b = 0; b < p.batch; ++b) {
+    const ReqInfo& ri = pl->reqs[b];
+    for (int i0 = 0; i0 < ri.q_len; i0 += kPage) {
+      const int ntok = std::min(kPage, ri.q_len - i0);
+      const int o_last = (ri.ctx + i0 + ntok - 1) / kPage;
+      for (int g = 0; g < p.num_kv_heads; ++g)
+        for (int hl = 0; hl < Hg; hl += nh)
+          for (int pb = 0; pb <= o_last; pb += chunk) {
+            IdxTask t;
+            t.req = b;
+            t.g = g;
+            t.h0 = g * Hg + hl;
+            t.nh = nh;
+            t.tok0 = ri.tok0 + i0;
+            t.ntok = ntok;
+            t.page_begin = pb;
+            t.page_end = std::min(o_last + 1, pb + chunk);
+            pl->idx_tasks[at[t.page_end - pb]++] = t;
+          }
     }
-    if ((int64_t)tasks.size() >= target || chunk <= 8) {
-      std::stable_sort(tasks.begin(), tasks.end(), [](const IdxTask& a, const IdxTask& b) {
-        return (a.page_end - a.page_begin) > (b.page_end - b.page_begin);
-      });
-      pl->idx_tasks.swap(tasks);
-      return;
-    }
-    chunk /= 2;
   }
 }
 
