@@ -10,7 +10,9 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -523,24 +525,12 @@ void build_attention_work(sps_plan* pl) {
   pl->att_num_merges = merges;
 }
 
-}  // namespace
-
-extern "C" {
-
-const char* sps_last_error(void) { return g_err.c_str(); }
-
-sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
-                               size_t* workspace_bytes) {
-  if (!out || !workspace_bytes) return fail(SPS_EINVAL, "plan/workspace_bytes out-pointers NULL");
-  *out = nullptr;
-  sps_status st = validate_problem(problem);
-  if (st != SPS_OK) return st;
-  sps_plan* pl = new (std::nothrow) sps_plan();
-  if (!pl) return fail(SPS_EINVAL, "out of host memory");
-  pl->pb = *problem;
+// Fills the plan of a valid problem (throws std::bad_alloc).
+void make_plan(const sps_problem& problem, sps_plan* pl) {
+  pl->pb = problem;
   const sps_problem& p = pl->pb;
-  pl->q_lens.assign(problem->q_lens, problem->q_lens + p.batch);
-  pl->ctx_lens.assign(problem->ctx_lens, problem->ctx_lens + p.batch);
+  pl->q_lens.assign(problem.q_lens, problem.q_lens + p.batch);
+  pl->ctx_lens.assign(problem.ctx_lens, problem.ctx_lens + p.batch);
   pl->pb.q_lens = pl->q_lens.data();
   pl->pb.ctx_lens = pl->ctx_lens.data();
   const int Hg = p.num_q_heads / p.num_kv_heads;
@@ -659,10 +649,29 @@ sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
   put(pl->off_att_merges, pl->att_merges.data(), sizeof(AttMerge) * pl->att_merges.size());
   put(pl->off_page_req, pl->page_req.data(), 4 * pl->page_req.size());
   put(pl->off_idx_tasks, pl->idx_tasks.data(), sizeof(IdxTask) * pl->idx_tasks.size());
+}
 
-  *out = pl;
-  *workspace_bytes = (size_t)pl->ws_bytes;
-  return SPS_OK;
+}  // namespace
+
+extern "C" {
+
+const char* sps_last_error(void) { return g_err.c_str(); }
+
+sps_status sparse_prefill_plan(const sps_problem* problem, sps_plan** out,
+                               size_t* workspace_bytes) {
+  if (!out || !workspace_bytes) return fail(SPS_EINVAL, "plan/workspace_bytes out-pointers NULL");
+  *out = nullptr;
+  sps_status st = validate_problem(problem);
+  if (st != SPS_OK) return st;
+  try {
+    std::unique_ptr<sps_plan> pl(new sps_plan());
+    make_plan(*problem, pl.get());
+    *workspace_bytes = (size_t)pl->ws_bytes;
+    *out = pl.release();
+    return SPS_OK;
+  } catch (const std::bad_alloc&) {
+    return fail(SPS_EINVAL, "out of host memory");
+  }
 }
 
 void sps_plan_destroy(sps_plan* plan) { delete plan; }
