@@ -459,7 +459,8 @@ sps_status sparse_prefill_fwd_noalloc(const sps_plan* plan, const void* q, float
  * The new tokens' own K/V are in the cache (sps_kv_append or sps_kv_append_rope).
  *   q            device, the plan's q_dtype: BF16 or E4M3, token i's H rows at
  *                q + i * q_token_stride (elements); 16-byte aligned, stride a multiple of 16 bytes
- *   q_scale      per-tensor multiplier of the decoded q (1 for BF16), finite and > 0
+ *   q_scale      per-tensor multiplier of the decoded q (1 for BF16), finite and > 0, as its product
+ *                with softmax_scale
  *   k_cache, v_cache, k_scales, v_scales, page_table   as for sparse_prefill_fwd; slots behind a
  *                request's last token may hold anything, NaN included, the others finite values
  *   out_bf16     device BF16, token i's H rows at out_bf16 + i * out_token_stride (16-byte aligned,

@@ -1053,7 +1053,7 @@ cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_
   a.out_lse = out_lse;
   a.part = static_cast<float*>(scratch);
   a.part_lse = a.part + 2ll * p.att_ctas * p.att_slot_rows * p.D;
-  a.c = p.sm_scale * q_scale * 1.4426950408889634f;
+  a.c = attention_factor(p.sm_scale, q_scale);
   a.skip_wait_ns = g_skip_wait_ns.load(std::memory_order_relaxed);
   const RowPack rp(p.Hg);
   const bool single = p.att_slot_rows <= rp.TB * rp.HB;

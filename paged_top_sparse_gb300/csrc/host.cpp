@@ -1165,6 +1165,9 @@ sps_status paged_attention_fwd(const sps_plan* pl, const void* q, int64_t q_stri
                             "4-byte aligned");
   if (!(q_scale > 0.f) || !std::isfinite(q_scale))
     return fail(SPS_EINVAL, "paged_attention_fwd: q_scale must be finite and > 0");
+  const float c = attention_factor(p.softmax_scale, q_scale);
+  if (!(c > 0.f) || !std::isfinite(c))
+    return fail(SPS_EINVAL, "paged_attention_fwd: softmax_scale x q_scale must stay within FP32");
   size_t need = 0;
   paged_attention_scratch(pl, &need);
   if (!scratch || !aligned(scratch, 256))

@@ -229,6 +229,11 @@ cudaError_t launch_qk_norm_rope(const DevPlan& p, const DevRope& r, const QkRope
 cudaError_t launch_kv_append_rope(const DevPlan& p, const DevRope& r, const KvRopeArgs& a,
                                   bool interleaved, bool nvfp4, cudaStream_t st);
 
+// The full attention's factor on a score: the scales, in base 2.
+inline float attention_factor(float softmax_scale, float q_scale) {
+  return softmax_scale * q_scale * 1.4426950408889634f;
+}
+
 // Full attention over the paged cache (BF16 Q and cache, or E4M3 Q and NVFP4 cache).
 cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_t q_stride,
                              float q_scale, const void* kc, const void* vc, const void* ks,

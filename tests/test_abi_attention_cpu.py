@@ -87,3 +87,17 @@ def test_scratch_follows_the_rows_a_cut_tile_can_have(L):
     # 16 rows a tile against 256
     assert one * 16 == pytest.approx(many, rel=0.01)
     assert one % 256 == 0 and many % 256 == 0
+
+
+def test_a_scale_that_leaves_fp32_is_refused(L):
+    """softmax_scale x q_scale is one FP32 factor of the scores: rounded to zero it would turn masked
+    scores into NaN (0 * infinity), rounded to infinity every equal one."""
+    for scale, softmax, status in ((1e-40, 1e-10, 1), (3e38, 4.0, 1), (3e38, 1.0, 1)):
+        plan = B.Plan([T], [10], H, G, D, 1, 1, 2, softmax_scale=softmax)
+        n = B.paged_attention_scratch(plan)
+        ws, scratch, buf = _aligned(plan.workspace_bytes), _aligned(n), _aligned(1 << 17)
+        pt = np.zeros(1, np.int32)
+        assert L.paged_attention_fwd(plan.handle, _ptr(buf), H * D, scale, _ptr(buf), _ptr(buf), None,
+                                     None, _ptr(pt), _ptr(buf), H * D, None, _ptr(scratch), n,
+                                     _ptr(ws), None) == status
+        assert b"scale" in L.sps_last_error()
