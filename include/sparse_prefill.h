@@ -353,9 +353,9 @@ typedef struct {
  *   q_weight, k_weight  device FP32 [D], 16-byte aligned, or NULL: no norm of those rows
  *   eps          added to the mean square (>= 0)
  *   rope         or NULL: no rotation
- *   q_out        device, [T][H][D] at q_out_token_stride: SPS_BF16, or SPS_E4M3 codes of
- *                y * (1 / q_scale) (FP32, nearest even, saturating; q_scale and its inverse finite
- *                and > 0)
+ *   q_out        device, [T][H][D] at q_out_token_stride: SPS_BF16, or SPS_E4M3 codes of the FP32
+ *                result divided by q_scale (sps_quantize_e4m3's rule; q_scale and its inverse
+ *                finite and > 0)
  *   k_out        device BF16, at k_out_token_stride
  * Buffers are 16-byte aligned; strides are multiples of 8 elements (16 for E4M3 codes) and at
  * least the rows of a token, so q and k may be views of one projection's output.  A BF16 output

@@ -1039,6 +1039,17 @@ sps_status make_rope(const sps_rope* rope, int head_dim, const char* who, DevRop
   return SPS_OK;
 }
 
+DevQuot make_quot(float s) {
+  DevQuot d{s, NAN, 0.f, 0.f};
+  if (!(s >= 0x1p-90f && s <= 0x1p90f)) return d;  // the kernel divides
+  const double inv = 1.0 / s;
+  d.r = 1.f / s;
+  d.hi = (float)inv;
+  if ((double)d.hi > inv) d.hi = std::nextafterf(d.hi, 0.f);
+  d.lo = (float)(inv - d.hi);
+  return d;
+}
+
 bool rows_ok(const void* x, int64_t stride, int64_t row_elems, int64_t multiple) {
   return x && aligned(x, 16) && stride >= row_elems && stride % multiple == 0;
 }
@@ -1088,7 +1099,7 @@ sps_status sps_qk_norm_rope(const sps_plan* pl, const void* q, int64_t q_stride,
   a.q_out_stride = q_out_stride;
   a.k_out_stride = k_out_stride;
   a.eps = eps;
-  a.q_scale_inv = e4m3 ? 1.f / q_scale : 1.f;
+  a.q_scale = make_quot(q_scale);
   return launched(launch_qk_norm_rope(make_dev_plan(pl, ws), r, a, rope && rope->interleaved, e4m3,
                                       reinterpret_cast<cudaStream_t>(stream)),
                   "q/k norm and rotation launch");

@@ -21,7 +21,7 @@
 // Bound: memory for many tokens.  8192 tokens x 34 rows x 128 (143 MB): 28.6 us, 5.0 TB/s, 0.73
 // of a plain copy; the rest is the start and end of a launch of 20 us of work (32768 tokens x 40
 // rows: 111 us, 6.0 TB/s, 0.89) and the angles in front of a token's rows.  With the angles and coefficients made per row group instead of per
-// token 41.7 us.  5.6K tokens x 28 rows to E4M3 on three axes: 20.4 us, 0.57 of a copy (the same
+// token 41.7 us.  5.6K tokens x 28 rows to E4M3 on three axes: 22.2 us, 0.53 of a copy (the same
 // arithmetic for fewer bytes).  64 tokens (1.1 MB): 2.8 us, a launch and a chain of three
 // dependent reads.  More passes in flight cost resident warps: four 29.6 us, eight 37; blocks of
 // 8 warps 40 against 33.
@@ -128,12 +128,13 @@ struct Rotation {
       B[i] = pack_f32x2(b[2 * i], b[2 * i + 1]);
     }
   }
-  // This lane's chunk `raw` of a row, normalised (where `norm`), rotated and multiplied by `scale`;
-  // all 32 lanes call it.
-  __device__ __forceinline__ void apply(const uint4& raw, bool norm, float eps, float scale,
+  // This lane's chunk `raw` of a row, normalised (where `norm`), rotated and times `sign`; all 32
+  // lanes call it.
+  __device__ __forceinline__ void apply(const uint4& raw, bool norm, float eps, float sign,
                                         uint64_t (&y)[4]) const {
     const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
     uint64_t v[4];
+    float scale = sign;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = pack_f32x2(bf16_lo(x[i]), bf16_hi(x[i]));
     if (norm) {
@@ -204,6 +205,39 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
   return r;
 }
 
+// E4M3 codes of -y / s, the quotient rounded to FP32 first as sps_quantize_e4m3 does it (it decides
+// the codes next to a border).
+//
+// A division costs ten instructions an element (5.6K tokens x 28 rows: 28.5 us, and 20.3 by a product
+// with the rounded 1 / s alone), so a quotient is made of products, in pairs (P. Markstein, IBM J.
+// Res. Dev. 34, 1990): q = y (hi + lo), hi + lo = 1 / s to 2^-47, is off by little more than half a unit
+// in the last place; the remainder q s - y of such a q is exact, and q - (q s - y) r with r = 1 / s
+// rounded to nearest is the rounded quotient.  hi is rounded towards zero, so that lo has its sign: with
+// y negated in advance a zero then keeps its own.  Where a product is infinite there is no remainder,
+// and where s is so small or large that remainders or r lose bits the host passes NaN for r: these take
+// the division.
+__device__ __forceinline__ void e4m3_codes(const uint64_t (&y)[4], const DevQuot& d, uint32_t (&o)[2]) {
+  const uint64_t s2 = pack_f32x2(d.s, d.s), nr = pack_f32x2(-d.r, -d.r);
+  const uint64_t nhi = pack_f32x2(-d.hi, -d.hi), nlo = pack_f32x2(-d.lo, -d.lo);
+  uint64_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q[i] = fma_f32x2(y[i], nhi, mul_f32x2(y[i], nlo));
+    q[i] = fma_f32x2(fma_f32x2(q[i], s2, y[i]), nr, q[i]);
+  }
+  float lo, hi;
+  unpack_f32x2(add_f32x2(add_f32x2(q[0], q[1]), add_f32x2(q[2], q[3])), lo, hi);
+  if (!(fabsf(lo + hi) <= 3.4e38f)) {  // an infinity became NaN (or large quotients' sum overflowed)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack_f32x2(y[i], lo, hi);
+      q[i] = pack_f32x2(__fdiv_rn(-lo, d.s), __fdiv_rn(-hi, d.s));
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) o[h] = f32x2_to_e4m3x2(q[2 * h]) | (f32x2_to_e4m3x2(q[2 * h + 1]) << 16);
+}
+
 // The rows [r0, r1) of one kind that warp `part` of a token walks; `at` counts the passes of the
 // kinds before it.
 template <int D>
@@ -246,13 +280,11 @@ qk_norm_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, QkRopeArgs a) 
     uint8_t* dst = static_cast<uint8_t*>(a.q_out) +
                    (tok * a.q_out_stride + chunk * 8) * (E4M3OUT ? 1 : 2);
     qw.run([&](int row, const uint4& raw) {
-      rt.apply(raw, a.q_weight != nullptr, a.eps, E4M3OUT ? a.q_scale_inv : 1.f, y);
+      rt.apply(raw, a.q_weight != nullptr, a.eps, E4M3OUT ? -1.f : 1.f, y);
       if (row >= q1) return;
       if (E4M3OUT) {
         uint32_t o[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          o[h] = f32x2_to_e4m3x2(y[2 * h]) | (f32x2_to_e4m3x2(y[2 * h + 1]) << 16);
+        e4m3_codes(y, a.q_scale, o);
         *reinterpret_cast<uint2*>(dst + (int64_t)row * D) = make_uint2(o[0], o[1]);
       } else {
         *reinterpret_cast<uint4*>(dst + (int64_t)row * D * 2) =

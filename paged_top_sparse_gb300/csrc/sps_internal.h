@@ -128,13 +128,19 @@ struct DevRope {
   int32_t rot;
   uint8_t axis[64];
 };
+// A divisor s, its inverse rounded to nearest (NaN: divide), and the inverse as a sum rounded towards
+// zero.
+struct DevQuot {
+  float s, r, hi, lo;
+};
 struct QkRopeArgs {
   const uint16_t *q, *k;  // k null: queries alone
   const float *q_weight, *k_weight;
   void* q_out;
   uint16_t* k_out;
   int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
-  float eps, q_scale_inv;
+  float eps;
+  DevQuot q_scale;
   int32_t passes, splits;  // of a warp, of a token; set by the launcher
 };
 struct KvRopeArgs {

@@ -330,3 +330,57 @@ def test_replay_in_a_graph_on_another_stream():
     B.sps_qk_norm_rope(plan, q, None, w, None, EPS, rope, eager, 1.0, None, ws)
     torch.cuda.synchronize()
     assert torch.equal(out, eager) and bool(out.any())
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_e4m3_queries_with_nothing_to_do_are_the_quantisers_codes(D):
+    """No norm and no rotation: sps_quantize_e4m3's codes, for every BF16 value but NaN.  With some of
+    these scales (6.5, 7 / 512) a product with 1 / q_scale in place of the division would move codes
+    next to a border; a significand one unit off a short one, all ones, the smallest and the largest
+    scales are where a corrected product could go wrong."""
+    from paged_top_sparse_gb300 import binding as B
+
+    bits = torch.arange(1 << 16, device=DEV).to(torch.int32)
+    bits[(bits & 0x7FFF) > 0x7F80] = 0
+    x = bits.to(torch.int16).view(torch.bfloat16).view(-1, 4, D).contiguous()
+    T = x.shape[0]
+    plan, ws, pos, _ = _plan([T], [0], 4, 2, D)
+    ulp = 2.0 ** -23
+    scales = [0.3, 0.7, 0.75, 1.5, 6.5, 0.013671875, 0.02, 3e-3, 1 + ulp, 1.125 - ulp, 1.25 + 3 * ulp,
+              2 - ulp, 0.875 * (1 - ulp), 1e-38, 3e-39, 1e-30, 2.0 ** -90, 2.0 ** 90, 1e30, 1e38]
+    scales += list(np.exp(np.random.default_rng(D).uniform(-8, 3, 30)))
+    for scale in scales:
+        scale = float(np.float32(scale))
+        got, want = (torch.zeros((T, 4, D), dtype=torch.uint8, device=DEV) for _ in range(2))
+        B.sps_qk_norm_rope(plan, x, None, None, None, EPS, None, got, scale, None, ws)
+        B.sps_quantize_e4m3(x, scale, want)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), (scale, int((got != want).sum()))
+
+
+def test_e4m3_codes_are_of_the_bf16_forms_quotient():
+    """A weight without a rotation, on rows whose norm is 1: FP32 results of 24 significant bits.  Their
+    codes equal those of the quotient in FP32, for scales of every kind of significand."""
+    from paged_top_sparse_gb300 import binding as B
+
+    T, D = 64, 128
+    rng = np.random.default_rng(9)
+    plan, ws, pos, _ = _plan([T], [0], 4, 2, D)
+    # elements of +-1 have the mean square 1: with eps 0 the result is +-w, bit for bit, if 1 / sqrt(1)
+    # is 1
+    q = torch.from_numpy(np.where(rng.random((T, 4, D)) < 0.5, -1.0, 1.0).astype(np.float32)).to(DEV).bfloat16()
+    out = torch.zeros((T, 4, D), dtype=torch.uint8, device=DEV)
+    ulp = 2.0 ** -23
+    for scale in (1 + ulp, 1.125 + ulp, 1.375 - 2 * ulp, 1.75 + 4 * ulp, 2 - ulp, 1.5, 0.0131, 4.5 / 448):
+        scale = np.float32(scale)
+        # weights within a few units of scale x border, and anything
+        m = (np.arange(16, 32) + 0.5) / 16 * np.exp2(rng.integers(-6, 8, (4, 16)))
+        near = (m.ravel()[:64].astype(np.float32) * scale)
+        near = (near.view(np.int32) + rng.integers(-2, 3, 64)).astype(np.int32).view(np.float32)
+        w = np.concatenate((near, (rng.standard_normal(64) * 200 * scale).astype(np.float32)))
+        B.sps_qk_norm_rope(plan, q, None, torch.from_numpy(w).to(DEV), None, 0.0, None, out, float(scale),
+                           None, ws)
+        torch.cuda.synchronize()
+        quot = (_f64(q).astype(np.float32) * w / scale).clip(-448, 448)
+        want = torch.from_numpy(quot).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(out.cpu(), want), (scale, int((out.cpu() != want).sum()))
