@@ -332,8 +332,9 @@ sps_status sps_kv_append(const sps_plan* plan, const void* k_new, const void* v_
  *   interleaved  pair j is dims (2 j, 2 j + 1) if non-zero, else (j, j + R / 2)
  *   pair_axis    axis of each pair, in [0, num_axes)
  * Pair j of a token turns by positions[pair_axis[j]] * inv_freq[j] radians:
- * (a, b) -> (a cos - b sin, b cos + a sin).  The angle is reduced exactly (in 64-bit fractions of
- * a turn), so far positions lose nothing.
+ * (a, b) -> (a cos - b sin, b cos + a sin).  The angle is kept as a 64-bit fraction of a turn, off by
+ * at most (|inv_freq| + 1) |position| 2^-64 + 2^-25 turns: for |inv_freq| <= 1, as rotations use,
+ * any 32-bit position is as good as a small one; 2^20 radians a position leave 2^-13 at the farthest.
  */
 typedef struct {
   const float* inv_freq;

@@ -8,9 +8,9 @@
 //   d >= R.
 // The angle of a far position does not fit FP32 (a position of 2^20 leaves 2^-4 of a radian), so
 // it is kept as a 64-bit fraction of a turn: F = inv_freq / 2 pi in 2^-64 turns, and position * F
-// modulo 2^64 is the angle modulo a whole turn, without a reduction; its top 32 bits go to
-// sincospi.  F is off by at most two units for inv_freq <= 1, so the angle by 2^-31 turns for any
-// 32-bit position.
+// modulo 2^64 is the angle modulo a whole turn, without a reduction; its top 32 bits, rounded to FP32
+// (2^-26 turns), go to sincospi.  F is off by at most |inv_freq| + 1 units (2^64 / 2 pi and the shift
+// are cut off), so for inv_freq <= 1 the angle by 2^-32 turns at any 32-bit position.
 //
 // Layout: D / 8 lanes hold a row, 8 elements (16 bytes) each; a warp takes one token and walks its
 // rows, 32 * 8 / D at a time, two such passes in flight.  Its lanes make the token's angles once

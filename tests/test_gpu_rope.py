@@ -384,3 +384,56 @@ def test_e4m3_codes_are_of_the_bf16_forms_quotient():
         quot = (_f64(q).astype(np.float32) * w / scale).clip(-448, 448)
         want = torch.from_numpy(quot).to(torch.float8_e4m3fn).view(torch.uint8)
         assert torch.equal(out.cpu(), want), (scale, int((out.cpu() != want).sum()))
+
+
+def _turns(bits):
+    """2^bits / (2 pi) as an integer, from pi = 16 atan(1/5) - 4 atan(1/239) (Machin)."""
+    one = 1 << (2 * bits)
+
+    def atan_inv(n):
+        total, term, k = 0, one // n, 0
+        while term:
+            total += (-1) ** k * (term // (2 * k + 1))
+            term //= n * n
+            k += 1
+        return total
+
+    pi = 16 * atan_inv(5) - 4 * atan_inv(239)
+    return (1 << (3 * bits)) // (2 * pi)
+
+
+def test_angles_of_large_frequencies_keep_the_stated_bound():
+    """(|f| + 1) |position| 2^-64 + 2^-25 turns, against angles from whole numbers of 300 bits."""
+    from paged_top_sparse_gb300 import binding as B
+
+    bits, D, T = 300, 128, 64
+    inv2pi = _turns(bits)
+    assert abs(inv2pi / 2 ** bits - 0.5 / np.pi) < 1e-16
+    rng = np.random.default_rng(77)
+    f = np.exp(rng.uniform(-3, np.log(1e9), D // 2)).astype(np.float32)
+    f[:6] = [1.0, 3.5, 1e6, 2.0 ** 20, 2.0 ** 24 + 2, 1.5e9]
+    f[10:20] *= -1
+    p = rng.integers(-(1 << 31), 1 << 31, T).astype(np.int32)
+    p[:5] = [0, 1, -1, -(1 << 31), (1 << 31) - 1]
+    p[20:40] = rng.integers(-5000, 5000, 20)
+    plan, ws, _, _ = _plan([T], [0], 1, 1, D)
+    # pairs (1, 0): the results are the cosine and the sine themselves
+    q = torch.zeros((T, 1, D), device=DEV)
+    q[..., 0::2] = 1.0
+    out = torch.empty((T, 1, D), dtype=torch.bfloat16, device=DEV)
+    B.sps_qk_norm_rope(plan, q.bfloat16(), None, None, None, EPS,
+                       B.Rope(torch.from_numpy(f).to(DEV), positions=torch.from_numpy(p).to(DEV),
+                              interleaved=True), out, 1.0, None, ws)
+    torch.cuda.synchronize()
+    got = _f64(out)[:, 0]
+    mask = (1 << bits) - 1
+    for j in range(D // 2):
+        m, e = np.frexp(np.float64(f[j]))
+        mi, e = int(m * 2 ** 24), int(e) - 24  # f = mi 2^e, whole
+        for t in range(T):
+            x = int(p[t]) * mi * inv2pi
+            x = (x << e if e >= 0 else x >> -e) & mask
+            a = 2 * np.pi * (x / 2 ** bits)
+            off = 2 * np.pi * ((abs(float(f[j])) + 1) * abs(int(p[t])) * 2.0 ** -64 + 2.0 ** -25)
+            for d, ref in ((0, np.cos(a)), (1, np.sin(a))):
+                assert abs(got[t, 2 * j + d] - ref) <= BF16_HALF * abs(ref) + NOISE + off, (j, t, d)
