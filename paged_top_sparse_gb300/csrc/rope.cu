@@ -20,11 +20,13 @@
 //
 // Bound: memory for many tokens.  8192 tokens x 34 rows x 128 (143 MB): 28.6 us, 5.0 TB/s, 0.73
 // of a plain copy; the rest is the start and end of a launch of 20 us of work (32768 tokens x 40
-// rows: 111 us, 6.0 TB/s, 0.89) and the angles in front of a token's rows.  With the angles and coefficients made per row group instead of per
-// token 41.7 us.  5.6K tokens x 28 rows to E4M3 on three axes: 22.2 us, 0.53 of a copy (the same
-// arithmetic for fewer bytes).  64 tokens (1.1 MB): 2.8 us, a launch and a chain of three
-// dependent reads.  More passes in flight cost resident warps: four 29.6 us, eight 37; blocks of
-// 8 warps 40 against 33.
+// rows: 111 us, 6.0 TB/s, 0.89) and the angles in front of a token's rows.  With the angles and
+// coefficients made per row group instead of per token an earlier form took 41.7 us.  5.6K tokens x 28
+// rows to E4M3 on three axes: 22.2 us, 0.53 of a copy (more arithmetic for fewer bytes).  64 tokens
+// (1.1 MB): 2.8 us, a launch and a chain of three dependent reads.  Append: 65536 tokens of 8 heads
+// (537 MB) into a BF16 cache 104 us, 5.2 TB/s; into an NVFP4 cache 147 us, the divisions of its rule.
+// More passes in flight cost resident warps, larger blocks leave more of them idle at the end: 8192
+// tokens four passes 29.9 us, eight 33.9, blocks of 8 warps 34.2; E4M3 26.4, 29.3 and 25.0.
 #include <algorithm>
 #include <cstring>
 
@@ -397,8 +399,8 @@ kv_append_rope_kernel(DevPlan p, const __grid_constant__ DevRope r, KvRopeArgs a
 
 // Passes a warp walks: all of a token's where that gives every SM 24 warps, else fewer, so that a
 // batch of few tokens still spreads over the GPU (a decode step of 64 tokens: a warp per pass).
-// From 20 to 32 warps measures the same; 64 as the target split tokens that need not be, 38.7
-// against 32.8 us for 8192 tokens, since each part makes the token's angles again.
+// From 20 to 32 warps measures the same; 64 as the target splits tokens that need not be, 31.0
+// against 28.6 us for 8192 tokens, since each part makes the token's angles again.
 template <typename K, typename A>
 cudaError_t launch_rows(K kern, const DevPlan& p, const DevRope& r, A a, int passes,
                         cudaStream_t st) {
