@@ -286,7 +286,13 @@ struct AttTiles {
   int max_pages = 0;
 };
 
-// What a split costs: its longest block, and its cut tiles' pieces to merge.
+// What a split costs: its longest block, and its cut tiles' pieces to merge.  One unit for kernels whose
+// page takes 0.7 us (single tokens over NVFP4) to 1.6 us (two row tiles): a rule of thumb.  Measured,
+// us, with the merge left out and with it doubled (H / H_kv 32 / 8, 32 / 2, 4 / 2 and 32 / 4):
+//   few rows   32 tokens after 1K 32.8 (38.0, 32.8), 64 after 2K over NVFP4 16.0 (28.1, 16.0), 20 after
+//              5K 74.2 (70.0, 74.3); one token after 8K or 128K the same
+//   many rows  a 512-token prompt 12.7 (14.5, 12.7), five ragged requests D 64 14.1 (14.1, 18.5), D 128
+//              21.0 (18.8, 21.0), four chunks over NVFP4 165 (171, 165)
 double split_estimate(int64_t longest, int64_t pieces, bool few_rows) {
   const double merge = few_rows ? 6 + 0.01 * pieces : 2.5 + 0.05 * pieces;
   return (double)longest + (pieces ? merge : 0);
