@@ -13,6 +13,7 @@
 #include <memory>
 #include <mutex>
 #include <new>
+#include <numeric>
 #include <string>
 #include <vector>
 
@@ -489,19 +490,17 @@ void build_attention_work(sps_plan* pl) {
 
   pl->att_heads.assign(ctas, AttHead{});
   pl->att_merges.assign(ctas, AttMerge{-1, 0, 0, 0, 0, 0, 0, 0});
-  pl->att_pieces.reserve(count + 2 * ctas);
+  pl->att_pieces.resize(count + 2 * ctas);  // (the blob's room)
+  AttPiece* next = pl->att_pieces.data();
   int merges = 0, cta = -1;
   auto run = [&](int tile, int page0, int page1) {  // a piece more of block `cta`
     const AttTile& t = tiles.list[tile];
     const ReqInfo& ri = pl->reqs[t.req];
-    const AttPiece x{t.req, t.vg, t.tile, page0, page1, ri.q_len, ri.ctx, ri.tok0};
     AttHead& h = pl->att_heads[cta];
-    if (h.count++ == 0) {
-      h.first = x;
-      h.next = (int32_t)pl->att_pieces.size();
-    } else {
-      pl->att_pieces.push_back(x);
-    }
+    AttPiece* x = &h.first;
+    if (h.count++ == 0) h.next = (int32_t)(next - pl->att_pieces.data());
+    else x = next++;
+    *x = AttPiece{t.req, t.vg, t.tile, page0, page1, ri.q_len, ri.ctx, ri.tok0};
     if (page0 == 0 && page1 < t.pages)
       pl->att_merges[merges++] = AttMerge{t.req, t.vg, t.tile, cta, cta, ri.q_len, ri.tok0, 0};
     else if (page0 > 0)
@@ -542,7 +541,9 @@ void make_plan(const sps_problem& problem, sps_plan* pl) {
   const int Hg = p.num_q_heads / p.num_kv_heads;
 
   // per-request info, per-token metadata
-  std::vector<int32_t> tok_pos, tok_req;
+  const size_t num_tokens = std::accumulate(pl->q_lens.begin(), pl->q_lens.end(), (size_t)0);
+  std::vector<int32_t> tok_pos(num_tokens), tok_req(num_tokens);
+  pl->reqs.reserve(p.batch);
   int32_t tok = 0, page_base = 0;
   for (int b = 0; b < p.batch; ++b) {
     ReqInfo ri{};
@@ -557,11 +558,9 @@ void make_plan(const sps_problem& problem, sps_plan* pl) {
     pl->inv_blocks += (int64_t)p.num_kv_heads * ri.ch_per_bucket;
     ri.ch_base = (int32_t)pl->num_chunks;
     pl->num_chunks += (int64_t)ri.npages * p.num_kv_heads * ri.ch_per_bucket;
-    for (int i = 0; i < ri.q_len; ++i) {
-      tok_pos.push_back(ri.ctx + i);
-      tok_req.push_back(b);
-    }
-    for (int pg = 0; pg < ri.npages; ++pg) pl->page_req.push_back(b);
+    std::iota(tok_pos.begin() + tok, tok_pos.begin() + tok + ri.q_len, ri.ctx);
+    std::fill_n(tok_req.begin() + tok, ri.q_len, b);
+    pl->page_req.insert(pl->page_req.end(), ri.npages, b);
     page_base += ri.npages;
     tok += ri.q_len;
     pl->reqs.push_back(ri);
