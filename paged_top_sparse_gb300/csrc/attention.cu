@@ -24,11 +24,11 @@
 // work tile is 2048 cycles of products; Q K^T reads 64 KB of operands per row tile (512 cycles at
 // 128 bytes a cycle, as long as its products), so copies into the ring and P's way through the
 // softmax show, and a page takes about 1.6 us (3000 cycles).  BF16, D 128, H 32 / H_kv 2: an
-// 8192-token prompt 367 us (1.50 PFLOP/s, 0.77 of a large library product at boost clocks, 0.86
-// of its sustained rate), 8 x 512 after 32K 1.40 ms (1.59).  Single tokens: the cache's bytes; 64
+// 8192-token prompt 365 us (1.51 PFLOP/s, 0.77 of a large library product at boost clocks, 0.86
+// of its sustained rate), 8 x 512 after 32K 1.39 ms (1.61).  Single tokens: the cache's bytes; 64
 // after 32K (2.16 GB) 320 us, 6.75 TB/s. An NVFP4 cache adds the conversion of each tile in the
-// same SM's issue slots: four chunks of 200 to 700 after 2K to 9K 138 us (0.99 PFLOP/s), 64 x 3
-// tokens after 32K 225 us.
+// same SM's issue slots: four chunks of 200 to 700 after 2K to 9K 139 us (0.99 PFLOP/s), 64 x 3
+// tokens after 32K 229 us.
 //
 // One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
 //   warp 0     page-table reads and the copies: Q tiles and the K, V tiles of a page into a ring
