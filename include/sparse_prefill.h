@@ -66,7 +66,9 @@ enum {
   SPS_DEV_TIMEOUT = 1,     /* a bounded wait gave up */
   SPS_DEV_BAD_PAGE = 2,    /* page_table entry outside [0, num_phys_pages) */
   SPS_DEV_BAD_INDEX = 3,   /* a selected page outside [0, own page] of its row */
-  SPS_DEV_OVERFLOW = 4     /* more work items than the plan sized the workspace for */
+  SPS_DEV_OVERFLOW = 4,    /* more work items than the plan sized the workspace for */
+  SPS_DEV_NO_PAGES = 5,    /* sps_page_tables: the list of free pages is too short for the batch */
+  SPS_DEV_BAD_LENGTH = 6   /* sps_page_tables: a length below zero, or no room for its tokens */
 };
 
 /*
@@ -83,9 +85,16 @@ enum {
  *                      at most 8192 (1M tokens) with top_k <= 16 and 1024 (128K tokens) with
  *                      larger top_k, else SPS_EUNSUPPORTED
  *   num_phys_pages     number of physical pages in the K/V caches
- *   q_dtype / kv_dtype           attention inputs: BF16/BF16 or E4M3/NVFP4
+ *   q_dtype / kv_dtype           attention inputs: BF16/BF16, E4M3/NVFP4, BF16/E4M3 or E4M3/E4M3
  *   idx_q_dtype / idx_k_dtype    indexer inputs: BF16/BF16, E4M3/E4M3 or E4M3/NVFP4
  *   softmax_scale      multiplier of q.k inside the softmax (typically 1/sqrt(D))
+ *
+ * An E4M3 K/V cache holds codes [num_phys_pages][H_kv][128][D], one byte an element, and for K and for
+ * V an FP32 scale for each page and KV head, [num_phys_pages][H_kv]: an element is code x scale.  The
+ * calls below take such scales as k_scales / v_scales (4-byte aligned), finite and >= 0; in
+ * paged_attention_fwd a V scale counts as at least 2^-40 and at most 2^40, the range that
+ * sps_kv_append writes.  Its codes are read by the attention calls and by no indexer (E4M3 index keys
+ * are a cache of their own, with one scale).
  */
 typedef struct {
   int32_t batch;
@@ -198,7 +207,9 @@ sps_status topk_select(const sps_plan* plan, const float* scores, int64_t score_
  * groups of 128 query rows, own-page-only causal mask; K1 also reads the split stride).
  *   q            device [T][H][D], q_dtype (BF16, or E4M3 with q_scale)
  *   k_cache, v_cache  device [num_phys_pages][H_kv][128][D] (BF16), or NVFP4 codes
- *                [..][128][D/2] with k_scales / v_scales [..][128][D/16] E4M3
+ *                [..][128][D/2] with k_scales / v_scales [..][128][D/16] E4M3, or E4M3 codes with
+ *                a scale for each page and KV head (sps_problem).  Slots behind a request's last
+ *                token hold finite values
  *   page_table   device int32 [batch][max_pages_per_req]
  *   idx          device int32 [T*H][top_k] from topk_select (or any selection obeying its
  *                contract: ascending, -1 padded, pages <= own page)
@@ -311,7 +322,14 @@ sps_status sparse_prefill_fwd_fp8qk(const sps_plan* plan, const void* q, float q
  *                 or NVFP4 codes [..][128][D/2] with k_scales / v_scales [..][128][D/16]:
  *                 per 16-element block scale = E4M3(absmax / 6), code = E2M1(x / scale), both
  *                 divisions in FP32, conversions to nearest even and saturating; a block whose
- *                 scale rounds to zero gets zero codes
+ *                 scale rounds to zero gets zero codes; or E4M3 codes with a scale for each page
+ *                 and KV head (sps_problem).  Over the new rows of a page and head, the new scale is
+ *                 the smallest power of two s with max |x| / s <= 448, within [2^-40, 2^40]; where the
+ *                 page holds earlier tokens of the request (slots below ctx_len % 128) it is at least
+ *                 the present scale, and if it is larger, their codes become E4M3(code x (old / new)),
+ *                 quotient and product in FP32.  New codes are E4M3(x / scale), nearest even and
+ *                 saturating (a NaN stays one and does not count for the maximum).  A page that is
+ *                 written belongs to one request of the batch
  *   workspace     the plan's uploaded workspace (token positions); a page-table entry outside
  *                 [0, num_phys_pages) sets SPS_DEV_BAD_PAGE and skips the row
  * Slots not written keep their contents.
@@ -374,7 +392,7 @@ sps_status sps_qk_norm_rope(const sps_plan* plan, const void* q, int64_t q_token
  * sps_kv_append_rope -- sps_kv_append with the key's norm and rotation on the way: key rows as
  * sps_qk_norm_rope makes them (k_weight NULL: no norm; rope NULL: no rotation), value rows as they
  * are, into the slots sps_kv_append writes.  A BF16 cache takes the FP32 result rounded once; an
- * NVFP4 cache takes it quantised by sps_kv_append's rule, with no rounding before that.
+ * NVFP4 or E4M3 cache takes it quantised by sps_kv_append's rule, with no rounding before that.
  *   k_new, v_new  device BF16, token i's H_kv rows at + i * {k,v}_token_stride elements (16-byte
  *                 aligned, strides multiples of 8, >= H_kv * D)
  * The other arguments and the device status are those of sps_kv_append.
@@ -472,7 +490,9 @@ sps_status sparse_prefill_fwd_noalloc(const sps_plan* plan, const void* q, float
  *                time need scratch of their own
  *   workspace    the plan's uploaded workspace
  * Accumulation, maxima and sums are FP32; P is rounded to the 16-bit type of the second product
- * (BF16; FP16 over an NVFP4 cache, whose code x scale products are exact there).  BF16 P takes V of
+ * (BF16; FP16 over an NVFP4 cache, whose code x scale products are exact there, and over an E4M3 cache,
+ * whose codes are: the page's V scale goes into P, its K scale into the scores' factor, whose product
+ * with softmax_scale and q_scale is to stay within FP32).  BF16 P takes V of
  * any magnitude as it is, where sparse_prefill_fwd's FP16 P needs V within FP16's range; it costs
  * precision: 2.35e-3 relative L2 on random data against 1.7e-3 with FP16 P (and with the output's
  * own rounding alone).  The result is the same bits from call to call.  A captured call may be replayed after another plan that differs
@@ -489,6 +509,37 @@ sps_status paged_attention_fwd(const sps_plan* plan, const void* q, int64_t q_to
                                const int32_t* page_table, void* out_bf16,
                                int64_t out_token_stride, float* out_lse, void* scratch,
                                size_t scratch_bytes, void* workspace, sps_stream_t stream);
+
+/*
+ * sps_page_tables -- page tables and slot maps of a batch's new tokens, built on the device from request
+ * lengths and a list of free pages: no plan, no host copy of the lengths, one launch (a captured call
+ * serves a decode loop).  Request b holds pages for its ctx_lens[b] tokens, ceil(ctx / 128) entries of
+ * its row; the pages that its q_lens[b] new tokens need beyond them are taken from the list, in request
+ * order, and written behind those entries.  What the append, the indexer and the attention read as
+ * page_table is then complete.
+ *   batch        requests, 1 .. 16384
+ *   q_lens, ctx_lens  device int32 [batch], >= 0
+ *   free_pages   device int32 [num_free]: physical pages in the order they are given out
+ *   free_state   device int32 [2]: [0] pages taken from the list so far, moved on by this call; [1]
+ *                the library's, 0 between calls.  Calls that share it are ordered on one stream
+ *   page_table   device int32 [batch][max_pages_per_req]; no other entry is written
+ *   slots        device int64 [max_tokens] or NULL: where each new token goes, request after request:
+ *                physical page * 128 + position % 128; -1 behind the last token, and where the page
+ *                is negative
+ *   positions    device int32 [max_tokens] or NULL: each new token's position (as sps_rope's
+ *                positions); 0 behind the last token
+ *   max_tokens   room of slots and positions
+ *   starts       device int32 [batch + 1] or NULL: new tokens before each request, and all of them
+ *   dev_status   device int32 or NULL: SPS_DEV_NO_PAGES, or SPS_DEV_BAD_LENGTH for a length below
+ *                zero, a request of more than max_pages_per_req pages, or more new tokens than
+ *                max_tokens.  Nothing is taken or entered then: slots are -1, positions and starts 0
+ * Plan-free: max_pages_per_req <= 131072.
+ */
+sps_status sps_page_tables(int32_t batch, const int32_t* q_lens, const int32_t* ctx_lens,
+                           const int32_t* free_pages, int64_t num_free, int32_t* free_state,
+                           int32_t* page_table, int32_t max_pages_per_req, int64_t* slots,
+                           int32_t* positions, int64_t max_tokens, int32_t* starts,
+                           int32_t* dev_status, sps_stream_t stream);
 
 /*
  * sps_check_wait_timeout -- health check of the failure path every kernel relies on: a

@@ -97,6 +97,7 @@ def lib(path: str | None = None):
     L.sps_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.sps_quantize_e4m3.argtypes = [vp, i64, f32, vp, vp]
     L.sps_absmax_bf16.argtypes = [vp, i64, vp, vp]
+    L.sps_page_tables.argtypes = [i32, vp, vp, vp, i64, vp, vp, i32, vp, vp, i64, vp, vp, vp]
     rp = ctypes.POINTER(RopeArgs)
     L.sps_qk_norm_rope.argtypes = [vp, vp, i64, vp, i64, vp, vp, f32, rp, vp, i64, ctypes.c_int,
                                    f32, vp, i64, vp, vp]
@@ -161,10 +162,13 @@ class Plan:
         n = len(q_lens)
         self._ql = (ctypes.c_int32 * n)(*[int(x) for x in q_lens])
         self._cl = (ctypes.c_int32 * n)(*[int(x) for x in ctx_lens])
+        # the indexer takes the attention's types, or, beside an E4M3 cache (whose scales by page it
+        # does not read), BF16 index queries and keys
+        idx = ("bf16", "bf16") if kv_dtype == "e4m3" else (q_dtype, kv_dtype)
         self.problem = Problem(
             n, self._ql, self._cl, num_q_heads, num_kv_heads, head_dim, page_size, top_k,
             max_pages_per_req, num_phys_pages, DTYPE_CODES[q_dtype], DTYPE_CODES[kv_dtype],
-            DTYPE_CODES[idx_q_dtype or q_dtype], DTYPE_CODES[idx_k_dtype or kv_dtype],
+            DTYPE_CODES[idx_q_dtype or idx[0]], DTYPE_CODES[idx_k_dtype or idx[1]],
             float(softmax_scale if softmax_scale is not None else head_dim ** -0.5))
         self.handle = ctypes.c_void_p()
         ws = ctypes.c_size_t()
@@ -177,10 +181,13 @@ class Plan:
         self.table_shape, self.table_size = (n, max_pages_per_req), n * max_pages_per_req
         self.q_codes = self.problem.q_dtype == E4M3
         self.quant_kv = self.problem.kv_dtype == NVFP4
-        # bytes of a cache (an NVFP4 one's scales: an eighth of them), and the types that may hold it
+        # bytes of a cache (an NVFP4 one's scales: an eighth of them), and the types that may hold it;
+        # an E4M3 one's FP32 scales: one for each page and KV head
         elems = num_phys_pages * num_kv_heads * page_size * head_dim
-        self.cache_bytes = elems // 2 if self.quant_kv else elems * 2
-        self.cache_types = _CODES if self.quant_kv else _BITS16
+        e4m3 = self.problem.kv_dtype == E4M3
+        self.cache_bytes = elems // 2 if self.quant_kv else elems if e4m3 else elems * 2
+        self.cache_types = _CODES if self.quant_kv else _CODES8 if e4m3 else _BITS16
+        self.page_scales = num_phys_pages * num_kv_heads if e4m3 else 0
         # shapes of a query, and of new keys or values
         self.q_shape = (self.num_tokens, num_q_heads, head_dim)
         self.kv_shape = (self.num_tokens, num_kv_heads, head_dim)
@@ -323,16 +330,17 @@ class Rope:
         self.ref = ctypes.pointer(self.args)
 
 
-_F32 = _I32 = _BF16 = _BITS16 = _CODES = None
+_F32 = _I32 = _I64 = _BF16 = _BITS16 = _CODES = _CODES8 = None
 
 
 def _load_types():
-    global _F32, _I32, _BF16, _BITS16, _CODES
+    global _F32, _I32, _I64, _BF16, _BITS16, _CODES, _CODES8
     import torch
 
-    _F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+    _F32, _I32, _I64, _BF16 = torch.float32, torch.int32, torch.int64, torch.bfloat16
     _BITS16 = {torch.bfloat16, torch.int16, torch.uint16}
     _CODES = {torch.uint8, torch.int8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)}
+    _CODES8 = {torch.uint8, torch.int8, torch.float8_e4m3fn}
 
 
 def _vector(t, dtype, numel, name):
@@ -353,7 +361,7 @@ def _table(t, plan):
 
 
 def _caches(plan, k, v, k_scales, v_scales):
-    """The addresses of the caches, and of an NVFP4 cache's scales: contiguous, of the plan's type (or
+    """The addresses of the caches, and of a quantised cache's scales: contiguous, of the plan's type (or
     raw elements of its size), with the plan's pages at least."""
     n, types = plan.cache_bytes, plan.cache_types
     if (k.nbytes < n or v.nbytes < n or k.dtype not in types or v.dtype not in types
@@ -361,7 +369,13 @@ def _caches(plan, k, v, k_scales, v_scales):
         for t, name in ((k, "k_cache"), (v, "v_cache")):
             if t.nbytes < n or t.dtype not in types or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous "
-                                 f"{'NVFP4 codes' if plan.quant_kv else 'bfloat16'} of >= {n} bytes")
+                                 f"{'NVFP4 codes' if plan.quant_kv else 'E4M3 codes' if plan.page_scales else 'bfloat16'}"
+                                 f" of >= {n} bytes")
+    if plan.page_scales:
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            if t is None or t.dtype is not _F32 or t.numel() < plan.page_scales or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous float32, >= {plan.page_scales} elements")
+        return k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr()
     if not plan.quant_kv:
         return k.data_ptr(), v.data_ptr(), None, None
     for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
@@ -446,6 +460,34 @@ def paged_attention_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_sc
         *_caches(plan, k_cache, v_cache, k_scales, v_scales),
         _table(page_table, plan), out.data_ptr(), _rows(out, qs, "out"), _ptr(out_lse),
         scratch.data_ptr(), scratch.nbytes, _workspace(workspace, plan), _stream(stream))
+    if st:
+        _check(st)
+
+
+def sps_page_tables(q_lens, ctx_lens, free_pages, free_state, page_table, slots=None, positions=None,
+                    starts=None, dev_status=None, stream=None):
+    """Page-table rows, slots and positions of a batch's new tokens from its lengths (int32 [batch], on
+    the device) and a list of free pages: page_table int32 [batch][pages a request]; slots int64,
+    positions int32 (of one length, room for the batch's tokens); starts int32 [batch + 1];
+    free_state int32 [2]; dev_status int32 [1]."""
+    n = q_lens.numel()
+    if _I32 is None:
+        _load_types()
+    rows = 0 if slots is None and positions is None else (positions if slots is None else slots).numel()
+    _vector(q_lens, _I32, n, "q_lens")
+    _vector(ctx_lens, _I32, n, "ctx_lens")
+    _vector(free_pages, _I32, free_pages.numel(), "free_pages")
+    _vector(free_state, _I32, 2, "free_state")
+    _vector(slots, _I64, rows, "slots")
+    _vector(positions, _I32, rows, "positions")
+    _vector(starts, _I32, n + 1, "starts")
+    _vector(dev_status, _I32, 1, "dev_status")
+    if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.shape[0] < n or not page_table.is_contiguous():
+        raise ValueError(f"page_table must be a contiguous int32 tensor of >= {n} rows")
+    st = (_lib or lib()).sps_page_tables(
+        n, q_lens.data_ptr(), ctx_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+        free_state.data_ptr(), page_table.data_ptr(), page_table.shape[1], _ptr(slots),
+        _ptr(positions), rows, _ptr(starts), _ptr(dev_status), _stream(stream))
     if st:
         _check(st)
 

@@ -1035,9 +1035,9 @@ extern "C" void sps_internal_attention_wait(int64_t limit_ns) {
   g_skip_wait_ns = limit_ns > 0 ? (uint64_t)limit_ns : kWaitLimitNs;
 }
 
-cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_t q_stride,
-                             float q_scale, const void* kc, const void* vc, const void* ks,
-                             const void* vs, const int32_t* page_table, void* out,
+cudaError_t launch_attention(const DevPlan& p, sps_dtype qt, sps_dtype kvt, const void* q,
+                             int64_t q_stride, float q_scale, const void* kc, const void* vc,
+                             const void* ks, const void* vs, const int32_t* page_table, void* out,
                              int64_t out_stride, float* out_lse, void* scratch, cudaStream_t st) {
   if (p.att_ctas < 1 || p.att_ctas > kMaxCtas) return cudaErrorInvalidConfiguration;
   AttArgs a{};
@@ -1055,6 +1055,8 @@ cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_
   a.part_lse = a.part + 2ll * p.att_ctas * p.att_slot_rows * p.D;
   a.c = attention_factor(p.sm_scale, q_scale);
   a.skip_wait_ns = g_skip_wait_ns.load(std::memory_order_relaxed);
+  if (kvt == SPS_E4M3) return launch_attention_e4m3(p, qt == SPS_E4M3, a, st);
+  const bool quant = kvt == SPS_NVFP4;
   const RowPack rp(p.Hg);
   const bool single = p.att_slot_rows <= rp.TB * rp.HB;
 #define SPS_ATT(DD, QQ) \

@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t pack_p(float a, float b) {
 }
 
 struct AttArgs {
-  const uint8_t *q, *kc, *vc, *ks, *vs;  // NVFP4 plans (and Q's codes)
+  const uint8_t *q, *kc, *vc, *ks, *vs;  // quantised plans (and Q); E4M3: ks, vs are FP32
   int64_t q_stride;
   const int32_t* page_table;
   uint16_t* out;
@@ -86,6 +86,9 @@ struct AttArgs {
 
 // Single tokens over an NVFP4 cache (tiles of at most 16 rows): the products' part of launch_attention.
 cudaError_t launch_decode_nvfp4(const DevPlan& p, const AttArgs& a, cudaStream_t st);
+
+// Full attention over an E4M3 cache with a scale for each page and KV head.
+cudaError_t launch_attention_e4m3(const DevPlan& p, bool q_e4m3, const AttArgs& a, cudaStream_t st);
 
 }  // namespace att
 }  // namespace sps

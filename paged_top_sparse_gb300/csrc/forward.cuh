@@ -37,6 +37,7 @@
 #include <cstring>
 #include <cuda_fp16.h>
 
+#include "e4m3.cuh"
 #include "nvfp4.cuh"
 #include "ptx.cuh"
 #include "sps_internal.h"
@@ -48,8 +49,11 @@ constexpr int kThreads = 512;  // 4 warpgroups
 
 // Operand modes: kModeBF16 (Q, K, V BF16), kModeF16 (Q FP16 -- the exact copy of E4M3 codes --
 // and NVFP4 K/V converted in the loader), kModeFP8QK (Q E4M3 bytes, NVFP4 K rounded to E4M3,
-// S on the FP8 tensor core; V FP16).
-constexpr int kModeBF16 = 0, kModeF16 = 1, kModeFP8QK = 2;
+// S on the FP8 tensor core; V FP16).  Over an E4M3 cache, whose pages have an FP32 scale per head:
+// kModeE4BF16 (Q BF16, K converted to BF16) and kModeE4F16 (Q FP16, K converted to FP16), both exactly,
+// V FP16; the scale of K multiplies the scores, that of V the partial output.
+constexpr int kModeBF16 = 0, kModeF16 = 1, kModeFP8QK = 2, kModeE4BF16 = 3, kModeE4F16 = 4;
+constexpr bool mode_e4(int mode) { return mode >= kModeE4BF16; }
 // Partial storage: FP32, BF16 or FP16 (nearest even).
 constexpr int kPF32 = 0, kPBF16 = 1, kPF16 = 2;
 
@@ -60,13 +64,16 @@ struct FwdSmem {
   static constexpr int PE = PT == kPF32 ? 4 : 2;         // bytes per partial element
   static constexpr int TQK = 128 * D * QE;  // 128-row Q or K tile
   static constexpr int TV = 128 * D * 2;    // 128-row V tile (16-bit)
-  static constexpr int RC = 128 * D / 2;    // NVFP4 codes of one tile
-  static constexpr int RSC = 128 * D / 16;  // its E4M3 scales
+  static constexpr bool E4 = mode_e4(MODE);
+  static constexpr int RC = E4 ? 128 * D : 128 * D / 2;  // codes of one tile
+  static constexpr int RSC = E4 ? 0 : 128 * D / 16;      // an NVFP4 tile's E4M3 scales
   static constexpr int RAWB = RAW ? RC + RSC : 16;
   static constexpr int EPR = D * PE + 16;  // staging row pitch (pad: conflict-free writes)
   static constexpr int EPB = 32 * EPR;     // one epilogue warp's 32 rows
   static constexpr int kBudget = 227 * 1024 - 1024;  // dynamic smem minus the alignment slack
-  static constexpr int FIXED = TQK + TV + 2 * RAWB + 4 * EPB + 4096;
+  // K's and V's codes have a staging area each, or share one (E4M3 codes beside FP32 partials)
+  static constexpr int RAWN = E4 && TQK + TV + 2 * RAWB + 4 * EPB + 4096 + 2 * TQK > kBudget ? 1 : 2;
+  static constexpr int FIXED = TQK + TV + RAWN * RAWB + 4 * EPB + 4096;
   static constexpr int QS0 = (kBudget - FIXED) / TQK;
   static constexpr int QS = QS0 > 4 ? 4 : QS0;  // Q ring stages
   static_assert(QS >= 2, "shared memory");
@@ -74,10 +81,12 @@ struct FwdSmem {
   uint8_t v[TV];
   uint8_t q[QS][TQK];
   alignas(16) uint8_t kraw[RAWB];
-  alignas(16) uint8_t vraw[RAWB];
+  alignas(16) uint8_t vraw[RAWN == 2 ? RAWB : 16];
   alignas(16) uint8_t ep[4][EPB];
   float inv_l[2][128];
   int2 rs[2][128];
+  float2 sc[E4 ? 4 : 1];  // scales of K and V of items n, n + 1, ...
+  uint64_t sc_full[E4 ? 4 : 1];
   uint64_t k_full, k_empty, v_full, v_empty, v_ready;
   uint64_t kraw_full, kraw_empty, vraw_full, vraw_empty;
   uint64_t q_full[QS], q_empty[QS];
@@ -125,14 +134,15 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   using Smem = FwdSmem<D, MODE, PT>;
   constexpr bool RAW = Smem::RAW;
   constexpr bool FP8QK = MODE == kModeFP8QK;
+  constexpr bool ONE_RAW = Smem::RAWN == 1;  // one staging area: K, V, K, V, ...
   constexpr int kQS = Smem::QS;
   constexpr int DB = D / 64;               // 128-byte column blocks of a 16-bit (V) row
   constexpr int DBQ = D * Smem::QE / 128;  // 128-byte column blocks of a Q / K row
   constexpr int TQK = Smem::TQK, TILE = Smem::TV;
   constexpr int QK_STEPS = D * Smem::QE / 32;  // one MMA per 32 bytes of K depth
   constexpr int PE = Smem::PE;
-  constexpr uint32_t IDESC_QK = idesc_mma(MODE == kModeBF16, MODE == kModeBF16, 128, 128, false,
-                                          false);
+  constexpr bool QK_BF16 = MODE == kModeBF16 || MODE == kModeE4BF16;
+  constexpr uint32_t IDESC_QK = idesc_mma(QK_BF16, QK_BF16, 128, 128, false, false);
   constexpr uint32_t IDESC_PV = idesc_mma(false, false, 128, D, false, true);
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -165,6 +175,8 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       mbar_init(smem_u32(&sm.st_empty[i]), 4);
     }
     mbar_init(smem_u32(&sm.done), 1);
+    if (Smem::E4)
+      for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sm.sc_full[i]), 1);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -218,16 +230,29 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
       } else {
         // codes and scales of K, then of V, one item ahead of the conversion
-        if (!mbar_wait(smem_u32(&sm.kraw_empty), (kv_it & 1) ^ 1, abort_flag, status)) break;
+        const uint32_t kn = ONE_RAW ? 2 * kv_it : kv_it, vn = ONE_RAW ? kn + 1 : kv_it;
+        if (!mbar_wait(smem_u32(&sm.kraw_empty), (kn & 1) ^ 1, abort_flag, status)) break;
         uint32_t f = smem_u32(&sm.kraw_full);
         mbar_expect_tx(f, Smem::RC + Smem::RSC);
         bulk_load(smem_u32(sm.kraw), kc + (int64_t)tile * Smem::RC, Smem::RC, f);
-        bulk_load(smem_u32(sm.kraw) + Smem::RC, ks + (int64_t)tile * Smem::RSC, Smem::RSC, f);
-        if (!mbar_wait(smem_u32(&sm.vraw_empty), (kv_it & 1) ^ 1, abort_flag, status)) break;
-        f = smem_u32(&sm.vraw_full);
+        if (Smem::E4) {
+          // (K of item n - 1 has been converted, so the last S of item n - 2 is done, and with it the
+          // softmax of item n - 4, the last reader of this entry)
+          sm.sc[kv_it & 3] = make_float2(__ldg(reinterpret_cast<const float*>(ks) + tile),
+                                         __ldg(reinterpret_cast<const float*>(vs) + tile));
+          mbar_arrive(smem_u32(&sm.sc_full[kv_it & 3]));
+        } else {
+          bulk_load(smem_u32(sm.kraw) + Smem::RC, ks + (int64_t)tile * Smem::RSC, Smem::RSC, f);
+        }
+        uint8_t* vraw = ONE_RAW ? sm.kraw : sm.vraw;
+        f = smem_u32(ONE_RAW ? &sm.kraw_full : &sm.vraw_full);
+        if (!mbar_wait(smem_u32(ONE_RAW ? &sm.kraw_empty : &sm.vraw_empty), (vn & 1) ^ 1, abort_flag,
+                       status))
+          break;
         mbar_expect_tx(f, Smem::RC + Smem::RSC);
-        bulk_load(smem_u32(sm.vraw), vc + (int64_t)tile * Smem::RC, Smem::RC, f);
-        bulk_load(smem_u32(sm.vraw) + Smem::RC, vs + (int64_t)tile * Smem::RSC, Smem::RSC, f);
+        bulk_load(smem_u32(vraw), vc + (int64_t)tile * Smem::RC, Smem::RC, f);
+        if (!Smem::E4)
+          bulk_load(smem_u32(vraw) + Smem::RC, vs + (int64_t)tile * Smem::RSC, Smem::RSC, f);
       }
       ++kv_it;
     }
@@ -349,26 +374,31 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.v_ready));
       } else {
-        // NVFP4 K once the previous item's last S is done, then V after its last P.V
-        if (!mbar_wait(smem_u32(&sm.kraw_full), ph, abort_flag, status) ||
+        // K once the previous item's last S is done, then V after its last P.V
+        uint8_t* vraw = ONE_RAW ? sm.kraw : sm.vraw;
+        uint64_t* vfull = ONE_RAW ? &sm.kraw_full : &sm.vraw_full;
+        uint64_t* vempty = ONE_RAW ? &sm.kraw_empty : &sm.vraw_empty;
+        if (!mbar_wait(smem_u32(&sm.kraw_full), ONE_RAW ? 0 : ph, abort_flag, status) ||
             !mbar_wait(smem_u32(&sm.k_empty), ph ^ 1, abort_flag, status))
           break;
-        nvfp4_tile_convert<D, FP8QK>(sm.kraw, sm.k, ct, 64);
+        if (Smem::E4) e4m3_tile_convert<D, QK_BF16>(sm.kraw, sm.k, ct, 64);
+        else nvfp4_tile_convert<D, FP8QK>(sm.kraw, sm.k, ct, 64);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm.k_full));
           mbar_arrive(smem_u32(&sm.kraw_empty));
         }
-        if (!mbar_wait(smem_u32(&sm.vraw_full), ph, abort_flag, status) ||
+        if (!mbar_wait(smem_u32(vfull), ONE_RAW ? 1 : ph, abort_flag, status) ||
             !mbar_wait(smem_u32(&sm.v_empty), ph ^ 1, abort_flag, status))
           break;
-        nvfp4_tile_convert<D, false>(sm.vraw, sm.v, ct, 64);
+        if (Smem::E4) e4m3_tile_convert<D, false>(vraw, sm.v, ct, 64);
+        else nvfp4_tile_convert<D, false>(vraw, sm.v, ct, 64);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm.v_ready));
-          mbar_arrive(smem_u32(&sm.vraw_empty));
+          mbar_arrive(smem_u32(vempty));
         }
       }
       ++kv_it;
@@ -380,10 +410,18 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const int quarter = warp % 4;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const float c = p.sm_scale * q_scale * 1.4426950408889634f;  // scale * log2(e)
-    uint32_t g_it = 0;
-    for (int ti = blockIdx.x; ti < ntasks; ti += gridDim.x) {
+    float c = p.sm_scale * q_scale * 1.4426950408889634f;  // scale * log2(e)
+    const float c_plan = c;
+    float v_scale = 1.f;
+    uint32_t g_it = 0, item = 0;
+    for (int ti = blockIdx.x; ti < ntasks; ti += gridDim.x, ++item) {
       const FwdTask t = p.fwd_tasks[ti];
+      if (Smem::E4) {
+        if (!mbar_wait(smem_u32(&sm.sc_full[item & 3]), (item >> 2) & 1, abort_flag, status)) break;
+        const float2 sc = sm.sc[item & 3];
+        c = c_plan * sc.x;
+        v_scale = sc.y;
+      }
       const int gp = t.bucket / p.Hkv;
       const int pg = gp - p.reqs[p.page_req[gp]].page_base;
       const int ngroups = (t.count + 127) / 128;
@@ -456,7 +494,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tmem_st_wait();
         // row statistics for the epilogue; LSE straight to global
         if (!mbar_wait(smem_u32(&sm.st_empty[b]), ph ^ 1, abort_flag, status)) { ok = false; break; }
-        sm.inv_l[b][row] = 1.f / l;
+        sm.inv_l[b][row] = Smem::E4 ? v_scale / l : 1.f / l;
         sm.rs[b][row] = rs;
         if (live) lse[rs.y * lse_split_stride + rs.x] = (mc + log2f(l)) * 0.6931471805599453f;
         tc_fence_before();
@@ -635,7 +673,8 @@ cudaError_t run_forward(const DevPlan& p, const void* q, const void* kc, const v
   const uint64_t R = (uint64_t)p.T * p.H;
   const uint64_t kv_rows = (uint64_t)p.num_phys * p.Hkv * 128;
   // tensor-map element types: BF16 (0), FP16 (1) or bytes (2); Q and K rows of 128 bytes
-  const int dq = MODE == kModeBF16 ? 0 : (MODE == kModeF16 ? 1 : 2);
+  const int dq = MODE == kModeBF16 || MODE == kModeE4BF16 ? 0
+                 : MODE == kModeF16 || MODE == kModeE4F16 ? 1 : 2;
   const uint64_t qe = MODE == kModeFP8QK ? 1 : 2;
   const uint32_t box_q = (uint32_t)(128 / qe);
   if (!encode_tmap_2d(&tmQ, dq, const_cast<void*>(q), D, R, (uint64_t)D * qe, box_q, 1, true))
@@ -675,6 +714,23 @@ cudaError_t launch_forward_pt(const DevPlan& p, sps_dtype qt, sps_dtype kvt, con
                                              split_stride, lse, lse_split_stride, q_scale, st);
     return run_forward<64, kModeBF16, PT>(p, q, kc, vc, nullptr, nullptr, page_table, partial,
                                           split_stride, lse, lse_split_stride, q_scale, st);
+  }
+  if (qt == SPS_BF16 && kvt == SPS_E4M3) {
+    if (p.D == 128)
+      return run_forward<128, kModeE4BF16, PT>(p, q, kc, vc, ks, vs, page_table, partial, split_stride,
+                                               lse, lse_split_stride, q_scale, st);
+    return run_forward<64, kModeE4BF16, PT>(p, q, kc, vc, ks, vs, page_table, partial, split_stride,
+                                            lse, lse_split_stride, q_scale, st);
+  }
+  if (qt == SPS_E4M3 && kvt == SPS_E4M3) {
+    if (!p.qconv) return cudaErrorInvalidValue;
+    cudaError_t e = launch_dequant(SPS_E4M3, q, nullptr, (int64_t)p.T * p.H * p.D, p.qconv, st);
+    if (e != cudaSuccess) return e;
+    if (p.D == 128)
+      return run_forward<128, kModeE4F16, PT>(p, p.qconv, kc, vc, ks, vs, page_table, partial,
+                                              split_stride, lse, lse_split_stride, q_scale, st);
+    return run_forward<64, kModeE4F16, PT>(p, p.qconv, kc, vc, ks, vs, page_table, partial,
+                                           split_stride, lse, lse_split_stride, q_scale, st);
   }
   if (qt == SPS_E4M3 && kvt == SPS_NVFP4) {
     if (!p.qconv) return cudaErrorInvalidValue;

@@ -151,6 +151,8 @@ struct sps_plan {
   int32_t att_ctas = 0, att_slot_rows = 0, att_num_merges = 0, att_merge_cap = 0;
   int64_t off_att_heads = 0, off_att_pieces = 0, off_att_merges = 0;
   int64_t att_tiles = 0;
+  std::vector<AppUnit> app_units;  // the pages an E4M3 cache's append touches
+  int64_t off_app_units = 0;
   int64_t upload_bytes = 0;  // [0, upload_bytes) of the workspace comes from `blob`
   std::vector<uint8_t> blob;
 };
@@ -173,8 +175,11 @@ sps_status validate_problem(const sps_problem* p) {
   if (!(p->softmax_scale > 0.f) || !std::isfinite(p->softmax_scale))
     return fail(SPS_EINVAL, "softmax_scale must be finite and > 0");
   bool attn_ok = (p->q_dtype == SPS_BF16 && p->kv_dtype == SPS_BF16) ||
-                 (p->q_dtype == SPS_E4M3 && p->kv_dtype == SPS_NVFP4);
-  if (!attn_ok) return fail(SPS_EUNSUPPORTED, "attention dtypes must be BF16/BF16 or E4M3/NVFP4");
+                 (p->q_dtype == SPS_E4M3 && p->kv_dtype == SPS_NVFP4) ||
+                 ((p->q_dtype == SPS_BF16 || p->q_dtype == SPS_E4M3) && p->kv_dtype == SPS_E4M3);
+  if (!attn_ok)
+    return fail(SPS_EUNSUPPORTED,
+                "attention dtypes must be BF16/BF16, E4M3/NVFP4, BF16/E4M3 or E4M3/E4M3");
   bool idx_ok = (p->idx_q_dtype == SPS_BF16 && p->idx_k_dtype == SPS_BF16) ||
                 (p->idx_q_dtype == SPS_E4M3 && p->idx_k_dtype == SPS_E4M3) ||
                 (p->idx_q_dtype == SPS_E4M3 && p->idx_k_dtype == SPS_NVFP4);
@@ -530,6 +535,22 @@ void build_attention_work(sps_plan* pl) {
   pl->att_num_merges = merges;
 }
 
+// The pages that the new tokens touch, for the append that keeps a scale for each page.  A request of
+// q tokens touches at most (q + 126) / 128 + 1 pages, whatever its context: that many entries.
+void build_append_units(sps_plan* pl) {
+  for (const ReqInfo& ri : pl->reqs) {
+    if (ri.q_len == 0) continue;
+    const int b = (int)(&ri - pl->reqs.data());
+    const size_t end = pl->app_units.size() + (ri.q_len + 126) / kPage + 1;
+    for (int i = 0; i < ri.q_len;) {
+      const int t = ri.ctx + i, n = std::min(ri.q_len - i, kPage - t % kPage);
+      pl->app_units.push_back(AppUnit{b, t / kPage, ri.tok0 + i, n, t % kPage, {0, 0, 0}});
+      i += n;
+    }
+    pl->app_units.resize(end, AppUnit{});
+  }
+}
+
 // Fills the plan of a valid problem (throws std::bad_alloc).
 void make_plan(const sps_problem& problem, sps_plan* pl) {
   pl->pb = problem;
@@ -574,6 +595,7 @@ void make_plan(const sps_problem& problem, sps_plan* pl) {
   pl->max_fwd_tasks = pl->max_entries / per_task + pl->num_buckets + 1;
   build_indexer_tasks(pl);
   build_attention_work(pl);
+  if (p.kv_dtype == SPS_E4M3) build_append_units(pl);
 
   // workspace layout
   int64_t off = 0;
@@ -588,6 +610,7 @@ void make_plan(const sps_problem& problem, sps_plan* pl) {
   pl->off_att_heads = take(sizeof(AttHead) * pl->att_heads.size());
   pl->off_att_merges = take(sizeof(AttMerge) * pl->att_merges.size());
   pl->off_att_pieces = take(sizeof(AttPiece) * (pl->att_tiles + 2 * pl->att_ctas));
+  if (!pl->app_units.empty()) pl->off_app_units = take(sizeof(AppUnit) * pl->app_units.size());
   pl->fwd_base = off;
   pl->off_status = take(4);
   pl->off_counters = take(16 * 4);
@@ -652,6 +675,7 @@ void make_plan(const sps_problem& problem, sps_plan* pl) {
   put(pl->off_att_heads, pl->att_heads.data(), sizeof(AttHead) * pl->att_heads.size());
   put(pl->off_att_pieces, pl->att_pieces.data(), sizeof(AttPiece) * pl->att_pieces.size());
   put(pl->off_att_merges, pl->att_merges.data(), sizeof(AttMerge) * pl->att_merges.size());
+  put(pl->off_app_units, pl->app_units.data(), sizeof(AppUnit) * pl->app_units.size());
   put(pl->off_page_req, pl->page_req.data(), 4 * pl->page_req.size());
   put(pl->off_idx_tasks, pl->idx_tasks.data(), sizeof(IdxTask) * pl->idx_tasks.size());
 }
@@ -755,6 +779,8 @@ DevPlan make_dev_plan(const sps_plan* pl, void* ws) {
   d.att_slot_rows = pl->att_slot_rows;
   d.att_num_merges = pl->att_num_merges;
   d.att_merge_cap = pl->att_merge_cap;
+  d.app_units = reinterpret_cast<const AppUnit*>(base + pl->off_app_units);
+  d.num_app_units = (int32_t)pl->app_units.size();
   return d;
 }
 
@@ -762,6 +788,17 @@ sps_status check_plan_ws(const sps_plan* pl, const void* ws) {
   if (!pl) return fail(SPS_EINVAL, "plan is NULL");
   if (!ws) return fail(SPS_EINVAL, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(SPS_EINVAL, "workspace must be 256-byte aligned");
+  return SPS_OK;
+}
+
+// The scales of a plan's K/V cache: E4M3 bytes (NVFP4) or FP32 (E4M3).
+sps_status check_kv_scales(const sps_problem& p, const void* ks, const void* vs, const char* who) {
+  const bool e4m3 = p.kv_dtype == SPS_E4M3;
+  if ((p.kv_dtype == SPS_NVFP4 || e4m3) && (!ks || !vs))
+    return fail(SPS_EINVAL, "%s: %s K/V need k_scales and v_scales", who, e4m3 ? "E4M3" : "NVFP4");
+  const uintptr_t a = e4m3 ? 4 : 16;
+  if ((ks && !aligned(ks, a)) || (vs && !aligned(vs, a)))
+    return fail(SPS_EINVAL, "%s: k_scales/v_scales must be %d-byte aligned", who, (int)a);
   return SPS_OK;
 }
 
@@ -847,10 +884,9 @@ sps_status fwd_common(const sps_plan* pl, const void* q, float q_scale, const vo
   const sps_problem& p = pl->pb;
   if (!q || !k_cache || !v_cache || !page_table || !idx || !partial || !lse)
     return fail(SPS_EINVAL, "sparse_prefill_fwd: NULL input/output pointer");
-  if (p.kv_dtype == SPS_NVFP4 && (!k_scales || !v_scales))
-    return fail(SPS_EINVAL, "sparse_prefill_fwd: NVFP4 K/V need k_scales and v_scales");
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      (k_scales && !aligned(k_scales, 16)) || (v_scales && !aligned(v_scales, 16)))
+  st = check_kv_scales(p, k_scales, v_scales, "sparse_prefill_fwd");
+  if (st != SPS_OK) return st;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
     return fail(SPS_EINVAL, "sparse_prefill_fwd: q/k/v buffers must be 16-byte aligned");
   if (!aligned(partial, 16)) return fail(SPS_EINVAL, "partial must be 16-byte aligned");
   const int64_t qa = p16 ? 8 : 4;  // elements per 16 bytes
@@ -1001,9 +1037,7 @@ sps_status sps_kv_append(const sps_plan* pl, const void* k_new, const void* v_ne
   sps_status st = check_plan_ws(pl, ws);
   if (st != SPS_OK) return st;
   const sps_problem& p = pl->pb;
-  const bool nvfp4 = p.kv_dtype == SPS_NVFP4;
-  if (p.kv_dtype != SPS_BF16 && !nvfp4)
-    return fail(SPS_EUNSUPPORTED, "sps_kv_append: the cache must be BF16 or NVFP4");
+  const bool nvfp4 = p.kv_dtype == SPS_NVFP4, e4m3 = p.kv_dtype == SPS_E4M3;
   if (!k_new || !v_new || !page_table || !k_cache || !v_cache)
     return fail(SPS_EINVAL, "sps_kv_append: NULL pointer");
   if (nvfp4 && (!k_scales || !v_scales))
@@ -1012,6 +1046,22 @@ sps_status sps_kv_append(const sps_plan* pl, const void* k_new, const void* v_ne
       !aligned(v_cache, 16) || !aligned(page_table, 4))
     return fail(SPS_EINVAL, "sps_kv_append: buffers must be 16-byte aligned");
   DevPlan d = make_dev_plan(pl, ws);
+  if (e4m3) {
+    st = check_kv_scales(p, k_scales, v_scales, "sps_kv_append");
+    if (st != SPS_OK) return st;
+    KvRopeArgs a{};
+    a.k = static_cast<const uint16_t*>(k_new);
+    a.v = static_cast<const uint16_t*>(v_new);
+    a.page_table = page_table;
+    a.kc = static_cast<uint8_t*>(k_cache);
+    a.vc = static_cast<uint8_t*>(v_cache);
+    a.ks = static_cast<uint8_t*>(k_scales);
+    a.vs = static_cast<uint8_t*>(v_scales);
+    a.k_stride = a.v_stride = (int64_t)p.num_kv_heads * p.head_dim;
+    return launched(launch_kv_append_e4m3(d, DevRope{}, a, false,
+                                          reinterpret_cast<cudaStream_t>(stream)),
+                    "kv append launch");
+  }
   return launched(launch_kv_append(d, nvfp4, k_new, v_new, page_table, k_cache, v_cache, k_scales,
                                    v_scales, reinterpret_cast<cudaStream_t>(stream)),
                   "kv append launch");
@@ -1118,11 +1168,13 @@ sps_status sps_kv_append_rope(const sps_plan* pl, const void* k_new, int64_t k_s
   sps_status st = check_plan_ws(pl, ws);
   if (st != SPS_OK) return st;
   const sps_problem& p = pl->pb;
-  const bool nvfp4 = p.kv_dtype == SPS_NVFP4;
-  if (p.kv_dtype != SPS_BF16 && !nvfp4)
-    return fail(SPS_EUNSUPPORTED, "sps_kv_append_rope: the cache must be BF16 or NVFP4");
-  if (!page_table || !k_cache || !v_cache || (nvfp4 && (!k_scales || !v_scales)))
-    return fail(SPS_EINVAL, "sps_kv_append_rope: NULL pointer (an NVFP4 cache needs its scales)");
+  const bool nvfp4 = p.kv_dtype == SPS_NVFP4, e4m3 = p.kv_dtype == SPS_E4M3;
+  if (!page_table || !k_cache || !v_cache || ((nvfp4 || e4m3) && (!k_scales || !v_scales)))
+    return fail(SPS_EINVAL, "sps_kv_append_rope: NULL pointer (a quantised cache needs its scales)");
+  if (e4m3) {
+    st = check_kv_scales(p, k_scales, v_scales, "sps_kv_append_rope");
+    if (st != SPS_OK) return st;
+  }
   const int64_t kn = (int64_t)p.num_kv_heads * p.head_dim;
   if (!rows_ok(k_new, k_stride, kn, 8) || !rows_ok(v_new, v_stride, kn, 8))
     return fail(SPS_EINVAL,
@@ -1148,6 +1200,10 @@ sps_status sps_kv_append_rope(const sps_plan* pl, const void* k_new, int64_t k_s
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   a.eps = eps;
+  if (e4m3)
+    return launched(launch_kv_append_e4m3(make_dev_plan(pl, ws), r, a, rope && rope->interleaved,
+                                          reinterpret_cast<cudaStream_t>(stream)),
+                    "kv append with rotation launch");
   return launched(launch_kv_append_rope(make_dev_plan(pl, ws), r, a, rope && rope->interleaved,
                                         nvfp4, reinterpret_cast<cudaStream_t>(stream)),
                   "kv append with rotation launch");
@@ -1167,18 +1223,22 @@ sps_status paged_attention_fwd(const sps_plan* pl, const void* q, int64_t q_stri
   sps_status st = check_plan_ws(pl, ws);
   if (st != SPS_OK) return st;
   const sps_problem& p = pl->pb;
-  const bool quant = p.kv_dtype == SPS_NVFP4;
+  const bool quant = p.kv_dtype != SPS_BF16;
   const int64_t n = (int64_t)p.num_q_heads * p.head_dim;
-  if (!rows_ok(q, q_stride, n, quant ? 16 : 8) || !rows_ok(out_bf16, out_stride, n, 8))
+  if (!rows_ok(q, q_stride, n, p.q_dtype == SPS_E4M3 ? 16 : 8) || !rows_ok(out_bf16, out_stride, n, 8))
     return fail(SPS_EINVAL,
                 "paged_attention_fwd: q and out must be non-NULL and 16-byte aligned, token "
                 "strides multiples of 16 bytes and at least num_q_heads * head_dim");
   if (!k_cache || !v_cache || !page_table || (quant && (!k_scales || !v_scales)))
-    return fail(SPS_EINVAL, "paged_attention_fwd: NULL pointer (an NVFP4 cache needs its scales)");
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || (quant && (!aligned(k_scales, 16) ||
-      !aligned(v_scales, 16))) || !aligned(page_table, 4) || (out_lse && !aligned(out_lse, 4)))
+    return fail(SPS_EINVAL, "paged_attention_fwd: NULL pointer (a quantised cache needs its scales)");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(page_table, 4) ||
+      (out_lse && !aligned(out_lse, 4)))
     return fail(SPS_EINVAL, "paged_attention_fwd: caches must be 16-byte, page_table and out_lse "
                             "4-byte aligned");
+  if (quant) {
+    st = check_kv_scales(p, k_scales, v_scales, "paged_attention_fwd");
+    if (st != SPS_OK) return st;
+  }
   if (!(q_scale > 0.f) || !std::isfinite(q_scale))
     return fail(SPS_EINVAL, "paged_attention_fwd: q_scale must be finite and > 0");
   const float c = attention_factor(p.softmax_scale, q_scale);
@@ -1194,10 +1254,46 @@ sps_status paged_attention_fwd(const sps_plan* pl, const void* q, int64_t q_stri
   if ((int64_t)p.num_phys_pages * p.num_kv_heads > 0x7fffffff / kPage)
     return fail(SPS_EUNSUPPORTED, "paged_attention_fwd: num_phys_pages x num_kv_heads must stay "
                                   "below 2^24");
-  return launched(launch_attention(make_dev_plan(pl, ws), quant, q, q_stride, q_scale, k_cache,
-                                   v_cache, k_scales, v_scales, page_table, out_bf16, out_stride,
-                                   out_lse, scratch, reinterpret_cast<cudaStream_t>(stream)),
+  return launched(launch_attention(make_dev_plan(pl, ws), p.q_dtype, p.kv_dtype, q, q_stride,
+                                   q_scale, k_cache, v_cache, k_scales, v_scales, page_table,
+                                   out_bf16, out_stride, out_lse, scratch,
+                                   reinterpret_cast<cudaStream_t>(stream)),
                   "paged attention launch");
+}
+
+sps_status sps_page_tables(int32_t batch, const int32_t* q_lens, const int32_t* ctx_lens,
+                           const int32_t* free_pages, int64_t num_free, int32_t* free_state,
+                           int32_t* page_table, int32_t max_pages_per_req, int64_t* slots,
+                           int32_t* positions, int64_t max_tokens, int32_t* starts,
+                           int32_t* dev_status, sps_stream_t stream) {
+  if (batch < 1) return fail(SPS_EINVAL, "sps_page_tables: batch must be >= 1 (got %d)", batch);
+  if (batch > kMaxTableBatch)
+    return fail(SPS_EUNSUPPORTED, "sps_page_tables: batch above %d is not supported", kMaxTableBatch);
+  if (max_pages_per_req < 1 || max_pages_per_req > (1 << 24) / kPage)
+    return fail(SPS_EINVAL, "sps_page_tables: max_pages_per_req must be in [1, %d]", (1 << 24) / kPage);
+  if (max_tokens < 0 || max_tokens > 0x7fffffffLL || num_free < 0 || num_free > 0x7fffffffLL)
+    return fail(SPS_EINVAL, "sps_page_tables: max_tokens and num_free must be in [0, 2^31)");
+  if (!q_lens || !ctx_lens || (!free_pages && num_free > 0) || !free_state || !page_table)
+    return fail(SPS_EINVAL, "sps_page_tables: NULL pointer");
+  if (!aligned(q_lens, 4) || !aligned(ctx_lens, 4) || !aligned(free_pages, 4) ||
+      !aligned(free_state, 4) || !aligned(page_table, 4) || !aligned(slots, 8) ||
+      !aligned(positions, 4) || !aligned(starts, 4) || !aligned(dev_status, 4))
+    return fail(SPS_EINVAL, "sps_page_tables: slots must be 8-byte, the other arrays 4-byte aligned");
+  PageTableArgs a{};
+  a.q_lens = q_lens;
+  a.ctx_lens = ctx_lens;
+  a.free_pages = free_pages;
+  a.free_state = free_state;
+  a.page_table = page_table;
+  a.slots = slots;
+  a.positions = positions;
+  a.starts = starts;
+  a.status = dev_status;
+  a.num_free = num_free;
+  a.max_tokens = max_tokens;
+  a.batch = batch;
+  a.max_pages = max_pages_per_req;
+  return launched(launch_page_tables(a, reinterpret_cast<cudaStream_t>(stream)), "page tables launch");
 }
 
 sps_status sps_quantize_e4m3(const void* x_bf16, int64_t n, float scale, void* codes,
@@ -1377,10 +1473,9 @@ sps_status sps_internal_fwd_noalloc(const sps_plan* pl, const void* q, float q_s
   const sps_problem& p = pl->pb;
   if (!q || !k_cache || !v_cache || !page_table || !idx || !partial || !lse)
     return fail(SPS_EINVAL, "sparse_prefill_fwd_noalloc: NULL input/output pointer");
-  if (p.kv_dtype == SPS_NVFP4 && (!k_scales || !v_scales))
-    return fail(SPS_EINVAL, "sparse_prefill_fwd_noalloc: NVFP4 K/V need k_scales and v_scales");
-  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      (k_scales && !aligned(k_scales, 16)) || (v_scales && !aligned(v_scales, 16)))
+  sps_status st = check_kv_scales(p, k_scales, v_scales, "sparse_prefill_fwd_noalloc");
+  if (st != SPS_OK) return st;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
     return fail(SPS_EINVAL, "sparse_prefill_fwd_noalloc: q/k/v buffers must be 16-byte aligned");
   if (!aligned(partial, 16)) return fail(SPS_EINVAL, "partial must be 16-byte aligned");
   if (split_stride < pl->R * p.head_dim || split_stride % 4)

@@ -18,6 +18,8 @@ enum : int32_t {
   DEV_BAD_PAGE = 2,       // a page-table entry outside [0, num_phys_pages)
   DEV_BAD_INDEX = 3,      // a selected page outside the row's visible range
   DEV_OVERFLOW = 4,       // more work items than the workspace was sized for
+  DEV_NO_PAGES = 5,       // the list of free pages does not hold the pages that a batch needs
+  DEV_BAD_LENGTH = 6,     // a length below zero, or more tokens than the tables have room for
 };
 
 __device__ __forceinline__ void set_status(int32_t* status, int32_t code) {

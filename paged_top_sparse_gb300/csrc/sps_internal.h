@@ -48,6 +48,13 @@ struct FwdTask {
   int32_t bucket, entry_begin, count, pad;
 };
 
+// A page that the append of an E4M3 cache touches: `count` new tokens of request `req` from flat token
+// tok0 on go to its slots slot0 .. ; slot0 > 0: the slots in front hold earlier tokens.
+struct AppUnit {
+  int32_t req, page, tok0, count;  // count 0: unused entry
+  int32_t slot0, pad[3];
+};
+
 // Everything a kernel needs about the plan, passed by value.
 struct AttPiece;
 struct AttHead;
@@ -100,6 +107,9 @@ struct DevPlan {
   const AttMerge* att_merges;
   int32_t att_ctas, att_slot_rows;
   int32_t att_num_merges, att_merge_cap;  // cut tiles of this plan, and of any with its q_lens
+  // the append of an E4M3 cache: as many entries as any plan of these q_lens can have
+  const AppUnit* app_units;
+  int32_t num_app_units;
 };
 
 // Full attention: pages [page0, page1) of query tile `tile` of head block `vg` (KV head
@@ -235,16 +245,34 @@ cudaError_t launch_qk_norm_rope(const DevPlan& p, const DevRope& r, const QkRope
 cudaError_t launch_kv_append_rope(const DevPlan& p, const DevRope& r, const KvRopeArgs& a,
                                   bool interleaved, bool nvfp4, cudaStream_t st);
 
+// The append (with or without norm and rotation) into an E4M3 cache with a scale per page and head.
+cudaError_t launch_kv_append_e4m3(const DevPlan& p, const DevRope& r, const KvRopeArgs& a,
+                                  bool interleaved, cudaStream_t st);
+
 // The full attention's factor on a score: the scales, in base 2.
 inline float attention_factor(float softmax_scale, float q_scale) {
   return softmax_scale * q_scale * 1.4426950408889634f;
 }
 
-// Full attention over the paged cache (BF16 Q and cache, or E4M3 Q and NVFP4 cache).
-cudaError_t launch_attention(const DevPlan& p, bool quant, const void* q, int64_t q_stride,
-                             float q_scale, const void* kc, const void* vc, const void* ks,
-                             const void* vs, const int32_t* page_table, void* out,
+// Full attention over the paged cache (BF16 Q and cache, E4M3 Q and NVFP4 cache, or BF16 or E4M3 Q
+// and E4M3 cache).
+cudaError_t launch_attention(const DevPlan& p, sps_dtype qt, sps_dtype kvt, const void* q,
+                             int64_t q_stride, float q_scale, const void* kc, const void* vc,
+                             const void* ks, const void* vs, const int32_t* page_table, void* out,
                              int64_t out_stride, float* out_lse, void* scratch, cudaStream_t st);
+
+// Page tables and slot maps from request lengths (sps_page_tables).
+constexpr int kMaxTableBatch = 16384;  // two running sums in shared memory
+struct PageTableArgs {
+  const int32_t *q_lens, *ctx_lens, *free_pages;
+  int32_t* free_state;  // pages taken from the list, and a ticket (0 between calls)
+  int32_t* page_table;
+  int64_t* slots;
+  int32_t *positions, *starts, *status;
+  int64_t num_free, max_tokens;
+  int32_t batch, max_pages;
+};
+cudaError_t launch_page_tables(const PageTableArgs& a, cudaStream_t st);
 
 // Copy of n bytes from device-accessible page-locked host memory (src) to device memory (dst),
 // both 16-byte aligned, by a kernel rather than the copy engine.
