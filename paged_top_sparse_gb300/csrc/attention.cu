@@ -84,22 +84,6 @@ struct AttSmem {
   int abort_flag;
 };
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-// Halves of sdesc_sw128: the low word of a shared address (or of an address in 16-byte units added
-// to the one of address 0), and the descriptor of a low word (1024 bytes between 8-row groups).
-__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
-  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
-}
-__device__ __forceinline__ uint64_t sdesc_hi(uint32_t lo) {
-  return (sdesc_sw128(0, 0, 1024) & 0xffffffff00000000ull) | lo;
-}
 // Scratch slot of piece i of a cut tile: a block's first piece goes to slot 2 block when it begins
 // inside its tile, its last piece to slot 2 block + 1 when it begins its tile.
 __device__ __forceinline__ int64_t piece_slot(const AttMerge& mg, int i) {
@@ -1029,6 +1013,10 @@ cudaError_t run_attention(const DevPlan& p, const AttArgs& a, const void* q, con
 std::atomic<uint64_t> g_skip_wait_ns{kWaitLimitNs};
 
 }  // namespace
+
+cudaError_t att::launch_merge(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
+  return p.D == 128 ? run_merge<128>(p, a, st) : run_merge<64>(p, a, st);
+}
 
 // Limit of the waits that follow the block's pieces, for a test of them (0: the library's).
 extern "C" void sps_internal_attention_wait(int64_t limit_ns) {

@@ -72,6 +72,22 @@ __device__ __forceinline__ uint32_t pack_p(float a, float b) {
   return r;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// Halves of sdesc_sw128: the low word of a shared address (or of an address in 16-byte units added
+// to the one of address 0), and the descriptor of a low word (1024 bytes between 8-row groups).
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t sdesc_hi(uint32_t lo) {
+  return (sdesc_sw128(0, 0, 1024) & 0xffffffff00000000ull) | lo;
+}
 struct AttArgs {
   const uint8_t *q, *kc, *vc, *ks, *vs;  // quantised plans (and Q); E4M3: ks, vs are FP32
   int64_t q_stride;
@@ -86,6 +102,9 @@ struct AttArgs {
 
 // Single tokens over an NVFP4 cache (tiles of at most 16 rows): the products' part of launch_attention.
 cudaError_t launch_decode_nvfp4(const DevPlan& p, const AttArgs& a, cudaStream_t st);
+
+// The merge of the tiles that the plan cut over blocks, behind any of the products' kernels.
+cudaError_t launch_merge(const DevPlan& p, const AttArgs& a, cudaStream_t st);
 
 // Full attention over an E4M3 cache with a scale for each page and KV head.
 cudaError_t launch_attention_e4m3(const DevPlan& p, bool q_e4m3, const AttArgs& a, cudaStream_t st);

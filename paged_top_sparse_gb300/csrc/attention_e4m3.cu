@@ -1,116 +1,782 @@
 // attention_e4m3.cu -- full causal attention over a paged cache held in 8 bits (E4M3 codes, one FP32
 // scale for each page and KV head): out_r = sum_j p_j vs_j v_j / sum_j p_j with
-// p_j = 2^(c ks_j q_r . k_j - m), c = scale * q_scale * log2 e, and the log-sum-exp.
+// p_j = 2^(c ks_j q_r . k_j - max), c = scale * q_scale * log2 e, and the log-sum-exp.
 //
-// The plain form: a warp per (token, head) row walks its request's keys four at a time, a lane holding
-// D / 32 dims of q and of the output, with a running maximum and sum in FP32.
+// Mathematics.  As in attention.cu: one pass over a row's pages with a lazily raised reference m, l and O
+// in FP32.  The scale of a page's keys multiplies its scores' factor.  The scale of its values, 2^e, goes
+// into the exponent, p' = 2^(c ks s + e - m), where m follows the largest c ks s + e: so P, rounded to FP16
+// for the second product, is largest where p times the value's size is, and pages whose values are
+// smaller by any factor cost no precision where they matter.  The row's sum takes p' 2^-e.  e is kept
+// within 2^-40 .. 2^40 (sps_kv_append's range), so that FP32 holds the sum whatever the order of the pages.
+//
+// The first product runs on the FP8 tensor core straight from the cache's codes: E4M3 queries as they are;
+// a BF16 query row, scaled by a power of two to at most 448, as the sum of two E4M3 rows (8 significant
+// bits are 4 + 4: exact for elements down to 2^-10 of the row's largest, off by 2^-18 of that below), two
+// products into one accumulator, which cost what one BF16 product does.  So K is copied by TMA into its
+// operand tile and never converted.  V is converted to FP16 (exactly) by four warps, since P needs more
+// than E4M3's four bits.
+//
+// Work, rows and merge are attention.cu's (256-row work tiles, the plan's pieces).
+//
+// One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
+//   warp 0     page-table reads and the copies: K tiles by TMA (128-byte or, D = 64, 64-byte swizzle) into
+//              one ring, V's codes by bulk copies into another;
+//   warp 1     one thread issues every MMA, as in attention.cu: two row tiles' chains alternate, or with one
+//              row tile its even and odd pages;
+//   warps 4-7, 8-11   softmax and epilogue of row tile 0 / 1, a thread per row;
+//   warps 12-15  Q tiles (and the row scales), and V into FP16 operand tiles, a thread per row.
+#include <cstring>
+
 #include "attention.cuh"
+#include "e4m3.cuh"
 
 namespace sps {
 namespace att {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr float kScaleLog2 = 40.f;  // log2 of the range of a V scale, either way
 
-// D / 32 consecutive codes at p as FP32.
-template <int E>
-__device__ __forceinline__ void load_codes(const uint8_t* p, float (&o)[E]) {
-  uint32_t w = E == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = e4m3_to_f32((w >> (8 * e)) & 0xffu);
+// QB: BF16 queries, two E4M3 planes.  SINGLE: every work tile of the batch has one row tile.
+template <int D, bool QB, bool SINGLE>
+struct E4Smem {
+  static constexpr int TK = 128 * D, TV = 128 * D * 2;  // bytes of a K (or raw V) and of an FP16 V tile
+  static constexpr int QT = SINGLE ? 1 : 2;
+  static constexpr int QPLANES = QB ? 2 : 1;
+  // the epilogue stages its rows (32 rows x 128 bytes a warp) in the Q tile
+  static constexpr int TQ = QPLANES * TK > 16384 ? QPLANES * TK : 16384;
+  static constexpr int kBudget = 227 * 1024 - 3072;  // less the barriers and row statistics
+  static constexpr int VS = 2;
+  static constexpr int S0 = (kBudget - QT * TQ - VS * TV) / (2 * TK);
+  static constexpr int S = S0 > 8 ? 8 : S0;  // stages of the K ring and of the raw V ring
+  static_assert(S >= 3, "shared memory");
+  uint8_t q[QT][TQ];
+  uint8_t k[S][TK];
+  uint8_t v[VS][TV];
+  uint8_t raw[S][TK];
+  uint64_t q_full[2], q_empty[2], k_full[S], k_empty[S], raw_full[S], raw_empty[S], v_full[VS], v_empty[VS];
+  uint64_t s_full[2], p_half[2], p_full[2];  // p_half: P of the first 64 keys
+  uint64_t o_done[2];                        // the piece's last P V product into O_t
+  uint64_t o_free[2], q_seen[2], stat_full, done;  // q_seen: the row scales, by warpgroup
+  float2 stat[128];      // (m, l) of the odd pages' rows
+  float q_mul[2][128];   // BF16 queries: the power of two that a row was divided by
+  uint32_t tmem_base;
+  uint32_t progress;  // pieces begun, by the MMA warp
+  int abort_flag;
+};
+
+// Byte of 16-byte chunk c of row r of a tile of D-byte rows, as TMA writes it and the tensor core reads it.
+template <int D>
+__device__ __forceinline__ uint32_t row_offset(uint32_t r, uint32_t c) {
+  return D == 128 ? sw128_offset(r, c) : r * 64u + (((c ^ (r >> 1)) & 3u) << 4);
+}
+// Descriptor of a K-major tile of D-byte rows from its low word.
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t lo) {
+  constexpr uint64_t sw64 = ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+  return D == 128 ? sdesc_hi(lo) : sw64 | lo;
 }
 
-template <int D, bool QE4M3>
-__global__ void __launch_bounds__(kWarps * 32)
-attention_e4m3_kernel(DevPlan p, AttArgs a) {
-  constexpr int E = D / 32;
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= (int64_t)p.T * p.H) return;
-  const int tok = (int)(row / p.H), head = (int)(row % p.H), g = head / p.Hg;
-  const int pos = __ldg(p.tok_pos + tok), req = __ldg(p.tok_req + tok);
-  const float* ks = reinterpret_cast<const float*>(a.ks);
-  const float* vs = reinterpret_cast<const float*>(a.vs);
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-  const int64_t at = tok * a.q_stride + (int64_t)head * D + lane * E;
-  if (QE4M3) {
-    load_codes<E>(a.q + at, q);
+// The power of two 2^k with amax 2^-k in (224, 448] (1 for zero, infinity and NaN).
+__device__ __forceinline__ float row_scale(float amax) {
+  const uint32_t b = __float_as_uint(amax), e = b >> 23;
+  if (e == 0 || e == 255) return 1.f;
+  const int k = (int)e - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float((uint32_t)max(1, k + 127) << 23);
+}
+
+// The log2 of a V scale within its range.
+__device__ __forceinline__ float scale_log2(float s) {
+  float x;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(x) : "f"(s));
+  return fminf(fmaxf(x, -kScaleLog2), kScaleLog2);
+}
+
+template <int D, bool QB, bool SINGLE>
+__global__ void __launch_bounds__(512, 1)
+attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArgs a) {
+  using Smem = E4Smem<D, QB, SINGLE>;
+  constexpr int TK = Smem::TK, TV = Smem::TV, TQ = Smem::TQ, S = Smem::S, VS = Smem::VS;
+  constexpr uint32_t IDESC_QK = idesc_mma(false, false, 128, 128, false, false);
+  constexpr uint32_t IDESC_PV = idesc_mma(false, false, 128, D, false, true);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int32_t* status = p.status;
+  const RowPack rp(p.Hg);
+
+  if (smem_u32(smem_raw) & 1023) {  // the swizzled tiles need it; dynamic shared memory has it
+    if (tid == 0) set_status(status, DEV_OVERFLOW);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_full[i]), 4);
+      mbar_init(smem_u32(&sm.q_empty[i]), 4);  // the epilogue's warps
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_half[i]), 4);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.o_done[i]), 1);
+      mbar_init(smem_u32(&sm.o_free[i]), 4);
+      mbar_init(smem_u32(&sm.q_seen[i]), 1);
+    }
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&sm.k_full[i]), 1);
+      mbar_init(smem_u32(&sm.k_empty[i]), 1);
+      mbar_init(smem_u32(&sm.raw_full[i]), 1);
+      mbar_init(smem_u32(&sm.raw_empty[i]), 4);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(smem_u32(&sm.v_full[i]), 4);
+      mbar_init(smem_u32(&sm.v_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&sm.stat_full), 4);
+    mbar_init(smem_u32(&sm.done), 1);
+    sm.progress = 0;
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();  // from here on: what earlier kernels wrote
+  const uint32_t tmem = sm.tmem_base;  // S0 S1 at columns 0, 128; O0 O1 at 256, 384
+  volatile int* abort_flag = &sm.abort_flag;
+  // The second softmax warpgroup skips pieces of one page and one row tile, so one wait of its may last as
+  // long as a block's other pieces: its deadline follows the pieces.
+  volatile uint32_t* progress = &sm.progress;
+  PieceList work(p);
+  Piece pc;
+
+  // Registers: (64 + 2 * 184 + 80) * 128 = 65536.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+      // ------------------------------------------------ copies
+      uint32_t it = 0;  // tiles copied before this piece
+      bool ok = true;
+      while (ok && work.next(p, rp, pc)) {
+        const int g = pc.vg / rp.blocks;
+        // K runs a page ahead of V: K_0, K_1, V_0, K_2, V_1, ...
+        const int n = pc.page1 - pc.page0;
+        const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
+        auto load_ids = [&](int first) {  // physical tiles of the lanes' pages first + lane
+          int id = 0;
+          if (first + lane < n) {
+            id = __ldg(pages + first + lane);
+            if (id < 0 || id >= p.num_phys) {
+              set_status(status, DEV_BAD_PAGE);
+              id = 0;
+            }
+          }
+          return id * p.Hkv + g;
+        };
+        int ids = load_ids(0), next_ids = 0, k_tile = 0;
+        for (int s = 0; s <= n && ok; ++s) {
+          const int at = s & 31, v_tile = k_tile;
+          if (s > 0 && at == 0) ids = next_ids;
+          if (at == 8) next_ids = load_ids(s - 8 + 32);
+          k_tile = __shfl_sync(0xffffffffu, ids, at);
+          if (lane == 0) {
+            if (s < n) {
+              const uint32_t sg = (it + s) % S, f = smem_u32(&sm.k_full[sg]);
+              ok = mbar_wait(smem_u32(&sm.k_empty[sg]), (((it + s) / S) & 1) ^ 1, abort_flag, status);
+              if (ok) {
+                mbar_expect_tx(f, TK);
+                tma_load_2d(smem_u32(sm.k[sg]), &tmK, 0, k_tile * 128, f);
+              }
+            }
+            if (ok && s > 0) {
+              const uint32_t i = it + s - 1, sg = i % S, f = smem_u32(&sm.raw_full[sg]);
+              ok = mbar_wait(smem_u32(&sm.raw_empty[sg]), ((i / S) & 1) ^ 1, abort_flag, status);
+              if (ok) {
+                mbar_expect_tx(f, TK);
+                bulk_load(smem_u32(sm.raw[sg]), a.vc + (int64_t)v_tile * TK, TK, f);
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        it += n;
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------ MMA issuer
+      // One thread alone runs the loop: descriptors and barrier addresses pass through registers that the
+      // warp's lanes share, so lanes that came apart at a wait must not run beside the one that issues (as
+      // a whole warp with an elected lane, D = 64 read wrong scores and lost arrivals).  Descriptors are
+      // a constant high word and a low word that grows by the operand's offset.
+      if (elect_one()) {
+        const uint32_t q_lo = sdesc_lo(smem_u32(sm.q[0]), 16), k_lo = sdesc_lo(smem_u32(sm.k[0]), 16),
+                       v_lo = sdesc_lo(smem_u32(sm.v[0]), 16384);
+        uint32_t qc0 = 0, qc1 = 0, sc[2] = {0, 0}, oc[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+          if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
+        };
+        struct Ring {
+          uint32_t stage, phase;
+          __device__ __forceinline__ Ring take(uint32_t n) {
+            const Ring x = *this;
+            if (++stage == n) {
+              stage = 0;
+              phase ^= 1;
+            }
+            return x;
+          }
+        };
+        Ring kr{0, 0}, vr{0, 0};
+        auto commit = [&](uint64_t& bar) {
+          mma_commit(smem_u32(&bar));
+        };
+        // S_t = Q_q K^T
+        auto issue_s = [&](int t, int q, const Ring& k) {
+          tc_fence_after();
+          const uint32_t qa = q_lo + q * (TQ >> 4), ka = k_lo + k.stage * (TK >> 4);
+#pragma unroll
+          for (int pl = 0; pl < Smem::QPLANES; ++pl)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_f8_ss(tmem + t * 128, sdesc_rows<D>(qa + ((pl * TK + kk * 32) >> 4)),
+                        sdesc_rows<D>(ka + (kk * 32 >> 4)), IDESC_QK, pl + kk > 0);
+          commit(sm.s_full[t]);
+        };
+        // O_t (+)= P_t V in two halves of 64 keys, the first as soon as its P is there
+        auto issue_pv = [&](int t, const Ring& v, bool first, bool last) {
+          const uint32_t va = v_lo + v.stage * (TV >> 4);
+          auto half = [&](int h) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                         sdesc_hi(va + kk * (2048 >> 4)), IDESC_PV, kk > 0 || !first);
+          };
+          wait(sm.p_half[t], sc[t] & 1);
+          if (first) {
+            wait(sm.o_free[t], (oc[t] & 1) ^ 1);
+            ++oc[t];
+          }
+          if (!ok) return;
+          half(0);
+          wait(sm.p_full[t], sc[t] & 1);
+          ++sc[t];
+          if (!ok) return;
+          half(1);
+          if (last) commit(sm.o_done[t]);
+        };
+        uint32_t begun = 0;
+        while (ok && work.next(p, rp, pc)) {
+          *progress = ++begun;
+          const int n = pc.page1 - pc.page0;
+          {
+            const Ring k = kr.take(S);
+            wait(sm.k_full[k.stage], k.phase);
+            wait(sm.q_full[0], qc0 & 1);
+            ++qc0;
+            if (!ok) break;
+            if (QB) {  // (a warpgroup that skips pieces could not follow q_full's phases)
+              mbar_arrive(smem_u32(&sm.q_seen[0]));
+              if ((SINGLE || pc.nt == 1) && n > 1) mbar_arrive(smem_u32(&sm.q_seen[1]));
+            }
+            issue_s(0, 0, k);
+            if (!SINGLE && pc.nt == 2) {
+              wait(sm.q_full[1], qc1 & 1);
+              ++qc1;
+              if (!ok) break;
+              if (QB) mbar_arrive(smem_u32(&sm.q_seen[1]));
+              issue_s(1, 1, k);
+            }
+            commit(sm.k_empty[k.stage]);
+          }
+          if (!SINGLE && pc.nt == 2) {
+            for (int j = 0; j < n; ++j) {
+              const bool more = j + 1 < n;
+              Ring k{};
+              if (more) k = kr.take(S);
+              const Ring v = vr.take(VS);
+              wait(sm.v_full[v.stage], v.phase);
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                if (ok) issue_pv(t, v, j == 0, !more);
+                if (ok && more) {
+                  if (t == 0) wait(sm.k_full[k.stage], k.phase);
+                  if (ok) issue_s(t, t, k);
+                }
+              }
+              if (!ok) break;
+              commit(sm.v_empty[v.stage]);
+              if (more) commit(sm.k_empty[k.stage]);
+            }
+          } else {
+            auto next_s = [&](int t) {  // S of the next page
+              const Ring k = kr.take(S);
+              wait(sm.k_full[k.stage], k.phase);
+              if (!ok) return;
+              issue_s(t, 0, k);
+              commit(sm.k_empty[k.stage]);
+            };
+            auto page = [&](int j, int t) {
+              const Ring v = vr.take(VS);
+              wait(sm.v_full[v.stage], v.phase);
+              if (ok) issue_pv(t, v, j < 2, j + 2 >= n);
+              if (!ok) return;
+              commit(sm.v_empty[v.stage]);
+              if (j + 2 < n) next_s(t);
+            };
+            if (n > 1) next_s(1);
+            for (int j = 0; j < n && ok; j += 2) {
+              page(j, 0);
+              if (j + 1 < n && ok) page(j + 1, 1);
+            }
+          }
+        }
+        commit(sm.done);
+        mbar_wait(smem_u32(&sm.done), 0, nullptr, status);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // ------------------------------------------------ softmax and epilogue of row tile w
+    const int w = warp >= 8, quarter = warp % 4, row = quarter * 32 + lane;
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t obase = tmem + lane_addr + 256 + w * 128;
+    const float* kscale = reinterpret_cast<const float*>(a.ks);
+    const float* vscale = reinterpret_cast<const float*>(a.vs);
+    const int ti = row / rp.HB, hh = row % rp.HB;
+    uint32_t su = 0, od = 0, sx = 0;  // uses of S_w, pieces in O_w, statistics received
+    bool ok = true;
+    while (ok && work.next(p, rp, pc)) {
+      // with one row tile, this warpgroup takes the pages of its parity
+      const bool split = SINGLE || pc.nt == 1;
+      const int np = pc.page1 - pc.page0, n = split ? (np + 1 - w) / 2 : np;
+      if (n == 0) continue;
+      const int step = split ? 2 : 1, page_a = pc.page0 + (split ? w : 0), g = pc.vg / rp.blocks;
+      const int tok = pc.tok0 + (split ? 0 : w * rp.TB) + ti;
+      const int hg = (pc.vg % rp.blocks) * 128 + hh;  // head within the KV head's group
+      const bool valid = ti < rp.TB && tok < pc.q_len && hg < p.Hg;
+      const int pos = pc.ctx + tok;
+      const bool active = __any_sync(0xffffffffu, valid);
+      // the scales of this warpgroup's pages, one page ahead (their place, two)
+      const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + page_a;
+      auto tile_of = [&](int j) {
+        const int id = j < n ? __ldg(pages + j * step) : 0;
+        return (int64_t)(id < 0 || id >= p.num_phys ? 0 : id) * p.Hkv + g;
+      };
+      int64_t tile1 = tile_of(0);
+      float ks1 = __ldg(kscale + tile1), vs1 = __ldg(vscale + tile1);
+      tile1 = tile_of(1);
+      float c = a.c;
+      if (QB) {
+        if (!mbar_wait_beside(smem_u32(&sm.q_seen[w]), od & 1, abort_flag, status, progress,
+                              a.skip_wait_ns))
+          break;
+        c = valid ? c * sm.q_mul[split ? 0 : w][row] : 0.f;
+      }
+      float m = 0.f, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        const int page = page_a + j * step;
+        const int nvis = valid ? pos - page * 128 + 1 : 128;
+        const bool masked = __any_sync(0xffffffffu, nvis < 128);
+        // (a factor of zero would make NaN of a masked score's infinity)
+        const float ck = fmaxf(c * ks1, 1.18e-38f), e = scale_log2(vs1);
+        ks1 = __ldg(kscale + tile1);
+        vs1 = __ldg(vscale + tile1);
+        tile1 = tile_of(j + 2);
+        if (!mbar_wait_beside(smem_u32(&sm.s_full[w]), su & 1, abort_flag, status, progress,
+                              a.skip_wait_ns)) {
+          ok = false;
+          break;
+        }
+        ++su;  // (a commit covers what its thread issued before: the last product into O_w too)
+        const uint32_t bar_half = smem_u32(&sm.p_half[w]), bar_full = smem_u32(&sm.p_full[w]);
+        bool half_sent = false;
+        if (active) {
+          tc_fence_after();
+          const uint32_t sbase = tmem + lane_addr + w * 128;
+          uint32_t v[4][32];
+          float red[4];
+          uint64_t lsum[2] = {0, 0};
+          const uint64_t c2 = pack_f32x2(ck, ck);
+          auto exps = [&](int cc, uint32_t* pk) {  // P of the keys 32 cc .. 32 cc + 31
+            const float off = e + kF16Bias - m;
+            const uint64_t off2 = pack_f32x2(off, off);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float x, y;
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[cc][i]), __uint_as_float(v[cc][i + 1])),
+                                     c2, off2), x, y);
+              x = fast_exp2(x);
+              y = fast_exp2(y);
+              lsum[(i >> 1) & 1] = add_f32x2(lsum[(i >> 1) & 1], pack_f32x2(x, y));
+              pk[i / 2] = pack_p<true>(x, y);
+            }
+          };
+          // The usual page (`fast`): the reference holds, so the first half's exponentials run under the
+          // second half's load.  The first page, a masked one, or one whose maximum asks for a rescale
+          // loads the whole row first.
+          bool fast = j > 0 && !masked;
+          uint32_t pk[32];
+          for (;;) {
+            if (fast) {
+#pragma unroll
+              for (int cc = 0; cc < 2; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int cc = 0; cc < 2; ++cc) {
+                reg_fence(v[cc]);
+                reg_fence1(red[cc]);
+              }
+#pragma unroll
+              for (int cc = 2; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+            } else {
+              for (bool again = true; again;) {
+                again = false;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                  reg_fence(v[cc]);
+                  reg_fence1(red[cc]);
+                }
+                float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+                if (masked) {
+                  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                  for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                      if (cc * 32 + i >= nvis) v[cc][i] = 0xff800000u;  // -inf
+                      mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(v[cc][i]));
+                    }
+                  mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                }
+                mb = fmaf(mb, ck, e);
+                const bool need = j > 0 && mb - m > kRescale;
+                if (j == 0) {
+                  m = mb == -INFINITY ? 0.f : mb;  // a row that sees nothing here keeps p = 0
+                } else if (__any_sync(0xffffffffu, need)) {
+                  const float f = need ? fast_exp2(m - mb) : 1.f;
+                  if (need) m = mb;
+                  l *= f;
+#pragma unroll 1
+                  for (int cc = 0; cc < D / 32; ++cc) {
+                    tmem_ld32(obase + cc * 32, v[0]);
+                    tmem_ld_wait();
+                    reg_fence(v[0]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                      v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
+                    tmem_st32(obase + cc * 32, v[0]);
+                  }
+                  tmem_st_wait();
+                  again = true;
+                }
+              }
+            }
+            lsum[0] = lsum[1] = 0;
+            exps(0, pk);
+            exps(1, pk + 16);
+            if (!fast) break;
+            tmem_ld_wait();
+#pragma unroll
+            for (int cc = 2; cc < 4; ++cc) {
+              reg_fence(v[cc]);
+              reg_fence1(red[cc]);
+            }
+            const float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+            if (!__any_sync(0xffffffffu, fmaf(mb, ck, e) - m > kRescale)) break;
+            fast = false;
+          }
+          tmem_st32(sbase, pk);
+          uint32_t pk2[32];
+          exps(2, pk2);  // under the store
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_half);  // the products of the first 64 keys may begin
+          half_sent = true;
+          exps(3, pk2 + 16);
+          tmem_st32(sbase + 32, pk2);
+          float x, y, z, t;
+          unpack_f32x2(lsum[0], x, y);
+          unpack_f32x2(lsum[1], z, t);
+          l = fmaf((x + y) + (z + t), fast_exp2(-e), l);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!half_sent) mbar_arrive(bar_half);
+          mbar_arrive(bar_full);
+        }
+      }
+      if (!ok) break;
+      if (!mbar_wait(smem_u32(&sm.o_done[w]), od & 1, abort_flag, status)) break;
+      ++od;
+      if (split && w == 1) {  // the odd pages' statistics; warpgroup 0 reads O_1 itself
+        sm.stat[row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.stat_full));
+        continue;
+      }
+      const bool two = split && np > 1;
+      float f0 = 1.f, f1 = 0.f;
+      if (two) {
+        if (!mbar_wait(smem_u32(&sm.stat_full), sx & 1, abort_flag, status)) break;
+        ++sx;
+        const float2 o = sm.stat[row];
+        if (o.y > 0.f) {  // (0: the row sees nothing in the odd pages)
+          const float mm = l > 0.f ? fmaxf(m, o.x) : o.x;
+          f0 = l > 0.f ? fast_exp2(m - mm) : 0.f;
+          f1 = fast_exp2(o.x - mm);
+          l = l * f0 + o.y * f1;
+          m = mm;
+        }
+      }
+      if (active) {
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float lse = l > 0.f ? (m - kF16Bias + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        f0 *= inv;
+        f1 *= inv;
+        const bool whole = pc.page0 == 0 && pc.page1 == pc.pages;
+        const int64_t slot = 2 * blockIdx.x + (pc.page0 > 0 ? 0 : 1);
+        const int64_t srow = slot * p.att_slot_rows + w * 128 + row;  // (split: w = 0)
+        const int64_t flat = pc.flat0 + tok;
+        const int head = (pc.vg / rp.blocks) * p.Hg + hg;
+        if (valid) {
+          if (!whole) a.part_lse[srow] = lse;
+          else if (a.out_lse) a.out_lse[flat * p.H + head] = lse;
+        }
+        // a thread holds a row; the warp turns 128 bytes of each of its 32 rows at a time in its
+        // staging area, so that eight lanes write 128 contiguous bytes of a row
+        uint8_t* stg = sm.q[SINGLE ? 0 : w] + quarter * 4096;
+        const uint32_t vrows = __ballot_sync(0xffffffffu, valid);
+        const int64_t obyte = whole ? (flat * a.out_stride + (int64_t)head * D) * 2 : srow * D * 4;
+        uint8_t* const base = whole ? reinterpret_cast<uint8_t*>(a.out)
+                                    : reinterpret_cast<uint8_t*>(a.part);
+        auto flush = [&](int piece) {  // 128-byte piece `piece` of every row
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + lane / 8;
+            const uint4 x = *reinterpret_cast<const uint4*>(stg + sw128_offset(r, lane % 8));
+            const int64_t at = __shfl_sync(0xffffffffu, obyte, r);
+            if (vrows >> r & 1)
+              *reinterpret_cast<uint4*>(base + at + piece * 128 + (lane % 8) * 16) = x;
+          }
+          __syncwarp();
+        };
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t v[32];
+          tmem_ld32(obase + cc * 32, v);
+          if (two) {
+            uint32_t x[32];
+            tmem_ld32(obase + 128 + cc * 32, x);
+            tmem_ld_wait();
+            reg_fence(v);
+            reg_fence(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = __float_as_uint(__uint_as_float(v[i]) * f0 + __uint_as_float(x[i]) * f1);
+          } else {
+            tmem_ld_wait();
+            reg_fence(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f0);
+          }
+          if (cc == D / 32 - 1) {  // O is read: the next work tile's products may begin
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&sm.o_free[w]));
+              if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
+            }
+          }
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                o[k] = pack_p<false>(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, (cc & 1) * 4 + i / 8)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if (cc & 1) flush(cc / 2);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, i / 4)) =
+                  make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            flush(cc);
+          }
+        }
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.o_free[w]));
+          if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
+        }
+      }
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[w]));  // staging and Q tile are free
+    }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ------------------------------------------------ Q tiles, and V into FP16 operand tiles
+    const int ct = tid - 384;
+    uint32_t it = 0, qc0 = 0, qc1 = 0;
+    bool ok = true;
+    while (ok && work.next(p, rp, pc)) {
+      const int h0 = (pc.vg % rp.blocks) * 128, g = pc.vg / rp.blocks;
+      const int n = pc.page1 - pc.page0;
+      for (int t = 0; t < (SINGLE ? 1 : pc.nt) && ok; ++t) {
+        uint32_t& qc = t ? qc1 : qc0;
+        const int tok_a = pc.tok0 + t * rp.TB;
+        const int rows = min(rp.TB, pc.q_len - tok_a) * rp.HB;  // (rows behind them may hold anything)
+        const uint8_t* src = a.q + ((pc.flat0 + tok_a) * a.q_stride + (int64_t)(g * p.Hg + h0) * D) * (QB ? 2 : 1);
+        // row r of the tile: head r % HB of token r / HB; false behind the group's last head
+        auto row_at = [&](int r, const uint8_t*& at) {
+          at = src + (r / rp.HB * a.q_stride + (int64_t)(r % rp.HB) * D) * (QB ? 2 : 1);
+          return r < rows && h0 + r % rp.HB < p.Hg;
+        };
+        constexpr int LPR = QB ? D / 8 : D / 16;  // lanes of a row, 16 bytes each
+        constexpr int RPP = 128 / LPR;            // rows of a pass
+        constexpr int GROUP = 8;                  // passes on the way together
+        const int r0 = ct / LPR, ch = ct % LPR;
+        bool waited = false;
+#pragma unroll 1
+        for (int b = 0; b < 128 && b < rows && ok; b += RPP * GROUP) {
+          uint4 x[GROUP];
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(a.q)[at + e]);
-  }
+          for (int i = 0; i < GROUP; ++i) {
+            const uint8_t* at;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (b + i * RPP < 128 && row_at(b + i * RPP + r0, at))
+              x[i] = __ldg(reinterpret_cast<const uint4*>(at) + ch);
+          }
+          if (!waited) ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
+          waited = true;
+          if (!ok) break;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int page = 0; page <= pos >> 7; ++page) {
-    const int phys = __ldg(a.page_table + (int64_t)req * p.max_pages + page);
-    if (phys < 0 || phys >= p.num_phys) {
-      if (lane == 0) set_status(p.status, DEV_BAD_PAGE);
-      return;
-    }
-    const int64_t tile = (int64_t)phys * p.Hkv + g;
-    const float ck = a.c * ks[tile], vscale = vs[tile];
-    const int n = min(128, pos - page * 128 + 1);
-    for (int j0 = 0; j0 < n; j0 += 4) {
-      float s[4], v[4][E];
+          for (int i = 0; i < GROUP; ++i) {
+            const int r = b + i * RPP + r0;
+            if (b + i * RPP >= 128) break;
+            if (!QB) {
+              *reinterpret_cast<uint4*>(sm.q[t] + row_offset<D>(r, ch)) = x[i];
+              continue;
+            }
+            const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float f[8], amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j] = 0.f;
-        if (j0 + j < n) {
-          float k[E];
-          load_codes<E>(a.kc + (tile * 128 + j0 + j) * D + lane * E, k);
-          load_codes<E>(a.vc + (tile * 128 + j0 + j) * D + lane * E, v[j]);
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = __uint_as_float(wd[k] << 16);
+              f[2 * k + 1] = __uint_as_float(wd[k] & 0xffff0000u);
+              amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+            }
 #pragma unroll
-          for (int e = 0; e < E; ++e) s[j] += q[e] * k[e];
+            for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float s = row_scale(amax), inv = 1.f / s;
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float u = f[2 * k] * inv, v = f[2 * k + 1] * inv;
+              const uint32_t h = f32x2_to_e4m3x2(pack_f32x2(u, v));
+              const uint32_t h2 = cvt_e4m3x2((uint16_t)h);
+              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+              const uint32_t d = f32x2_to_e4m3x2(pack_f32x2(u - back.x, v - back.y));
+              hi[k / 2] |= h << (16 * (k & 1));
+              lo[k / 2] |= d << (16 * (k & 1));
+            }
+            uint8_t* dst = sm.q[t] + row_offset<D>(r, ch / 2) + (ch & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + TK) = make_uint2(lo[0], lo[1]);
+            if (ch == 0) sm.q_mul[t][r] = s;
+          }
+        }
+        if (!ok) break;
+        ++qc;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[t]));
+      }
+      for (int j = 0; j < n && ok; ++j, ++it) {
+        const uint32_t r = it % S, sg = it % VS;
+        constexpr int CPR = D / 16;
+        if (!mbar_wait(smem_u32(&sm.raw_full[r]), (it / S) & 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        uint4 x[CPR];
+        const uint4* codes = reinterpret_cast<const uint4*>(sm.raw[r]) + ct * CPR;
+        const int turn = CPR == 8 ? ct : ct >> 1;  // (a column of its own: distinct banks)
+#pragma unroll
+        for (int k = 0; k < CPR; ++k) x[k] = codes[(k + turn) % CPR];
+        // rows behind the request's last token become zero, whatever the slots hold
+        if (pc.ctx + pc.q_len <= (pc.page0 + j) * 128 + ct) {
+#pragma unroll
+          for (int k = 0; k < CPR; ++k) x[k] = make_uint4(0, 0, 0, 0);
+        }
+        if (!mbar_wait(smem_u32(&sm.v_empty[sg]), ((it / VS) & 1) ^ 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int k = 0; k < CPR; ++k) e4m3_store16<false>(x[k], sm.v[sg], ct, (k + turn) % CPR);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.v_full[sg]));
+          mbar_arrive(smem_u32(&sm.raw_empty[r]));
         }
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
-      float mx = m;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j] = j0 + j < n ? s[j] * ck : -INFINITY;
-        mx = fmaxf(mx, s[j]);
-      }
-      const float f = exp2f(m - mx);
-      m = mx;
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j0 + j < n) {
-          const float x = exp2f(s[j] - m);
-          l += x;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += x * vscale * v[j][e];
-        }
     }
   }
-  uint16_t* out = a.out + tok * a.out_stride + (int64_t)head * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(out + e) = pack_p<false>(acc[e] / l, acc[e + 1] / l);
-  if (lane == 0 && a.out_lse) a.out_lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+  settle_after_abort(abort_flag);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-template <int D, bool QE4M3>
+template <int D, bool QB, bool SINGLE>
 cudaError_t run(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
-  const int64_t blocks = ((int64_t)p.T * p.H + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cudaError_t e = launch_pdl(attention_e4m3_kernel<D, QE4M3>, dim3((unsigned)blocks),
-                             dim3(kWarps * 32), 0, st, p, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  alignas(64) CUtensorMap tmK;
+  memset(&tmK, 0, sizeof tmK);
+  const uint64_t rows = (uint64_t)p.num_phys * p.Hkv * 128;
+  if (!encode_tmap_2d_bytes(&tmK, a.kc, D, rows, D, D, 128)) return cudaErrorInvalidValue;
+  const int smem = (int)sizeof(E4Smem<D, QB, SINGLE>);
+  static_assert(sizeof(E4Smem<D, QB, SINGLE>) <= 227 * 1024, "shared memory");
+  auto kern = attention_e4m3_kernel<D, QB, SINGLE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(p.att_ctas), dim3(512), smem, st, tmK, p, a);
+  if (e != cudaSuccess) return e;
+  return launch_merge(p, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_e4m3(const DevPlan& p, bool q_e4m3, const AttArgs& a, cudaStream_t st) {
-  if (p.D == 128) return q_e4m3 ? run<128, true>(p, a, st) : run<128, false>(p, a, st);
-  return q_e4m3 ? run<64, true>(p, a, st) : run<64, false>(p, a, st);
+  const RowPack rp(p.Hg);
+  const bool single = p.att_slot_rows <= rp.TB * rp.HB;
+#define SPS_E4(DD, QQ) return single ? run<DD, QQ, true>(p, a, st) : run<DD, QQ, false>(p, a, st)
+  if (p.D == 128) {
+    if (q_e4m3) SPS_E4(128, false);
+    SPS_E4(128, true);
+  }
+  if (q_e4m3) SPS_E4(64, false);
+  SPS_E4(64, true);
+#undef SPS_E4
 }
 
 }  // namespace att

@@ -306,6 +306,9 @@ bool encode_tmap_3d(void* map, int dtype_code, void* base, uint64_t d0, uint64_t
 bool encode_tmap_2d_f32_sw64(void* map, const void* base, uint64_t inner, uint64_t outer,
                              uint64_t outer_stride_bytes, uint32_t box_inner,
                              uint32_t box_outer);
+// Bytes, swizzled by the box's row: box_inner 128 or 64.
+bool encode_tmap_2d_bytes(void* map, const void* base, uint64_t inner, uint64_t outer,
+                          uint64_t outer_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 int num_sms();
 
 }  // namespace sps
