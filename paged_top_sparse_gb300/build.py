@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libsps.so")
 SOURCES = ["host.cpp", "combine.cu", "topk.cu", "inversion.cu", "indexer.cu", "forward.cu",
            "forward_p16.cu", "noalloc.cu", "dequant.cu", "selftest.cu", "kvappend.cu", "rope.cu",
-           "attention.cu", "attention_decode.cu", "attention_e4m3.cu", "kvappend_e4m3.cu",
+           "attention.cu", "attention_decode.cu", "attention_e4m3.cu",
+           "attention_decode_e4m3.cu", "kvappend_e4m3.cu",
            "pagetable.cu", "upload.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")

@@ -88,6 +88,49 @@ __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
 __device__ __forceinline__ uint64_t sdesc_hi(uint32_t lo) {
   return (sdesc_sw128(0, 0, 1024) & 0xffffffff00000000ull) | lo;
 }
+// Warp-level products and exchanges of the single-token kernels.
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values, transposed over the warp.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The largest, or the sum, of a row's values over the lanes that share the row.
+template <int ROWS, typename Op>
+__device__ __forceinline__ float row_reduce(float x, Op op) {
+#pragma unroll
+  for (int o = ROWS == 16 ? 1 : 4; o < (ROWS == 16 ? 4 : 32); o <<= 1)
+    x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+constexpr float kScaleLog2 = 40.f;  // log2 of the range of a V scale, either way
+
+// The power of two 2^k with amax 2^-k in (224, 448] (1 for zero, infinity and NaN).
+__device__ __forceinline__ float row_scale(float amax) {
+  const uint32_t b = __float_as_uint(amax), e = b >> 23;
+  if (e == 0 || e == 255) return 1.f;
+  const int k = (int)e - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float((uint32_t)max(1, k + 127) << 23);
+}
+
+// The log2 of a V scale within its range.
+__device__ __forceinline__ float scale_log2(float s) {
+  float x;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(x) : "f"(s));
+  return fminf(fmaxf(x, -kScaleLog2), kScaleLog2);
+}
+
 struct AttArgs {
   const uint8_t *q, *kc, *vc, *ks, *vs;  // quantised plans (and Q); E4M3: ks, vs are FP32
   int64_t q_stride;
@@ -105,6 +148,9 @@ cudaError_t launch_decode_nvfp4(const DevPlan& p, const AttArgs& a, cudaStream_t
 
 // The merge of the tiles that the plan cut over blocks, behind any of the products' kernels.
 cudaError_t launch_merge(const DevPlan& p, const AttArgs& a, cudaStream_t st);
+
+// The products over an E4M3 cache for tiles of at most 16 rows (single tokens).
+cudaError_t launch_decode_e4m3(const DevPlan& p, bool q_e4m3, const AttArgs& a, cudaStream_t st);
 
 // Full attention over an E4M3 cache with a scale for each page and KV head.
 cudaError_t launch_attention_e4m3(const DevPlan& p, bool q_e4m3, const AttArgs& a, cudaStream_t st);

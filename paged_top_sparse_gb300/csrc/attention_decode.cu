@@ -70,31 +70,6 @@ struct DecSmem {
   int abort_flag;
 };
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// An 8 x 8 matrix of 16-bit values, transposed over the warp.
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-// The largest, or the sum, of a row's values over the lanes that share the row.
-template <int ROWS, typename Op>
-__device__ __forceinline__ float row_reduce(float x, Op op) {
-#pragma unroll
-  for (int o = ROWS == 16 ? 1 : 4; o < (ROWS == 16 ? 4 : 32); o <<= 1)
-    x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-
 template <int D, int ROWS>
 __global__ void __launch_bounds__(32 * (kWarps<D, ROWS> + kCopyWarps), 1)
 decode_nvfp4_kernel(DevPlan p, AttArgs a) {

@@ -34,8 +34,6 @@ namespace sps {
 namespace att {
 namespace {
 
-constexpr float kScaleLog2 = 40.f;  // log2 of the range of a V scale, either way
-
 // QB: BF16 queries, two E4M3 planes.  SINGLE: every work tile of the batch has one row tile.
 template <int D, bool QB, bool SINGLE>
 struct E4Smem {
@@ -74,21 +72,6 @@ template <int D>
 __device__ __forceinline__ uint64_t sdesc_rows(uint32_t lo) {
   constexpr uint64_t sw64 = ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
   return D == 128 ? sdesc_hi(lo) : sw64 | lo;
-}
-
-// The power of two 2^k with amax 2^-k in (224, 448] (1 for zero, infinity and NaN).
-__device__ __forceinline__ float row_scale(float amax) {
-  const uint32_t b = __float_as_uint(amax), e = b >> 23;
-  if (e == 0 || e == 255) return 1.f;
-  const int k = (int)e - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return __uint_as_float((uint32_t)max(1, k + 127) << 23);
-}
-
-// The log2 of a V scale within its range.
-__device__ __forceinline__ float scale_log2(float s) {
-  float x;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(x) : "f"(s));
-  return fminf(fmaxf(x, -kScaleLog2), kScaleLog2);
 }
 
 template <int D, bool QB, bool SINGLE>
@@ -767,6 +750,10 @@ cudaError_t run(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attention_e4m3(const DevPlan& p, bool q_e4m3, const AttArgs& a, cudaStream_t st) {
+  if (p.att_slot_rows <= 16) {
+    cudaError_t e = launch_decode_e4m3(p, q_e4m3, a, st);
+    return e != cudaSuccess ? e : launch_merge(p, a, st);
+  }
   const RowPack rp(p.Hg);
   const bool single = p.att_slot_rows <= rp.TB * rp.HB;
 #define SPS_E4(DD, QQ) return single ? run<DD, QQ, true>(p, a, st) : run<DD, QQ, false>(p, a, st)
