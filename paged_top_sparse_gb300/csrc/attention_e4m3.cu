@@ -40,8 +40,7 @@ struct E4Smem {
   static constexpr int TK = 128 * D, TV = 128 * D * 2;  // bytes of a K (or raw V) and of an FP16 V tile
   static constexpr int QT = SINGLE ? 1 : 2;
   static constexpr int QPLANES = QB ? 2 : 1;
-  // the epilogue stages its rows (32 rows x 128 bytes a warp) in the Q tile
-  static constexpr int TQ = QPLANES * TK > 16384 ? QPLANES * TK : 16384;
+  static constexpr int TQ = QPLANES * TK;
   static constexpr int kBudget = 227 * 1024 - 3072;  // less the barriers and row statistics
   static constexpr int VS = 2;
   static constexpr int S0 = (kBudget - QT * TQ - VS * TV) / (2 * TK);
@@ -56,7 +55,8 @@ struct E4Smem {
   uint64_t o_done[2];                        // the piece's last P V product into O_t
   uint64_t o_free[2], q_seen[2], stat_full, done;  // q_seen: the row scales, by warpgroup
   float2 stat[128];      // (m, l) of the odd pages' rows
-  float q_mul[2][128];   // BF16 queries: the power of two that a row was divided by
+  // BF16 queries: the power of two that a row was divided by (its exponent field), by piece parity
+  uint8_t q_exp[2][2][128];
   uint32_t tmem_base;
   uint32_t progress;  // pieces begun, by the MMA warp
   int abort_flag;
@@ -72,6 +72,25 @@ template <int D>
 __device__ __forceinline__ uint64_t sdesc_rows(uint32_t lo) {
   constexpr uint64_t sw64 = ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
   return D == 128 ? sdesc_hi(lo) : sw64 | lo;
+}
+
+// Eight lanes' rows of eight 16-byte chunks each, transposed: lane l gets chunk l of the eight rows.
+__device__ __forceinline__ void transpose_chunks(uint32_t (&x)[32], int lane) {
+#pragma unroll
+  for (int m = 4; m; m >>= 1) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i & m) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &lo = x[4 * i + e], &hi = x[4 * (i | m) + e];
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo : hi, m);
+        if (up) lo = y;
+        else hi = y;
+      }
+    }
+  }
 }
 
 template <int D, bool QB, bool SINGLE>
@@ -94,7 +113,7 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.q_full[i]), 4);
-      mbar_init(smem_u32(&sm.q_empty[i]), 4);  // the epilogue's warps
+      mbar_init(smem_u32(&sm.q_empty[i]), 1);
       mbar_init(smem_u32(&sm.s_full[i]), 1);
       mbar_init(smem_u32(&sm.p_half[i]), 4);
       mbar_init(smem_u32(&sm.p_full[i]), 4);
@@ -134,9 +153,9 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
   PieceList work(p);
   Piece pc;
 
-  // Registers: (64 + 2 * 184 + 80) * 128 = 65536.
+  // Registers: (80 + 2 * 176 + 80) * 128 = 65536.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 0) {
       // ------------------------------------------------ copies
       uint32_t it = 0;  // tiles copied before this piece
@@ -194,7 +213,7 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
       if (elect_one()) {
         const uint32_t q_lo = sdesc_lo(smem_u32(sm.q[0]), 16), k_lo = sdesc_lo(smem_u32(sm.k[0]), 16),
                        v_lo = sdesc_lo(smem_u32(sm.v[0]), 16384);
-        uint32_t qc0 = 0, qc1 = 0, sc[2] = {0, 0}, oc[2] = {0, 0};
+        uint32_t qc = 0, sc = 0, oc = 0;  // a phase bit for each tile
         bool ok = true;
         auto wait = [&](uint64_t& bar, uint32_t parity) {
           if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
@@ -217,7 +236,8 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
         // S_t = Q_q K^T
         auto issue_s = [&](int t, int q, const Ring& k) {
           tc_fence_after();
-          const uint32_t qa = q_lo + q * (TQ >> 4), ka = k_lo + k.stage * (TK >> 4);
+          uint32_t qa = q_lo + q * (TQ >> 4), ka = k_lo + k.stage * (TK >> 4);
+          asm volatile("" : "+r"(qa), "+r"(ka));  // (sums made here, not kept from outside the loops)
 #pragma unroll
           for (int pl = 0; pl < Smem::QPLANES; ++pl)
 #pragma unroll
@@ -228,7 +248,8 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
         };
         // O_t (+)= P_t V in two halves of 64 keys, the first as soon as its P is there
         auto issue_pv = [&](int t, const Ring& v, bool first, bool last) {
-          const uint32_t va = v_lo + v.stage * (TV >> 4);
+          uint32_t va = v_lo + v.stage * (TV >> 4);
+          asm volatile("" : "+r"(va));
           auto half = [&](int h) {
             tc_fence_after();
 #pragma unroll
@@ -236,15 +257,15 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
               mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
                          sdesc_hi(va + kk * (2048 >> 4)), IDESC_PV, kk > 0 || !first);
           };
-          wait(sm.p_half[t], sc[t] & 1);
+          wait(sm.p_half[t], sc >> t & 1);
           if (first) {
-            wait(sm.o_free[t], (oc[t] & 1) ^ 1);
-            ++oc[t];
+            wait(sm.o_free[t], (oc >> t & 1) ^ 1);
+            oc ^= 1u << t;
           }
           if (!ok) return;
           half(0);
-          wait(sm.p_full[t], sc[t] & 1);
-          ++sc[t];
+          wait(sm.p_full[t], sc >> t & 1);
+          sc ^= 1u << t;
           if (!ok) return;
           half(1);
           if (last) commit(sm.o_done[t]);
@@ -253,65 +274,44 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
         while (ok && work.next(p, rp, pc)) {
           *progress = ++begun;
           const int n = pc.page1 - pc.page0;
-          {
-            const Ring k = kr.take(S);
-            wait(sm.k_full[k.stage], k.phase);
-            wait(sm.q_full[0], qc0 & 1);
-            ++qc0;
-            if (!ok) break;
-            if (QB) {  // (a warpgroup that skips pieces could not follow q_full's phases)
-              mbar_arrive(smem_u32(&sm.q_seen[0]));
-              if ((SINGLE || pc.nt == 1) && n > 1) mbar_arrive(smem_u32(&sm.q_seen[1]));
-            }
-            issue_s(0, 0, k);
-            if (!SINGLE && pc.nt == 2) {
-              wait(sm.q_full[1], qc1 & 1);
-              ++qc1;
+          // Steps: P V of a page and row tile (or chain), then S of the page that follows it there; two
+          // steps of S alone in front.  (One copy of each part: a block that walks through long code
+          // waits for its instructions.)
+          const bool split = SINGLE || pc.nt == 1;
+          const int steps = split ? n : 2 * n;
+          Ring k{0, 0}, v{0, 0};
+#pragma unroll 1
+          for (int i = -2; i < steps && ok; ++i) {
+            const int t = i & 1, pv = split ? i : i >> 1, sn = split ? i + 2 : pv + 1;
+            const bool one = split || t == 0, both = split || t == 1;  // begins, ends with a K or V tile
+            if (i >= 0) {
+              if (one) {
+                v = vr.take(VS);
+                wait(sm.v_full[v.stage], v.phase);
+              }
+              if (ok) issue_pv(t, v, split ? pv < 2 : pv == 0, split ? pv + 2 >= n : pv + 1 == n);
               if (!ok) break;
-              if (QB) mbar_arrive(smem_u32(&sm.q_seen[1]));
-              issue_s(1, 1, k);
+              if (both) commit(sm.v_empty[v.stage]);
             }
-            commit(sm.k_empty[k.stage]);
-          }
-          if (!SINGLE && pc.nt == 2) {
-            for (int j = 0; j < n; ++j) {
-              const bool more = j + 1 < n;
-              Ring k{};
-              if (more) k = kr.take(S);
-              const Ring v = vr.take(VS);
-              wait(sm.v_full[v.stage], v.phase);
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                if (ok) issue_pv(t, v, j == 0, !more);
-                if (ok && more) {
-                  if (t == 0) wait(sm.k_full[k.stage], k.phase);
-                  if (ok) issue_s(t, t, k);
+            if (sn < n) {
+              const int q = split ? 0 : t;
+              if (one) {
+                k = kr.take(S);
+                wait(sm.k_full[k.stage], k.phase);
+              }
+              if (i < 0 && (i == -2 || !split)) {
+                wait(sm.q_full[q], qc >> q & 1);
+                qc ^= 1u << q;
+                // (a warpgroup that skips pieces could not follow q_full's phases)
+                if (QB && ok) {
+                  mbar_arrive(smem_u32(&sm.q_seen[q]));
+                  if (split && n > 1) mbar_arrive(smem_u32(&sm.q_seen[1]));
                 }
               }
               if (!ok) break;
-              commit(sm.v_empty[v.stage]);
-              if (more) commit(sm.k_empty[k.stage]);
-            }
-          } else {
-            auto next_s = [&](int t) {  // S of the next page
-              const Ring k = kr.take(S);
-              wait(sm.k_full[k.stage], k.phase);
-              if (!ok) return;
-              issue_s(t, 0, k);
-              commit(sm.k_empty[k.stage]);
-            };
-            auto page = [&](int j, int t) {
-              const Ring v = vr.take(VS);
-              wait(sm.v_full[v.stage], v.phase);
-              if (ok) issue_pv(t, v, j < 2, j + 2 >= n);
-              if (!ok) return;
-              commit(sm.v_empty[v.stage]);
-              if (j + 2 < n) next_s(t);
-            };
-            if (n > 1) next_s(1);
-            for (int j = 0; j < n && ok; j += 2) {
-              page(j, 0);
-              if (j + 1 < n && ok) page(j + 1, 1);
+              issue_s(t, q, k);
+              if (both) commit(sm.k_empty[k.stage]);
+              if (sn + 1 == n) commit(sm.q_empty[q]);
             }
           }
         }
@@ -321,7 +321,7 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
       __syncwarp();
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ------------------------------------------------ softmax and epilogue of row tile w
     const int w = warp >= 8, quarter = warp % 4, row = quarter * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
@@ -331,7 +331,9 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
     const int ti = row / rp.HB, hh = row % rp.HB;
     uint32_t su = 0, od = 0, sx = 0;  // uses of S_w, pieces in O_w, statistics received
     bool ok = true;
+    uint32_t parity = 1;  // of the piece
     while (ok && work.next(p, rp, pc)) {
+      parity ^= 1;
       // with one row tile, this warpgroup takes the pages of its parity
       const bool split = SINGLE || pc.nt == 1;
       const int np = pc.page1 - pc.page0, n = split ? (np + 1 - w) / 2 : np;
@@ -344,30 +346,30 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
       const bool active = __any_sync(0xffffffffu, valid);
       // the scales of this warpgroup's pages, one page ahead (their place, two)
       const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + page_a;
-      auto tile_of = [&](int j) {
-        const int id = j < n ? __ldg(pages + j * step) : 0;
-        return (int64_t)(id < 0 || id >= p.num_phys ? 0 : id) * p.Hkv + g;
-      };
-      int64_t tile1 = tile_of(0);
+      auto id_of = [&](int j) { return j < n ? __ldg(pages + j * step) : 0; };
+      auto tile_of = [&](int id) { return ((uint32_t)id < (uint32_t)p.num_phys ? id : 0) * p.Hkv + g; };
+      int tile1 = tile_of(id_of(0));
       float ks1 = __ldg(kscale + tile1), vs1 = __ldg(vscale + tile1);
-      tile1 = tile_of(1);
+      int id1 = id_of(1);
+      int vis = pos + 1 - page_a * 128;  // keys of the page that the row sees (128 and more: all)
       float c = a.c;
       if (QB) {
         if (!mbar_wait_beside(smem_u32(&sm.q_seen[w]), od & 1, abort_flag, status, progress,
                               a.skip_wait_ns))
           break;
-        c = valid ? c * sm.q_mul[split ? 0 : w][row] : 0.f;
+        c = valid ? c * __uint_as_float((uint32_t)sm.q_exp[parity][split ? 0 : w][row] << 23) : 0.f;
       }
       float m = 0.f, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int page = page_a + j * step;
-        const int nvis = valid ? pos - page * 128 + 1 : 128;
+        const int nvis = valid ? vis : 128;
+        vis -= step * 128;
         const bool masked = __any_sync(0xffffffffu, nvis < 128);
         // (a factor of zero would make NaN of a masked score's infinity)
         const float ck = fmaxf(c * ks1, 1.18e-38f), e = scale_log2(vs1);
+        tile1 = tile_of(id1);
         ks1 = __ldg(kscale + tile1);
         vs1 = __ldg(vscale + tile1);
-        tile1 = tile_of(j + 2);
+        id1 = id_of(j + 2);
         if (!mbar_wait_beside(smem_u32(&sm.s_full[w]), su & 1, abort_flag, status, progress,
                               a.skip_wait_ns)) {
           ok = false;
@@ -536,28 +538,25 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
           if (!whole) a.part_lse[srow] = lse;
           else if (a.out_lse) a.out_lse[flat * p.H + head] = lse;
         }
-        // a thread holds a row; the warp turns 128 bytes of each of its 32 rows at a time in its
-        // staging area, so that eight lanes write 128 contiguous bytes of a row
-        uint8_t* stg = sm.q[SINGLE ? 0 : w] + quarter * 4096;
+        // a thread holds a row; eight lanes exchange the 16-byte chunks of 128 bytes of their rows, so that
+        // they then write 128 contiguous bytes of a row together (a thread writing its own row would
+        // cost a memory transaction per 16 bytes)
         const uint32_t vrows = __ballot_sync(0xffffffffu, valid);
         const int64_t obyte = whole ? (flat * a.out_stride + (int64_t)head * D) * 2 : srow * D * 4;
         uint8_t* const base = whole ? reinterpret_cast<uint8_t*>(a.out)
                                     : reinterpret_cast<uint8_t*>(a.part);
-        auto flush = [&](int piece) {  // 128-byte piece `piece` of every row
-          __syncwarp();
+        auto flush = [&](uint32_t (&x)[32], int piece) {  // 128-byte piece `piece` of every row
+          transpose_chunks(x, lane);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + lane / 8;
-            const uint4 x = *reinterpret_cast<const uint4*>(stg + sw128_offset(r, lane % 8));
+            const int r = (lane & 24) + i;
             const int64_t at = __shfl_sync(0xffffffffu, obyte, r);
             if (vrows >> r & 1)
-              *reinterpret_cast<uint4*>(base + at + piece * 128 + (lane % 8) * 16) = x;
+              *reinterpret_cast<uint4*>(base + at + piece * 128 + (lane & 7) * 16) =
+                  make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
-          __syncwarp();
         };
-#pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t v[32];
+        auto load = [&](int cc, uint32_t (&v)[32]) {  // the row's dims 32 cc .. 32 cc + 31
           tmem_ld32(obase + cc * 32, v);
           if (two) {
             uint32_t x[32];
@@ -582,23 +581,27 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
               if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
             }
           }
-          if (whole) {
+        };
+        if (whole) {
+#pragma unroll 1
+          for (int h = 0; h < D / 64; ++h) {
+            uint32_t o[32];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t o[4];
+            for (int u = 0; u < 2; ++u) {
+              uint32_t v[32];
+              load(2 * h + u, v);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                o[k] = pack_p<false>(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
-              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, (cc & 1) * 4 + i / 8)) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
+              for (int i = 0; i < 16; ++i)
+                o[16 * u + i] = pack_p<false>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
             }
-            if (cc & 1) flush(cc / 2);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(stg + sw128_offset(lane, i / 4)) =
-                  make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            flush(cc);
+            flush(o, h);
+          }
+        } else {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t v[32];
+            load(cc, v);
+            flush(v, cc);
           }
         }
       } else {
@@ -609,83 +612,80 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
           if (two) mbar_arrive(smem_u32(&sm.o_free[1]));
         }
       }
-      if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[w]));  // staging and Q tile are free
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     // ------------------------------------------------ Q tiles, and V into FP16 operand tiles
     const int ct = tid - 384;
-    uint32_t it = 0, qc0 = 0, qc1 = 0;
+    uint32_t it = 0, qc0 = 0, qc1 = 0, parity = 1;
     bool ok = true;
     while (ok && work.next(p, rp, pc)) {
       const int h0 = (pc.vg % rp.blocks) * 128, g = pc.vg / rp.blocks;
       const int n = pc.page1 - pc.page0;
-      for (int t = 0; t < (SINGLE ? 1 : pc.nt) && ok; ++t) {
+      parity ^= 1;
+      for (int t = 0; t < (SINGLE ? 1 : pc.nt) && ok; ++t) {  // Q, a row a thread
         uint32_t& qc = t ? qc1 : qc0;
-        const int tok_a = pc.tok0 + t * rp.TB;
-        const int rows = min(rp.TB, pc.q_len - tok_a) * rp.HB;  // (rows behind them may hold anything)
-        const uint8_t* src = a.q + ((pc.flat0 + tok_a) * a.q_stride + (int64_t)(g * p.Hg + h0) * D) * (QB ? 2 : 1);
-        // row r of the tile: head r % HB of token r / HB; false behind the group's last head
-        auto row_at = [&](int r, const uint8_t*& at) {
-          at = src + (r / rp.HB * a.q_stride + (int64_t)(r % rp.HB) * D) * (QB ? 2 : 1);
-          return r < rows && h0 + r % rp.HB < p.Hg;
+        const int tok = pc.tok0 + t * rp.TB + ct / rp.HB, hg = h0 + ct % rp.HB;
+        const bool valid = ct < rp.TB * rp.HB && tok < pc.q_len && hg < p.Hg;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((pc.flat0 + tok) * a.q_stride + (int64_t)(g * p.Hg + hg) * D) * (QB ? 2 : 1));
+        constexpr int CH = QB ? D / 8 : D / 16, XN = QB ? 4 : CH;  // 16-byte chunks, and on the way together
+        uint4 x[XN];
+        auto fetch = [&](int b) {
+#pragma unroll
+          for (int k = 0; k < XN; ++k) x[k] = valid ? __ldg(src + b + k) : make_uint4(0, 0, 0, 0);
         };
-        constexpr int LPR = QB ? D / 8 : D / 16;  // lanes of a row, 16 bytes each
-        constexpr int RPP = 128 / LPR;            // rows of a pass
-        constexpr int GROUP = 8;                  // passes on the way together
-        const int r0 = ct / LPR, ch = ct % LPR;
-        bool waited = false;
+        float inv = 1.f, mul = 1.f;
+        if (QB) {
+          uint32_t mx = 0;  // bits of a non-negative float order like the float
 #pragma unroll 1
-        for (int b = 0; b < 128 && b < rows && ok; b += RPP * GROUP) {
-          uint4 x[GROUP];
+          for (int b = CH - XN; b >= 0; b -= XN) {
+            fetch(b);
 #pragma unroll
-          for (int i = 0; i < GROUP; ++i) {
-            const uint8_t* at;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (b + i * RPP < 128 && row_at(b + i * RPP + r0, at))
-              x[i] = __ldg(reinterpret_cast<const uint4*>(at) + ch);
+            for (int k = 0; k < XN; ++k) {
+              const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mx = max(mx, max((wd[i] & 0x7fffu) << 16, wd[i] & 0x7fff0000u));
+            }
           }
-          if (!waited) ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
-          waited = true;
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < GROUP; ++i) {
-            const int r = b + i * RPP + r0;
-            if (b + i * RPP >= 128) break;
-            if (!QB) {
-              *reinterpret_cast<uint4*>(sm.q[t] + row_offset<D>(r, ch)) = x[i];
-              continue;
-            }
-            const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float f[8], amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] = __uint_as_float(wd[k] << 16);
-              f[2 * k + 1] = __uint_as_float(wd[k] & 0xffff0000u);
-              amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
-            }
-#pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float s = row_scale(amax), inv = 1.f / s;
-            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float u = f[2 * k] * inv, v = f[2 * k + 1] * inv;
-              const uint32_t h = f32x2_to_e4m3x2(pack_f32x2(u, v));
-              const uint32_t h2 = cvt_e4m3x2((uint16_t)h);
-              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-              const uint32_t d = f32x2_to_e4m3x2(pack_f32x2(u - back.x, v - back.y));
-              hi[k / 2] |= h << (16 * (k & 1));
-              lo[k / 2] |= d << (16 * (k & 1));
-            }
-            uint8_t* dst = sm.q[t] + row_offset<D>(r, ch / 2) + (ch & 1) * 8;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dst + TK) = make_uint2(lo[0], lo[1]);
-            if (ch == 0) sm.q_mul[t][r] = s;
-          }
+          mul = row_scale(__uint_as_float(mx));
+          inv = 1.f / mul;
+        } else {
+          fetch(0);
         }
+        ok = mbar_wait(smem_u32(&sm.q_empty[t]), (qc & 1) ^ 1, abort_flag, status);
         if (!ok) break;
         ++qc;
+        if (QB) {
+          sm.q_exp[parity][t][ct] = (uint8_t)(__float_as_uint(mul) >> 23);
+#pragma unroll 1
+          for (int b = 0; b < CH; b += XN) {
+            if (b > 0) fetch(b);
+#pragma unroll
+            for (int k = 0; k < XN; k += 2) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4& y = x[k + i / 4];
+                const uint32_t wd = i % 4 == 0 ? y.x : i % 4 == 1 ? y.y : i % 4 == 2 ? y.z : y.w;
+                const uint64_t f = mul_f32x2(pack_f32x2(__uint_as_float(wd << 16),
+                                                        __uint_as_float(wd & 0xffff0000u)),
+                                             pack_f32x2(inv, inv));
+                const uint32_t h = f32x2_to_e4m3x2(f), h2 = cvt_e4m3x2((uint16_t)h);
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                const uint32_t d = f32x2_to_e4m3x2(add_f32x2(f, pack_f32x2(-back.x, -back.y)));
+                hi[i / 2] = i % 2 ? hi[i / 2] | (h << 16) : h;
+                lo[i / 2] = i % 2 ? lo[i / 2] | (d << 16) : d;
+              }
+              uint8_t* dst = sm.q[t] + row_offset<D>(ct, (b + k) / 2);
+              *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(dst + TK) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < XN; ++k) *reinterpret_cast<uint4*>(sm.q[t] + row_offset<D>(ct, k)) = x[k];
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[t]));
