@@ -153,6 +153,7 @@ struct sps_plan {
   int64_t att_tiles = 0;
   std::vector<AppUnit> app_units;  // the pages an E4M3 cache's append touches
   int64_t off_app_units = 0;
+  int32_t app_max_rows = 0;
   int64_t upload_bytes = 0;  // [0, upload_bytes) of the workspace comes from `blob`
   std::vector<uint8_t> blob;
 };
@@ -542,6 +543,7 @@ void build_append_units(sps_plan* pl) {
     if (ri.q_len == 0) continue;
     const int b = (int)(&ri - pl->reqs.data());
     const size_t end = pl->app_units.size() + (ri.q_len + 126) / kPage + 1;
+    pl->app_max_rows = std::max(pl->app_max_rows, std::min(ri.q_len, kPage));
     for (int i = 0; i < ri.q_len;) {
       const int t = ri.ctx + i, n = std::min(ri.q_len - i, kPage - t % kPage);
       pl->app_units.push_back(AppUnit{b, t / kPage, ri.tok0 + i, n, t % kPage, {0, 0, 0}});
@@ -781,6 +783,7 @@ DevPlan make_dev_plan(const sps_plan* pl, void* ws) {
   d.att_merge_cap = pl->att_merge_cap;
   d.app_units = reinterpret_cast<const AppUnit*>(base + pl->off_app_units);
   d.num_app_units = (int32_t)pl->app_units.size();
+  d.app_max_rows = pl->app_max_rows;
   return d;
 }
 

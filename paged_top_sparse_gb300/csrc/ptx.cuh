@@ -259,6 +259,11 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
+// 16 bytes global -> shared (both 16-byte aligned) by this thread, and the wait for all it began.
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Orders this thread's generic-proxy shared-memory writes before later async-proxy reads
 // (tensor core operands, bulk stores).
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -109,7 +109,7 @@ struct DevPlan {
   int32_t att_num_merges, att_merge_cap;  // cut tiles of this plan, and of any with its q_lens
   // the append of an E4M3 cache: as many entries as any plan of these q_lens can have
   const AppUnit* app_units;
-  int32_t num_app_units;
+  int32_t num_app_units, app_max_rows;  // the most new tokens of a request in one page
 };
 
 // Full attention: pages [page0, page1) of query tile `tile` of head block `vg` (KV head
