@@ -51,16 +51,19 @@ constexpr int kThreads = 512;  // 4 warpgroups
 // and NVFP4 K/V converted in the loader), kModeFP8QK (Q E4M3 bytes, NVFP4 K rounded to E4M3,
 // S on the FP8 tensor core; V FP16).  Over an E4M3 cache, whose pages have an FP32 scale per head:
 // kModeE4BF16 (Q BF16, K converted to BF16) and kModeE4F16 (Q FP16, K converted to FP16), both exactly,
-// V FP16; the scale of K multiplies the scores, that of V the partial output.
-constexpr int kModeBF16 = 0, kModeF16 = 1, kModeFP8QK = 2, kModeE4BF16 = 3, kModeE4F16 = 4;
+// and kModeE4Q (Q E4M3 bytes, S on the FP8 tensor core from the codes as they are; D = 128); V FP16; the
+// scale of K multiplies the scores, that of V the partial output.
+constexpr int kModeBF16 = 0, kModeF16 = 1, kModeFP8QK = 2, kModeE4BF16 = 3, kModeE4F16 = 4, kModeE4Q = 5;
 constexpr bool mode_e4(int mode) { return mode >= kModeE4BF16; }
+constexpr bool mode_qk8(int mode) { return mode == kModeFP8QK || mode == kModeE4Q; }
 // Partial storage: FP32, BF16 or FP16 (nearest even).
 constexpr int kPF32 = 0, kPBF16 = 1, kPF16 = 2;
 
 template <int D, int MODE, int PT>
 struct FwdSmem {
   static constexpr bool RAW = MODE != kModeBF16;  // K/V arrive as NVFP4 codes + scales
-  static constexpr int QE = MODE == kModeFP8QK ? 1 : 2;  // bytes per Q / K element
+  static constexpr bool KRAW = RAW && MODE != kModeE4Q;  // K is converted
+  static constexpr int QE = mode_qk8(MODE) ? 1 : 2;      // bytes per Q / K element
   static constexpr int PE = PT == kPF32 ? 4 : 2;         // bytes per partial element
   static constexpr int TQK = 128 * D * QE;  // 128-row Q or K tile
   static constexpr int TV = 128 * D * 2;    // 128-row V tile (16-bit)
@@ -72,15 +75,15 @@ struct FwdSmem {
   static constexpr int EPB = 32 * EPR;     // one epilogue warp's 32 rows
   static constexpr int kBudget = 227 * 1024 - 1024;  // dynamic smem minus the alignment slack
   // K's and V's codes have a staging area each, or share one (E4M3 codes beside FP32 partials)
-  static constexpr int RAWN = E4 && TQK + TV + 2 * RAWB + 4 * EPB + 4096 + 2 * TQK > kBudget ? 1 : 2;
-  static constexpr int FIXED = TQK + TV + RAWN * RAWB + 4 * EPB + 4096;
+  static constexpr int RAWN = E4 && KRAW && TQK + TV + 2 * RAWB + 4 * EPB + 4096 + 2 * TQK > kBudget ? 1 : 2;
+  static constexpr int FIXED = TQK + TV + (RAWN + KRAW - 1) * RAWB + 4 * EPB + 4096;
   static constexpr int QS0 = (kBudget - FIXED) / TQK;
   static constexpr int QS = QS0 > 4 ? 4 : QS0;  // Q ring stages
   static_assert(QS >= 2, "shared memory");
   uint8_t k[TQK];
   uint8_t v[TV];
   uint8_t q[QS][TQK];
-  alignas(16) uint8_t kraw[RAWB];
+  alignas(16) uint8_t kraw[KRAW ? RAWB : 16];
   alignas(16) uint8_t vraw[RAWN == 2 ? RAWB : 16];
   alignas(16) uint8_t ep[4][EPB];
   float inv_l[2][128];
@@ -133,7 +136,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                float q_scale) {
   using Smem = FwdSmem<D, MODE, PT>;
   constexpr bool RAW = Smem::RAW;
-  constexpr bool FP8QK = MODE == kModeFP8QK;
+  constexpr bool FP8QK = mode_qk8(MODE), KRAW = Smem::KRAW;
   constexpr bool ONE_RAW = Smem::RAWN == 1;  // one staging area: K, V, K, V, ...
   constexpr int kQS = Smem::QS;
   constexpr int DB = D / 64;               // 128-byte column blocks of a 16-bit (V) row
@@ -152,7 +155,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   const int64_t R = (int64_t)p.T * p.H;
 
   if (tid == 0) {
-    mbar_init(smem_u32(&sm.k_full), RAW ? 2 : 1);  // the converter warps, or the TMA bytes
+    mbar_init(smem_u32(&sm.k_full), KRAW ? 2 : 1);  // the converter warps, or the TMA bytes
     mbar_init(smem_u32(&sm.k_empty), 1);
     mbar_init(smem_u32(&sm.v_full), 1);
     mbar_init(smem_u32(&sm.v_empty), 1);
@@ -231,13 +234,15 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       } else {
         // codes and scales of K, then of V, one item ahead of the conversion
         const uint32_t kn = ONE_RAW ? 2 * kv_it : kv_it, vn = ONE_RAW ? kn + 1 : kv_it;
-        if (!mbar_wait(smem_u32(&sm.kraw_empty), (kn & 1) ^ 1, abort_flag, status)) break;
-        uint32_t f = smem_u32(&sm.kraw_full);
-        mbar_expect_tx(f, Smem::RC + Smem::RSC);
-        bulk_load(smem_u32(sm.kraw), kc + (int64_t)tile * Smem::RC, Smem::RC, f);
+        uint32_t f = smem_u32(KRAW ? &sm.kraw_full : &sm.k_full);
+        if (!mbar_wait(smem_u32(KRAW ? &sm.kraw_empty : &sm.k_empty), (kn & 1) ^ 1, abort_flag, status))
+          break;
+        mbar_expect_tx(f, KRAW ? Smem::RC + Smem::RSC : TQK);
+        if (KRAW) bulk_load(smem_u32(sm.kraw), kc + (int64_t)tile * Smem::RC, Smem::RC, f);
+        else tma_load_2d(smem_u32(sm.k), &tmK, 0, tile * 128, f);
         if (Smem::E4) {
-          // (K of item n - 1 has been converted, so the last S of item n - 2 is done, and with it the
-          // softmax of item n - 4, the last reader of this entry)
+          // (K of item n - 1 has been converted, so the last S of item n - 2 is done, or that of item
+          // n - 1 is, and with it the softmax of item n - 4, the last reader of this entry)
           sm.sc[kv_it & 3] = make_float2(__ldg(reinterpret_cast<const float*>(ks) + tile),
                                          __ldg(reinterpret_cast<const float*>(vs) + tile));
           mbar_arrive(smem_u32(&sm.sc_full[kv_it & 3]));
@@ -378,16 +383,18 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         uint8_t* vraw = ONE_RAW ? sm.kraw : sm.vraw;
         uint64_t* vfull = ONE_RAW ? &sm.kraw_full : &sm.vraw_full;
         uint64_t* vempty = ONE_RAW ? &sm.kraw_empty : &sm.vraw_empty;
-        if (!mbar_wait(smem_u32(&sm.kraw_full), ONE_RAW ? 0 : ph, abort_flag, status) ||
-            !mbar_wait(smem_u32(&sm.k_empty), ph ^ 1, abort_flag, status))
-          break;
-        if (Smem::E4) e4m3_tile_convert<D, QK_BF16>(sm.kraw, sm.k, ct, 64);
-        else nvfp4_tile_convert<D, FP8QK>(sm.kraw, sm.k, ct, 64);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&sm.k_full));
-          mbar_arrive(smem_u32(&sm.kraw_empty));
+        if (KRAW) {
+          if (!mbar_wait(smem_u32(&sm.kraw_full), ONE_RAW ? 0 : ph, abort_flag, status) ||
+              !mbar_wait(smem_u32(&sm.k_empty), ph ^ 1, abort_flag, status))
+            break;
+          if (Smem::E4) e4m3_tile_convert<D, QK_BF16>(sm.kraw, sm.k, ct, 64);
+          else nvfp4_tile_convert<D, FP8QK>(sm.kraw, sm.k, ct, 64);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.k_full));
+            mbar_arrive(smem_u32(&sm.kraw_empty));
+          }
         }
         if (!mbar_wait(smem_u32(vfull), ONE_RAW ? 1 : ph, abort_flag, status) ||
             !mbar_wait(smem_u32(&sm.v_empty), ph ^ 1, abort_flag, status))
@@ -675,13 +682,16 @@ cudaError_t run_forward(const DevPlan& p, const void* q, const void* kc, const v
   // tensor-map element types: BF16 (0), FP16 (1) or bytes (2); Q and K rows of 128 bytes
   const int dq = MODE == kModeBF16 || MODE == kModeE4BF16 ? 0
                  : MODE == kModeF16 || MODE == kModeE4F16 ? 1 : 2;
-  const uint64_t qe = MODE == kModeFP8QK ? 1 : 2;
+  const uint64_t qe = mode_qk8(MODE) ? 1 : 2;
   const uint32_t box_q = (uint32_t)(128 / qe);
   if (!encode_tmap_2d(&tmQ, dq, const_cast<void*>(q), D, R, (uint64_t)D * qe, box_q, 1, true))
     return cudaErrorInvalidValue;
   if (MODE == kModeBF16 &&
       (!encode_tmap_2d(&tmK, 0, const_cast<void*>(kc), D, kv_rows, (uint64_t)D * 2, 64, 128, true) ||
        !encode_tmap_2d(&tmV, 0, const_cast<void*>(vc), D, kv_rows, (uint64_t)D * 2, 64, 128, true)))
+    return cudaErrorInvalidValue;
+  if (MODE == kModeE4Q &&
+      !encode_tmap_2d(&tmK, 2, const_cast<void*>(kc), D, kv_rows, (uint64_t)D, 128, 128, true))
     return cudaErrorInvalidValue;
   const int smem = (int)sizeof(FwdSmem<D, MODE, PT>) + 1024;
   auto kern = forward_kernel<D, MODE, PT>;
@@ -723,12 +733,12 @@ cudaError_t launch_forward_pt(const DevPlan& p, sps_dtype qt, sps_dtype kvt, con
                                             lse, lse_split_stride, q_scale, st);
   }
   if (qt == SPS_E4M3 && kvt == SPS_E4M3) {
+    if (p.D == 128)
+      return run_forward<128, kModeE4Q, PT>(p, q, kc, vc, ks, vs, page_table, partial, split_stride,
+                                            lse, lse_split_stride, q_scale, st);
     if (!p.qconv) return cudaErrorInvalidValue;
     cudaError_t e = launch_dequant(SPS_E4M3, q, nullptr, (int64_t)p.T * p.H * p.D, p.qconv, st);
     if (e != cudaSuccess) return e;
-    if (p.D == 128)
-      return run_forward<128, kModeE4F16, PT>(p, p.qconv, kc, vc, ks, vs, page_table, partial,
-                                              split_stride, lse, lse_split_stride, q_scale, st);
     return run_forward<64, kModeE4F16, PT>(p, p.qconv, kc, vc, ks, vs, page_table, partial,
                                            split_stride, lse, lse_split_stride, q_scale, st);
   }

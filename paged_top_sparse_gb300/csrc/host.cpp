@@ -637,7 +637,8 @@ void make_plan(const sps_problem& problem, sps_plan* pl) {
   // not with the physical pool.  The forward dequantises NVFP4 K/V inside its loader, and
   // E4M3 x E4M3 indexing runs on the FP8 tensor core directly; neither needs a copy.
   const bool idx_fp16 = p.idx_k_dtype == SPS_NVFP4;
-  if (p.q_dtype == SPS_E4M3 || (idx_fp16 && p.idx_q_dtype == SPS_E4M3))
+  const bool q_direct = p.kv_dtype == SPS_E4M3 && p.head_dim == 128;  // E4M3 Q x E4M3 K as they are
+  if ((p.q_dtype == SPS_E4M3 && !q_direct) || (idx_fp16 && p.idx_q_dtype == SPS_E4M3))
     pl->off_qconv = take(2 * pl->R * p.head_dim);
   if (idx_fp16)
     pl->off_kconv = take(2 * std::max<int64_t>(1, pl->total_pages) * p.num_kv_heads * kPage *
