@@ -6,14 +6,19 @@
 // are small, so the codes go from shared memory to registers once, become FP16 fragments there, and feed
 // the warp-level tensor instruction (mma.sync m16n8k16, FP32 accumulation).
 //
+// Bound: HBM.  64 tokens after 32K, H 32 / H_kv 2, D 128 (1.08 GB): 176 us, of which 161 are the read at the
+// rate of a plain copy and most of the rest start, fill and merge (204 in the tcgen05 kernel); H_kv 4 311 us,
+// 6.9 TB/s; D 64 99 us; one token after 128K 17 us.  A second copy warp and ring stages of 64 keys
+// measured the same.
+//
 // Mathematics as in attention_e4m3.cu: the scale of a page's keys multiplies its scores' factor, that of its
 // values, 2^e, the exponent; the reference m follows both; l takes p' 2^-e.  A BF16 query row becomes
 // FP16 after division by a power of two (its largest element then lies in (224, 448]: exact but for
 // elements 2^-22 of it and less, which are off by 2^-33 of it at most).
 //
-// One persistent CTA per SM: two warps copy pages (K and V codes, by TMA with the swizzle that keeps the
-// fragment reads below on distinct banks) into a ring; eight take the pages' 32-key chunks in turn, each
-// with a running (m, l, O) of its own, merged through shared memory at the end of a piece.
+// One persistent CTA per SM: a warp copies pages (K and V codes, by TMA with the swizzle that keeps the
+// fragment reads below on distinct banks) into a ring; the others take the pages' 32-key chunks in turn,
+// each with a running (m, l, O) of its own, merged through shared memory at the end of a piece.
 //
 // Fragments.  Lane (g, t) = (lane / 4, lane % 4).  For Q K^T a lane reads D / 4 dims of a key, a word of
 // four codes to a k-step; for P V the pairs of a B register run along keys, so the bytes of two keys'
@@ -29,22 +34,20 @@ namespace att {
 namespace {
 
 constexpr int kChunks = 4;     // 32-key chunks of a page
-constexpr int kCopyWarps = 2;  // a warp copies every kCopyWarps-th page
-constexpr int kProducts = 8;   // product warps
+constexpr int kWarps = 8;      // product warps (D 64: 12 measured 101 us for 64 tokens after 32K, 8 99)
 
 template <int D, int ROWS>
 struct DecSmem {
-  static constexpr int WARPS = kProducts;
+  static constexpr int WARPS = kWarps;
   static constexpr int STEP = WARPS / kChunks;  // a warp takes a chunk of every STEP-th page
-  static constexpr int UNIT = STEP % kCopyWarps ? STEP * kCopyWarps : STEP;
   static constexpr int TILE = 128 * D;    // codes of K, or of V
   static constexpr int PAGE = 2 * TILE;
   static constexpr int S0 = (227 * 1024 - WARPS * ROWS * (D * 4 + 8) - D * 32 - 1024) / PAGE;
-  // A multiple of STEP and kCopyWarps: a warp then finds in a stage, each time round, the page after
+  // A multiple of STEP: a warp then finds in a stage, each time round, the page after
   // one that it took itself, so that the phase it waits for is never more than one ahead of the
   // barrier's.  Between pieces the warps meet.
-  static constexpr int STAGES = (S0 > 8 ? 8 : S0) / UNIT * UNIT;
-  static_assert(WARPS % kChunks == 0 && UNIT % STEP == 0 && UNIT % kCopyWarps == 0 && STAGES >= 4, "stages");
+  static constexpr int STAGES = (S0 > 9 ? 9 : S0) / STEP * STEP;
+  static_assert(WARPS % kChunks == 0 && STAGES >= 4, "stages");
   uint8_t page[STAGES][PAGE];
   float o[WARPS][ROWS][D];
   float2 stat[WARPS][ROWS];  // (m, l)
@@ -61,7 +64,7 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
 }
 
 template <int D, int ROWS, bool QB>
-__global__ void __launch_bounds__(32 * (kProducts + kCopyWarps), 1)
+__global__ void __launch_bounds__(32 * (kWarps + 1), 1)
 decode_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    DevPlan p, AttArgs a) {
   using Smem = DecSmem<D, ROWS>;
@@ -102,13 +105,10 @@ decode_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     while (ok && work.next(p, rp, pc)) {
       const int n = pc.page1 - pc.page0;
       const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
-      // this warp's pages of the piece: s0, s0 + kCopyWarps, ...; a lane holds every one's tile
-      const int s0 = (int)((warp - WARPS + kCopyWarps - page_it % kCopyWarps) % kCopyWarps);
-      auto load_ids = [&](int k) {  // physical tiles of its pages k + lane
-        const int s = s0 + (k + lane) * kCopyWarps;
+      auto load_ids = [&](int k) {  // physical tiles of pages k + lane
         int id = 0;
-        if (s < n) {
-          id = __ldg(pages + s);
+        if (k + lane < n) {
+          id = __ldg(pages + k + lane);
           if (id < 0 || id >= p.num_phys) {
             set_status(status, DEV_BAD_PAGE);
             id = 0;
@@ -117,10 +117,10 @@ decode_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         return id * p.Hkv + pc.vg;
       };
       int ids = load_ids(0), next_ids = 0;
-      for (int s = s0, k = 0; s < n && ok; s += kCopyWarps, ++k) {
-        if (k > 0 && (k & 31) == 0) ids = next_ids;
-        if ((k & 31) == 8) next_ids = load_ids(k + 24);
-        const int tile = __shfl_sync(0xffffffffu, ids, k & 31);
+      for (int s = 0; s < n && ok; ++s) {
+        if (s > 0 && (s & 31) == 0) ids = next_ids;
+        if ((s & 31) == 8) next_ids = load_ids(s + 24);
+        const int tile = __shfl_sync(0xffffffffu, ids, s & 31);
         const uint32_t it = page_it + s, st = it % S;
         if (lane == 0) {
           ok = mbar_wait(smem_u32(&sm.empty[st]), ((it / S) & 1) ^ 1, abort_flag, status);
@@ -464,7 +464,7 @@ cudaError_t run_decode(const DevPlan& p, const AttArgs& a, cudaStream_t st) {
   auto kern = decode_e4m3_kernel<D, ROWS, QB>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(p.att_ctas), dim3(32 * (kProducts + kCopyWarps)), smem, st, tmK, tmV, p, a);
+  return launch_pdl(kern, dim3(p.att_ctas), dim3(32 * (kWarps + 1)), smem, st, tmK, tmV, p, a);
 }
 
 template <int D, int ROWS>

@@ -18,13 +18,24 @@
 //
 // Work, rows and merge are attention.cu's (256-row work tiles, the plan's pieces).
 //
+// Bound, prompts and chunks: the chain of a row tile, its softmax (some 1300 cycles a page) and its own
+// products (256 or 512 cycles of Q K^T, 512 of P V), beside the other tile's; then the power limit.  D 128, H 32 /
+// H_kv 2: an 8192-token prompt 358 us with BF16 queries and 313 with E4M3 ones (1.54 and 1.76 PFLOP/s),
+// 8 x 512 after 32K 1220 and 1116 us (1.82 and 1.99; over a BF16 cache 1394); D 64 314 and 291 us, where the
+// softmax's issue slots are the limit.  Few rows: the cache's bytes, 64 x 3 tokens after 32K 179 us (6.0 TB/s).
+//
+// What the roles' code costs in instruction fetches shows: the four roles of a scheduler share little, and
+// with every inner loop unrolled the prompt took 531 us.  So the MMA steps, the filling of Q and the
+// epilogue have one copy each.
+//
 // One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
 //   warp 0     page-table reads and the copies: K tiles by TMA (128-byte or, D = 64, 64-byte swizzle) into
 //              one ring, V's codes by bulk copies into another;
 //   warp 1     one thread issues every MMA, as in attention.cu: two row tiles' chains alternate, or with one
 //              row tile its even and odd pages;
 //   warps 4-7, 8-11   softmax and epilogue of row tile 0 / 1, a thread per row;
-//   warps 12-15  Q tiles (and the row scales), and V into FP16 operand tiles, a thread per row.
+//   warps 12-15  Q tiles (with the row scales), as soon as the piece before has used them last, and V into
+//              FP16 operand tiles, a thread per row.
 #include <cstring>
 
 #include "attention.cuh"
