@@ -281,7 +281,8 @@ sps_status partial_combine_bf16(int64_t rows, int32_t splits, int32_t head_dim,
  *   partial_f16  device FP16; element (s, r, d) at partial_f16[s * split_stride + r * D + d]
  *                (elements); 16-byte aligned, split_stride a multiple of 8 and >= rows * D
  * Every other argument, the LSE and the output are those of sparse_prefill_fwd and
- * partial_combine.  The forward rounds each normalised partial to FP16 (nearest even); the
+ * partial_combine.  Over an E4M3 cache, whose scale is applied to the partial, FP16's range asks for
+ * |code x scale| < 65504.  The forward rounds each normalised partial to FP16 (nearest even); the
  * combine widens them exactly to FP32 and accumulates in FP32.
  */
 sps_status sparse_prefill_fwd_f16(const sps_plan* plan, const void* q, float q_scale,
@@ -492,7 +493,8 @@ sps_status sparse_prefill_fwd_noalloc(const sps_plan* plan, const void* q, float
  * Accumulation, maxima and sums are FP32; P is rounded to the 16-bit type of the second product
  * (BF16; FP16 over an NVFP4 cache, whose code x scale products are exact there, and over an E4M3 cache,
  * whose codes are: the page's V scale goes into P, its K scale into the scores' factor, whose product
- * with softmax_scale and q_scale is to stay within FP32).  BF16 P takes V of
+ * with softmax_scale and q_scale is to stay within FP32; a BF16 query row is taken to 2^-17 of its largest
+ * element there, in tiles of more than 16 rows as the sum of two E4M3 rows).  BF16 P takes V of
  * any magnitude as it is, where sparse_prefill_fwd's FP16 P needs V within FP16's range; it costs
  * precision: 2.35e-3 relative L2 on random data against 1.7e-3 with FP16 P (and with the output's
  * own rounding alone).  The result is the same bits from call to call.  A captured call may be replayed after another plan that differs

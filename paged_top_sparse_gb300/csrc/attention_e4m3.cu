@@ -11,7 +11,7 @@
 //
 // The first product runs on the FP8 tensor core straight from the cache's codes: E4M3 queries as they are;
 // a BF16 query row, scaled by a power of two to at most 448, as the sum of two E4M3 rows (8 significant
-// bits are 4 + 4: exact for elements down to 2^-10 of the row's largest, off by 2^-18 of that below), two
+// bits are 4 + 4: exact for elements down to 2^-10 of the row's largest, off by 2^-17 of that below), two
 // products into one accumulator, which cost what one BF16 product does.  So K is copied by TMA into its
 // operand tile and never converted.  V is converted to FP16 (exactly) by four warps, since P needs more
 // than E4M3's four bits.

@@ -426,6 +426,51 @@ def test_sparse_forward_of_all_pages_is_full_attention():
     assert bool(((out.view(c.T, 8, 128).double() - c.out.double()).abs() <= tol).all())
 
 
+def test_sparse_step_with_index_keys_of_its_own():
+    """Indexer over BF16 index keys, selection, forward over the E4M3 cache and combine."""
+    from paged_top_sparse_gb300 import binding as B
+
+    H, G, D, k = 8, 2, 128, 4
+    c = Case(61, [200, 1, 70], [1300, 700, 128], H, G, D, top_k=k, nan_tail=False)
+    R = c.T * H
+    index_keys = torch.where(torch.isfinite(c.kd), c.kd, 0.0).bfloat16()
+    n = c.pt.shape[1]
+    scores = torch.full((R, (n + 3) // 4 * 4), float("nan"), device=DEV)
+    idx = torch.empty((R, k), dtype=torch.int32, device=DEV)
+    partial, lse = torch.empty((k, R, D), device=DEV), torch.empty((k, R), device=DEV)
+    out_lse = torch.empty((R,), device=DEV)
+    B.indexer_scores(c.plan, c.q, 1.0, index_keys, None, 1.0, c.pt, scores, c.ws)
+    B.topk_select(c.plan, scores, idx, c.ws)
+    B.sparse_prefill_fwd(c.plan, c.q, 1.0, c.kc, c.vc, c.ks, c.vs, c.pt, idx, partial, lse, c.ws)
+    B.partial_combine(partial, lse, c.out.view(R, D), out_lse)
+    torch.cuda.synchronize()
+    assert B.sps_read_device_status(c.plan, c.ws) == 0
+    sel = idx.view(c.T, H, k)
+    pos = torch.cat([torch.arange(a, a + m, device=DEV) for a, m in zip(c.ctx, c.q_lens)])
+    assert bool(((sel == (pos // 128)[:, None, None]).sum(-1) == 1).all())  # the own page is there
+    out, rlse, mag, top, keys = c.reference(sel=sel)
+    tol = (2.0 ** -11 + 2.0 ** -13) * mag + 2.0 ** -8 * out.abs() + (keys * 2.0 ** -24 * top)[..., None]
+    assert bool(((c.out.double() - out).abs() <= tol).all())
+    assert bool(((out_lse.view(c.T, H).double() - rlse).abs() <= 2.0 ** -12 + rlse.abs() * 2.0 ** -22).all())
+
+
+@pytest.mark.parametrize("q", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,G,D,q_lens,ctx", [(16, 1, 128, [300, 9, 140] * 60, [0, 500, 90] * 60),
+                                              (8, 2, 64, [70] * 150, [33 * i for i in range(150)]),
+                                              (32, 2, 128, [3] * 200, [0, 120, 127, 1000] * 50)])
+def test_blocks_of_many_pieces(H, G, D, q_lens, ctx, q):
+    """More work tiles than blocks: a block goes through pieces of one and two row tiles, of one and many
+    pages, in turn, and does so alike each time."""
+    c = Case(len(q_lens), q_lens, ctx, H, G, D, q)
+    c.run()
+    c.check()
+    first = c.out.clone()
+    for _ in range(20):
+        c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, first)
+
+
 def test_fp8qk_wants_an_nvfp4_cache():
     from paged_top_sparse_gb300 import binding as B
 

@@ -209,6 +209,55 @@ def test_append_with_rotation(q_lens, ctx, D, R, interleaved, norm):
     assert bool(same[~written].all())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_heads_share_a_block(D):
+    """Enough (page, head) tiles that a block takes several heads of a page, one behind the other; rows of
+    a fused projection; new tokens behind earlier ones."""
+    q_lens, ctx, G = [1500, 700, 130], [77, 0, 1000], 40
+    b = Batch(q_lens, ctx, G, D, seed=D, kv_pad=1)
+    f = (1e4 ** (-torch.arange(D // 2, device=DEV, dtype=torch.float64) * 2 / D)).float()
+    pos = torch.cat([torch.arange(c, c + n, device=DEV) for c, n in zip(ctx, q_lens)])
+    w = 1 + 0.2 * torch.randn(D, generator=b.g, device=DEV)
+    want_v = append_rule(b.v.double(), q_lens, ctx, b.pt, b.vc, b.vs)
+    want_k = append_rule(rotated(b.k, pos, f, w, 1e-6, False), q_lens, ctx, b.pt, b.kc, b.ks)
+    b.B.sps_kv_append_rope(b.plan, b.k, b.v, w, 1e-6, b.B.Rope(f), b.pt, b.kc, b.vc, b.ks, b.vs, b.ws)
+    torch.cuda.synchronize()
+    assert b.status() == 0
+    assert torch.equal(want_v[1], b.vs) and torch.equal(want_v[0].view(torch.uint8), b.vc.view(torch.uint8))
+    assert torch.equal(want_k[1], b.ks)
+    # a key next to a code's border may go either way: by a step at most, and few of them (the FP32 row is
+    # off by 2^-19 of its size, a step is 2^-4 of a code at least: less than one in a thousand)
+    x, y = want_k[0].double(), b.kc.double()
+    step = torch.maximum(x.abs(), y.abs()).clamp(min=2.0 ** -6) * 2.0 ** -3
+    assert bool(((x - y).abs() <= step).all()) and float((x != y).double().mean()) < 1e-3
+
+
+def test_positions_of_their_own_axes():
+    """Rotation by positions on three axes, as sps_rope gives them, into the E4M3 cache."""
+    q_lens, ctx, G, D, R = [140, 3], [100, 127], 2, 128, 64
+    b = Batch(q_lens, ctx, G, D, 9)
+    T = sum(q_lens)
+    f = (1e4 ** (-torch.arange(R // 2, device=DEV, dtype=torch.float64) * 2 / R)).float()
+    pos = torch.randint(-500, 70000, (3, T), generator=b.g, device=DEV, dtype=torch.int32)
+    axis = [j * 3 // (R // 2) for j in range(R // 2)]
+    for inter in (False, True):
+        rope = b.B.Rope(f, positions=pos, pair_axis=axis, interleaved=inter)
+        x = b.k.double()
+        a = pos[torch.tensor(axis, device=DEV)].T.double() * f.double()
+        c, s = a.cos()[:, None], a.sin()[:, None]
+        u, v = (x[..., 0:R:2], x[..., 1:R:2]) if inter else (x[..., :R // 2], x[..., R // 2:R])
+        r = (torch.stack((u * c - v * s, v * c + u * s), -1).flatten(-2) if inter
+             else torch.cat((u * c - v * s, v * c + u * s), -1))
+        rows = torch.cat((r, x[..., R:]), -1)
+        codes, scales = append_rule(rows, q_lens, ctx, b.pt, b.kc, b.ks)
+        b.B.sps_kv_append_rope(b.plan, b.k, b.v, None, 0.0, rope, b.pt, b.kc, b.vc, b.ks, b.vs, b.ws)
+        torch.cuda.synchronize()
+        assert torch.equal(scales, b.ks)
+        y, z = codes.double(), b.kc.double()
+        step = torch.maximum(y.abs(), z.abs()).clamp(min=2.0 ** -6) * 2.0 ** -3
+        assert bool(((y - z).abs() <= step).all()) and float((y != z).double().mean()) < 1e-3
+
+
 def test_token_by_token_reaches_the_values_of_one_append():
     """300 tokens at once, and one at a time: the same scales, and the same values but where a code fell
     below 2^-6 of its scale on the way (rounded twice)."""
