@@ -24,6 +24,11 @@
 // 8 x 512 after 32K 1220 and 1116 us (1.82 and 1.99; over a BF16 cache 1394); D 64 314 and 291 us, where the
 // softmax's issue slots are the limit.  Few rows: the cache's bytes, 64 x 3 tokens after 32K 179 us (6.0 TB/s).
 //
+// What is left of that chain is instructions and hand-offs: with the exponentials, three quarters of both
+// products and the conversion left out (a copy, for its time alone) a page still takes 2150 of its 2580
+// cycles.  Half a page at a time, so that products and exponentials of one tile overlap, doubles the
+// hand-offs and the reads of Q: 509 and 406 us for the prompt.
+//
 // What the roles' code costs in instruction fetches shows: the four roles of a scheduler share little, and
 // with every inner loop unrolled the prompt took 531 us.  So the MMA steps, the filling of Q and the
 // epilogue have one copy each.

@@ -53,7 +53,7 @@ constexpr int kThreads = 512;  // 4 warpgroups
 // kModeE4BF16 (Q BF16, K converted to BF16) and kModeE4F16 (Q FP16, K converted to FP16), both exactly,
 // and kModeE4Q (Q E4M3 bytes, S on the FP8 tensor core from the codes as they are; D = 128); V FP16; the
 // scale of K multiplies the scores, that of V the partial output.  Measured at D 128: a prompt of 8192
-// tokens (32 of 64 pages kept) 505 us with BF16 queries (467 over a BF16 cache, which has no K to convert
+// tokens (16 pages a row) 505 us with BF16 queries (467 over a BF16 cache, which has no K to convert
 // and needs no second buffer for it); chunks with E4M3 queries 161 us in kModeE4Q, 185 through FP16.
 constexpr int kModeBF16 = 0, kModeF16 = 1, kModeFP8QK = 2, kModeE4BF16 = 3, kModeE4F16 = 4, kModeE4Q = 5;
 constexpr bool mode_e4(int mode) { return mode >= kModeE4BF16; }
