@@ -168,3 +168,58 @@ def test_relative_error_of_random_data(q):
         err = (c.out[t0:t1].double() - out[t0:t1]).norm() / out[t0:t1].norm()
         # (one row set of 16 x 128 elements: the mean square's own deviation is 2 %)
         assert float(err) <= 1.8e-3 * (1.06 if t1 - t0 < 3 else 1.0), float(err)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("q_lens,ctx", [([150, 1], [300, 0]), ([1, 2], [500, 700])])
+def test_pages_whose_offsets_pass_32_bits(q_lens, ctx, quant):
+    """The same append, attention and sparse forward in a small pool and in pages at the end of one of
+    4.6 GB: the same bits."""
+    from paged_top_sparse_gb300 import binding as B
+
+    H, G, D, pool = 16, 2, 128, 140_000
+    g = torch.Generator(device=DEV)
+    g.manual_seed(len(q_lens) + ctx[0])
+    total = [a + b for a, b in zip(q_lens, ctx)]
+    pages = [(n + 127) // 128 for n in total]
+    T, S = sum(q_lens), sum(total)
+    k, v = (torch.randn((S, G, D), generator=g, device=DEV).bfloat16() for _ in "kv")
+    q = torch.randn((T, H, D), generator=g, device=DEV) * 4
+    q = q.to(F8) if quant else q.bfloat16()
+    qt, width = "e4m3" if quant else "bf16", max(pages)
+    sel = torch.full((T, H, 8), -1, dtype=torch.int32, device=DEV)
+    pos = torch.cat([torch.arange(c, c + n, device=DEV) for n, c in zip(q_lens, ctx)])
+    page = torch.arange(8, device=DEV, dtype=torch.int32).expand(T, H, 8)
+    sel = torch.where(page <= (pos // 128)[:, None, None], page, sel)
+    results = []
+    for phys in (sum(pages), pool):
+        table = torch.full((len(q_lens), width), -1, dtype=torch.int32, device=DEV)
+        at = phys - 1
+        for b, n in enumerate(pages):
+            table[b, :n] = torch.arange(at, at - n, -1, device=DEV, dtype=torch.int32)
+            at -= n
+        used = torch.cat([table[b, :n] for b, n in enumerate(pages)]).long()
+        kc, vc = (torch.empty((phys, G, 128, D), dtype=torch.uint8, device=DEV) for _ in "kv")
+        ks, vs = (torch.zeros((phys, G), device=DEV) for _ in "kv")
+        kc[used] = 0
+        vc[used] = 0
+        kc, vc = kc.view(F8), vc.view(F8)
+        out, lse = torch.empty((T, H, D), dtype=torch.bfloat16, device=DEV), torch.empty((T, H), device=DEV)
+        part, plse = torch.zeros((8, T * H, D), device=DEV), torch.empty((8, T * H), device=DEV)
+        fill = B.Plan(total, [0] * len(total), H, G, D, 1, width, phys, q_dtype=qt, kv_dtype="e4m3")
+        plan = B.Plan(q_lens, ctx, H, G, D, 8, width, phys, q_dtype=qt, kv_dtype="e4m3")
+        for p in (fill, plan):
+            ws = torch.zeros(p.workspace_bytes, dtype=torch.uint8, device=DEV)
+            B.sps_plan_upload(p, ws)
+            if p is fill:
+                B.sps_kv_append(p, k, v, table, kc, vc, ks, vs, ws)
+        scratch = torch.empty(B.paged_attention_scratch(plan), dtype=torch.uint8, device=DEV)
+        B.paged_attention_fwd(plan, q, 0.5, kc, vc, ks, vs, table, out, lse, scratch, ws)
+        B.sparse_prefill_fwd(plan, q, 0.5, kc, vc, ks, vs, table, sel, part, plse, ws)
+        torch.cuda.synchronize()
+        assert B.sps_read_device_status(plan, ws) == 0
+        results.append([x.clone() for x in (kc.view(torch.uint8)[used], vc.view(torch.uint8)[used], ks[used],
+                                            vs[used], out.view(torch.int16), lse, part, plse)])
+    assert int(results[0][0].count_nonzero()) > 0 and bool(results[0][4].any())
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
