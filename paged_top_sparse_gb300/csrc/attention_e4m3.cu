@@ -18,20 +18,20 @@
 //
 // Work, rows and merge are attention.cu's (256-row work tiles, the plan's pieces).
 //
-// Bound, prompts and chunks: the chain of a row tile, its softmax (some 1300 cycles a page) and its own
-// products (256 or 512 cycles of Q K^T, 512 of P V), beside the other tile's; then the power limit.  D 128, H 32 /
-// H_kv 2: an 8192-token prompt 358 us with BF16 queries and 313 with E4M3 ones (1.54 and 1.76 PFLOP/s),
-// 8 x 512 after 32K 1220 and 1116 us (1.82 and 1.99; over a BF16 cache 1394); D 64 314 and 291 us, where the
-// softmax's issue slots are the limit.  Few rows: the cache's bytes, 64 x 3 tokens after 32K 179 us (6.0 TB/s).
+// Bound, prompts and chunks: the chain of a row tile, its softmax and its own products (256 or 512 cycles of
+// Q K^T, 512 of P V) with the hand-offs between, beside the other tile's; then the power limit.  D 128, H 32 /
+// H_kv 2: an 8192-token prompt 333 us with BF16 queries and 283 with E4M3 ones (1.65 and 1.94 PFLOP/s),
+// 8 x 512 after 32K 1136 and 998 us (1.95 and 2.22; over a BF16 cache 1394); D 64 278 and 264 us, where the
+// softmax's issue slots are the limit.  Few rows: the cache's bytes, 64 x 3 tokens after 32K 178 us (6.0 TB/s).
 //
-// What is left of that chain is instructions and hand-offs: with the exponentials, three quarters of both
-// products and the conversion left out (a copy, for its time alone) a page still takes 2150 of its 2580
-// cycles.  Half a page at a time, so that products and exponentials of one tile overlap, doubles the
-// hand-offs and the reads of Q: 509 and 406 us for the prompt.
-//
-// What the roles' code costs in instruction fetches shows: the four roles of a scheduler share little, and
-// with every inner loop unrolled the prompt took 531 us.  So the MMA steps, the filling of Q and the
-// epilogue have one copy each.
+// What a role executes per page is laid out by two measurements.  The four roles of a scheduler share little
+// code, and what they go through together does not fit next to the scheduler: with every inner loop unrolled
+// the prompt took 531 us in place of 390, and a second copy of the MMA steps 7 % more.  And a jump costs about
+// a hundred cycles of fetching: products in loops of one instruction took 480 us where straight lines took
+// 313.  So the page that is the rule, in the MMA's loop and in the softmax's, is a straight line; every
+// other page (first, masked, last, one that asks for a rescale) goes through rolled code beside it.  The straight
+// lines took the prompt from 358 to 333 us (BF16 queries) and from 313 to 283.  Half a page at a time, so
+// that products and exponentials of one tile overlap, doubles the hand-offs and the reads of Q (509 and 406).
 //
 // One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
 //   warp 0     page-table reads and the copies: K tiles by TMA (128-byte or, D = 64, 64-byte swizzle) into
@@ -71,6 +71,7 @@ struct E4Smem {
   uint64_t o_done[2];                        // the piece's last P V product into O_t
   uint64_t o_free[2], q_seen[2], stat_full, done;  // q_seen: the row scales, by warpgroup
   float2 stat[128];      // (m, l) of the odd pages' rows
+  float2 scale[64];      // of a page: K's, and V's as a power of two; a ring over the block's pages
   // BF16 queries: the power of two that a row was divided by (its exponent field), by piece parity
   uint8_t q_exp[2][2][128];
   uint32_t tmem_base;
@@ -79,11 +80,11 @@ struct E4Smem {
 };
 
 // Registers of a thread by role: of the copies and the MMA, the softmax, and the tiles' filling.  The block is
-// launched with 512 x 128 of them.  8 x 512 tokens after 32K: BF16 queries 1224 us, with 64 + 184 + 80 1248;
-// E4M3 queries 1119 us, with 80 + 168 + 88 1132.
+// launched with 512 x 128 of them.  D 64, BF16 queries: 283 us, with 88 + 168 + 88 292 (the filling spills); the
+// other forms are within 1 % with any split of the kind.
 template <bool QB>
 struct E4Regs {
-  static constexpr int kIssue = QB ? 80 : 64, kSoftmax = QB ? 168 : 184, kFill = QB ? 96 : 80;
+  static constexpr int kIssue = 80, kSoftmax = QB ? 168 : 176, kFill = QB ? 96 : 80;
   static_assert(kIssue + 2 * kSoftmax + kFill == 4 * 128, "registers");
 };
 template <int N>
@@ -93,6 +94,13 @@ __device__ __forceinline__ void reg_dec() {
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The wait for a barrier that has usually been reached, or is within a first try's patience: what follows
+// it stays next to what goes before.
+__device__ __forceinline__ bool wait_soon(uint64_t& bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  if (__builtin_expect(mbar_try_wait(smem_u32(&bar), parity), 1)) return true;
+  return mbar_wait(smem_u32(&bar), parity, abort, status);
 }
 
 // Byte of 16-byte chunk c of row r of a tile of D-byte rows, as TMA writes it and the tensor core reads it.
@@ -191,14 +199,17 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
     reg_dec<Regs::kIssue>();
     if (warp == 0) {
       // ------------------------------------------------ copies
+      const float* kscale = reinterpret_cast<const float*>(a.ks);
+      const float* vscale = reinterpret_cast<const float*>(a.vs);
       uint32_t it = 0;  // tiles copied before this piece
       bool ok = true;
       while (ok && work.next(p, rp, pc)) {
         const int g = pc.vg / rp.blocks;
         // K runs a page ahead of V: K_0, K_1, V_0, K_2, V_1, ...
         const int n = pc.page1 - pc.page0;
+        float ks, vs;
         const int32_t* pages = a.page_table + (int64_t)pc.req * p.max_pages + pc.page0;
-        auto load_ids = [&](int first) {  // physical tiles of the lanes' pages first + lane
+        auto load_ids = [&](int first) {  // tiles of the lanes' pages first + lane, and their scales
           int id = 0;
           if (first + lane < n) {
             id = __ldg(pages + first + lane);
@@ -207,12 +218,25 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
               id = 0;
             }
           }
-          return id * p.Hkv + g;
+          id = id * p.Hkv + g;
+          ks = __ldg(kscale + id);
+          vs = __ldg(vscale + id);
+          return id;
+        };
+        // A page's scales reach the softmax by way of its K tile's barrier and the MMA thread.  (They are at
+        // most 32 + S + 2 pages old when the ring comes round: S of a page waits for P of an earlier one.)
+        auto send_scales = [&](int first) {
+          sm.scale[(it + first + lane) & 63] = make_float2(ks, scale_log2(vs));
+          __syncwarp();
         };
         int ids = load_ids(0), next_ids = 0, k_tile = 0;
+        send_scales(0);
         for (int s = 0; s <= n && ok; ++s) {
           const int at = s & 31, v_tile = k_tile;
-          if (s > 0 && at == 0) ids = next_ids;
+          if (s > 0 && at == 0) {
+            ids = next_ids;
+            send_scales(s);
+          }
           if (at == 8) next_ids = load_ids(s - 8 + 32);
           k_tile = __shfl_sync(0xffffffffu, ids, at);
           if (lane == 0) {
@@ -251,6 +275,7 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
         auto wait = [&](uint64_t& bar, uint32_t parity) {
           if (ok) ok = mbar_wait(smem_u32(&bar), parity, abort_flag, status);
         };
+        auto soon = [&](uint64_t& bar, uint32_t parity) { return ok = wait_soon(bar, parity, abort_flag, status); };
         struct Ring {
           uint32_t stage, phase;
           __device__ __forceinline__ Ring take(uint32_t n) {
@@ -266,41 +291,45 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
         auto commit = [&](uint64_t& bar) {
           mma_commit(smem_u32(&bar));
         };
-        // S_t = Q_q K^T
-        auto issue_s = [&](int t, int q, const Ring& k) {
-          tc_fence_after();
-          uint32_t qa = q_lo + q * (TQ >> 4), ka = k_lo + k.stage * (TK >> 4);
-          asm volatile("" : "+r"(qa), "+r"(ka));  // (sums made here, not kept from outside the loops)
+        // S_t = Q K^T from the operands' descriptors
+        auto mma_s = [&](int t, uint32_t tm, uint32_t qa, uint32_t ka) {
 #pragma unroll
           for (int pl = 0; pl < Smem::QPLANES; ++pl)
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8_ss(tmem + t * 128, sdesc_rows<D>(qa + ((pl * TK + kk * 32) >> 4)),
+              mma_f8_ss(tm + t * 128, sdesc_rows<D>(qa + ((pl * TK + kk * 32) >> 4)),
                         sdesc_rows<D>(ka + (kk * 32 >> 4)), IDESC_QK, pl + kk > 0);
+        };
+        // O_t (+)= P_t V for half a page's keys
+        auto pv_half = [&](int t, int h, uint32_t tm, uint32_t va, bool add) {
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            mma_f16_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_hi(va + kk * (2048 >> 4)), IDESC_PV,
+                       kk > 0 || add);
+        };
+        auto issue_s = [&](int t, int q, const Ring& k) {
+          tc_fence_after();
+          uint32_t qa = q_lo + q * (TQ >> 4), ka = k_lo + k.stage * (TK >> 4);
+          asm volatile("" : "+r"(qa), "+r"(ka));  // (sums made here, not kept from outside the loops)
+          mma_s(t, tmem, qa, ka);
           commit(sm.s_full[t]);
         };
-        // O_t (+)= P_t V in two halves of 64 keys, the first as soon as its P is there
+        // P V in two halves, the first as soon as its P is there
         auto issue_pv = [&](int t, const Ring& v, bool first, bool last) {
           uint32_t va = v_lo + v.stage * (TV >> 4);
           asm volatile("" : "+r"(va));
-          auto half = [&](int h) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-              mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                         sdesc_hi(va + kk * (2048 >> 4)), IDESC_PV, kk > 0 || !first);
-          };
           wait(sm.p_half[t], sc >> t & 1);
           if (first) {
             wait(sm.o_free[t], (oc >> t & 1) ^ 1);
             oc ^= 1u << t;
           }
           if (!ok) return;
-          half(0);
+          pv_half(t, 0, tmem, va, !first);
           wait(sm.p_full[t], sc >> t & 1);
           sc ^= 1u << t;
           if (!ok) return;
-          half(1);
+          pv_half(t, 1, tmem, va, true);
           if (last) commit(sm.o_done[t]);
         };
         uint32_t begun = 0;
@@ -308,13 +337,47 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
           *progress = ++begun;
           const int n = pc.page1 - pc.page0;
           // Steps: P V of a page and row tile (or chain), then S of the page that follows it there; two
-          // steps of S alone in front.  (One copy of each part: a block that walks through long code
-          // waits for its instructions.)
+          // steps of S alone in front.
           const bool split = SINGLE || pc.nt == 1;
           const int steps = split ? n : 2 * n;
           Ring k{0, 0}, v{0, 0};
 #pragma unroll 1
           for (int i = -2; i < steps && ok; ++i) {
+            // The steps between, in a straight line
+            if (i == 2 && (SINGLE || !split)) {
+#pragma unroll 1
+              for (; ok && i + (SINGLE ? 3 : 2) < steps; i += 2) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  if (SINGLE || t == 0) {
+                    v = vr.take(VS);
+                    if (!soon(sm.v_full[v.stage], v.phase)) break;
+                  }
+                  uint32_t va = v_lo + v.stage * (TV >> 4), qa = q_lo + (SINGLE ? 0 : t) * (TQ >> 4), tm = tmem;
+                  asm volatile("" : "+r"(va), "+r"(qa), "+r"(tm));  // (sums made here)
+                  if (!soon(sm.p_half[t], sc >> t & 1)) break;
+                  pv_half(t, 0, tm, va, true);
+                  if (!soon(sm.p_full[t], sc >> t & 1)) break;
+                  pv_half(t, 1, tm, va, true);
+                  if (SINGLE || t == 0) {
+                    k = kr.take(S);
+                    if (!soon(sm.k_full[k.stage], k.phase)) break;
+                  }
+                  uint32_t ka = k_lo + k.stage * (TK >> 4);
+                  asm volatile("" : "+r"(ka));
+                  mma_s(t, tm, qa, ka);
+                  commit(sm.s_full[t]);
+                  if (SINGLE || t == 1) {
+                    commit(sm.v_empty[v.stage]);
+                    commit(sm.k_empty[k.stage]);
+                  }
+                  if (i + 2 + (SINGLE ? t + 1 : 2) == steps) commit(sm.q_empty[SINGLE ? 0 : t]);
+                }
+                if (!ok) break;
+                sc ^= 3;
+              }
+              if (!ok) break;
+            }
             const int t = i & 1, pv = split ? i : i >> 1, sn = split ? i + 2 : pv + 1;
             const bool one = split || t == 0, both = split || t == 1;  // begins, ends with a K or V tile
             if (i >= 0) {
@@ -359,8 +422,6 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
     const int w = warp >= 8, quarter = warp % 4, row = quarter * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const uint32_t obase = tmem + lane_addr + 256 + w * 128;
-    const float* kscale = reinterpret_cast<const float*>(a.ks);
-    const float* vscale = reinterpret_cast<const float*>(a.vs);
     // The registers of this loop are a page's scores: what else lives through it is kept to little.  A
     // piece is read from the list where it is needed (again for the epilogue), and phases share a word.
     constexpr uint32_t kS = 1, kO = 2, kStat = 4, kQ = 8;  // uses of S_w, pieces in O_w, statistics, pieces
@@ -394,25 +455,26 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
       return r;
     };
     bool ok = true;
+    uint32_t next_at = 0;  // the block's pages before the next piece
     for (int i = 0; i < pieces && ok; ++i) {
       phase ^= kQ;
       bool split, active;
-      int n, step, g, vis;  // vis: keys of the page that the row sees (128 and more: all)
-      const int32_t* ids;   // the warpgroup's page-table entries, two ahead
+      int n, step, vis;  // vis: keys of the page that the row sees (128 and more: all)
+      uint32_t at = next_at;
       float c = a.c;
       {
         const Place r = read_piece(i, pc);
         // with one row tile, this warpgroup takes the pages of its parity
         split = r.split;
         n = pc.page1 - pc.page0;
+        next_at += n;
         step = split ? 2 : 1;
         if (split) n = (n + 1 - w) / 2;
         if (n == 0) continue;
-        const int page_a = pc.page0 + (split ? w : 0);
-        g = pc.vg / rp.blocks;
+        const int skip = split ? w : 0;
+        at += skip;
         active = __any_sync(0xffffffffu, r.valid);
-        ids = a.page_table + (int64_t)pc.req * p.max_pages + page_a;
-        vis = r.valid ? pc.ctx + r.tok + 1 - page_a * 128 : 0x40000000;
+        vis = r.valid ? pc.ctx + r.tok + 1 - (pc.page0 + skip) * 128 : 0x40000000;
         if (QB) {
           if (!mbar_wait_beside(smem_u32(&sm.q_seen[w]), is(kO), abort_flag, status, progress,
                                 a.skip_wait_ns))
@@ -420,100 +482,125 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
           c = r.valid ? c * __uint_as_float((uint32_t)sm.q_exp[is(kQ)][split ? 0 : w][row] << 23) : 0.f;
         }
       }
-      // the scales of this warpgroup's pages, one page ahead (their place, two)
-      auto tile_of = [&](int id) { return ((uint32_t)id < (uint32_t)p.num_phys ? id : 0) * p.Hkv + g; };
-      float ks1, vs1;
-      int id1 = __ldg(ids);
-      {
-        const int tile = tile_of(id1);
-        ks1 = __ldg(kscale + tile);
-        vs1 = __ldg(vscale + tile);
-        ids += step;
-        id1 = n > 1 ? __ldg(ids) : 0;
-      }
       float m = 0.f, l = 0.f;
       for (int j = 0; j < n; ++j) {
         const int nvis = vis;
         vis -= step * 128;
         const bool masked = __any_sync(0xffffffffu, nvis < 128);
-        // (a factor of zero would make NaN of a masked score's infinity)
-        const float ck = fmaxf(c * ks1, 1.18e-38f), e = scale_log2(vs1);
-        {
-          const int tile = tile_of(id1);
-          ks1 = __ldg(kscale + tile);
-          vs1 = __ldg(vscale + tile);
-          ids += step;
-          id1 = j + 2 < n ? __ldg(ids) : 0;
-        }
-        if (!mbar_wait_beside(smem_u32(&sm.s_full[w]), is(kS), abort_flag, status, progress,
-                              a.skip_wait_ns)) {
-          ok = false;
-          break;
+        if (__builtin_expect(!mbar_try_wait(smem_u32(&sm.s_full[w]), is(kS)), 0)) {
+          if (!mbar_wait_beside(smem_u32(&sm.s_full[w]), is(kS), abort_flag, status, progress,
+                                a.skip_wait_ns)) {
+            ok = false;
+            break;
+          }
         }
         phase ^= kS;  // (a commit covers what its thread issued before: the last product into O_w too)
         const uint32_t bar_half = smem_u32(&sm.p_half[w]), bar_full = smem_u32(&sm.p_full[w]);
-        bool half_sent = false;
-        if (active) {
-          tc_fence_after();
-          const uint32_t sbase = tmem + lane_addr + w * 128;
-          uint32_t v[4][32];
+        const float2 sc = sm.scale[at & 63];
+        at += step;
+        // (a factor of zero would make NaN of a masked score's infinity)
+        const float ck = fmaxf(c * sc.x, 1.18e-38f), e = sc.y;
+        const uint32_t sbase = tmem + lane_addr + w * 128;
+        auto exps = [&](const uint32_t (&v)[32], uint32_t* pk, uint64_t (&lsum)[2]) {  // P of 32 keys
+          const float off = e + kF16Bias - m;
+          const uint64_t c2 = pack_f32x2(ck, ck), off2 = pack_f32x2(off, off);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float x, y;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, off2), x, y);
+            x = fast_exp2(x);
+            y = fast_exp2(y);
+            lsum[(i >> 1) & 1] = add_f32x2(lsum[(i >> 1) & 1], pack_f32x2(x, y));
+            pk[i / 2] = pack_p<true>(x, y);
+          }
+        };
+        auto add_l = [&](const uint64_t (&lsum)[2]) {
+          float x, y, z, t;
+          unpack_f32x2(lsum[0], x, y);
+          unpack_f32x2(lsum[1], z, t);
+          l = fmaf((x + y) + (z + t), fast_exp2(-e), l);
+        };
+        tc_fence_after();
+        // The usual page, a straight line: the reference holds, so the first half's exponentials run under the
+        // second half's load.
+        bool usual = j > 0 && !masked && active;
+        if (__builtin_expect(usual, 1)) {
+          uint32_t v[4][32], pk[32];
           float red[4];
           uint64_t lsum[2] = {0, 0};
-          const uint64_t c2 = pack_f32x2(ck, ck);
-          auto exps = [&](int cc, uint32_t* pk) {  // P of the keys 32 cc .. 32 cc + 31
-            const float off = e + kF16Bias - m;
-            const uint64_t off2 = pack_f32x2(off, off);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x, y;
-              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[cc][i]), __uint_as_float(v[cc][i + 1])),
-                                     c2, off2), x, y);
-              x = fast_exp2(x);
-              y = fast_exp2(y);
-              lsum[(i >> 1) & 1] = add_f32x2(lsum[(i >> 1) & 1], pack_f32x2(x, y));
-              pk[i / 2] = pack_p<true>(x, y);
-            }
-          };
-          // The usual page (`fast`): the reference holds, so the first half's exponentials run under the
-          // second half's load.  The first page, a masked one, or one whose maximum asks for a rescale
-          // loads the whole row first.
-          bool fast = j > 0 && !masked;
-          uint32_t pk[32];
-          for (;;) {
-            if (fast) {
+          for (int cc = 0; cc < 2; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+          tmem_ld_wait();
 #pragma unroll
-              for (int cc = 0; cc < 2; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+          for (int cc = 0; cc < 2; ++cc) {
+            reg_fence(v[cc]);
+            reg_fence1(red[cc]);
+          }
+#pragma unroll
+          for (int cc = 2; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
+          exps(v[0], pk, lsum);
+          exps(v[1], pk + 16, lsum);
+          tmem_ld_wait();
+#pragma unroll
+          for (int cc = 2; cc < 4; ++cc) {
+            reg_fence(v[cc]);
+            reg_fence1(red[cc]);
+          }
+          const float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+          usual = !__any_sync(0xffffffffu, fmaf(mb, ck, e) - m > kRescale);
+          if (__builtin_expect(usual, 1)) {
+            tmem_st32(sbase, pk);
+            uint32_t pk2[32];
+            exps(v[2], pk2, lsum);  // under the store
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_half);  // the products of the first 64 keys may begin
+            tmem_st16(sbase + 32, *reinterpret_cast<uint32_t(*)[16]>(pk2));
+            exps(v[3], pk2 + 16, lsum);
+            tmem_st16(sbase + 48, *reinterpret_cast<uint32_t(*)[16]>(pk2 + 16));
+            add_l(lsum);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_full);
+          }
+        }
+        if (__builtin_expect(!usual, 0)) {
+          // The first page, a masked one, or one whose maximum asks for a rescale: the whole row's maximum
+          // first.  The second half is read for it, then the first, which becomes P, and the second again.
+          if (active) {
+            uint32_t v[2][32], pk[32];
+            float mb = -INFINITY;
+            uint64_t lsum[2] = {0, 0};
+#pragma unroll 1
+            for (int s = 0; s < 3; ++s) {
+              const int h = s == 1 ? 0 : 1;
+              float red[2];
+#pragma unroll
+              for (int cc = 0; cc < 2; ++cc) red[cc] = tmem_ld32_max(sbase + h * 64 + cc * 32, v[cc]);
               tmem_ld_wait();
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 reg_fence(v[cc]);
                 reg_fence1(red[cc]);
               }
+              if (masked) {
+                const int left = nvis - h * 64;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int cc = 2; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
-            } else {
-              for (bool again = true; again;) {
-                again = false;
+                for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) red[cc] = tmem_ld32_max(sbase + cc * 32, v[cc]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                  reg_fence(v[cc]);
-                  reg_fence1(red[cc]);
-                }
-                float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-                if (masked) {
-                  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                  for (int cc = 0; cc < 4; ++cc)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                      if (cc * 32 + i >= nvis) v[cc][i] = 0xff800000u;  // -inf
-                      mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(v[cc][i]));
-                    }
-                  mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                }
+                  for (int i = 0; i < 32; ++i) {
+                    if (cc * 32 + i >= left) v[cc][i] = 0xff800000u;  // -inf
+                    mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(v[cc][i]));
+                  }
+                red[0] = fmaxf(mx[0], mx[1]);
+                red[1] = fmaxf(mx[2], mx[3]);
+              }
+              if (s < 2) mb = fmaxf(mb, fmaxf(red[0], red[1]));
+              if (s == 0) continue;
+              if (s == 1) {
                 mb = fmaf(mb, ck, e);
                 const bool need = j > 0 && mb - m > kRescale;
                 if (j == 0) {
@@ -523,55 +610,34 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
                   if (need) m = mb;
                   l *= f;
 #pragma unroll 1
-                  for (int cc = 0; cc < D / 32; ++cc) {
-                    tmem_ld32(obase + cc * 32, v[0]);
+                  for (int d = 0; d < D / 32; ++d) {
+                    tmem_ld32(obase + d * 32, pk);
                     tmem_ld_wait();
-                    reg_fence(v[0]);
+                    reg_fence(pk);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                      v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
-                    tmem_st32(obase + cc * 32, v[0]);
+                    for (int i = 0; i < 32; ++i) pk[i] = __float_as_uint(__uint_as_float(pk[i]) * f);
+                    tmem_st32(obase + d * 32, pk);
                   }
                   tmem_st_wait();
-                  again = true;
                 }
               }
+              exps(v[0], pk, lsum);
+              exps(v[1], pk + 16, lsum);
+              tmem_st32(sbase + h * 32, pk);  // (over scores that have been read)
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(h ? bar_full : bar_half);
             }
-            lsum[0] = lsum[1] = 0;
-            exps(0, pk);
-            exps(1, pk + 16);
-            if (!fast) break;
-            tmem_ld_wait();
-#pragma unroll
-            for (int cc = 2; cc < 4; ++cc) {
-              reg_fence(v[cc]);
-              reg_fence1(red[cc]);
+            add_l(lsum);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar_half);
+              mbar_arrive(bar_full);
             }
-            const float mb = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-            if (!__any_sync(0xffffffffu, fmaf(mb, ck, e) - m > kRescale)) break;
-            fast = false;
           }
-          tmem_st32(sbase, pk);
-          uint32_t pk2[32];
-          exps(2, pk2);  // under the store
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_half);  // the products of the first 64 keys may begin
-          half_sent = true;
-          exps(3, pk2 + 16);
-          tmem_st32(sbase + 32, pk2);
-          float x, y, z, t;
-          unpack_f32x2(lsum[0], x, y);
-          unpack_f32x2(lsum[1], z, t);
-          l = fmaf((x + y) + (z + t), fast_exp2(-e), l);
-          tmem_st_wait();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (!half_sent) mbar_arrive(bar_half);
-          mbar_arrive(bar_full);
         }
       }
       if (!ok) break;
@@ -769,7 +835,7 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
       for (int j = 0; j < n && ok; ++j, ++it) {
         const uint32_t r = it % S, sg = it % VS;
         constexpr int CPR = D / 16;
-        if (!mbar_wait(smem_u32(&sm.raw_full[r]), (it / S) & 1, abort_flag, status)) {
+        if (!wait_soon(sm.raw_full[r], (it / S) & 1, abort_flag, status)) {
           ok = false;
           break;
         }
@@ -783,7 +849,7 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
 #pragma unroll
           for (int k = 0; k < CPR; ++k) x[k] = make_uint4(0, 0, 0, 0);
         }
-        if (!mbar_wait(smem_u32(&sm.v_empty[sg]), ((it / VS) & 1) ^ 1, abort_flag, status)) {
+        if (!wait_soon(sm.v_empty[sg], ((it / VS) & 1) ^ 1, abort_flag, status)) {
           ok = false;
           break;
         }
