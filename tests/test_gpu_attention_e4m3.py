@@ -261,6 +261,22 @@ def test_strided_views_without_lse_and_repeated_bits(q):
     assert torch.equal(c.out, first)
 
 
+@pytest.mark.parametrize("q", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,D", [(6, 128), (40, 64)])
+def test_outputs_that_are_16_byte_aligned_only(H, D, q):
+    """Rows of the output 16 bytes off every 32-byte border, or every other row of them, between guards."""
+    for pad, off in ((16, 8), (8, 0), (8, 8)):
+        c = Case(29, [200, 1, 64], [500, 70, 3], H, 2, D, q)
+        flat = torch.full((c.T + 1, H * D + pad), 7.0, dtype=torch.bfloat16, device=DEV)
+        c.out = flat[:c.T, off:off + H * D].view(c.T, H, D)
+        assert c.out.data_ptr() % 32 == 2 * off
+        c.run()
+        c.check()
+        guards = flat.clone()
+        guards[:c.T, off:off + H * D] = 7.0
+        assert bool((guards == 7.0).all())
+
+
 @pytest.mark.parametrize("q_lens,ctx,H", [([3, 130], [300, 0], 4), ([1, 1], [300, 0], 4), ([20, 20], [300, 0], 4)])
 def test_bad_page_is_reported(q_lens, ctx, H):
     c = Case(29, q_lens, ctx, H, 2, 64)
