@@ -57,7 +57,7 @@ struct E4Smem {
   static constexpr int QT = SINGLE ? 1 : 2;
   static constexpr int QPLANES = QB ? 2 : 1;
   static constexpr int TQ = QPLANES * TK;
-  static constexpr int kBudget = 227 * 1024 - 3072;  // less the barriers and row statistics
+  static constexpr int kBudget = 224 * 1024;  // 227 KB less the barriers and statistics
   static constexpr int VS = 2;
   static constexpr int S0 = (kBudget - QT * TQ - VS * TV) / (2 * TK);
   static constexpr int S = S0 > 8 ? 8 : S0;  // stages of the K ring and of the raw V ring
