@@ -271,7 +271,10 @@ cudaError_t run(const DevPlan& p, const DevRope& r, const KvRopeArgs& a, cudaStr
   auto kern = kv_append_e4m3_kernel<D, INTER, THREADS, ROWS>;  // ROWS: of a page, at most
   const int smem = ROWS * (D * 2 + r.rot * 4);
   if (smem > 32 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the room of the largest rotation, whatever this one is: the limit is the kernel's, and another thread
+    // may be between its own setting and its launch
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         ROWS * (D * 2 + D * 4));
     if (e != cudaSuccess) return e;
   }
   // heads a block: one, until the blocks fill the GPU several times; then a page's angles serve more
