@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(PageTableArgs a) 
 
 cudaError_t launch_page_tables(const PageTableArgs& a, cudaStream_t st) {
   const size_t smem = 8 * ((size_t)a.batch + 1);
-  if (smem > 48 * 1024) {
+  if (smem > 32 * 1024) {  // (48 KB without asking, less what the kernel declares itself)
     cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          8 * (kMaxTableBatch + 1));
     if (e != cudaSuccess) return e;
