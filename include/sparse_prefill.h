@@ -209,7 +209,7 @@ sps_status topk_select(const sps_plan* plan, const float* scores, int64_t score_
  *   k_cache, v_cache  device [num_phys_pages][H_kv][128][D] (BF16), or NVFP4 codes
  *                [..][128][D/2] with k_scales / v_scales [..][128][D/16] E4M3, or E4M3 codes with
  *                a scale for each page and KV head (sps_problem).  Slots behind a request's last
- *                token hold finite values
+ *                token hold finite values; in an E4M3 cache they may hold anything, NaN included
  *   page_table   device int32 [batch][max_pages_per_req]
  *   idx          device int32 [T*H][top_k] from topk_select (or any selection obeying its
  *                contract: ascending, -1 padded, pages <= own page)

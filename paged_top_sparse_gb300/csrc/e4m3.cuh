@@ -46,4 +46,14 @@ __device__ __forceinline__ void e4m3_tile_convert(const uint8_t* raw, uint8_t* d
   }
 }
 
+// Zeros in place of the rows from `rows` on, each 16 codes' by the thread that converted them.
+template <int D>
+__device__ __forceinline__ void e4m3_tile_clear(uint8_t* dst, int t, int nt, int rows) {
+#pragma unroll 1
+  for (int c = t; c < 128 * (D / 16); c += nt) {
+    const int row = c % 128, i = (c / 128 + row) % (D / 16);
+    if (row >= rows) e4m3_store16<false>(make_uint4(0, 0, 0, 0), dst, row, i);
+  }
+}
+
 }  // namespace sps
