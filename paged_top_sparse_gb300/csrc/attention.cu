@@ -587,9 +587,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (!mbar_wait(smem_u32(&sm.stat_full), sx & 1, abort_flag, status)) break;
         ++sx;
         const float2 o = sm.stat[row];
-        if (o.y > 0.f) {  // (0: the row sees nothing in the odd pages)
-          const float mm = l > 0.f ? fmaxf(m, o.x) : o.x;
-          f0 = l > 0.f ? fast_exp2((m - mm) * c) : 0.f;
+        if (o.y != 0.f) {  // (0: the row sees nothing in the odd pages; a NaN is no such row)
+          const float mm = l != 0.f ? fmaxf(m, o.x) : o.x;
+          f0 = l != 0.f ? fast_exp2((m - mm) * c) : 0.f;
           f1 = fast_exp2((o.x - mm) * c);
           l = l * f0 + o.y * f1;
           m = mm;
@@ -597,8 +597,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       if (active) {
         tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float lse = l > 0.f ? (m * c - bias + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const float lse = l != 0.f ? (m * c - bias + log2f(l)) * 0.6931471805599453f : -INFINITY;
         f0 *= inv;
         f1 *= inv;
         const bool whole = pc.page0 == 0 && pc.page1 == pc.pages;
@@ -866,13 +866,13 @@ attention_merge_rows_kernel(DevPlan p, AttArgs a) {
   sum += __shfl_xor_sync(0xffffffffu, sum, 8);
   sum += __shfl_xor_sync(0xffffffffu, sum, 16);
   if (ii == 0 && mine.live && a.out_lse)
-    a.out_lse[mine.flat * p.H + mine.head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+    a.out_lse[mine.flat * p.H + mine.head] = sum != 0.f ? mx + logf(sum) : -INFINITY;
 #pragma unroll
   for (int r = 0; r < kMergeRows; ++r) {
     const float s = __shfl_sync(0xffffffffu, sum, r);
     if (live >> r & 1)
       merge_store<D>(p, a, merge_row(p, rp, mg, lr0 + r), lane, acc[r],
-                     s > 0.f ? 1.f / s : 0.f);
+                     s != 0.f ? 1.f / s : 0.f);
   }
 }
 
@@ -950,9 +950,9 @@ attention_merge_pieces_kernel(DevPlan p, AttArgs a) {
 #pragma unroll
   for (int e = 0; e < E; ++e)
     for (int k = 1; k < 8; ++k) acc[e] += sums[k][lane * E + e];
-  merge_store<D>(p, a, row, lane, acc, sum > 0.f ? 1.f / sum : 0.f);
+  merge_store<D>(p, a, row, lane, acc, sum != 0.f ? 1.f / sum : 0.f);
   if (lane == 0 && a.out_lse)
-    a.out_lse[row.flat * p.H + row.head] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+    a.out_lse[row.flat * p.H + row.head] = sum != 0.f ? mx + logf(sum) : -INFINITY;
 }
 
 template <int D>

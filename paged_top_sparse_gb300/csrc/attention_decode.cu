@@ -387,12 +387,12 @@ decode_nvfp4_kernel(DevPlan p, AttArgs a) {
         for (int k = 0; k < WARPS; ++k) {
           const float2 x = sm.stat[k][r];
           f[k] = x.x;
-          if (x.y > 0.f) mx = fmaxf(mx, x.x);
+          if (x.y != 0.f) mx = fmaxf(mx, x.x);  // (0: nothing seen; a NaN is no such row)
         }
 #pragma unroll
         for (int k = 0; k < WARPS; ++k) {
           const float lk = sm.stat[k][r].y;
-          f[k] = lk > 0.f ? fast_exp2((f[k] - mx) * c) : 0.f;
+          f[k] = lk != 0.f ? fast_exp2((f[k] - mx) * c) : 0.f;
           sum += lk * f[k];
         }
 #pragma unroll
@@ -409,10 +409,10 @@ decode_nvfp4_kernel(DevPlan p, AttArgs a) {
               acc[e + 3] += f[k] * x.w;
             }
           }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
         if (tok < pc.q_len && tok < rp.TB) {
           const float lse =
-              sum > 0.f ? (mx * c - kF16Bias + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+              sum != 0.f ? (mx * c - kF16Bias + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           const int64_t flat = pc.flat0 + tok;
           const int head = pc.vg * p.Hg + hd;
           if (pc.page0 == 0 && pc.page1 == pc.pages) {

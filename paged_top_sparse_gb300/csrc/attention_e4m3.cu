@@ -657,9 +657,9 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
         if (!mbar_wait(smem_u32(&sm.stat_full), is(kStat), abort_flag, status)) break;
         phase ^= kStat;
         const float2 o = sm.stat[row];
-        if (o.y > 0.f) {  // (0: the row sees nothing in the odd pages)
-          const float mm = l > 0.f ? fmaxf(m, o.x) : o.x;
-          f0 = l > 0.f ? fast_exp2(m - mm) : 0.f;
+        if (o.y != 0.f) {  // (0: the row sees nothing in the odd pages; a NaN is no such row)
+          const float mm = l != 0.f ? fmaxf(m, o.x) : o.x;
+          f0 = l != 0.f ? fast_exp2(m - mm) : 0.f;
           f1 = fast_exp2(o.x - mm);
           l = l * f0 + o.y * f1;
           m = mm;
@@ -667,8 +667,8 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
       }
       if (active) {
         tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float lse = l > 0.f ? (m - kF16Bias + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const float lse = l != 0.f ? (m - kF16Bias + log2f(l)) * 0.6931471805599453f : -INFINITY;
         f0 *= inv;
         f1 *= inv;
         const bool whole = pc.page0 == 0 && pc.page1 == pc.pages;
