@@ -494,7 +494,8 @@ sps_status sparse_prefill_fwd_noalloc(const sps_plan* plan, const void* q, float
  * (BF16; FP16 over an NVFP4 cache, whose code x scale products are exact there, and over an E4M3 cache,
  * whose codes are: the page's V scale goes into P, its K scale into the scores' factor, whose product
  * with softmax_scale and q_scale is to stay within FP32; a BF16 query row is taken to 2^-17 of its largest
- * element there, in tiles of more than 16 rows as the sum of two E4M3 rows).  BF16 P takes V of
+ * element there, in tiles of more than 16 rows as the sum of two E4M3 rows, and to NaN where it holds an
+ * infinity).  BF16 P takes V of
  * any magnitude as it is, where sparse_prefill_fwd's FP16 P needs V within FP16's range; it costs
  * precision: 2.35e-3 relative L2 on random data against 1.7e-3 with FP16 P (and with the output's
  * own rounding alone).  The result is the same bits from call to call.  A captured call may be replayed after another plan that differs

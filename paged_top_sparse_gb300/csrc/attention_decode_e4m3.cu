@@ -179,7 +179,8 @@ decode_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
           float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const float s = row_scale(amax), inv = 1.f / s;
+          // (a row with an infinity becomes NaN, as in attention_e4m3.cu)
+          const float s = row_scale(amax), inv = isinf(amax) ? __uint_as_float(0x7fc00000u) : 1.f / s;
           f0 = pack_p<true>(f[0] * inv, f[1] * inv);
           f1 = pack_p<true>(f[2] * inv, f[3] * inv);
           if (lane == 0) sm.q_mul[r] = s;

@@ -791,7 +791,8 @@ attention_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, DevPlan p, AttArg
             }
           }
           mul = row_scale(__uint_as_float(mx));
-          inv = 1.f / mul;
+          // (an infinity has no E4M3 code: its row becomes NaN, which it would be at the end)
+          inv = mx < 0x7f800000u ? 1.f / mul : __uint_as_float(0x7fc00000u);
         } else {
           fetch(0);
         }

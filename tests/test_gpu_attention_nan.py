@@ -54,6 +54,13 @@ def test_rows_over_an_e4m3_cache(q_lens, ctx, H, G, D, q):
     _check_e4m3(q_lens, ctx, H, G, D, q, "nan")
 
 
+@pytest.mark.parametrize("value", ["inf", "-inf"])
+@pytest.mark.parametrize("q_lens,ctx,H,G,D", SHAPES)
+def test_an_infinite_query_over_an_e4m3_cache(q_lens, ctx, H, G, D, value):
+    """Its scores are infinite or NaN: so is their softmax."""
+    _check_e4m3(q_lens, ctx, H, G, D, "bf16", value)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
 @pytest.mark.parametrize("q_lens,ctx,H,G,D", SHAPES)
 def test_rows_over_the_other_caches(q_lens, ctx, H, G, D, kv):
