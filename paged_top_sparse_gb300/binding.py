@@ -215,6 +215,10 @@ def sps_plan_upload(plan: Plan, workspace, stream=None):
 
 def indexer_scores(plan: Plan, q_idx, q_scale, k_idx_cache, k_idx_scales, k_scale, page_table,
                    scores, workspace, stream=None):
+    """Page scores of every row.  Over an E4M3 K/V cache ``k_idx_cache`` is a cache of its own, of the plan's
+    idx_k_dtype (BF16 by default)."""
+    if plan.page_scales:
+        _index_keys(plan, k_idx_cache, k_idx_scales)
     _check(lib().indexer_scores(plan.handle, _ptr(q_idx), float(q_scale), _ptr(k_idx_cache),
                                 _ptr(k_idx_scales), float(k_scale), _ptr(page_table), _ptr(scores),
                                 scores.stride(0), _ptr(workspace), _stream(stream)))
@@ -229,40 +233,37 @@ def sparse_prefill_fwd(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_sca
                        idx, partial, lse, workspace, stream=None):
     """``partial`` is a [splits][rows][D] view (its stride(0) is the split stride); ``lse`` is
     [splits][rows] (stride(0) is the LSE split stride)."""
-    _check(lib().sparse_prefill_fwd(plan.handle, _ptr(q), float(q_scale), _ptr(k_cache),
-                                    _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
-                                    _ptr(idx), _ptr(partial), partial.stride(0), _ptr(lse),
-                                    lse.stride(0), _ptr(workspace), _stream(stream)))
+    _check(lib().sparse_prefill_fwd(plan.handle, _ptr(q), float(q_scale),
+                                    *_cache_ptrs(plan, k_cache, v_cache, k_scales, v_scales),
+                                    _ptr(page_table), _ptr(idx), _ptr(partial), partial.stride(0),
+                                    _ptr(lse), lse.stride(0), _ptr(workspace), _stream(stream)))
 
 
 def sparse_prefill_fwd_bf16(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_scales,
                             page_table, idx, partial, lse, workspace, stream=None):
     """As ``sparse_prefill_fwd`` with ``partial`` a BF16 [splits][rows][D] view."""
-    _check(lib().sparse_prefill_fwd_bf16(plan.handle, _ptr(q), float(q_scale), _ptr(k_cache),
-                                         _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                                         _ptr(page_table), _ptr(idx), _ptr(partial),
-                                         partial.stride(0), _ptr(lse), lse.stride(0),
-                                         _ptr(workspace), _stream(stream)))
+    _check(lib().sparse_prefill_fwd_bf16(plan.handle, _ptr(q), float(q_scale),
+                                         *_cache_ptrs(plan, k_cache, v_cache, k_scales, v_scales),
+                                         _ptr(page_table), _ptr(idx), _ptr(partial), partial.stride(0),
+                                         _ptr(lse), lse.stride(0), _ptr(workspace), _stream(stream)))
 
 
 def sparse_prefill_fwd_f16(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_scales,
                            page_table, idx, partial, lse, workspace, stream=None):
     """As ``sparse_prefill_fwd`` with ``partial`` an FP16 [splits][rows][D] view."""
-    _check(lib().sparse_prefill_fwd_f16(plan.handle, _ptr(q), float(q_scale), _ptr(k_cache),
-                                        _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                                        _ptr(page_table), _ptr(idx), _ptr(partial),
-                                        partial.stride(0), _ptr(lse), lse.stride(0),
-                                        _ptr(workspace), _stream(stream)))
+    _check(lib().sparse_prefill_fwd_f16(plan.handle, _ptr(q), float(q_scale),
+                                        *_cache_ptrs(plan, k_cache, v_cache, k_scales, v_scales),
+                                        _ptr(page_table), _ptr(idx), _ptr(partial), partial.stride(0),
+                                        _ptr(lse), lse.stride(0), _ptr(workspace), _stream(stream)))
 
 
 def sparse_prefill_fwd_fp8qk(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_scales,
                              page_table, idx, partial, lse, workspace, stream=None):
     """As ``sparse_prefill_fwd``: E4M3 Q, NVFP4 K rounded to E4M3, FP8 Q K^T (the pages' route)."""
-    _check(lib().sparse_prefill_fwd_fp8qk(plan.handle, _ptr(q), float(q_scale), _ptr(k_cache),
-                                          _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                                          _ptr(page_table), _ptr(idx), _ptr(partial),
-                                          partial.stride(0), _ptr(lse), lse.stride(0),
-                                          _ptr(workspace), _stream(stream)))
+    _check(lib().sparse_prefill_fwd_fp8qk(plan.handle, _ptr(q), float(q_scale),
+                                          *_cache_ptrs(plan, k_cache, v_cache, k_scales, v_scales),
+                                          _ptr(page_table), _ptr(idx), _ptr(partial), partial.stride(0),
+                                          _ptr(lse), lse.stride(0), _ptr(workspace), _stream(stream)))
 
 
 def sparse_prefill_fwd_noalloc(plan: Plan, q, q_scale, k_cache, v_cache, k_scales, v_scales,
@@ -270,9 +271,9 @@ def sparse_prefill_fwd_noalloc(plan: Plan, q, q_scale, k_cache, v_cache, k_scale
     """sparse_prefill_fwd without a workspace: the library's own fixed scratch array is used
     (for callers that cannot allocate device memory; see the header for the rules)."""
     _check(lib().sparse_prefill_fwd_noalloc(
-        plan.handle, _ptr(q), float(q_scale), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
-        _ptr(v_scales), _ptr(page_table), _ptr(idx), _ptr(partial), partial.stride(0), _ptr(lse),
-        lse.stride(0), _ptr(dev_status), _stream(stream)))
+        plan.handle, _ptr(q), float(q_scale),
+        *_cache_ptrs(plan, k_cache, v_cache, k_scales, v_scales), _ptr(page_table), _ptr(idx),
+        _ptr(partial), partial.stride(0), _ptr(lse), lse.stride(0), _ptr(dev_status), _stream(stream)))
 
 
 def partial_combine(partial, lse, out, out_lse=None, dev_status=None, stream=None):
@@ -303,7 +304,7 @@ def sps_kv_append(plan: Plan, k_new, v_new, page_table, k_cache, v_cache, k_scal
                   workspace, stream=None):
     """New tokens' K/V [T][H_kv][D] BF16 into the paged cache (the plan's kv dtype)."""
     _check(lib().sps_kv_append(plan.handle, _ptr(k_new), _ptr(v_new), _ptr(page_table),
-                               _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+                               *_cache_ptrs(plan, k_cache, v_cache, k_scales, v_scales),
                                _ptr(workspace), _stream(stream)))
 
 
@@ -382,6 +383,27 @@ def _caches(plan, k, v, k_scales, v_scales):
         if (t is None or t.element_size() != 1 or t.nbytes < n // 8 or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous bytes, >= {n // 8}")
     return k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr()
+
+
+def _cache_ptrs(plan, k, v, k_scales, v_scales):
+    """The addresses of the caches and scales; those of an E4M3 cache as ``_caches`` checks them (scales of
+    another type or of a smaller pool would be read, and by the append written, past their end)."""
+    if plan.page_scales:
+        return _caches(plan, k, v, k_scales, v_scales)
+    return _ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales)
+
+
+def _index_keys(plan, k, scales):
+    """Index keys beside an E4M3 cache: a cache of their own, of the plan's index type.  The E4M3 cache itself
+    is none (its scales differ from page to page)."""
+    elems = plan.cache_bytes
+    n, types, what = {BF16: (elems * 2, _BITS16, "bfloat16"), E4M3: (elems, _CODES8, "E4M3 codes"),
+                      NVFP4: (elems // 2, _CODES, "NVFP4 codes")}[plan.problem.idx_k_dtype]
+    if k.nbytes < n or k.dtype not in types or not k.is_contiguous():
+        raise ValueError(f"k_idx_cache must be contiguous {what} of >= {n} bytes, the plan's index keys")
+    if plan.problem.idx_k_dtype == NVFP4 and (scales is None or scales.element_size() != 1
+                                              or scales.nbytes < n // 8 or not scales.is_contiguous()):
+        raise ValueError(f"k_idx_scales must be contiguous bytes, >= {n // 8}")
 
 
 def _workspace(t, plan):
