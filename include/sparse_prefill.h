@@ -93,7 +93,7 @@ enum {
  * V an FP32 scale for each page and KV head, [num_phys_pages][H_kv]: an element is code x scale.  The
  * calls below take such scales as k_scales / v_scales (4-byte aligned), finite and >= 0; in
  * paged_attention_fwd a V scale counts as at least 2^-40 and at most 2^40, the range that
- * sps_kv_append writes.  Its codes are read by the attention calls and by no indexer (E4M3 index keys
+ * sps_kv_append writes (the sparse forwards take it as it is).  Its codes are read by the attention calls and by no indexer (E4M3 index keys
  * are a cache of their own, with one scale).
  */
 typedef struct {

@@ -19,19 +19,24 @@
 // Work, rows and merge are attention.cu's (256-row work tiles, the plan's pieces).
 //
 // Bound, prompts and chunks: the chain of a row tile, its softmax and its own products (256 or 512 cycles of
-// Q K^T, 512 of P V) with the hand-offs between, beside the other tile's; then the power limit.  D 128, H 32 /
-// H_kv 2: an 8192-token prompt 333 us with BF16 queries and 283 with E4M3 ones (1.65 and 1.94 PFLOP/s),
-// 8 x 512 after 32K 1136 and 998 us (1.95 and 2.22; over a BF16 cache 1394); D 64 278 and 264 us, where the
-// softmax's issue slots are the limit.  Few rows: the cache's bytes, 64 x 3 tokens after 32K 178 us (6.0 TB/s).
+// Q K^T, 512 of P V) with the hand-offs between, beside the other tile's; then the power limit.  No unit is
+// full: at D 128 the tensor pipe is 72 % busy (64 % with E4M3 queries) and the issue slots 44 %, at D 64 the
+// issue slots 46 %, exp2 and the tensor pipe 42 %.  H 32 / H_kv 2, an 8192-token prompt: 334 us with BF16
+// queries and 281 with E4M3 ones (1.65 and 1.95 PFLOP/s), D 64 279 and 265, where pages are alike; where
+// keys and values differ in size from page to page, by up to 3 and 16, 347 and 293 (294 and 279), by 4 and 8
+// 371 and 318 (298 and 283): a page above the reference takes the rolled code and rescales O.
+// 8 x 512 after 32K 1166 and 1023 us in short runs (1.90 and 2.17 PFLOP/s), 1205 to 1240 and 1026 to 1060 in
+// long ones, under the power limit.  Few rows: the cache's bytes, 64 x 3 tokens after 32K 178 us (6.0 TB/s).
 //
-// What a role executes per page is laid out by two measurements.  The four roles of a scheduler share little
-// code, and what they go through together does not fit next to the scheduler: with every inner loop unrolled
-// the prompt took 531 us in place of 390, and a second copy of the MMA steps 7 % more.  And a jump costs about
-// a hundred cycles of fetching: products in loops of one instruction took 480 us where straight lines took
-// 313.  So the page that is the rule, in the MMA's loop and in the softmax's, is a straight line; every
-// other page (first, masked, last, one that asks for a rescale) goes through rolled code beside it.  The straight
-// lines took the prompt from 358 to 333 us (BF16 queries) and from 313 to 283.  Half a page at a time, so
-// that products and exponentials of one tile overlap, doubles the hand-offs and the reads of Q (509 and 406).
+// What a role executes per page is laid out by two measurements (the prompt, pages of one scale).  The four roles
+// of a scheduler share little code, and what they go through together does not fit next to the scheduler: with
+// every inner loop unrolled the prompt took 531 us in place of 390, and a second copy of the MMA steps 7 % more.
+// And a jump costs about a hundred cycles of fetching: products in loops of one instruction took 480 us where
+// straight lines took 313.  So the page that is the rule, in the MMA's loop and in the softmax's, is a straight
+// line; every other page (first, masked, last, one that asks for a rescale) goes through rolled code beside it.
+// The straight lines took the prompt from 358 to 333 us (BF16 queries) and from 313 to 283.  Half a page at a
+// time, so that products and exponentials of one tile overlap, doubles the hand-offs and the reads of Q (509 and
+// 406).
 //
 // One persistent CTA per SM (512-column TMEM: S0 S1 O0 O1, 128 columns each):
 //   warp 0     page-table reads and the copies: K tiles by TMA (128-byte or, D = 64, 64-byte swizzle) into

@@ -16,8 +16,9 @@
 // angles are made once for all heads, and each row is worked out twice: for the maximum, then for the
 // codes.  D / 8 lanes hold a row, 8 elements (16 bytes) each.
 //
-// Bound: many tokens, the arithmetic of the rows worked out twice (65536 tokens of 8 heads, 403 MB: 153 us,
-// 2.6 TB/s); results kept in registers instead halve the warps on an SM (186 us), and rows unrolled cost
+// Bound: many tokens, the rows worked out twice: 65536 tokens of 8 heads, 403 MB, take 153 us (2.6 TB/s) with
+// the issue slots 68 % and the ALU 45 % busy, so that no unit is full and the waits between a row's steps
+// count as well; results kept in registers instead halve the warps on an SM (186 us), and rows unrolled cost
 // instruction fetches (349).  Angles read a lane's own pairs in a row put every fourth lane on one bank:
 // 332 us against 204.  4096 tokens of 2 heads 8.1 us, a decode step of 64 3.3 (a chain of the list, the
 // page table, the rows, the maximum): `sps_kv_append_rope` into a BF16 cache takes 5.3 and 2.3.

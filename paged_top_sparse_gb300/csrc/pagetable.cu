@@ -9,10 +9,12 @@
 // counter is read by every block and advanced by the last one to have read it, which a ticket beside it
 // shows; results do not depend on the order.
 //
-// What it reads and writes is a few hundred KB at most (64 single tokens: 4 KB), so it is bound by one
+// It writes 12 bytes for each of max_tokens and reads 8 bytes for each request in every block.  At the sizes
+// of a step that is little (64 single tokens 4 KB, 64K tokens of 256 requests 0.8 MB), so it is bound by one
 // pass of latency: the counter, the lengths, two scans, the bisections (8 steps for 256 requests).  64
 // requests of one token take 2.8 us on the GPU, 256 requests of 64K tokens together 4.5 us.  A launch for
-// the sums and one for the maps would take two such passes.
+// the sums and one for the maps would take two such passes.  A thread's lengths lie in a row, so a large
+// batch costs each block strided reads: 1000 requests of one token 4.0 us, 4096 10.4, 16384 53.
 #include <algorithm>
 
 #include "ptx.cuh"
